@@ -381,6 +381,96 @@ TPMLP_API tpmlp_status tpmlp_sp_backward_fp8(const void* const* X_chunks, const 
                                              void* dbeta, void* dHq_out, void* workspace, size_t workspace_bytes,
                                              tpmlp_stream_t stream);
 
+/* ------------------------------------------------------------------ block-scaled FP8
+ * Next to the per-tensor scales above (deep-dive page, section "FP8 하이브리드
+ * 정밀도 및 지연 스케일링"): 8-bit operands that carry one fp32 scale for each block
+ * of 128 elements along K, taken from the block's own values, so that a large
+ * channel or token costs its block's precision only and no amax history is
+ * needed.  Conventions of the calls of this section:
+ *  - Q [R x K], row-major bytes, stands for Q * scale.  Scale layouts:
+ *    block_rows = 1:   one scale per row and block of 128 columns, stored
+ *                      [ceil(K / 128) x R_pad], R_pad = 128 ceil(R / 128): entry
+ *                      kb R_pad + r.  Entries r >= R are neither written nor
+ *                      used;
+ *    block_rows = 128: one scale per tile of 128 x 128, stored
+ *                      [ceil(R / 128) x ceil(K / 128)].
+ *    A last block shorter than 128 is a block of its own.
+ *  - A block with largest magnitude amax has scale = a / F and the codes
+ *    FP8(x * (F / a)), a = min(max(amax, 2^-100), FLT_MAX), F = 448 (E4M3) or
+ *    57344 (E5M2); both quotients and the product in fp32, the cast to nearest
+ *    even and saturating.  A NaN stays a NaN and does not count for amax; an
+ *    infinity becomes +-F.
+ *  - Formats: 0 = E4M3, 1 = E5M2.  Pointers are 16-byte aligned.  No call of this
+ *    section uses atomics or a workspace other than its own argument: results do
+ *    not change from run to run. */
+
+/* Residual RMS norm into the gathered buffer (tpmlp_rmsnorm_gather with the
+ * block's residual addition and an 8-bit output):
+ *   s = bf16(X_j + R_j) (X_j itself when R_chunks == NULL),
+ *   y = s rsqrt(mean(s^2) + eps) weight, the statistics and y in fp32,
+ *   S_chunks[j] = s, Xg = bf16(y), Xq / x_scales = y in E4M3 with 1 x 128 blocks.
+ * y is rounded once, to each output; tpmlp_rmsnorm_gather rounds x rstd to bf16
+ * before the weight, as its listing does.
+ *   X_chunks, R_chunks, S_chunks: host arrays of N pointers [T/N x d]; R_chunks and
+ *   S_chunks may be NULL (S_chunks without R_chunks is an error), and S_chunks[j]
+ *   may be X_chunks[j] or R_chunks[j] (the sum in place).  Xg: NULL or [T x d] bf16.
+ *   Xq: NULL or [T x d] E4M3, with x_scales (block_rows = 1, R = T); d % 16 == 0 then.
+ *   At least one of Xg and Xq.  d <= 32768 (TPMLP_ERR_UNSUPPORTED otherwise). */
+TPMLP_API tpmlp_status tpmlp_rmsnorm_add_gather(const void* const* X_chunks, const void* const* R_chunks,
+                                                const void* weight, float eps, const tpmlp_shape* shape,
+                                                void* const* S_chunks, void* Xg, void* Xq, float* x_scales,
+                                                tpmlp_stream_t stream);
+
+/* Bytes of workspace tpmlp_rmsnorm_add_backward needs (host arithmetic only). */
+TPMLP_API tpmlp_status tpmlp_rmsnorm_add_backward_workspace_size(const tpmlp_shape* shape, size_t* bytes);
+
+/* Backward of tpmlp_rmsnorm_add_gather: with xhat = s rsqrt(mean(s^2) + eps) and
+ * g = dXg weight, dX = rstd (g - xhat mean(g xhat)) + dS, the gradient of X and of R
+ * alike; dweight = sum over all T rows of dXg xhat (fp32 [d]).
+ *   S_chunks: the forward's sums (its X_chunks when it had no residual); dXg
+ *   [T x d] bf16; dS_chunks: the gradient that reaches the sum on the residual
+ *   stream, or NULL; dX_chunks out, [T/N x d] bf16 each; dX_chunks[j] may be
+ *   dS_chunks[j] or S_chunks[j].  d <= 32768. */
+TPMLP_API tpmlp_status tpmlp_rmsnorm_add_backward(const void* const* S_chunks, const void* weight, float eps,
+                                                  const void* dXg, const void* const* dS_chunks,
+                                                  const tpmlp_shape* shape, void* const* dX_chunks, float* dweight,
+                                                  void* workspace, size_t workspace_bytes, tpmlp_stream_t stream);
+
+/* Block quantiser, the block-scaled counterpart of tpmlp_cast_e4m3 / _e5m2: src
+ * [rows x cols] bf16 with ld elements between rows (ld % 8 == 0, ld >= cols,
+ * cols % 16 == 0), as it stands, transposed, or both from one read of src:
+ *   q [rows x cols] with scales (R = rows, K = cols), or both NULL;
+ *   qT [cols x P], P = 16 ceil(rows / 16), with scalesT (R = cols, K = rows), or
+ *   both NULL; its bytes r >= rows are zero, so that P serves as a K.
+ * block_rows 1 or 128.  With 128 both outputs hold the same codes; with 1 the
+ * blocks of q run along a row of src, those of qT along a column. */
+TPMLP_API tpmlp_status tpmlp_quantize_block(const void* src, int64_t ld, int64_t rows, int64_t cols, int block_rows,
+                                            int fmt, void* q, float* scales, void* qT, float* scalesT,
+                                            tpmlp_stream_t stream);
+
+/* C = A8 B8^T + bias on block-scaled operands: each block of 128 along K is summed
+ * on the tensor cores, scaled by both its scales and added to an fp32 sum.
+ *   A8 [M x K] (a_fmt) with a_scales of block_rows = 1; B8 [N x K] (b_fmt) with
+ *   b_scales of b_block_rows 1 (a weight gradient, K = tokens) or 128 (weights);
+ *   bias [N] bf16 or NULL; C [M x N] in c_dtype (TPMLP_BF16 or TPMLP_FP32) with ldc
+ *   elements between rows.  K % 16 == 0, N % 8 == 0, ldc % 8 == 0, ldc >= N. */
+TPMLP_API tpmlp_status tpmlp_gemm_fp8_block(const void* A8, int a_fmt, const float* a_scales, const void* B8, int b_fmt,
+                                            const float* b_scales, int b_block_rows, int64_t M, int64_t N, int64_t K,
+                                            const void* bias, void* C, int c_dtype, int64_t ldc,
+                                            tpmlp_stream_t stream);
+
+/* Column-parallel GEMM on block-scaled E4M3 operands with its activation:
+ * P = Xq AqT^T + bias, Hq / h_scales = GeLU(P) in E4M3 with 1 x 128 blocks (R = T,
+ * K = F), Hpre (NULL or [T x F] bf16) = P.  Xq [T x d] with x_scales (block_rows =
+ * 1), AqT [F x d] with a_scales (block_rows = 128), bias [F] bf16 or NULL, Hq
+ * [T x F].  d % 16 == 0, F % 16 == 0.  (Xq, x_scales) are
+ * tpmlp_rmsnorm_add_gather's outputs, (AqT, a_scales) the transposed ones of
+ * tpmlp_quantize_block of A, and (Hq, h_scales) an A operand of
+ * tpmlp_gemm_fp8_block. */
+TPMLP_API tpmlp_status tpmlp_gemm1_fp8_block(const void* Xq, const float* x_scales, const void* AqT,
+                                             const float* a_scales, const void* bias, const tpmlp_shape* shape,
+                                             void* Hq, float* h_scales, void* Hpre, tpmlp_stream_t stream);
+
 /* ------------------------------------------------------------------ single steps (bf16)
  * Each step is one kernel launch (plus a small fixed-order reduction where
  * noted); the block calls above are sequences of these.  They take explicit

@@ -1,8 +1,9 @@
 """Python binding of ``libtpmlp.so`` (the C ABI in ``include/tpmlp.h``).
 
-Argument marshalling only: every function here checks nothing the library
-does not check itself, computes nothing, and calls exactly one ABI entry
-point with the same name.  Tensors are torch tensors on the current CUDA
+Argument marshalling only: every function here computes nothing and calls
+exactly one ABI entry point with the same name, and checks nothing the library
+does not check itself (the block-scaled FP8 calls add checks of layouts and
+sizes, see there).  Tensors are torch tensors on the current CUDA
 device; shapes are read from them.  PyTorch is used only for device memory
 (the workspace) and streams.  If the library is missing the first call
 raises; there is no fallback path.
@@ -118,6 +119,15 @@ _SIGS = {
                                     ctypes.c_int),
     "tpmlp_sp_backward_fp8": ([_PP, _P, ctypes.c_float, _P, _P, _P, _P, _P, _PP, _FP, _FP, _SP, _PP, _P, _P, _P, _P,
                                _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "tpmlp_rmsnorm_add_gather": ([_PP, _PP, _P, ctypes.c_float, _SP, _PP, _P, _P, _P, _P], ctypes.c_int),
+    "tpmlp_rmsnorm_add_backward_workspace_size": ([_SP, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
+    "tpmlp_rmsnorm_add_backward": ([_PP, _P, ctypes.c_float, _P, _PP, _SP, _PP, _P, _P, ctypes.c_size_t, _P],
+                                   ctypes.c_int),
+    "tpmlp_quantize_block": ([_P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int, _P, _P,
+                              _P, _P, _P], ctypes.c_int),
+    "tpmlp_gemm_fp8_block": ([_P, ctypes.c_int, _P, _P, ctypes.c_int, _P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
+                              ctypes.c_int64, _P, _P, ctypes.c_int, ctypes.c_int64, _P], ctypes.c_int),
+    "tpmlp_gemm1_fp8_block": ([_P, _P, _P, _P, _P, _SP, _P, _P, _P, _P], ctypes.c_int),
 }
 
 
@@ -603,6 +613,119 @@ def tpmlp_attention_tp_backward(X, Wqkv, Wo, QKV, O, LSE, dY, S, B, H, N, dX, dW
         _ptr(dX), _ptr(dWqkv), _ptr(dbqkv), _ptr(dWo), _ptr(dbo), _ptr(dQKV_out), _ptr(ws), ws.numel(),
         _stream(stream)))
     return dX
+
+
+# ----------------------------------------------------------------------------- block-scaled FP8
+#
+# These functions also refuse (ERR_INVALID_ARG) tensors whose layout the ABI cannot express or whose size does not
+# fit the others': the library sees addresses only, and a scale buffer that is too small would be read past its end.
+
+def block_scales_shape(rows, cols, block_rows=1):
+    """Shape of the fp32 scales of an 8-bit operand [rows x cols] with blocks of block_rows x 128."""
+    kb = (cols + 127) // 128
+    return (kb, (rows + 127) // 128 * 128) if block_rows == 1 else ((rows + 127) // 128, kb)
+
+
+def _fits(t, itemsize, numel):
+    return t is None or (t.is_contiguous() and t.element_size() == itemsize and t.numel() >= numel)
+
+
+def _refuse_unless(ok, fn):
+    if not ok:
+        raise TpMlpError(fn, ERR_INVALID_ARG)
+
+
+def _chunks_fit(chunks, n, numel):
+    return chunks is None or (len(chunks) == n and all(_fits(t, 2, numel) for t in chunks))
+
+
+def _scale_count(rows, cols, block_rows=1):
+    a, b = block_scales_shape(rows, cols, block_rows)
+    return a * b
+
+
+def tpmlp_rmsnorm_add_gather(X_chunks, weight, N, R_chunks=None, S_chunks=None, Xg=None, Xq=None, x_scales=None,
+                             eps=1e-5, stream=None):
+    """S_j = X_j + R_j; Xg and / or (Xq, x_scales) = the RMS norm of S, gathered, in bf16 and / or block-scaled E4M3."""
+    rows, d = X_chunks[0].shape
+    T = rows * N
+    _refuse_unless(_chunks_fit(X_chunks, N, rows * d) and _chunks_fit(R_chunks, N, rows * d) and
+                   _chunks_fit(S_chunks, N, rows * d) and _fits(weight, 2, d) and _fits(Xg, 2, T * d) and
+                   _fits(Xq, 1, T * d) and _fits(x_scales, 4, _scale_count(T, d)), "tpmlp_rmsnorm_add_gather")
+    shape = make_shape(T, d, d * N, N)
+    xp, _xa = _ptrs(X_chunks)
+    rp, _ra = _opt_ptrs(R_chunks)
+    sp, _sa = _opt_ptrs(S_chunks)
+    _check("tpmlp_rmsnorm_add_gather", lib().tpmlp_rmsnorm_add_gather(
+        xp, rp, _ptr(weight), eps, ctypes.byref(shape), sp, _ptr(Xg), _ptr(Xq), _ptr(x_scales), _stream(stream)))
+
+
+def tpmlp_rmsnorm_add_backward_workspace_size(T, d, N) -> int:
+    n = ctypes.c_size_t(0)
+    _check("tpmlp_rmsnorm_add_backward_workspace_size", lib().tpmlp_rmsnorm_add_backward_workspace_size(
+        ctypes.byref(make_shape(T, d, d * N, N)), ctypes.byref(n)))
+    return n.value
+
+
+def tpmlp_rmsnorm_add_backward(S_chunks, weight, dXg, N, dX_chunks, dweight, dS_chunks=None, eps=1e-5, ws=None,
+                               stream=None):
+    rows, d = S_chunks[0].shape
+    T = rows * N
+    _refuse_unless(_chunks_fit(S_chunks, N, rows * d) and _chunks_fit(dS_chunks, N, rows * d) and
+                   _chunks_fit(dX_chunks, N, rows * d) and _fits(weight, 2, d) and _fits(dXg, 2, T * d) and
+                   _fits(dweight, 4, d), "tpmlp_rmsnorm_add_backward")
+    shape = make_shape(T, d, d * N, N)
+    if ws is None:
+        ws = torch.empty(max(tpmlp_rmsnorm_add_backward_workspace_size(T, d, N), 256), dtype=torch.uint8,
+                         device=weight.device)
+    xp, _xa = _ptrs(S_chunks)
+    rp, _ra = _opt_ptrs(dS_chunks)
+    dp, _da = _ptrs(dX_chunks)
+    _check("tpmlp_rmsnorm_add_backward", lib().tpmlp_rmsnorm_add_backward(
+        xp, _ptr(weight), eps, _ptr(dXg), rp, ctypes.byref(shape), dp, _ptr(dweight), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def tpmlp_quantize_block(src, block_rows=1, fmt=E4M3, q=None, scales=None, qT=None, scalesT=None, stream=None):
+    """8-bit codes and block scales of src [rows x cols] bf16 (rows may be strided), as it stands and / or transposed."""
+    rows, cols = src.shape
+    _refuse_unless((rows <= 1 or cols == 0 or src.stride(1) == 1) and src.element_size() == 2 and
+                   _fits(q, 1, rows * cols) and _fits(scales, 4, _scale_count(rows, cols, block_rows)) and
+                   _fits(qT, 1, cols * ((rows + 15) // 16 * 16)) and
+                   _fits(scalesT, 4, _scale_count(cols, rows, block_rows)), "tpmlp_quantize_block")
+    ld = src.stride(0) if rows > 1 else cols
+    _check("tpmlp_quantize_block", lib().tpmlp_quantize_block(
+        _ptr(src), ld, rows, cols, block_rows, fmt, _ptr(q), _ptr(scales), _ptr(qT), _ptr(scalesT), _stream(stream)))
+
+
+def tpmlp_gemm_fp8_block(A8, a_scales, B8, b_scales, C, bias=None, b_block_rows=128, a_fmt=E4M3, b_fmt=E4M3,
+                         stream=None):
+    """C [M x N] (bf16 or fp32, rows may be strided) = A8 [M x K] . B8 [N x K]^T with their block scales, + bias."""
+    M, K = A8.shape
+    N = B8.shape[0]
+    _refuse_unless(B8.shape[1] == K and C.shape[0] == M and C.shape[1] == N and _fits(A8, 1, M * K) and
+                   _fits(B8, 1, N * K) and _fits(a_scales, 4, _scale_count(M, K)) and
+                   _fits(b_scales, 4, _scale_count(N, K, b_block_rows)) and _fits(bias, 2, N) and
+                   (N <= 1 or C.stride(1) == 1) and C.dtype in (torch.bfloat16, torch.float32),
+                   "tpmlp_gemm_fp8_block")
+    ldc = C.stride(0) if M > 1 else N
+    _check("tpmlp_gemm_fp8_block", lib().tpmlp_gemm_fp8_block(
+        _ptr(A8), a_fmt, _ptr(a_scales), _ptr(B8), b_fmt, _ptr(b_scales), b_block_rows, M, N, K, _ptr(bias), _ptr(C),
+        _dtype_code(C), ldc, _stream(stream)))
+
+
+def tpmlp_gemm1_fp8_block(Xq, x_scales, AqT, a_scales, bias, N, Hq, h_scales, Hpre=None, stream=None):
+    """(Hq, h_scales) = GeLU(Xq . AqT^T + bias) in block-scaled E4M3; Hpre = the pre-activation in bf16."""
+    T, d = Xq.shape
+    F = AqT.shape[0]
+    _refuse_unless(AqT.shape[1] == d and _fits(Xq, 1, T * d) and _fits(AqT, 1, F * d) and
+                   _fits(x_scales, 4, _scale_count(T, d)) and _fits(a_scales, 4, _scale_count(F, d, 128)) and
+                   _fits(bias, 2, F) and _fits(Hq, 1, T * F) and _fits(h_scales, 4, _scale_count(T, F)) and
+                   _fits(Hpre, 2, T * F), "tpmlp_gemm1_fp8_block")
+    shape = make_shape(T, d, F, N)
+    _check("tpmlp_gemm1_fp8_block", lib().tpmlp_gemm1_fp8_block(
+        _ptr(Xq), _ptr(x_scales), _ptr(AqT), _ptr(a_scales), _ptr(bias), ctypes.byref(shape), _ptr(Hq),
+        _ptr(h_scales), _ptr(Hpre), _stream(stream)))
 
 
 def tpmlp_selftest_wait_timeout(budget_us: int, stream=None):

@@ -9,6 +9,7 @@
 #include <utility>
 
 #include "../../include/tpmlp.h"
+#include "block_fp8.h"
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -1324,6 +1325,154 @@ tpmlp_status tpmlp_sp_backward_fp8(const void* const* X_chunks, const void* gamm
   if (e == cudaSuccess)
     e = launch_fp8_update(grad->scale, grad->amax, grad->history, 2, grad->history_len, 57344.f, grad->margin, s);
   return cuda_status(e);
+}
+
+// ------------------------------------------------------------------ block-scaled FP8
+
+tpmlp_status tpmlp_rmsnorm_add_gather(const void* const* X_chunks, const void* const* R_chunks, const void* weight,
+                                      float eps, const tpmlp_shape* shape, void* const* S_chunks, void* Xg, void* Xq,
+                                      float* x_scales, tpmlp_stream_t stream) {
+  tpmlp_status st = check_shape(shape, true, true);
+  if (st != TPMLP_OK) return st;
+  if (shape->tokens == 0) return TPMLP_OK;  // empty batch: nothing to launch, pointers may be NULL
+  const int n = shape->n_shards;
+  if (!ptrs_ok({weight}) || !chunks_ok(X_chunks, n) || (R_chunks != nullptr && !chunks_ok(R_chunks, n)) ||
+      (S_chunks != nullptr && (R_chunks == nullptr || !chunks_ok(S_chunks, n))) || !opt_ok(Xg) || !opt_ok(Xq) ||
+      !opt_ok(x_scales) || (Xq == nullptr) != (x_scales == nullptr) || (Xg == nullptr && Xq == nullptr) ||
+      (Xq != nullptr && shape->d % 16 != 0) || !(eps >= 0.f))
+    return TPMLP_ERR_INVALID_ARG;
+  if (shape->d > kBlockMaxD) return TPMLP_ERR_UNSUPPORTED;
+  DeviceCtx c;
+  if ((st = device_ctx(&c)) != TPMLP_OK) return st;
+  RmsBlockParams p{};
+  p.x = to_const_chunks(X_chunks, n);
+  if (R_chunks != nullptr) p.r = to_const_chunks(R_chunks, n);
+  if (S_chunks != nullptr) p.s = to_chunks(S_chunks, n);
+  p.weight = weight;
+  p.xg = Xg;
+  p.xq = static_cast<uint8_t*>(Xq);
+  p.scales = x_scales;
+  p.rows = static_cast<int>(shape->tokens);
+  p.d = static_cast<int>(shape->d);
+  p.n_chunks = n;
+  p.rows_per_chunk = p.rows / n;
+  p.rows_pad = pad128(p.rows);
+  p.eps = eps;
+  return cuda_status(launch_rmsnorm_add(p, c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tpmlp_status tpmlp_rmsnorm_add_backward_workspace_size(const tpmlp_shape* shape, size_t* bytes) {
+  if (bytes == nullptr) return TPMLP_ERR_INVALID_ARG;
+  const tpmlp_status st = check_shape(shape, true, true);
+  if (st != TPMLP_OK) return st;
+  if (shape->d > kBlockMaxD) return TPMLP_ERR_UNSUPPORTED;
+  *bytes = align_up(rmsnorm_add_bwd_scratch_floats(static_cast<int>(shape->tokens), static_cast<int>(shape->d)) * 4);
+  return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_rmsnorm_add_backward(const void* const* S_chunks, const void* weight, float eps, const void* dXg,
+                                        const void* const* dS_chunks, const tpmlp_shape* shape,
+                                        void* const* dX_chunks, float* dweight, void* workspace,
+                                        size_t workspace_bytes, tpmlp_stream_t stream) {
+  tpmlp_status st = check_shape(shape, true, true);
+  if (st != TPMLP_OK) return st;
+  if (shape->tokens == 0) return TPMLP_OK;  // empty batch: nothing to launch, pointers may be NULL
+  const int n = shape->n_shards;
+  if (!ptrs_ok({weight, dXg, dweight}) || !chunks_ok(S_chunks, n) || !chunks_ok(dX_chunks, n) ||
+      (dS_chunks != nullptr && !chunks_ok(dS_chunks, n)) || !(eps >= 0.f))
+    return TPMLP_ERR_INVALID_ARG;
+  size_t need = 0;
+  if ((st = tpmlp_rmsnorm_add_backward_workspace_size(shape, &need)) != TPMLP_OK) return st;
+  if (workspace == nullptr || !al16(workspace) || workspace_bytes < need) return TPMLP_ERR_WORKSPACE;
+  DeviceCtx c;
+  if ((st = device_ctx(&c)) != TPMLP_OK) return st;
+  RmsBlockParams p{};
+  p.x = to_const_chunks(S_chunks, n);
+  if (dS_chunks != nullptr) p.r = to_const_chunks(dS_chunks, n);
+  p.s = to_chunks(dX_chunks, n);
+  p.weight = weight;
+  p.dy = dXg;
+  p.partial = static_cast<float*>(workspace);
+  p.rows = static_cast<int>(shape->tokens);
+  p.d = static_cast<int>(shape->d);
+  p.n_chunks = n;
+  p.rows_per_chunk = p.rows / n;
+  p.eps = eps;
+  return cuda_status(launch_rmsnorm_add_bwd(p, dweight, c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tpmlp_status tpmlp_quantize_block(const void* src, int64_t ld, int64_t rows, int64_t cols, int block_rows, int fmt,
+                                  void* q, float* scales, void* qT, float* scalesT, tpmlp_stream_t stream) {
+  if (rows < 0 || cols < 0 || cols % 16 != 0 || ld < cols || ld % 8 != 0 || (block_rows != 1 && block_rows != 128) ||
+      (fmt != 0 && fmt != 1))
+    return TPMLP_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return TPMLP_OK;
+  if (!ptrs_ok({src}) || !opt_ok(q) || !opt_ok(scales) || !opt_ok(qT) || !opt_ok(scalesT) ||
+      (q == nullptr) != (scales == nullptr) || (qT == nullptr) != (scalesT == nullptr) ||
+      (q == nullptr && qT == nullptr))
+    return TPMLP_ERR_INVALID_ARG;
+  if (rows > INT_MAX / 2 || cols > INT_MAX / 2 || (rows + kBlock - 1) / kBlock > 65535) return TPMLP_ERR_UNSUPPORTED;
+  QuantBlockParams p{src, ld, static_cast<int>(rows), static_cast<int>(cols), block_rows, fmt,
+                     static_cast<uint8_t*>(q), scales, static_cast<uint8_t*>(qT), scalesT};
+  return cuda_status(launch_quantize_block(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tpmlp_status tpmlp_gemm_fp8_block(const void* A8, int a_fmt, const float* a_scales, const void* B8, int b_fmt,
+                                  const float* b_scales, int b_block_rows, int64_t M, int64_t N, int64_t K,
+                                  const void* bias, void* C, int c_dtype, int64_t ldc, tpmlp_stream_t stream) {
+  if (M < 0 || N < 0 || K < 0 || K % 16 != 0 || N % 8 != 0 || ldc < N || ldc % 8 != 0 ||
+      (a_fmt != 0 && a_fmt != 1) || (b_fmt != 0 && b_fmt != 1) || (b_block_rows != 1 && b_block_rows != 128) ||
+      (c_dtype != TPMLP_BF16 && c_dtype != TPMLP_FP32))
+    return TPMLP_ERR_INVALID_ARG;
+  if (M > INT_MAX / 2 || N > INT_MAX / 2 || K > INT_MAX / 2) return TPMLP_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return TPMLP_OK;
+  if (!ptrs_ok({A8, a_scales, B8, b_scales, C}) || !opt_ok(bias) || K == 0) return TPMLP_ERR_INVALID_ARG;
+  DeviceCtx c;
+  const tpmlp_status st = device_ctx(&c);
+  if (st != TPMLP_OK) return st;
+  GemmBlockLaunch g{};
+  g.a = static_cast<const uint8_t*>(A8);
+  g.b = static_cast<const uint8_t*>(B8);
+  g.a_scales = a_scales;
+  g.b_scales = b_scales;
+  g.b_block_rows = b_block_rows;
+  g.a_fmt = a_fmt;
+  g.b_fmt = b_fmt;
+  g.M = static_cast<int>(M);
+  g.N = static_cast<int>(N);
+  g.K = static_cast<int>(K);
+  g.bias = bias;
+  g.c = C;
+  g.c_fp32 = c_dtype == TPMLP_FP32 ? 1 : 0;
+  g.ldc = ldc;
+  return cuda_status(launch_gemm_block(g, c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tpmlp_status tpmlp_gemm1_fp8_block(const void* Xq, const float* x_scales, const void* AqT, const float* a_scales,
+                                   const void* bias, const tpmlp_shape* shape, void* Hq, float* h_scales, void* Hpre,
+                                   tpmlp_stream_t stream) {
+  tpmlp_status st = check_shape(shape, false, true);
+  if (st != TPMLP_OK) return st;
+  if ((st = check_fp8(shape)) != TPMLP_OK) return st;
+  if (shape->tokens == 0) return TPMLP_OK;  // empty batch: nothing to launch, pointers may be NULL
+  if (!ptrs_ok({Xq, x_scales, AqT, a_scales, Hq, h_scales}) || !opt_ok(bias) || !opt_ok(Hpre))
+    return TPMLP_ERR_INVALID_ARG;
+  DeviceCtx c;
+  if ((st = device_ctx(&c)) != TPMLP_OK) return st;
+  GemmBlockLaunch g{};
+  g.a = static_cast<const uint8_t*>(Xq);
+  g.b = static_cast<const uint8_t*>(AqT);
+  g.a_scales = x_scales;
+  g.b_scales = a_scales;
+  g.b_block_rows = 128;
+  g.M = static_cast<int>(shape->tokens);
+  g.N = static_cast<int>(shape->ffn);
+  g.K = static_cast<int>(shape->d);
+  g.bias = bias;
+  g.hq = static_cast<uint8_t*>(Hq);
+  g.h_scales = h_scales;
+  g.pre = Hpre;
+  return cuda_status(launch_gemm_block(g, c, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

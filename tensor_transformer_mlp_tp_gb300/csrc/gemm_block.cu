@@ -1,0 +1,108 @@
+// Matrix products of block-scaled 8-bit operands:
+//   C[m, n] = sum_kb sA[kb, m] sB[kb, n] sum_{k in block kb} A8[m, k] B8[n, k]  (+ bias[n]).
+// The sum over a block of 128 is scaled as a whole and added to an fp32 accumulator.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "block_fp8.cuh"
+
+namespace tpmlp {
+namespace {
+
+struct GemmBlockParams {
+  GemmBlockLaunch g;
+  long long m_pad, n_pad;
+  int kb_count;
+};
+
+__device__ __forceinline__ float fp8_value(uint8_t b, int fmt) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, fmt == 0 ? __NV_E4M3 : __NV_E5M2)));
+}
+
+// CUDA-core form: a 32 x 128 tile per block of 256 threads; warp w holds rows 4 w .. 4 w + 3, lane l columns
+// 4 l .. 4 l + 3, so the 128 columns of a row (one block of the 8-bit output) lie in one warp.
+__global__ void __launch_bounds__(256) k_gemm_block_simt(const GemmBlockParams p) {
+  __shared__ float sa[32][33];
+  __shared__ float sb[128][33];
+  const GemmBlockLaunch& g = p.g;
+  const int m0 = blockIdx.y * 32, n0 = blockIdx.x * 128;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float acc[4][4] = {}, part[4][4] = {};
+  for (int k0 = 0; k0 < g.K; k0 += 32) {
+    for (int i = threadIdx.x; i < 32 * 32; i += 256) {
+      const int r = i >> 5, k = i & 31;
+      sa[r][k] = m0 + r < g.M && k0 + k < g.K ? fp8_value(g.a[static_cast<long long>(m0 + r) * g.K + k0 + k], g.a_fmt) : 0.f;
+    }
+    for (int i = threadIdx.x; i < 128 * 32; i += 256) {
+      const int r = i >> 5, k = i & 31;
+      sb[r][k] = n0 + r < g.N && k0 + k < g.K ? fp8_value(g.b[static_cast<long long>(n0 + r) * g.K + k0 + k], g.b_fmt) : 0.f;
+    }
+    __syncthreads();
+    for (int k = 0; k < 32; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part[i][j] = fmaf(sa[warp * 4 + i][k], sb[lane * 4 + j][k], part[i][j]);
+    __syncthreads();
+    if ((k0 & 127) == 96 || k0 + 32 >= g.K) {
+      const long long kb = k0 >> 7;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = m0 + warp * 4 + i;
+        const float ra = m < g.M ? g.a_scales[kb * p.m_pad + m] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int n = n0 + lane * 4 + j;
+          const float cb = n >= g.N ? 0.f
+                           : g.b_block_rows == 1 ? g.b_scales[kb * p.n_pad + n]
+                                                 : g.b_scales[(n >> 7) * static_cast<long long>(p.kb_count) + kb];
+          acc[i][j] = fmaf(ra * cb, part[i][j], acc[i][j]);
+          part[i][j] = 0.f;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = m0 + warp * 4 + i;
+    if (m >= g.M) continue;
+    float h[4], amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + lane * 4 + j;
+      h[j] = 0.f;
+      if (n >= g.N) continue;
+      float v = acc[i][j];
+      if (g.bias != nullptr) v += __bfloat162float(static_cast<const __nv_bfloat16*>(g.bias)[n]);
+      if (g.c != nullptr) {
+        if (g.c_fp32)
+          static_cast<float*>(g.c)[m * g.ldc + n] = v;
+        else
+          static_cast<__nv_bfloat16*>(g.c)[m * g.ldc + n] = __float2bfloat16_rn(v);
+      } else {
+        if (g.pre != nullptr) static_cast<__nv_bfloat16*>(g.pre)[static_cast<long long>(m) * g.N + n] = __float2bfloat16_rn(v);
+        h[j] = gelu_f(v);
+        amax = fmaxf(amax, fabsf(h[j]));
+      }
+    }
+    if (g.hq != nullptr) {
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const BlockScale b = block_scale(amax, 448.f);
+      if (n0 + lane * 4 < g.N)
+        *reinterpret_cast<uint32_t*>(g.hq + static_cast<long long>(m) * g.N + n0 + lane * 4) = e4m3x4(h[0], h[1], h[2], h[3], b.inv);
+      if (lane == 0) g.h_scales[blockIdx.x * p.m_pad + m] = b.scale;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_block(const GemmBlockLaunch& g, const DeviceCtx&, cudaStream_t s) {
+  GemmBlockParams p{g, pad128(g.M), pad128(g.N), (g.K + kBlock - 1) / kBlock};
+  const dim3 grid((g.N + 127) / 128, (g.M + 31) / 32);
+  k_gemm_block_simt<<<grid, 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace tpmlp
