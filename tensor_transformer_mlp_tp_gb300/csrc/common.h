@@ -23,6 +23,10 @@ enum WaitSite : uint32_t {
   kSiteEpiTmemFull = 4,
   kSiteEpiStageDrained = 5,
   kSiteEpiStageFilled = 6,
+  kSiteBlockProducer = 7,   // block-scaled GEMM: ring slot free
+  kSiteBlockMmaFull = 8,    // ring slot filled
+  kSiteBlockMmaEmpty = 9,   // partial sums read
+  kSiteBlockPromote = 10,   // partial sums written
 };
 
 // GEMM tile: BM x BN output, BK-deep k-blocks (64 bf16 = one 128-byte swizzle row).

@@ -4,16 +4,13 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
-#include "block_fp8.cuh"
+#include <atomic>
+#include <cstring>
+
+#include "gemm_block_pair.cuh"
 
 namespace tpmlp {
 namespace {
-
-struct GemmBlockParams {
-  GemmBlockLaunch g;
-  long long m_pad, n_pad;
-  int kb_count;
-};
 
 __device__ __forceinline__ float fp8_value(uint8_t b, int fmt) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, fmt == 0 ? __NV_E4M3 : __NV_E5M2)));
@@ -55,7 +52,7 @@ __global__ void __launch_bounds__(256) k_gemm_block_simt(const GemmBlockParams p
           const int n = n0 + lane * 4 + j;
           const float cb = n >= g.N ? 0.f
                            : g.b_block_rows == 1 ? g.b_scales[kb * p.n_pad + n]
-                                                 : g.b_scales[(n >> 7) * static_cast<long long>(p.kb_count) + kb];
+                                                 : g.b_scales[(n >> 7) * static_cast<long long>(p.k_blocks) + kb];
           acc[i][j] = fmaf(ra * cb, part[i][j], acc[i][j]);
           part[i][j] = 0.f;
         }
@@ -96,13 +93,89 @@ __global__ void __launch_bounds__(256) k_gemm_block_simt(const GemmBlockParams p
   }
 }
 
+// Largest number of co-resident clusters of `kern` on the current device (cached per device).
+template <typename K>
+int max_clusters(K kern, int cluster, int smem, int threads, std::atomic<int>* cache) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  const int known = cache[dev & 63].load(std::memory_order_relaxed);
+  if (known > 0) return known;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) n = 1;
+  cache[dev & 63].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <int OUT, bool BVEC>
+cudaError_t run_pair(const GemmBlockParams& p, cudaStream_t s) {
+  using S = BlockPairShape<BVEC>;
+  auto kern = k_gemm_block_pair<OUT, BVEC>;
+  static std::atomic<int> cache[64] = {};
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  const int pairs = max_clusters(kern, 2, S::kSmem, S::kThreads, cache);
+  const int tiles = p.m_blocks * p.n_blocks;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (tiles < pairs ? tiles : pairs));
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 }  // namespace
 
-cudaError_t launch_gemm_block(const GemmBlockLaunch& g, const DeviceCtx&, cudaStream_t s) {
-  GemmBlockParams p{g, pad128(g.M), pad128(g.N), (g.K + kBlock - 1) / kBlock};
-  const dim3 grid((g.N + 127) / 128, (g.M + 31) / 32);
-  k_gemm_block_simt<<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_gemm_block(const GemmBlockLaunch& g, const DeviceCtx& ctx, cudaStream_t s) {
+  GemmBlockParams p;
+  memset(&p, 0, sizeof(p));
+  p.g = g;
+  p.m_pad = pad128(g.M);
+  p.n_pad = pad128(g.N);
+  p.k_blocks = (g.K + kBlock - 1) / kBlock;
+  p.err = ctx.err;
+  p.timeout_ns = ctx.timeout_ns;
+  if (g.M <= 16) {
+    const dim3 grid((g.N + 127) / 128, (g.M + 31) / 32);
+    k_gemm_block_simt<<<grid, 256, 0, s>>>(p);
+    return cudaGetLastError();
+  }
+  p.m_blocks = (g.M + 255) / 256;
+  p.n_blocks = (g.N + 255) / 256;
+  p.group_m = 8;
+  bool ok = encode_tile_map(&p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.a, g.K, g.M, g.K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
+            encode_tile_map(&p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.b, g.K, g.N, g.K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (g.c != nullptr && g.c_fp32)
+    ok = ok && encode_tile_map(&p.tmC, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.c, g.N, g.M, g.ldc, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+  else if (g.c != nullptr)
+    ok = ok && encode_tile_map(&p.tmC, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.c, g.N, g.M, g.ldc, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (g.pre != nullptr)
+    ok = ok && encode_tile_map(&p.tmC, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.pre, g.N, g.M, g.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (g.hq != nullptr)
+    ok = ok && encode_tile_map(&p.tmH, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.hq, g.N, g.M, g.N, 128, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!ok) return cudaErrorInvalidValue;
+  if (g.hq != nullptr) return run_pair<kOutGelu8, false>(p, s);  // weights have 128-row tiles
+  if (g.b_block_rows == 1) return g.c_fp32 ? run_pair<kOutFp32, true>(p, s) : run_pair<kOutBf16, true>(p, s);
+  return g.c_fp32 ? run_pair<kOutFp32, false>(p, s) : run_pair<kOutBf16, false>(p, s);
 }
 
 }  // namespace tpmlp

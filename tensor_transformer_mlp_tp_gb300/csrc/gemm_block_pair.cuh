@@ -1,0 +1,356 @@
+// The block-scaled product on CTA pairs (tcgen05, cta_group::2): a cluster of two CTAs computes a 256 x 256 tile.
+//
+// Each k-block of 128 is summed by the tensor cores into a partial sum in TMEM (four 256 x 256 x 32 UMMAs, the first
+// of them overwriting), and eight promotion warps per CTA add it, scaled, to fp32 sums in registers: warp w owns the
+// 32 rows of TMEM quadrant w % 4 and 128 of the tile's 256 columns, so a thread keeps 128 sums of one row -- one 1 x 128
+// block of an 8-bit output, whose amax needs no exchange.  The partial sums are double-buffered (2 x 256 TMEM columns),
+// so the UMMAs of k-block i + 1 run while block i is promoted.
+//
+// Synchronisation as in the per-tensor pair kernel: full / empty of the TMA ring, tfull / tempty of the partial sums,
+// the barriers that count both CTAs in the even one.  All waits are bounded.
+#pragma once
+
+#include "block_fp8.cuh"
+
+namespace tpmlp {
+
+struct GemmBlockParams {
+  CUtensorMap tmA, tmB;   // [M x K], [N x K] bytes; boxes of 128 bytes x 128 rows
+  CUtensorMap tmC;        // C (bf16 / fp32) or the pre-activation (bf16), 32 x 32 boxes
+  CUtensorMap tmH;        // 8-bit output, boxes of 128 bytes x 32 rows
+  GemmBlockLaunch g;
+  int m_blocks, n_blocks, k_blocks, group_m;
+  long long m_pad, n_pad;
+  unsigned int* err;
+  unsigned long long timeout_ns;
+};
+
+enum BlockOut : int { kOutBf16 = 0, kOutFp32 = 1, kOutGelu8 = 2 };
+
+template <bool BVEC>
+struct BlockPairShape {
+  static constexpr int kStages = 5;
+  static constexpr int kATile = 128 * 128, kBTile = 128 * 128;
+  static constexpr int kStage = kATile + kBTile;
+  static constexpr int kPromoteWarps = 8;
+  static constexpr int kThreads = 64 + 32 * kPromoteWarps;
+  static constexpr int kOutBuf = 4096;                       // per promotion warp
+  // per promotion warp, a ring of kScaleSlots k-blocks: the scales of its 32 rows, and of its 128 columns (BVEC) or
+  // of their tile
+  static constexpr int kScaleSlots = 4;
+  static constexpr int kSlotFloats = 32 + (BVEC ? 128 : 4);
+  static constexpr int kScaleRing = kScaleSlots * kSlotFloats * 4;
+  static constexpr int kSmem = 1024 + kStages * kStage + kPromoteWarps * (kOutBuf + kScaleRing) + 256;
+  static_assert(kSmem <= 232448, "shared memory per block");
+};
+
+// Store 32 columns of a warp's 32 rows (thread = row) through a 2 KB (bf16) or 4 KB (fp32) box in `buf`; the two 2 KB
+// halves of the warp's buffer alternate.
+__device__ __forceinline__ void block_box_bf16(const CUtensorMap* map, uint8_t* buf, const float2* v, uint32_t lane,
+                                               int col0, int row0, bool in) {
+  uint8_t* r = buf + lane * 64;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(r + ((j ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(pack_bf16x2(v[4 * j].x, v[4 * j].y), pack_bf16x2(v[4 * j + 1].x, v[4 * j + 1].y),
+                   pack_bf16x2(v[4 * j + 2].x, v[4 * j + 2].y), pack_bf16x2(v[4 * j + 3].x, v[4 * j + 3].y));
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (in) tma_store_2d(map, buf, col0, row0);
+    bulk_commit_group();  // an empty group where nothing is stored: the waits count groups
+  }
+}
+
+template <int OUT, bool BVEC>
+__global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_block_pair(const __grid_constant__ GemmBlockParams p) {
+  using S = BlockPairShape<BVEC>;
+  constexpr int STAGES = S::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + STAGES * S::kATile;
+  uint8_t* out_bufs = sB + STAGES * S::kBTile;
+  uint8_t* scale_rings = out_bufs + S::kPromoteWarps * S::kOutBuf;
+  uint64_t* full = reinterpret_cast<uint64_t*>(scale_rings + S::kPromoteWarps * S::kScaleRing);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31u;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull + a, 1);
+      mbar_init(tempty + a, 2 * S::kPromoteWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.tmA);
+    tma_prefetch_desc(&p.tmB);
+    tma_prefetch_desc(OUT == kOutGelu8 ? &p.tmH : &p.tmC);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync_all();  // the peer's barriers are initialised before any remote arrive or copy
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const WaitCtx wc{abort_flag, p.err, p.timeout_ns};
+  const int num_tiles = p.m_blocks * p.n_blocks;
+  const int cluster_id = blockIdx.x >> 1;
+  const int num_clusters = gridDim.x >> 1;
+  const int group = p.group_m * p.n_blocks;
+  auto tile_at = [&](int t, int& mb, int& nb) {
+    const int first = t / group * p.group_m;
+    const int gm = min(p.m_blocks - first, p.group_m);
+    mb = first + t % group % gm;
+    nb = t % group / gm;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------------ producer (both CTAs)
+      const uint64_t pol_a = policy_evict_normal(), pol_b = policy_evict_last();
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_parity = 0;
+      bool ok = true;
+      for (int t = cluster_id; ok && t < num_tiles; t += num_clusters) {
+        int mb, nb;
+        tile_at(t, mb, nb);
+        const int m0 = mb * 256 + static_cast<int>(rank) * 128, n0 = nb * 256 + static_cast<int>(rank) * 128;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!wait_bounded(empty + stage, phase ^ 1u, wc, kSiteBlockProducer)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_arrive_expect_tx(full + stage, 2 * S::kStage);
+          const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
+          tma_load_2d_pair(sA + stage * S::kATile, &p.tmA, bar, kb * 128, m0, pol_a);
+          tma_load_2d_pair(sB + stage * S::kBTile, &p.tmB, bar, kb * 128, n0, pol_b);
+          issued |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // copies in flight land before shared memory is released (the odd CTA is held at the closing cluster barrier)
+      if (leader)
+        for (int s = 0; s < STAGES; ++s)
+          if (issued & (1u << s)) wait_drain(full + s, (issued_parity >> s) & 1u, p.timeout_ns);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ------------------------------------------------------------------ MMA issuer (even CTA)
+      const uint32_t idesc = idesc_f8_f32(256, 256, static_cast<uint32_t>(p.g.a_fmt), static_cast<uint32_t>(p.g.b_fmt),
+                                          false, false);
+      int stage = 0;
+      uint32_t phase = 0, blk = 0;
+      bool ok = true;
+      for (int t = cluster_id; ok && t < num_tiles; t += num_clusters) {
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++blk) {
+          const uint32_t acc = blk & 1u;
+          if (!wait_bounded(tempty + acc, ((blk >> 1) & 1u) ^ 1u, wc, kSiteBlockMmaEmpty) ||
+              !wait_bounded(full + stage, phase, wc, kSiteBlockMmaFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t a_base = smem_u32(sA + stage * S::kATile), b_base = smem_u32(sB + stage * S::kBTile);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_f8_pair(tmem_base + acc * 256, sdesc_sw128(a_base + k * 32, 16, 1024),
+                         sdesc_sw128(b_base + k * 32, 16, 1024), idesc, k != 0 ? 1u : 0u);
+          umma_commit_pair_multicast(tfull + acc, 0x3);
+          umma_commit_pair_multicast(empty + stage, 0x3);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      umma_commit_pair(drain);
+      wait_drain(drain, 0, p.timeout_ns);
+    }
+  } else {
+    // -------------------------------------------------------------------- promotion and epilogue (both CTAs)
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* buf = out_bufs + (warp - 2) * S::kOutBuf;
+    float* ring = reinterpret_cast<float*>(scale_rings + (warp - 2) * S::kScaleRing);
+    const uint32_t trow = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half * 128);
+    uint32_t blk = 0;
+    bool ok = true;
+    for (int t = cluster_id; ok && t < num_tiles; t += num_clusters) {
+      int mb, nb;
+      tile_at(t, mb, nb);
+      const int row0 = mb * 256 + static_cast<int>(rank) * 128 + quad * 32;
+      const int row = row0 + static_cast<int>(lane);
+      const int col0 = nb * 256 + half * 128;
+      // The scales of k-block kb + 3 are copied while block kb is used (a load into a register that the loop carries
+      // would be waited for at the end of its own iteration).  One group of copies per k-block, empty past the last.
+      const bool row_in = row < p.m_pad, col_in = col0 < p.n_pad;
+      const float* sa = p.g.a_scales + (row_in ? row : 0);
+      const float* sb = p.g.b_scales + (!col_in ? 0 : BVEC ? col0 + 4 * static_cast<long long>(lane)
+                                                           : static_cast<long long>(col0 >> 7) * p.k_blocks);
+      auto copy_scales = [&](int kb) {
+        if (kb < p.k_blocks) {
+          float* slot = ring + (kb & (S::kScaleSlots - 1)) * S::kSlotFloats;
+          cp_async_4(slot + lane, sa + kb * p.m_pad, row_in);
+          if (BVEC)
+            cp_async_16(slot + 32 + 4 * lane, sb + kb * p.n_pad, col_in);
+          else if (lane == 0)
+            cp_async_4(slot + 32, sb + kb, col_in);
+        }
+        cp_async_commit();
+      };
+      __syncwarp();  // the warp has read the last tile's scales
+#pragma unroll
+      for (int kb = 0; kb < S::kScaleSlots - 1; ++kb) copy_scales(kb);
+      float2 acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int kb = 0; kb < p.k_blocks; ++kb, ++blk) {
+        const uint32_t ab = blk & 1u;
+        cp_async_wait<S::kScaleSlots - 2>();  // this block's scales have landed, for every lane,
+        __syncwarp();                         // and the warp has read the slot that the next copy fills
+        copy_scales(kb + S::kScaleSlots - 1);
+        const float* slot = ring + (kb & (S::kScaleSlots - 1)) * S::kSlotFloats;
+        const float* cs = slot + 32;
+        const float sr = BVEC ? slot[lane] : slot[lane] * cs[0];
+        const float2 s2 = make_float2(sr, sr);
+        ok = wait_bounded(tfull + ab, (blk >> 1) & 1u, wc, kSiteBlockPromote);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after_sync();
+        uint32_t r[2][16];
+        tmem_load_16cols_async(trow + ab * 256, r[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t(&v)[16] = r[c & 1];
+          tmem_wait_ld(v);
+          if (c < 7) tmem_load_16cols_async(trow + ab * 256 + (c + 1) * 16, r[(c + 1) & 1]);
+          if (c == 7) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_relaxed(mapa_shared(smem_u32(tempty + ab), 0));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            float2 q0 = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            float2 q1 = make_float2(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3]));
+            if constexpr (BVEC) {
+              const float4 c4 = *reinterpret_cast<const float4*>(cs + c * 16 + 2 * i);
+              q0 = __fmul2_rn(q0, make_float2(c4.x, c4.y));
+              q1 = __fmul2_rn(q1, make_float2(c4.z, c4.w));
+            }
+            acc[c * 8 + i] = __ffma2_rn(q0, s2, acc[c * 8 + i]);
+            acc[c * 8 + i + 1] = __ffma2_rn(q1, s2, acc[c * 8 + i + 1]);
+          }
+        }
+      }
+      if (!ok) break;
+      // ------------------------------------------------------------------ epilogue of the tile
+      const bool in_m = row0 < p.g.M;
+      if (p.g.bias != nullptr) {
+        const uint4* bias = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.g.bias) + col0);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint4 u = col0 + 8 * j < p.g.N ? __ldg(bias + j) : make_uint4(0, 0, 0, 0);
+          acc[4 * j] = __fadd2_rn(acc[4 * j], unpack_bf16x2(u.x));
+          acc[4 * j + 1] = __fadd2_rn(acc[4 * j + 1], unpack_bf16x2(u.y));
+          acc[4 * j + 2] = __fadd2_rn(acc[4 * j + 2], unpack_bf16x2(u.z));
+          acc[4 * j + 3] = __fadd2_rn(acc[4 * j + 3], unpack_bf16x2(u.w));
+        }
+      }
+      if (OUT == kOutBf16 || (OUT == kOutGelu8 && p.g.pre != nullptr)) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          // what was stored from this half of the buffer has left it
+          if (lane == 0) {
+            if (c == 0) bulk_wait_read_all();
+            if (c >= 2) bulk_wait_read_1();
+          }
+          __syncwarp();
+          block_box_bf16(&p.tmC, buf + (c & 1) * 2048, acc + 16 * c, lane, col0 + 32 * c, row0, in_m && col0 + 32 * c < p.g.N);
+        }
+      }
+      if constexpr (OUT == kOutFp32) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 lo = acc[16 * c + 2 * j], hi = acc[16 * c + 2 * j + 1];
+            *reinterpret_cast<float4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(lo.x, lo.y, hi.x, hi.y);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && in_m && col0 + 32 * c < p.g.N) {
+            tma_store_2d(&p.tmC, buf, col0 + 32 * c, row0);
+            bulk_commit_group();
+          }
+        }
+      }
+      if constexpr (OUT == kOutGelu8) {
+        // GeLU and the thread's own 1 x 128 block (columns at or past N hold zeros, GeLU(0) = 0)
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          acc[i] = gelu2(acc[i]);
+          amax = fmaxf(amax, fmaxf(fabsf(acc[i].x), fabsf(acc[i].y)));
+        }
+        const BlockScale b = block_scale(amax, 448.f);
+        if (row < p.g.M && col0 < p.g.N) p.g.h_scales[(col0 >> 7) * p.m_pad + row] = b.scale;
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2* h = acc + 8 * j;
+          *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+              make_uint4(e4m3x4(h[0].x, h[0].y, h[1].x, h[1].y, b.inv), e4m3x4(h[2].x, h[2].y, h[3].x, h[3].y, b.inv),
+                         e4m3x4(h[4].x, h[4].y, h[5].x, h[5].y, b.inv), e4m3x4(h[6].x, h[6].y, h[7].x, h[7].y, b.inv));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && in_m && col0 < p.g.N) {
+          tma_store_2d(&p.tmH, buf, col0, row0);
+          bulk_commit_group();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();  // box stores complete before the block's shared memory is released
+  }
+
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+}  // namespace tpmlp

@@ -54,6 +54,11 @@ struct GemmLaunch {
   int a_fmt = 0, b_fmt = 0;          // 0 = E4M3, 1 = E5M2
 };
 
+// Tensor map of a row-major matrix of `outer` rows of `inner` elements, `ld` elements apart; copies fill zeros out of
+// bounds.  False where the driver refuses it.
+bool encode_tile_map(CUtensorMap* m, CUtensorMapDataType type, int elem_bytes, const void* base, long long inner,
+                     long long outer, long long ld, int box_inner, int box_outer, CUtensorMapSwizzle swizzle);
+
 struct DeviceCtx {
   unsigned int* err;           // device error words
   unsigned long long timeout_ns;
