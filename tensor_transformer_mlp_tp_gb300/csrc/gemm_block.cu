@@ -164,6 +164,9 @@ cudaError_t launch_gemm_block(const GemmBlockLaunch& g, const DeviceCtx& ctx, cu
   p.group_m = 8;
   bool ok = encode_tile_map(&p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.a, g.K, g.M, g.K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
             encode_tile_map(&p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.b, g.K, g.N, g.K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  ok = ok && encode_tile_map(&p.tmSA, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.a_scales, p.m_pad, p.k_blocks, p.m_pad, 128, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (g.b_block_rows == 1)
+    ok = ok && encode_tile_map(&p.tmSB, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.b_scales, p.n_pad, p.k_blocks, p.n_pad, 256, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (g.c != nullptr && g.c_fp32)
     ok = ok && encode_tile_map(&p.tmC, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.c, g.N, g.M, g.ldc, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   else if (g.c != nullptr)

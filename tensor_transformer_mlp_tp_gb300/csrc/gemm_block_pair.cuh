@@ -16,6 +16,7 @@ namespace tpmlp {
 
 struct GemmBlockParams {
   CUtensorMap tmA, tmB;   // [M x K], [N x K] bytes; boxes of 128 bytes x 128 rows
+  CUtensorMap tmSA, tmSB; // scales by rows, [k_blocks x m_pad] / [k_blocks x n_pad] fp32, boxes of one k-block
   CUtensorMap tmC;        // C (bf16 / fp32) or the pre-activation (bf16), 32 x 32 boxes
   CUtensorMap tmH;        // 8-bit output, boxes of 128 bytes x 32 rows
   GemmBlockLaunch g;
@@ -33,15 +34,21 @@ struct BlockPairShape {
   static constexpr int kATile = 128 * 128, kBTile = 128 * 128;
   static constexpr int kStage = kATile + kBTile;
   static constexpr int kPromoteWarps = 8;
-  static constexpr int kThreads = 64 + 32 * kPromoteWarps;
-  static constexpr int kOutBuf = 4096;                       // per promotion warp
-  // per promotion warp, a ring of kScaleSlots k-blocks: the scales of its 32 rows, and of its 128 columns (BVEC) or
-  // of their tile
-  static constexpr int kScaleSlots = 4;
-  static constexpr int kSlotFloats = 32 + (BVEC ? 128 : 4);
-  static constexpr int kScaleRing = kScaleSlots * kSlotFloats * 4;
-  static constexpr int kSmem = 1024 + kStages * kStage + kPromoteWarps * (kOutBuf + kScaleRing) + 256;
+  static constexpr int kThreads = 128 + 32 * kPromoteWarps;
+  static constexpr int kOutBuf = 4096;  // per promotion warp
+  // Scales of a k-block: of the CTA's 128 rows, and of the tile's 256 columns (BVEC).  They are copied with the
+  // k-block's operands and counted with them, so that partial sums that are there imply scales that are there.  A slot
+  // is rewritten 16 k-blocks later.  The producer is at most kStages blocks ahead of the UMMAs, and those at most 2
+  // ahead of the promotion, so by then every warp has left the slot's k-block; no barrier says so.
+  static constexpr int kScaleSlots = 16;
+  static constexpr int kSlotFloats = 128 + (BVEC ? 256 : 0);
+  static constexpr int kSmem = 1024 + kStages * kStage + kPromoteWarps * kOutBuf + kScaleSlots * kSlotFloats * 4 + 512;
+  static_assert(kStages + 4 < kScaleSlots, "see kScaleSlots");
+  static constexpr int kStageBytes = kStage + kSlotFloats * 4;  // copied by a CTA for a k-block
   static_assert(kSmem <= 232448, "shared memory per block");
+  // registers of the two warpgroups' kinds; together at most what the block is launched with (168 a thread)
+  static constexpr int kIssueRegs = 40, kPromoteRegs = 232;
+  static_assert(128 * kIssueRegs + 32 * kPromoteWarps * kPromoteRegs <= 168 * kThreads, "setmaxnreg split");
 };
 
 // Store 32 columns of a warp's 32 rows (thread = row) through a 2 KB (bf16) or 4 KB (fp32) box in `buf`; the two 2 KB
@@ -62,6 +69,14 @@ __device__ __forceinline__ void block_box_bf16(const CUtensorMap* map, uint8_t* 
   }
 }
 
+// A warp's wait: short tries first, which cover the gaps of the pipeline's steady state, then the bounded wait.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, uint32_t site) {
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait_short(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, w, site));
+}
+
 template <int OUT, bool BVEC>
 __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_block_pair(const __grid_constant__ GemmBlockParams p) {
   using S = BlockPairShape<BVEC>;
@@ -71,8 +86,8 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
   uint8_t* sA = smem;
   uint8_t* sB = sA + STAGES * S::kATile;
   uint8_t* out_bufs = sB + STAGES * S::kBTile;
-  uint8_t* scale_rings = out_bufs + S::kPromoteWarps * S::kOutBuf;
-  uint64_t* full = reinterpret_cast<uint64_t*>(scale_rings + S::kPromoteWarps * S::kScaleRing);
+  float* scale_ring = reinterpret_cast<float*>(out_bufs + S::kPromoteWarps * S::kOutBuf);
+  uint64_t* full = reinterpret_cast<uint64_t*>(scale_ring + S::kScaleSlots * S::kSlotFloats);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
@@ -128,26 +143,31 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
     nb = t % group / gm;
   };
 
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kIssueRegs));
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------------ producer (both CTAs)
       const uint64_t pol_a = policy_evict_normal(), pol_b = policy_evict_last();
       int stage = 0;
-      uint32_t phase = 0, issued = 0, issued_parity = 0;
+      uint32_t phase = 0, issued = 0, issued_parity = 0, blk = 0;
       bool ok = true;
       for (int t = cluster_id; ok && t < num_tiles; t += num_clusters) {
         int mb, nb;
         tile_at(t, mb, nb);
         const int m0 = mb * 256 + static_cast<int>(rank) * 128, n0 = nb * 256 + static_cast<int>(rank) * 128;
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++blk) {
           if (!wait_bounded(empty + stage, phase ^ 1u, wc, kSiteBlockProducer)) {
             ok = false;
             break;
           }
-          if (leader) mbar_arrive_expect_tx(full + stage, 2 * S::kStage);
+          if (leader) mbar_arrive_expect_tx(full + stage, 2 * S::kStageBytes);
           const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
           tma_load_2d_pair(sA + stage * S::kATile, &p.tmA, bar, kb * 128, m0, pol_a);
           tma_load_2d_pair(sB + stage * S::kBTile, &p.tmB, bar, kb * 128, n0, pol_b);
+          float* slot = scale_ring + (blk & (S::kScaleSlots - 1)) * S::kSlotFloats;
+          tma_load_2d_pair(slot, &p.tmSA, bar, m0, kb, pol_a);
+          if (BVEC) tma_load_2d_pair(slot + 128, &p.tmSB, bar, nb * 256, kb, pol_a);
           issued |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) {
@@ -162,43 +182,53 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
           if (issued & (1u << s)) wait_drain(full + s, (issued_parity >> s) & 1u, p.timeout_ns);
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       // ------------------------------------------------------------------ MMA issuer (even CTA)
+      // The whole warp walks the loop and one elected lane issues: descriptors are then warp-uniform, and an issue
+      // costs a few cycles where a loop of one lane alone took about 75 for each (measured, clock64).
       const uint32_t idesc = idesc_f8_f32(256, 256, static_cast<uint32_t>(p.g.a_fmt), static_cast<uint32_t>(p.g.b_fmt),
                                           false, false);
+      const bool elected = elect_one();
       int stage = 0;
       uint32_t phase = 0, blk = 0;
       bool ok = true;
       for (int t = cluster_id; ok && t < num_tiles; t += num_clusters) {
         for (int kb = 0; kb < p.k_blocks; ++kb, ++blk) {
           const uint32_t acc = blk & 1u;
-          if (!wait_bounded(tempty + acc, ((blk >> 1) & 1u) ^ 1u, wc, kSiteBlockMmaEmpty) ||
-              !wait_bounded(full + stage, phase, wc, kSiteBlockMmaFull)) {
+          if (!warp_wait(full + stage, phase, wc, kSiteBlockMmaFull) ||
+              !warp_wait(tempty + acc, ((blk >> 1) & 1u) ^ 1u, wc, kSiteBlockMmaEmpty)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
           const uint32_t a_base = smem_u32(sA + stage * S::kATile), b_base = smem_u32(sB + stage * S::kBTile);
+          if (elected) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_f8_pair(tmem_base + acc * 256, sdesc_sw128(a_base + k * 32, 16, 1024),
-                         sdesc_sw128(b_base + k * 32, 16, 1024), idesc, k != 0 ? 1u : 0u);
-          umma_commit_pair_multicast(tfull + acc, 0x3);
-          umma_commit_pair_multicast(empty + stage, 0x3);
+            for (int k = 0; k < 4; ++k)
+              umma_f8_pair(tmem_base + acc * 256, sdesc_sw128(a_base + k * 32, 16, 1024),
+                           sdesc_sw128(b_base + k * 32, 16, 1024), idesc, k != 0 ? 1u : 0u);
+            umma_commit_pair_multicast(tfull + acc, 0x3);
+            umma_commit_pair_multicast(empty + stage, 0x3);
+          }
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      umma_commit_pair(drain);
-      wait_drain(drain, 0, p.timeout_ns);
+      if (elected) {
+        umma_commit_pair(drain);
+        wait_drain(drain, 0, p.timeout_ns);
+      }
     }
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kPromoteRegs));
     // -------------------------------------------------------------------- promotion and epilogue (both CTAs)
-    const int quad = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* buf = out_bufs + (warp - 2) * S::kOutBuf;
-    float* ring = reinterpret_cast<float*>(scale_rings + (warp - 2) * S::kScaleRing);
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    uint8_t* buf = out_bufs + (warp - 4) * S::kOutBuf;
+    const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0), tempty1 = mapa_shared(smem_u32(tempty + 1), 0);
     const uint32_t trow = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half * 128);
     uint32_t blk = 0;
     bool ok = true;
@@ -208,53 +238,47 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
       const int row0 = mb * 256 + static_cast<int>(rank) * 128 + quad * 32;
       const int row = row0 + static_cast<int>(lane);
       const int col0 = nb * 256 + half * 128;
-      // The scales of k-block kb + 3 are copied while block kb is used (a load into a register that the loop carries
-      // would be waited for at the end of its own iteration).  One group of copies per k-block, empty past the last.
-      const bool row_in = row < p.m_pad, col_in = col0 < p.n_pad;
-      const float* sa = p.g.a_scales + (row_in ? row : 0);
-      const float* sb = p.g.b_scales + (!col_in ? 0 : BVEC ? col0 + 4 * static_cast<long long>(lane)
-                                                           : static_cast<long long>(col0 >> 7) * p.k_blocks);
-      auto copy_scales = [&](int kb) {
-        if (kb < p.k_blocks) {
-          float* slot = ring + (kb & (S::kScaleSlots - 1)) * S::kSlotFloats;
-          cp_async_4(slot + lane, sa + kb * p.m_pad, row_in);
-          if (BVEC)
-            cp_async_16(slot + 32 + 4 * lane, sb + kb * p.n_pad, col_in);
-          else if (lane == 0)
-            cp_async_4(slot + 32, sb + kb, col_in);
-        }
-        cp_async_commit();
-      };
-      __syncwarp();  // the warp has read the last tile's scales
-#pragma unroll
-      for (int kb = 0; kb < S::kScaleSlots - 1; ++kb) copy_scales(kb);
+      // Weight scales (one per 128 columns and k-block): lane l holds that of block 32 j + l.
+      const float* sb = p.g.b_scales + (BVEC || col0 >= p.n_pad ? 0 : static_cast<long long>(col0 >> 7) * p.k_blocks);
+      float sb_cur = 0.f, sb_next = 0.f;
+      if (!BVEC) {
+        if (static_cast<int>(lane) < p.k_blocks) sb_cur = __ldg(sb + lane);
+        if (32 + static_cast<int>(lane) < p.k_blocks) sb_next = __ldg(sb + 32 + lane);
+      }
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
       for (int kb = 0; kb < p.k_blocks; ++kb, ++blk) {
         const uint32_t ab = blk & 1u;
-        cp_async_wait<S::kScaleSlots - 2>();  // this block's scales have landed, for every lane,
-        __syncwarp();                         // and the warp has read the slot that the next copy fills
-        copy_scales(kb + S::kScaleSlots - 1);
-        const float* slot = ring + (kb & (S::kScaleSlots - 1)) * S::kSlotFloats;
-        const float* cs = slot + 32;
-        const float sr = BVEC ? slot[lane] : slot[lane] * cs[0];
-        const float2 s2 = make_float2(sr, sr);
-        ok = wait_bounded(tfull + ab, (blk >> 1) & 1u, wc, kSiteBlockPromote);
-        ok = __all_sync(0xffffffffu, ok);
+        const float* slot = scale_ring + (blk & (S::kScaleSlots - 1)) * S::kSlotFloats;
+        ok = warp_wait(tfull + ab, (blk >> 1) & 1u, wc, kSiteBlockPromote);
         if (!ok) break;
         tc_fence_after_sync();
-        uint32_t r[2][16];
-        tmem_load_16cols_async(trow + ab * 256, r[0]);
+        uint32_t r[3][16];
+        const uint32_t tcol = trow + ab * 256;
+#pragma unroll
+        for (int c = 0; c < 3; ++c) tmem_load_16cols_async(tcol + c * 16, r[c]);
+        float sr = slot[quad * 32 + lane];
+        const float* cs = slot + 128 + half * 128;
+        if (!BVEC) sr *= __shfl_sync(0xffffffffu, sb_cur, kb & 31);
+        const float2 s2 = make_float2(sr, sr);
+        if (!BVEC && (kb & 31) == 31) {
+          sb_cur = sb_next;
+          const int next = kb + 33 + static_cast<int>(lane);
+          sb_next = next < p.k_blocks ? __ldg(sb + next) : 0.f;
+        }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          uint32_t(&v)[16] = r[c & 1];
+          uint32_t(&v)[16] = r[c % 3];
           tmem_wait_ld(v);
-          if (c < 7) tmem_load_16cols_async(trow + ab * 256 + (c + 1) * 16, r[(c + 1) & 1]);
-          if (c == 7) {
+          if (c == 6) {  // every load has returned: the buffer is free before the last sums, not after them
+            tmem_wait_ld(r[1]);
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote_relaxed(mapa_shared(smem_u32(tempty + ab), 0));
+            if (lane == 0) {
+              if (leader) mbar_arrive(tempty + ab);
+              else mbar_arrive_remote_relaxed(ab ? tempty1 : tempty0);
+            }
           }
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
@@ -268,6 +292,7 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
             acc[c * 8 + i] = __ffma2_rn(q0, s2, acc[c * 8 + i]);
             acc[c * 8 + i + 1] = __ffma2_rn(q1, s2, acc[c * 8 + i + 1]);
           }
+          if (c < 5) tmem_load_16cols_async(tcol + (c + 3) * 16, v);
         }
       }
       if (!ok) break;
