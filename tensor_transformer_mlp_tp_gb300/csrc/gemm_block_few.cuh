@@ -1,0 +1,246 @@
+// The block-scaled product for few rows of A (decoded tokens): every weight byte is read once, so the time is that of
+// streaming B.  The operands change sides: a CTA takes 128 rows of B (output columns) as the UMMA's M and up to BT rows
+// of A as its N (128 x BT x 32 UMMAs, cta_group::1), and the K blocks are split over a cluster of CTAs, whose fp32 sums
+// are joined through distributed shared memory in rank order -- no workspace, no atomics, one launch.
+//
+// Warp 0 copies (TMA ring), warp 1 issues, warps 2-5 promote: a thread holds one output column's BT sums, scaled per
+// k-block by its own row scale of B and the BT scales of A.  With BT columns a partial sum, several fit in TMEM, so the
+// promotion's latency is hidden.  In the end each CTA of the cluster finishes BT / C of the rows: a warp per row, four
+// consecutive columns a lane, which makes a 1 x 128 block of an 8-bit output one warp's.
+#pragma once
+
+#include "gemm_block_pair.cuh"
+
+namespace tpmlp {
+
+template <int BT, bool BVEC>
+struct BlockFewShape {
+  static_assert(BT == 16 || BT == 32 || BT == 64 || BT == 128, "BT");
+  // two CTAs share an SM up to BT = 64
+  static constexpr int kStages = BT <= 32 ? 5 : BT == 64 ? 4 : 6;
+  static constexpr int kWTile = 128 * 128, kTTile = BT * 128;
+  static constexpr int kStage = kWTile + kTTile;
+  static constexpr int kBufs = BT == 128 ? 2 : 4;  // partial sums in TMEM
+  static constexpr int kTmemCols = kBufs * BT;
+  static constexpr int kThreads = 192;
+  // Slots of the k-blocks' scales, rewritten 16 blocks later (see BlockPairShape): the producer is at most kStages
+  // blocks ahead of the UMMAs, those at most kBufs ahead of the promotion.
+  static constexpr int kScaleSlots = 16;
+  static constexpr int kRowFloats = BT < 32 ? 32 : BT;  // a copy starts on a 128-byte boundary
+  static constexpr int kSlotFloats = kRowFloats + (BVEC ? 128 : 0);
+  static constexpr int kStageBytes = kStage + (BT + (BVEC ? 128 : 0)) * 4;
+  static constexpr int kSmem = 1024 + kStages * kStage + kScaleSlots * kSlotFloats * 4 + 256;
+  static_assert(kStages + kBufs + 2 < kScaleSlots, "see kScaleSlots");
+  static_assert(kStages * kStage >= BT * 128 * 4, "the sums are joined in the ring's memory");
+  static_assert(kSmem <= 232448, "shared memory per block");
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
+// grid: (cluster size x column tiles, row tiles).  p.tmA: A [M x K], boxes of 128 bytes x BT rows; p.tmB: B [N x K],
+// 128 bytes x 128 rows; p.tmSA boxes of BT scales, p.tmSB (BVEC) of 128.
+template <int BT, int OUT, bool BVEC>
+__global__ void __launch_bounds__(192, BT == 128 ? 1 : 2) k_gemm_block_few(const __grid_constant__ GemmBlockParams p) {
+  using S = BlockFewShape<BT, BVEC>;
+  constexpr int STAGES = S::kStages, BUFS = S::kBufs;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sW = smem;
+  uint8_t* sT = sW + STAGES * S::kWTile;
+  float* scale_ring = reinterpret_cast<float*>(sT + STAGES * S::kTTile);
+  uint64_t* full = reinterpret_cast<uint64_t*>(scale_ring + S::kScaleSlots * S::kSlotFloats);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + BUFS;
+  uint64_t* drain = tempty + BUFS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31u;
+  const int rank = static_cast<int>(cluster_ctarank()), ranks = p.group_m;  // CTAs of the cluster
+  const int n0 = static_cast<int>(blockIdx.x) / ranks * 128, m0 = static_cast<int>(blockIdx.y) * BT;
+  const int kb0 = static_cast<int>(static_cast<long long>(p.k_blocks) * rank / ranks);
+  const int kbs = static_cast<int>(static_cast<long long>(p.k_blocks) * (rank + 1) / ranks) - kb0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int a = 0; a < BUFS; ++a) {
+      mbar_init(tfull + a, 1);
+      mbar_init(tempty + a, 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.tmA);
+    tma_prefetch_desc(&p.tmB);
+    tma_prefetch_desc(&p.tmSA);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, S::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+  const WaitCtx wc{abort_flag, p.err, p.timeout_ns};
+
+  float acc[BT];
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_normal();
+      uint32_t issued = 0, issued_parity = 0;
+      for (int b = 0; b < kbs; ++b) {
+        const int stage = b % STAGES;
+        const uint32_t phase = static_cast<uint32_t>(b / STAGES) & 1u;
+        if (!wait_bounded(empty + stage, phase ^ 1u, wc, kSiteBlockProducer)) break;
+        mbar_arrive_expect_tx(full + stage, S::kStageBytes);
+        tma_load_2d(sW + stage * S::kWTile, &p.tmB, full + stage, (kb0 + b) * 128, n0, pol);
+        tma_load_2d(sT + stage * S::kTTile, &p.tmA, full + stage, (kb0 + b) * 128, m0, pol);
+        float* slot = scale_ring + (b & (S::kScaleSlots - 1)) * S::kSlotFloats;
+        tma_load_2d(slot, &p.tmSA, full + stage, m0, kb0 + b, pol);
+        if (BVEC) tma_load_2d(slot + S::kRowFloats, &p.tmSB, full + stage, n0, kb0 + b, pol);
+        issued |= 1u << stage;
+        issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+      }
+      for (int s = 0; s < STAGES; ++s)  // copies in flight land before their memory is used again
+        if (issued & (1u << s)) wait_drain(full + s, (issued_parity >> s) & 1u, p.timeout_ns);
+    }
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_f8_f32(128, BT, static_cast<uint32_t>(p.g.b_fmt), static_cast<uint32_t>(p.g.a_fmt),
+                                        false, false);
+    const bool elected = elect_one();
+    for (int b = 0; b < kbs; ++b) {
+      const int stage = b % STAGES, buf = b % BUFS;
+      if (!warp_wait(full + stage, static_cast<uint32_t>(b / STAGES) & 1u, wc, kSiteBlockMmaFull) ||
+          !warp_wait(tempty + buf, (static_cast<uint32_t>(b / BUFS) & 1u) ^ 1u, wc, kSiteBlockMmaEmpty))
+        break;
+      tc_fence_after_sync();
+      const uint32_t w_base = smem_u32(sW + stage * S::kWTile), t_base = smem_u32(sT + stage * S::kTTile);
+      if (elected) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          umma_f8(tmem_base + buf * BT, sdesc_sw128(w_base + k * 32, 16, 1024), sdesc_sw128(t_base + k * 32, 16, 1024),
+                  idesc, k != 0 ? 1u : 0u);
+        umma_commit(tfull + buf);
+        umma_commit(empty + stage);
+      }
+      __syncwarp();
+    }
+    if (elected) {
+      umma_commit(drain);
+      wait_drain(drain, 0, p.timeout_ns);
+    }
+  } else {
+    const int quad = warp & 3;
+    const uint32_t trow = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+    const float* sb = p.g.b_scales + (BVEC ? 0 : static_cast<long long>(n0 >> 7) * p.k_blocks + kb0);
+    float sb_cur = 0.f, sb_next = 0.f;  // weight scales: lane l holds that of block 32 j + l
+    if (!BVEC) {
+      if (static_cast<int>(lane) < kbs) sb_cur = __ldg(sb + lane);
+      if (32 + static_cast<int>(lane) < kbs) sb_next = __ldg(sb + 32 + lane);
+    }
+#pragma unroll
+    for (int j = 0; j < BT; ++j) acc[j] = 0.f;
+    for (int b = 0; b < kbs; ++b) {
+      const int buf = b % BUFS;
+      if (!warp_wait(tfull + buf, static_cast<uint32_t>(b / BUFS) & 1u, wc, kSiteBlockPromote)) break;
+      tc_fence_after_sync();
+      const float* slot = scale_ring + (b & (S::kScaleSlots - 1)) * S::kSlotFloats;
+      const float sr = BVEC ? slot[S::kRowFloats + quad * 32 + lane] : __shfl_sync(0xffffffffu, sb_cur, b & 31);
+      if (!BVEC && (b & 31) == 31) {
+        sb_cur = sb_next;
+        const int next = b + 33 + static_cast<int>(lane);
+        sb_next = next < kbs ? __ldg(sb + next) : 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < BT; c += 16) {
+        uint32_t r[16];
+        tmem_load_16cols_async(trow + buf * BT + c, r);
+        tmem_wait_ld(r);
+        if (c + 16 == BT) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty + buf);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 s = *reinterpret_cast<const float4*>(slot + c + j);
+          acc[c + j] = fmaf(__uint_as_float(r[j]), sr * s.x, acc[c + j]);
+          acc[c + j + 1] = fmaf(__uint_as_float(r[j + 1]), sr * s.y, acc[c + j + 1]);
+          acc[c + j + 2] = fmaf(__uint_as_float(r[j + 2]), sr * s.z, acc[c + j + 2]);
+          acc[c + j + 3] = fmaf(__uint_as_float(r[j + 3]), sr * s.w, acc[c + j + 3]);
+        }
+      }
+    }
+  }
+  __syncthreads();  // the ring is drained: its memory holds the CTA's sums [BT][128] from here on
+  float* red = reinterpret_cast<float*>(smem);
+  if (warp >= 2) {
+#pragma unroll
+    for (int j = 0; j < BT; ++j) red[j * 128 + (warp & 3) * 32 + lane] = acc[j];
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, S::kTmemCols);
+  }
+  cluster_sync_all();  // every CTA's sums are written (a cluster of one: a block barrier)
+  const int col = n0 + static_cast<int>(lane) * 4;
+  const bool col_in = col < p.g.N;
+  float b4[4] = {0.f, 0.f, 0.f, 0.f};
+  if (p.g.bias != nullptr && col_in) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.g.bias) + col));
+    const float2 lo = unpack_bf16x2(u.x), hi = unpack_bf16x2(u.y);
+    b4[0] = lo.x; b4[1] = lo.y; b4[2] = hi.x; b4[3] = hi.y;
+  }
+  const uint32_t red_addr = smem_u32(red) + lane * 16;
+  const int rows = min(BT, p.g.M - m0);
+  for (int j = rank + ranks * warp; j < rows; j += ranks * 6) {
+    const int row = m0 + j;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < ranks; ++r) {
+      const float4 q = ld_cluster_f4(mapa_shared(red_addr + j * 512, static_cast<uint32_t>(r)));
+      v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += b4[i];
+    if constexpr (OUT == kOutFp32) {
+      if (col_in) *reinterpret_cast<float4*>(static_cast<float*>(p.g.c) + row * p.g.ldc + col) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      const uint2 u = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      if constexpr (OUT == kOutBf16) {
+        if (col_in) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.g.c) + row * p.g.ldc + col) = u;
+      } else {
+        const long long at = static_cast<long long>(row) * p.g.N + col;
+        if (p.g.pre != nullptr && col_in) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.g.pre) + at) = u;
+        const float2 h0 = gelu2(make_float2(v[0], v[1])), h1 = gelu2(make_float2(v[2], v[3]));
+        float amax = col_in ? fmaxf(fmaxf(fabsf(h0.x), fabsf(h0.y)), fmaxf(fabsf(h1.x), fabsf(h1.y))) : 0.f;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const BlockScale b = block_scale(amax, 448.f);
+        if (col_in) *reinterpret_cast<uint32_t*>(p.g.hq + at) = e4m3x4(h0.x, h0.y, h1.x, h1.y, b.inv);
+        if (lane == 0) p.g.h_scales[(n0 >> 7) * p.m_pad + row] = b.scale;
+      }
+    }
+  }
+  cluster_sync_all();  // the cluster has read this CTA's sums
+}
+
+}  // namespace tpmlp

@@ -51,20 +51,50 @@ struct BlockPairShape {
   static_assert(128 * kIssueRegs + 32 * kPromoteWarps * kPromoteRegs <= 168 * kThreads, "setmaxnreg split");
 };
 
-// Store 32 columns of a warp's 32 rows (thread = row) through a 2 KB (bf16) or 4 KB (fp32) box in `buf`; the two 2 KB
-// halves of the warp's buffer alternate.
-__device__ __forceinline__ void block_box_bf16(const CUtensorMap* map, uint8_t* buf, const float2* v, uint32_t lane,
-                                               int col0, int row0, bool in) {
-  uint8_t* r = buf + lane * 64;
+// Where a warp's promotion leaves its 32 x 128 sums: float2 i of a thread.
+//   rows (BVEC = false, tcgen05.ld 32x32b): row = lane, columns 2 i, 2 i + 1;
+//   fragments (BVEC = true, 16x256b): i = 16 q + 8 h + 2 g + j, row 16 h + 8 j + lane / 4, columns 32 q + 8 g + 2 (lane % 4).
+// The second form keeps only 32 columns a thread, so the columns' scales are 16 8-byte reads of shared memory a
+// k-block and warp; with a row per thread they are 32 16-byte reads, every lane taking all of them, 1000 cycles of the
+// SM's shared-memory bandwidth a k-block.
+
+// Stage columns 32 q .. 32 q + 31 of the warp's rows as a box in `buf` (swizzled as the tensor maps say) and store it.
+template <bool BVEC, bool F32>
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* buf, const float2 (&acc)[64], int q,
+                                          uint32_t lane, int col0, int row0, bool in) {
+  if constexpr (BVEC) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint4*>(r + ((j ^ ((lane >> 1) & 3)) << 4)) =
-        make_uint4(pack_bf16x2(v[4 * j].x, v[4 * j].y), pack_bf16x2(v[4 * j + 1].x, v[4 * j + 1].y),
-                   pack_bf16x2(v[4 * j + 2].x, v[4 * j + 2].y), pack_bf16x2(v[4 * j + 3].x, v[4 * j + 3].y));
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 v = acc[16 * q + 8 * h + 2 * g + j];
+          const uint32_t row = 16 * h + 8 * j + (lane >> 2);
+          if constexpr (F32)
+            *reinterpret_cast<float2*>(buf + row * 128 + (((2 * g + ((lane & 3) >> 1)) ^ (row & 7)) << 4) + 8 * (lane & 1)) = v;
+          else
+            *reinterpret_cast<uint32_t*>(buf + row * 64 + ((g ^ ((row >> 1) & 3)) << 4) + 4 * (lane & 3)) = pack_bf16x2(v.x, v.y);
+        }
+  } else if constexpr (F32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 lo = acc[16 * q + 2 * j], hi = acc[16 * q + 2 * j + 1];
+      *reinterpret_cast<float4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(lo.x, lo.y, hi.x, hi.y);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2* v = acc + 16 * q + 4 * j;
+      *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+          make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                     pack_bf16x2(v[3].x, v[3].y));
+    }
+  }
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
-    if (in) tma_store_2d(map, buf, col0, row0);
+    if (in) tma_store_2d(map, buf, col0 + 32 * q, row0);
     bulk_commit_group();  // an empty group where nothing is stored: the waits count groups
   }
 }
@@ -80,6 +110,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 template <int OUT, bool BVEC>
 __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_block_pair(const __grid_constant__ GemmBlockParams p) {
   using S = BlockPairShape<BVEC>;
+  constexpr bool kFrag = BVEC;  // layout of the sums, see store_box
   constexpr int STAGES = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -256,20 +287,50 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
         tc_fence_after_sync();
         uint32_t r[3][16];
         const uint32_t tcol = trow + ab * 256;
+        auto load = [&](int c, uint32_t (&v)[16]) {
+          if constexpr (kFrag)
+            tmem_load_16x32_async(tcol + (static_cast<uint32_t>((c & 1) * 16) << 16) + (c >> 1) * 32, v);
+          else
+            tmem_load_16cols_async(tcol + c * 16, v);
+        };
 #pragma unroll
-        for (int c = 0; c < 3; ++c) tmem_load_16cols_async(tcol + c * 16, r[c]);
-        float sr = slot[quad * 32 + lane];
-        const float* cs = slot + 128 + half * 128;
-        if (!BVEC) sr *= __shfl_sync(0xffffffffu, sb_cur, kb & 31);
-        const float2 s2 = make_float2(sr, sr);
-        if (!BVEC && (kb & 31) == 31) {
-          sb_cur = sb_next;
-          const int next = kb + 33 + static_cast<int>(lane);
-          sb_next = next < p.k_blocks ? __ldg(sb + next) : 0.f;
+        for (int c = 0; c < 3; ++c) load(c, r[c]);
+        float2 rs[kFrag ? 4 : 1];
+        const float* cs = slot + 128 + half * 128 + (kFrag ? 2 * (lane & 3) : 0);
+        if constexpr (kFrag) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float f = slot[quad * 32 + 8 * i + (lane >> 2)];
+            rs[i] = make_float2(f, f);
+          }
+        } else {
+          float f = slot[quad * 32 + lane];
+          if constexpr (!BVEC) f *= __shfl_sync(0xffffffffu, sb_cur, kb & 31);
+          rs[0] = make_float2(f, f);
+          if (!BVEC && (kb & 31) == 31) {
+            sb_cur = sb_next;
+            const int next = kb + 33 + static_cast<int>(lane);
+            sb_next = next < p.k_blocks ? __ldg(sb + next) : 0.f;
+          }
         }
+        float2 c2[kFrag ? 4 : 8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           uint32_t(&v)[16] = r[c % 3];
+          if constexpr (BVEC && kFrag) {
+            if ((c & 1) == 0) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) c2[g] = *reinterpret_cast<const float2*>(cs + (c >> 1) * 32 + 8 * g);
+            }
+          }
+          if constexpr (BVEC && !kFrag) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const float4 f = *reinterpret_cast<const float4*>(cs + c * 16 + 4 * g);
+              c2[2 * g] = make_float2(f.x, f.y);
+              c2[(2 * g + 1) & (kFrag ? 3 : 7)] = make_float2(f.z, f.w);
+            }
+          }
           tmem_wait_ld(v);
           if (c == 6) {  // every load has returned: the buffer is free before the last sums, not after them
             tmem_wait_ld(r[1]);
@@ -281,62 +342,54 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
             }
           }
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            float2 q0 = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            float2 q1 = make_float2(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3]));
-            if constexpr (BVEC) {
-              const float4 c4 = *reinterpret_cast<const float4*>(cs + c * 16 + 2 * i);
-              q0 = __fmul2_rn(q0, make_float2(c4.x, c4.y));
-              q1 = __fmul2_rn(q1, make_float2(c4.z, c4.w));
-            }
-            acc[c * 8 + i] = __ffma2_rn(q0, s2, acc[c * 8 + i]);
-            acc[c * 8 + i + 1] = __ffma2_rn(q1, s2, acc[c * 8 + i + 1]);
+          for (int i = 0; i < 8; ++i) {
+            float2 q = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            if constexpr (BVEC) q = __fmul2_rn(q, c2[kFrag ? i >> 1 : i]);
+            acc[c * 8 + i] = __ffma2_rn(q, rs[kFrag ? (c & 1) * 2 + (i & 1) : 0], acc[c * 8 + i]);
           }
-          if (c < 5) tmem_load_16cols_async(tcol + (c + 3) * 16, v);
+          if (c < 5) load(c + 3, v);
         }
       }
       if (!ok) break;
       // ------------------------------------------------------------------ epilogue of the tile
       const bool in_m = row0 < p.g.M;
       if (p.g.bias != nullptr) {
-        const uint4* bias = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.g.bias) + col0);
+        const __nv_bfloat16* bias = static_cast<const __nv_bfloat16*>(p.g.bias) + col0;
+        if constexpr (kFrag) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint4 u = col0 + 8 * j < p.g.N ? __ldg(bias + j) : make_uint4(0, 0, 0, 0);
-          acc[4 * j] = __fadd2_rn(acc[4 * j], unpack_bf16x2(u.x));
-          acc[4 * j + 1] = __fadd2_rn(acc[4 * j + 1], unpack_bf16x2(u.y));
-          acc[4 * j + 2] = __fadd2_rn(acc[4 * j + 2], unpack_bf16x2(u.z));
-          acc[4 * j + 3] = __fadd2_rn(acc[4 * j + 3], unpack_bf16x2(u.w));
+          for (int g = 0; g < 16; ++g) {
+            const int c = 8 * g + 2 * static_cast<int>(lane & 3);
+            const float2 b = col0 + c < p.g.N ? unpack_bf16x2(__ldg(reinterpret_cast<const uint32_t*>(bias + c)))
+                                              : make_float2(0.f, 0.f);
+#pragma unroll
+            for (int hj = 0; hj < 4; ++hj) {
+              float2& a = acc[16 * (g >> 2) + 8 * (hj >> 1) + 2 * (g & 3) + (hj & 1)];
+              a = __fadd2_rn(a, b);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint4 u = col0 + 8 * j < p.g.N ? __ldg(reinterpret_cast<const uint4*>(bias) + j) : make_uint4(0, 0, 0, 0);
+            acc[4 * j] = __fadd2_rn(acc[4 * j], unpack_bf16x2(u.x));
+            acc[4 * j + 1] = __fadd2_rn(acc[4 * j + 1], unpack_bf16x2(u.y));
+            acc[4 * j + 2] = __fadd2_rn(acc[4 * j + 2], unpack_bf16x2(u.z));
+            acc[4 * j + 3] = __fadd2_rn(acc[4 * j + 3], unpack_bf16x2(u.w));
+          }
         }
       }
-      if (OUT == kOutBf16 || (OUT == kOutGelu8 && p.g.pre != nullptr)) {
+      if (OUT != kOutGelu8 || p.g.pre != nullptr) {
+        constexpr bool kF32 = OUT == kOutFp32;  // a 4 KB box, or 2 KB boxes in the halves of the buffer
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          // what was stored from this half of the buffer has left it
+        for (int q = 0; q < 4; ++q) {
+          // what was stored from this part of the buffer has left it
           if (lane == 0) {
-            if (c == 0) bulk_wait_read_all();
-            if (c >= 2) bulk_wait_read_1();
+            if (kF32 || q == 0) bulk_wait_read_all();
+            else if (q >= 2) bulk_wait_read_1();
           }
           __syncwarp();
-          block_box_bf16(&p.tmC, buf + (c & 1) * 2048, acc + 16 * c, lane, col0 + 32 * c, row0, in_m && col0 + 32 * c < p.g.N);
-        }
-      }
-      if constexpr (OUT == kOutFp32) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (lane == 0) bulk_wait_read_all();
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 lo = acc[16 * c + 2 * j], hi = acc[16 * c + 2 * j + 1];
-            *reinterpret_cast<float4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_float4(lo.x, lo.y, hi.x, hi.y);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && in_m && col0 + 32 * c < p.g.N) {
-            tma_store_2d(&p.tmC, buf, col0 + 32 * c, row0);
-            bulk_commit_group();
-          }
+          store_box<kFrag, kF32>(&p.tmC, buf + (kF32 ? 0 : (q & 1) * 2048), acc, q, lane, col0, row0,
+                                in_m && col0 + 32 * q < p.g.N);
         }
       }
       if constexpr (OUT == kOutGelu8) {
