@@ -185,8 +185,8 @@ def _opt_ptrs(ts):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -617,47 +617,71 @@ def tpmlp_attention_tp_backward(X, Wqkv, Wo, QKV, O, LSE, dY, S, B, H, N, dX, dW
 
 # ----------------------------------------------------------------------------- block-scaled FP8
 #
-# These functions also refuse (ERR_INVALID_ARG) tensors whose layout the ABI cannot express or whose size does not
-# fit the others': the library sees addresses only, and a scale buffer that is too small would be read past its end.
+# These functions also refuse (ERR_INVALID_ARG) tensors whose type or layout the ABI cannot express or whose size does
+# not fit the others': the library sees addresses only, and a scale buffer that is too small would be read past its
+# end.  A decoded token's kernels take a few microseconds, less than marshalling through ctypes objects does, so
+# addresses are passed as plain integers and the pointer-array types are made once.
+
+_ARRAYS = {}
+_BF16, _FP32 = torch.bfloat16, torch.float32
+
 
 def block_scales_shape(rows, cols, block_rows=1):
     """Shape of the fp32 scales of an 8-bit operand [rows x cols] with blocks of block_rows x 128."""
-    kb = (cols + 127) // 128
-    return (kb, (rows + 127) // 128 * 128) if block_rows == 1 else ((rows + 127) // 128, kb)
+    kb = (cols + 127) >> 7
+    return (kb, (rows + 127) & -128) if block_rows == 1 else ((rows + 127) >> 7, kb)
 
 
-def _fits(t, itemsize, numel):
-    return t is None or (t.is_contiguous() and t.element_size() == itemsize and t.numel() >= numel)
+def _refuse(fn):
+    raise TpMlpError(fn, ERR_INVALID_ARG)
 
 
-def _refuse_unless(ok, fn):
-    if not ok:
-        raise TpMlpError(fn, ERR_INVALID_ARG)
+def _typed(t, dtype, numel, fn):
+    """Address of a contiguous tensor of `dtype` with at least `numel` elements (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() < numel or not t.is_contiguous():
+        _refuse(fn)
+    return t.data_ptr()
 
 
-def _chunks_fit(chunks, n, numel):
-    return chunks is None or (len(chunks) == n and all(_fits(t, 2, numel) for t in chunks))
+def _bytes(t, numel, fn):
+    """Address of a contiguous tensor of 8-bit elements (uint8 or a float8 type)."""
+    if t is None:
+        return None
+    if t.element_size() != 1 or t.numel() < numel or not t.is_contiguous():
+        _refuse(fn)
+    return t.data_ptr()
 
 
-def _scale_count(rows, cols, block_rows=1):
+def _scales(t, rows, cols, block_rows, fn):
     a, b = block_scales_shape(rows, cols, block_rows)
-    return a * b
+    return _typed(t, _FP32, a * b, fn)
+
+
+def _chunk_array(chunks, n, numel, fn):
+    if chunks is None:
+        return None
+    if len(chunks) != n:
+        _refuse(fn)
+    kind = _ARRAYS.get(n)
+    if kind is None:
+        kind = _ARRAYS[n] = ctypes.c_void_p * n
+    return kind(*[_typed(t, _BF16, numel, fn) for t in chunks])
 
 
 def tpmlp_rmsnorm_add_gather(X_chunks, weight, N, R_chunks=None, S_chunks=None, Xg=None, Xq=None, x_scales=None,
                              eps=1e-5, stream=None):
     """S_j = X_j + R_j; Xg and / or (Xq, x_scales) = the RMS norm of S, gathered, in bf16 and / or block-scaled E4M3."""
+    fn = "tpmlp_rmsnorm_add_gather"
     rows, d = X_chunks[0].shape
-    T = rows * N
-    _refuse_unless(_chunks_fit(X_chunks, N, rows * d) and _chunks_fit(R_chunks, N, rows * d) and
-                   _chunks_fit(S_chunks, N, rows * d) and _fits(weight, 2, d) and _fits(Xg, 2, T * d) and
-                   _fits(Xq, 1, T * d) and _fits(x_scales, 4, _scale_count(T, d)), "tpmlp_rmsnorm_add_gather")
-    shape = make_shape(T, d, d * N, N)
-    xp, _xa = _ptrs(X_chunks)
-    rp, _ra = _opt_ptrs(R_chunks)
-    sp, _sa = _opt_ptrs(S_chunks)
-    _check("tpmlp_rmsnorm_add_gather", lib().tpmlp_rmsnorm_add_gather(
-        xp, rp, _ptr(weight), eps, ctypes.byref(shape), sp, _ptr(Xg), _ptr(Xq), _ptr(x_scales), _stream(stream)))
+    T, n = rows * N, rows * d
+    st = (_lib or lib()).tpmlp_rmsnorm_add_gather(
+        _chunk_array(X_chunks, N, n, fn), _chunk_array(R_chunks, N, n, fn), _typed(weight, _BF16, d, fn), eps,
+        Shape(T, d, d * N, N, BF16), _chunk_array(S_chunks, N, n, fn), _typed(Xg, _BF16, T * d, fn),
+        _bytes(Xq, T * d, fn), _scales(x_scales, T, d, 1, fn), _stream(stream))
+    if st:
+        raise TpMlpError(fn, st)
 
 
 def tpmlp_rmsnorm_add_backward_workspace_size(T, d, N) -> int:
@@ -669,63 +693,66 @@ def tpmlp_rmsnorm_add_backward_workspace_size(T, d, N) -> int:
 
 def tpmlp_rmsnorm_add_backward(S_chunks, weight, dXg, N, dX_chunks, dweight, dS_chunks=None, eps=1e-5, ws=None,
                                stream=None):
+    fn = "tpmlp_rmsnorm_add_backward"
     rows, d = S_chunks[0].shape
-    T = rows * N
-    _refuse_unless(_chunks_fit(S_chunks, N, rows * d) and _chunks_fit(dS_chunks, N, rows * d) and
-                   _chunks_fit(dX_chunks, N, rows * d) and _fits(weight, 2, d) and _fits(dXg, 2, T * d) and
-                   _fits(dweight, 4, d), "tpmlp_rmsnorm_add_backward")
-    shape = make_shape(T, d, d * N, N)
+    T, n = rows * N, rows * d
     if ws is None:
         ws = torch.empty(max(tpmlp_rmsnorm_add_backward_workspace_size(T, d, N), 256), dtype=torch.uint8,
                          device=weight.device)
-    xp, _xa = _ptrs(S_chunks)
-    rp, _ra = _opt_ptrs(dS_chunks)
-    dp, _da = _ptrs(dX_chunks)
-    _check("tpmlp_rmsnorm_add_backward", lib().tpmlp_rmsnorm_add_backward(
-        xp, _ptr(weight), eps, _ptr(dXg), rp, ctypes.byref(shape), dp, _ptr(dweight), _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream)))
+    st = (_lib or lib()).tpmlp_rmsnorm_add_backward(
+        _chunk_array(S_chunks, N, n, fn), _typed(weight, _BF16, d, fn), eps, _typed(dXg, _BF16, T * d, fn),
+        _chunk_array(dS_chunks, N, n, fn), Shape(T, d, d * N, N, BF16), _chunk_array(dX_chunks, N, n, fn),
+        _typed(dweight, _FP32, d, fn), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
+    if st:
+        raise TpMlpError(fn, st)
 
 
 def tpmlp_quantize_block(src, block_rows=1, fmt=E4M3, q=None, scales=None, qT=None, scalesT=None, stream=None):
     """8-bit codes and block scales of src [rows x cols] bf16 (rows may be strided), as it stands and / or transposed."""
+    fn = "tpmlp_quantize_block"
     rows, cols = src.shape
-    _refuse_unless((rows <= 1 or cols == 0 or src.stride(1) == 1) and src.element_size() == 2 and
-                   _fits(q, 1, rows * cols) and _fits(scales, 4, _scale_count(rows, cols, block_rows)) and
-                   _fits(qT, 1, cols * ((rows + 15) // 16 * 16)) and
-                   _fits(scalesT, 4, _scale_count(cols, rows, block_rows)), "tpmlp_quantize_block")
-    ld = src.stride(0) if rows > 1 else cols
-    _check("tpmlp_quantize_block", lib().tpmlp_quantize_block(
-        _ptr(src), ld, rows, cols, block_rows, fmt, _ptr(q), _ptr(scales), _ptr(qT), _ptr(scalesT), _stream(stream)))
+    ld, step = src.stride()
+    if src.dtype is not _BF16 or (step != 1 and cols > 1):
+        _refuse(fn)
+    st = (_lib or lib()).tpmlp_quantize_block(
+        src.data_ptr(), ld if rows > 1 else cols, rows, cols, block_rows, fmt, _bytes(q, rows * cols, fn),
+        _scales(scales, rows, cols, block_rows, fn), _bytes(qT, cols * ((rows + 15) & -16), fn),
+        _scales(scalesT, cols, rows, block_rows, fn), _stream(stream))
+    if st:
+        raise TpMlpError(fn, st)
 
 
 def tpmlp_gemm_fp8_block(A8, a_scales, B8, b_scales, C, bias=None, b_block_rows=128, a_fmt=E4M3, b_fmt=E4M3,
                          stream=None):
     """C [M x N] (bf16 or fp32, rows may be strided) = A8 [M x K] . B8 [N x K]^T with their block scales, + bias."""
+    fn = "tpmlp_gemm_fp8_block"
     M, K = A8.shape
-    N = B8.shape[0]
-    _refuse_unless(B8.shape[1] == K and C.shape[0] == M and C.shape[1] == N and _fits(A8, 1, M * K) and
-                   _fits(B8, 1, N * K) and _fits(a_scales, 4, _scale_count(M, K)) and
-                   _fits(b_scales, 4, _scale_count(N, K, b_block_rows)) and _fits(bias, 2, N) and
-                   (N <= 1 or C.stride(1) == 1) and C.dtype in (torch.bfloat16, torch.float32),
-                   "tpmlp_gemm_fp8_block")
-    ldc = C.stride(0) if M > 1 else N
-    _check("tpmlp_gemm_fp8_block", lib().tpmlp_gemm_fp8_block(
-        _ptr(A8), a_fmt, _ptr(a_scales), _ptr(B8), b_fmt, _ptr(b_scales), b_block_rows, M, N, K, _ptr(bias), _ptr(C),
-        _dtype_code(C), ldc, _stream(stream)))
+    N, k = B8.shape
+    ldc, step = C.stride()
+    c_type = C.dtype
+    if k != K or C.shape != (M, N) or (step != 1 and N > 1) or (c_type is not _BF16 and c_type is not _FP32):
+        _refuse(fn)
+    st = (_lib or lib()).tpmlp_gemm_fp8_block(
+        _bytes(A8, M * K, fn), a_fmt, _scales(a_scales, M, K, 1, fn), _bytes(B8, N * K, fn), b_fmt,
+        _scales(b_scales, N, K, b_block_rows, fn), b_block_rows, M, N, K, _typed(bias, _BF16, N, fn), C.data_ptr(),
+        FP32 if c_type is _FP32 else BF16, ldc if M > 1 else N, _stream(stream))
+    if st:
+        raise TpMlpError(fn, st)
 
 
 def tpmlp_gemm1_fp8_block(Xq, x_scales, AqT, a_scales, bias, N, Hq, h_scales, Hpre=None, stream=None):
     """(Hq, h_scales) = GeLU(Xq . AqT^T + bias) in block-scaled E4M3; Hpre = the pre-activation in bf16."""
+    fn = "tpmlp_gemm1_fp8_block"
     T, d = Xq.shape
-    F = AqT.shape[0]
-    _refuse_unless(AqT.shape[1] == d and _fits(Xq, 1, T * d) and _fits(AqT, 1, F * d) and
-                   _fits(x_scales, 4, _scale_count(T, d)) and _fits(a_scales, 4, _scale_count(F, d, 128)) and
-                   _fits(bias, 2, F) and _fits(Hq, 1, T * F) and _fits(h_scales, 4, _scale_count(T, F)) and
-                   _fits(Hpre, 2, T * F), "tpmlp_gemm1_fp8_block")
-    shape = make_shape(T, d, F, N)
-    _check("tpmlp_gemm1_fp8_block", lib().tpmlp_gemm1_fp8_block(
-        _ptr(Xq), _ptr(x_scales), _ptr(AqT), _ptr(a_scales), _ptr(bias), ctypes.byref(shape), _ptr(Hq),
-        _ptr(h_scales), _ptr(Hpre), _stream(stream)))
+    F, k = AqT.shape
+    if k != d:
+        _refuse(fn)
+    st = (_lib or lib()).tpmlp_gemm1_fp8_block(
+        _bytes(Xq, T * d, fn), _scales(x_scales, T, d, 1, fn), _bytes(AqT, F * d, fn),
+        _scales(a_scales, F, d, 128, fn), _typed(bias, _BF16, F, fn), Shape(T, d, F, N, BF16), _bytes(Hq, T * F, fn),
+        _scales(h_scales, T, F, 1, fn), _typed(Hpre, _BF16, T * F, fn), _stream(stream))
+    if st:
+        raise TpMlpError(fn, st)
 
 
 def tpmlp_selftest_wait_timeout(budget_us: int, stream=None):
