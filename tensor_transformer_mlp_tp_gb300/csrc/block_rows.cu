@@ -31,65 +31,283 @@ __device__ __forceinline__ T* chunk_at(T* const* chunks, int rows_per_chunk, int
   return chunks[j] + static_cast<long long>(row - j * rows_per_chunk) * elems_per_row;
 }
 
-// s = bf16(x + r), y = s rsqrt(mean(s^2) + eps) w.  One block per row; thread t holds the 16-byte vectors
-// t + k blockDim (k < V) in registers, so the row is read once and the 16 vectors of a 1 x 128 block sit on
-// the 16 lanes of a half warp.  The statistics are of the stored (rounded) sum, the value the backward reads;
-// y is rounded once, to bf16 or to E4M3.
+// s = bf16(x + r), y = s rsqrt(mean(s^2) + eps) w.  A team of TW warps per row; thread t of the team holds the 16-byte
+// vectors t + 32 TW k (k < V) in registers, so the row is read once, all its loads in flight together, and the 16 vectors
+// of a 1 x 128 block sit on the 16 lanes of a half warp.  The statistics are of the stored (rounded) sum, the value the
+// backward reads; y is rounded once, to bf16 or to E4M3.
 template <int V>
-__global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_rmsnorm_add(const RmsBlockParams p) {
+__global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_rmsnorm_add(const RmsBlockParams p, int tw) {
   __shared__ float red[32];
-  const int row = blockIdx.x, nv = p.d / 8;
-  const int j = row / p.rows_per_chunk;
-  const long long off = static_cast<long long>(row - j * p.rows_per_chunk) * nv;
+  const int warp = threadIdx.x >> 5, team = warp / tw, nv = p.d / 8;
+  const int step = 32 * tw, j0 = threadIdx.x - team * step;
+  const int row = blockIdx.x * (static_cast<int>(blockDim.x >> 5) / tw) + team;
+  const bool valid = row < p.rows;
+  const int j = valid ? row / p.rows_per_chunk : 0;
+  const long long off = valid ? static_cast<long long>(row - j * p.rows_per_chunk) * nv : 0;
   const uint4* x4 = static_cast<const uint4*>(p.x.p[j]) + off;
+  const uint4* r4 = static_cast<const uint4*>(p.r.p[j]) + off;
   const bool has_r = p.r.p[0] != nullptr;
-  float f[V][8];
+  uint4 x[V], r[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int v = j0 + k * step;
+    x[k] = valid && v < nv ? x4[v] : make_uint4(0, 0, 0, 0);
+  }
+  if (has_r) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int v = j0 + k * step;
+      r[k] = valid && v < nv ? r4[v] : make_uint4(0, 0, 0, 0);
+    }
+  }
   float q = 0.f;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int v = threadIdx.x + k * blockDim.x;
+    float f[8];
+    unpack_vec8(x[k], f);
+    if (has_r) {
+      float g[8];
+      unpack_vec8(r[k], g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[k][e] = 0.f;
-    if (v < nv) {
-      unpack_vec8(x4[v], f[k]);
-      if (has_r) {
-        float r[8];
-        unpack_vec8((static_cast<const uint4*>(p.r.p[j]) + off)[v], r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[k][e] += r[e];
-        const uint4 s = pack_vec8(f[k]);
-        if (p.s.p[0] != nullptr) (static_cast<uint4*>(p.s.p[j]) + off)[v] = s;
-        unpack_vec8(s, f[k]);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q += f[k][e] * f[k][e];
+      for (int e = 0; e < 8; ++e) f[e] += g[e];
+      x[k] = pack_vec8(f);
+      const int v = j0 + k * step;
+      if (p.s.p[0] != nullptr && valid && v < nv) (static_cast<uint4*>(p.s.p[j]) + off)[v] = x[k];
+      unpack_vec8(x[k], f);
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q += f[e] * f[e];
   }
-  const float rstd = rsqrtf(block_add(q, red) / static_cast<float>(p.d) + p.eps);
-  const long long row_off = static_cast<long long>(row) * nv;
+  q = warp_add(q);
+  if (tw > 1) {
+    if ((threadIdx.x & 31) == 0) red[warp] = q;
+    __syncthreads();
+    q = 0.f;
+    for (int w = 0; w < tw; ++w) q += red[team * tw + w];
+  }
+  const float rstd = rsqrtf(q / static_cast<float>(p.d) + p.eps);
+  const long long row_off = static_cast<long long>(valid ? row : 0) * nv;
+  float y[V][8], amax = 0.f;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int v = threadIdx.x + k * blockDim.x;
-    const bool in = v < nv;
-    float w[8], y[8];
-    unpack_vec8(in ? __ldg(static_cast<const uint4*>(p.weight) + v) : make_uint4(0, 0, 0, 0), w);
+    const int v = j0 + k * step;
+    float f[8], w[8];
+    unpack_vec8(x[k], f);
+    unpack_vec8(v < nv ? __ldg(static_cast<const uint4*>(p.weight) + v) : make_uint4(0, 0, 0, 0), w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = f[k][e] * rstd * w[e];
-    if (p.xg != nullptr && in) (static_cast<uint4*>(p.xg) + row_off)[v] = pack_vec8(y);
+    for (int e = 0; e < 8; ++e) y[k][e] = f[e] * rstd * w[e];
+    if (p.xg != nullptr && valid && v < nv) (static_cast<uint4*>(p.xg) + row_off)[v] = pack_vec8(y[k]);
     if (p.xq != nullptr) {
-      const BlockScale b = block_scale(half_warp_max(abs_max8(y)), 448.f);
-      if (in) (reinterpret_cast<uint2*>(p.xq) + row_off)[v] = fp8x8<0>(y, b.inv);
-      if (in && (v & 15) == 0) p.scales[(v >> 4) * p.rows_pad + row] = b.scale;
+      const float a = half_warp_max(abs_max8(y[k]));
+      if ((threadIdx.x & (V - 1)) == k) amax = a;
     }
+  }
+  if (p.xq == nullptr) return;
+  // the divisions of the thread's V blocks are shared out: lane k of each half warp makes those of block k
+  const BlockScale b = block_scale(amax, 448.f);
+  const int kl = threadIdx.x & 15, block = (j0 + kl * step) >> 4;
+  if (kl < V && valid && block * 16 < nv) p.scales[block * p.rows_pad + row] = b.scale;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int v = j0 + k * step;
+    const float inv = __shfl_sync(0xffffffffu, b.inv, k, 16);
+    if (valid && v < nv) (reinterpret_cast<uint2*>(p.xq) + row_off)[v] = fp8x8<0>(y[k], inv);
   }
 }
 
 // With xhat = s rstd and g = dy w:  dx = rstd (g - xhat mean(g xhat)) + ds,  dweight = sum over rows of dy xhat.
-// Blocks walk rows blockIdx, blockIdx + gridDim, ... and keep their dweight sums in registers (fp32); the
-// blocks' partial rows are summed in a fixed order by a second kernel.
+//
+// One persistent block an SM.  Warp 0 keeps the next rows of s, dy and ds coming into a ring in shared memory (bulk
+// copies; about 190 KB in flight an SM), teams of TW of the 16 consumer warps take a row each: thread j of a team has
+// the vectors j + 32 TW k (k < 4), reads them once for the two sums and once for the output (shared memory is cheap
+// here, registers are not), and keeps the weights and its dweight sums in registers.  Row i of the block belongs to team
+// i % teams, so the order of every sum is fixed.
+constexpr int kBwdConsumers = 16;
+constexpr int kBwdMaxD = 256 * 4 * kBwdConsumers;
+constexpr uint32_t kSiteRmsProducer = 32, kSiteRmsConsumer = 33;
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
+    k_rmsnorm_add_bwd(const RmsBlockParams p, int tw, int slots, unsigned int* err, unsigned long long timeout_ns) {
+  extern __shared__ __align__(128) uint8_t bwd_smem[];
+  __shared__ float2 red[2][kBwdConsumers];
+  __shared__ int vote[2][kBwdConsumers];
+  __shared__ __align__(8) uint64_t full[32], empty[32];
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool has_r = p.r.p[0] != nullptr;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.d) * 2u, slot_bytes = row_bytes * 3u;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < slots; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, tw);
+    }
+    abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  const WaitCtx wc{&abort_flag, err, timeout_ns};
+  const int grid = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
+  const int n_rows = (p.rows - first + grid - 1) / grid;
+  const int cw = warp - 1, team = cw / tw, teams = kBwdConsumers / tw;
+  const int nv = p.d / 8, step = 32 * tw, j = (cw - team * tw) * 32 + lane;
+  float2 dw[4][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) dw[k][w] = make_float2(0.f, 0.f);
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t phase = 0;
+      int slot = 0, issued = 0;
+      for (int i = 0; i < n_rows; ++i) {
+        if (!wait_bounded(empty + slot, phase ^ 1u, wc, kSiteRmsProducer)) break;
+        const int row = first + i * grid, c = row / p.rows_per_chunk;
+        const long long off = static_cast<long long>(row - c * p.rows_per_chunk) * row_bytes;
+        uint8_t* dst = bwd_smem + static_cast<long long>(slot) * slot_bytes;
+        mbar_arrive_expect_tx(full + slot, has_r ? slot_bytes : 2u * row_bytes);
+        bulk_load(dst, static_cast<const uint8_t*>(p.x.p[c]) + off, row_bytes, full + slot);
+        bulk_load(dst + row_bytes, static_cast<const uint8_t*>(p.dy) + static_cast<long long>(row) * row_bytes, row_bytes,
+                  full + slot);
+        if (has_r) bulk_load(dst + 2 * row_bytes, static_cast<const uint8_t*>(p.r.p[c]) + off, row_bytes, full + slot);
+        ++issued;
+        if (++slot == slots) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+      // copies in flight land before their memory is used again
+      for (int i = issued > slots ? issued - slots : 0; i < issued; ++i)
+        wait_drain(full + i % slots, static_cast<uint32_t>(i / slots) & 1u, timeout_ns);
+    }
+  } else {
+    uint4 w4[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w4[k] = j + k * step < nv ? __ldg(static_cast<const uint4*>(p.weight) + j + k * step) : make_uint4(0, 0, 0, 0);
+    const float inv_d = 1.f / static_cast<float>(p.d);
+    int par = 0;
+    for (int i = team; i < n_rows; i += teams, par ^= 1) {
+      const int slot = i % slots;
+      // every warp waits (bounded) on its own; the outcomes are voted on, so a team leaves the loop together
+      const bool ok = __all_sync(0xffffffffu, wait_bounded(full + slot, static_cast<uint32_t>(i / slots) & 1u, wc, kSiteRmsConsumer));
+      const uint4* xs = reinterpret_cast<const uint4*>(bwd_smem + static_cast<long long>(slot) * slot_bytes);
+      const uint4* ys = xs + nv;
+      const uint4* rs = ys + nv;
+      float2 sq = make_float2(0.f, 0.f), sg = sq;
+      if (ok) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int v = j + k * step;
+          if (v >= nv) continue;
+          const uint4 x = xs[v], y = ys[v];
+          const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
+          const uint32_t wa[4] = {w4[k].x, w4[k].y, w4[k].z, w4[k].w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float2 xf = unpack_bf16x2(xa[w]);
+            sq = __ffma2_rn(xf, xf, sq);
+            sg = __ffma2_rn(__fmul2_rn(unpack_bf16x2(ya[w]), unpack_bf16x2(wa[w])), xf, sg);
+          }
+        }
+      }
+      float2 t = make_float2(warp_add(sq.x + sq.y), warp_add(sg.x + sg.y));
+      bool team_ok = ok;
+      if (tw > 1) {
+        if (lane == 0) {
+          red[par][cw] = t;
+          vote[par][cw] = ok ? 1 : 0;
+        }
+        bar_sync(1 + team, step);
+        t = make_float2(0.f, 0.f);
+        for (int w = 0; w < tw; ++w) {
+          t.x += red[par][team * tw + w].x;
+          t.y += red[par][team * tw + w].y;
+          team_ok = team_ok && vote[par][team * tw + w] != 0;
+        }
+      }
+      if (!team_ok) break;
+      const float rstd = rsqrtf(t.x * inv_d + p.eps);
+      const float c = t.y * rstd * rstd * rstd * inv_d;  // rstd mean(g xhat) rstd
+      const float2 r2 = make_float2(rstd, rstd), nc2 = make_float2(-c, -c);
+      const int row = first + i * grid, ch = row / p.rows_per_chunk;
+      uint4* out = static_cast<uint4*>(p.s.p[ch]) + static_cast<long long>(row - ch * p.rows_per_chunk) * nv;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int v = j + k * step;
+        if (v >= nv) continue;
+        const uint4 x = xs[v], y = ys[v];
+        const uint4 r = has_r ? rs[v] : make_uint4(0, 0, 0, 0);
+        const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w}, ra[4] = {r.x, r.y, r.z, r.w};
+        const uint32_t wa[4] = {w4[k].x, w4[k].y, w4[k].z, w4[k].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 xf = unpack_bf16x2(xa[w]), yr = __fmul2_rn(unpack_bf16x2(ya[w]), r2);
+          dw[k][w] = __ffma2_rn(yr, xf, dw[k][w]);
+          const float2 dx = __fadd2_rn(__ffma2_rn(xf, nc2, __fmul2_rn(yr, unpack_bf16x2(wa[w]))), unpack_bf16x2(ra[w]));
+          o[w] = pack_bf16x2(dx.x, dx.y);
+        }
+        out[v] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + slot);
+    }
+  }
+  __syncthreads();  // the producer has drained its copies: the ring's memory is free for the teams' sums [teams][d]
+  float* acc = reinterpret_cast<float*>(bwd_smem);
+  if (warp > 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int v = j + k * step;
+      if (v >= nv) continue;
+      float4* a = reinterpret_cast<float4*>(acc + static_cast<long long>(team) * p.d + v * 8);
+      a[0] = make_float4(dw[k][0].x, dw[k][0].y, dw[k][1].x, dw[k][1].y);
+      a[1] = make_float4(dw[k][2].x, dw[k][2].y, dw[k][3].x, dw[k][3].y);
+    }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
+    float t = 0.f;
+    for (int tm = 0; tm < teams; ++tm) t += acc[static_cast<long long>(tm) * p.d + c];
+    p.partial[static_cast<long long>(first) * p.d + c] = t;
+  }
+}
+
+// dweight[c] = the sum of the blocks' partial rows, in a fixed order: 32 columns a block, rows over its 8 warps.
+__global__ void __launch_bounds__(256) k_dweight_sum(const float* partial, int rows, int d, float* dweight) {
+  __shared__ float red[8][33];
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
+  if (c < d) {
+    int r = warp;
+    for (; r + 24 < rows; r += 32)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) a[u] += partial[static_cast<long long>(r + 8 * u) * d + c];
+    for (int u = 0; r < rows; r += 8, ++u) a[u & 3] += partial[static_cast<long long>(r) * d + c];
+  }
+  red[warp][lane] = (a[0] + a[1]) + (a[2] + a[3]);
+  __syncthreads();
+  if (warp == 0 && c < d) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += red[w][lane];
+    dweight[c] = t;
+  }
+}
+
+// Rows wider than the ring kernel's, in registers: one block per row at a time, blocks walk the rows.
 template <int V>
-__global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_rmsnorm_add_bwd(const RmsBlockParams p) {
+__global__ void __launch_bounds__(1024) k_rmsnorm_add_bwd_wide(const RmsBlockParams p) {
   __shared__ float red[32];
+  griddep_launch_dependents();
   const int nv = p.d / 8;
   const bool has_r = p.r.p[0] != nullptr;
   float dw[V][8];
@@ -149,91 +367,165 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_rmsnorm_add_bwd(const R
   }
 }
 
-constexpr int kBwdMaxBlocks = 592;  // dweight partial rows
-
-struct RowLaunch {
-  int threads, v;
-};
-RowLaunch row_launch(int d) {
-  const int nv = d / 8;
-  const int v = nv <= 512 ? 1 : nv <= 1024 ? 2 : 4;
-  return {(nv + v * 32 - 1) / (v * 32) * 32, v};
-}
+constexpr int kBwdSmem = 196608;    // most shared memory of the ring; the teams' sums take 64 KB at most
+constexpr int kBwdMaxBlocks = 160;  // dweight partial rows at most (one block an SM)
 
 // ----------------------------------------------------------------------------- quantiser
 
-// One 128 x 128 tile per block of 256 threads, through shared memory: thread t reads 16-byte vectors t % 16 of
-// rows t / 16 + 16 i.  A row's (or the tile's) amax comes from shuffles, a column's from shared memory.
-constexpr int kQPitch = 130;  // bf16 elements: rows start 65 words apart, so a column walk is conflict-free
+// One 128 x 128 tile per block of 256 threads.  Thread t holds the 16-byte vectors t % 16 of rows t / 16 + 16 i (i < 8)
+// in registers, all eight loads in flight at once; src is read once for both outputs.
+//   q:  the 16 vectors of a row are on the 16 lanes of a half warp: amax by shuffles, codes stored from registers.
+//   qT: column amaxes over a thread's rows, its half warps (shuffle) and the eight warps (shared memory); the codes
+//       cross a 16 KB byte tile and leave as 16 consecutive bytes of a destination row, eight lanes a 128-byte line.
+// In the byte tile, word w of row r sits at word w ^ 4 (r / 16): a warp's reads (four words of rows 16 g + i, g < 8) and
+// its 8-byte writes are then free of bank conflicts.
 template <int FMT, bool TILE>
 __global__ void __launch_bounds__(256) k_quantize_block(const QuantBlockParams p) {
-  __shared__ __nv_bfloat16 tile[kBlock * kQPitch];
-  __shared__ float red[8];
+  __shared__ __align__(16) uint32_t tile[kBlock * kBlock / 4];
+  __shared__ float red[8][kBlock];  // column amaxes of the warps; row 0: the columns' factors.  TILE: red[0][warp]
   const int r0 = blockIdx.y * kBlock, c0 = blockIdx.x * kBlock;
-  const int t = threadIdx.x, vc = t & 15, vr = t >> 4;
+  const int t = threadIdx.x, vc = t & 15, vr = t >> 4, warp = t >> 5;
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.src);
-  float m = 0.f;
+  const int c = c0 + vc * 8;
+  uint4 u[8];
+#pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int r = r0 + vr + 16 * i, c = c0 + vc * 8;
-    const uint4 u = r < p.rows && c < p.cols ? *reinterpret_cast<const uint4*>(src + r * p.ld + c) : make_uint4(0, 0, 0, 0);
-    uint32_t* row = reinterpret_cast<uint32_t*>(tile + (vr + 16 * i) * kQPitch + vc * 8);
-    row[0] = u.x;
-    row[1] = u.y;
-    row[2] = u.z;
-    row[3] = u.w;
-    float f[8];
-    unpack_vec8(u, f);
-    m = fmaxf(m, abs_max8(f));
+    const int r = r0 + vr + 16 * i;
+    u[i] = r < p.rows && c < p.cols ? __ldg(reinterpret_cast<const uint4*>(src + r * p.ld + c)) : make_uint4(0, 0, 0, 0);
   }
+  constexpr float kF = fp8_max(FMT);
   BlockScale b{};
   if constexpr (TILE) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float f[8];
+      unpack_vec8(u[i], f);
+      m = fmaxf(m, abs_max8(f));
+    }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((t & 31) == 0) red[t >> 5] = m;
+    if ((t & 31) == 0) red[0][warp] = m;
     __syncthreads();
-    for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
-    b = block_scale(m, fp8_max(FMT));
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, red[0][w]);
+    b = block_scale(m, kF);
     if (t == 0) {
       if (p.scales != nullptr) p.scales[static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x] = b.scale;
       if (p.scales_t != nullptr) p.scales_t[static_cast<long long>(blockIdx.x) * gridDim.y + blockIdx.y] = b.scale;
     }
-  }
-  __syncthreads();
-  if (p.q != nullptr) {
-    const long long rows_pad = static_cast<long long>(gridDim.y) * kBlock;
-    for (int i = 0; i < 8; ++i) {
-      const int r = r0 + vr + 16 * i, c = c0 + vc * 8;
-      const uint32_t* row = reinterpret_cast<const uint32_t*>(tile + (vr + 16 * i) * kQPitch + vc * 8);
-      float f[8];
-      unpack_vec8(make_uint4(row[0], row[1], row[2], row[3]), f);
-      if constexpr (!TILE) b = block_scale(half_warp_max(abs_max8(f)), fp8_max(FMT));
-      if (r < p.rows && c < p.cols)
-        *reinterpret_cast<uint2*>(p.q + static_cast<long long>(r) * p.cols + c) = fp8x8<FMT>(f, b.inv);
-      if (!TILE && vc == 0 && r < p.rows) p.scales[blockIdx.x * rows_pad + r] = b.scale;
-    }
-  }
-  if (p.qt != nullptr) {
-    const long long cols_pad = static_cast<long long>(gridDim.x) * kBlock;
-    const long long pitch = (p.rows + 15) / 16 * 16;
-    for (int i = 0; i < 8; ++i) {  // destination row (source column) vr + 16 i, source rows 8 vc .. + 7
-      const int c = c0 + vr + 16 * i, r = r0 + vc * 8;
-      float f[8];
+  } else if (p.qt != nullptr) {
+    float m[8] = {};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = __bfloat162float(tile[(vc * 8 + e) * kQPitch + vr + 16 * i]);
-      if constexpr (!TILE) b = block_scale(half_warp_max(abs_max8(f)), fp8_max(FMT));
-      if (c < p.cols && r < pitch) *reinterpret_cast<uint2*>(p.qt + c * pitch + r) = fp8x8<FMT>(f, b.inv);
-      if (!TILE && vc == 0 && c < p.cols) p.scales_t[blockIdx.y * cols_pad + c] = b.scale;
+    for (int i = 0; i < 8; ++i) {
+      float f[8];
+      unpack_vec8(u[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m[e] = fmaxf(m[e], fabsf(f[e]));
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], 16));
+    if ((t & 16) == 0) {
+      reinterpret_cast<float4*>(red[warp] + vc * 8)[0] = make_float4(m[0], m[1], m[2], m[3]);
+      reinterpret_cast<float4*>(red[warp] + vc * 8)[1] = make_float4(m[4], m[5], m[6], m[7]);
+    }
+    __syncthreads();
+    if (t < kBlock) {
+      float a = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) a = fmaxf(a, red[w][t]);
+      const BlockScale col = block_scale(a, kF);
+      red[0][t] = col.inv;
+      if (c0 + t < p.cols)
+        p.scales_t[blockIdx.y * (static_cast<long long>(gridDim.x) * kBlock) + c0 + t] = col.scale;
+    }
+    __syncthreads();
+  }
+  float inv[8];
+  if (p.qt != nullptr) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) inv[e] = TILE ? b.inv : red[0][vc * 8 + e];
+  }
+  const long long rows_pad = static_cast<long long>(gridDim.y) * kBlock;
+  float row_inv = 0.f;  // lane vc < 8 of a half warp: of row vr + 16 vc
+  if (!TILE && p.q != nullptr) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float f[8];
+      unpack_vec8(u[i], f);
+      const float a = half_warp_max(abs_max8(f));
+      if ((vc & 7) == i) m = a;
+    }
+    const BlockScale row = block_scale(m, kF);
+    row_inv = row.inv;
+    const int r = r0 + vr + 16 * (vc & 7);
+    if (vc < 8 && r < p.rows) p.scales[blockIdx.x * rows_pad + r] = row.scale;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + vr + 16 * i;
+    float f[8];
+    unpack_vec8(u[i], f);
+    if constexpr (TILE) {
+      const uint2 codes = fp8x8<FMT>(f, b.inv);
+      if (p.q != nullptr && r < p.rows && c < p.cols)
+        *reinterpret_cast<uint2*>(p.q + static_cast<long long>(r) * p.cols + c) = codes;
+      if (p.qt != nullptr) *reinterpret_cast<uint2*>(tile + (vr + 16 * i) * 32 + ((2 * vc) ^ (4 * i))) = codes;
+    } else {
+      if (p.q != nullptr) {
+        const float row = __shfl_sync(0xffffffffu, row_inv, i, 16);
+        if (r < p.rows && c < p.cols)
+          *reinterpret_cast<uint2*>(p.q + static_cast<long long>(r) * p.cols + c) = fp8x8<FMT>(f, row);
+      }
+      if (p.qt != nullptr) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= inv[e];
+        *reinterpret_cast<uint2*>(tile + (vr + 16 * i) * 32 + ((2 * vc) ^ (4 * i))) = fp8x8<FMT>(f, 1.f);
+      }
+    }
+  }
+  if (p.qt == nullptr) return;
+  __syncthreads();
+  // lane: rows 16 g .. + 15 (g = lane % 8) of the four columns of word w
+  const int g = t & 7, w = (t >> 3) & 31;
+  const long long pitch = (p.rows + 15) / 16 * 16;
+  uint32_t out[4][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {  // a 4 x 4 byte transpose: words of rows 16 g + 4 k .. + 3
+    uint32_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = tile[(16 * g + 4 * k + i) * 32 + (w ^ (4 * g))];
+    const uint32_t lo01 = __byte_perm(x[0], x[1], 0x5140), hi01 = __byte_perm(x[0], x[1], 0x7362);
+    const uint32_t lo23 = __byte_perm(x[2], x[3], 0x5140), hi23 = __byte_perm(x[2], x[3], 0x7362);
+    out[0][k] = __byte_perm(lo01, lo23, 0x5410);
+    out[1][k] = __byte_perm(lo01, lo23, 0x7632);
+    out[2][k] = __byte_perm(hi01, hi23, 0x5410);
+    out[3][k] = __byte_perm(hi01, hi23, 0x7632);
+  }
+  const int r = r0 + 16 * g;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int oc = c0 + 4 * w + e;
+    if (oc < p.cols && r < pitch)
+      *reinterpret_cast<uint4*>(p.qt + oc * pitch + r) = make_uint4(out[e][0], out[e][1], out[e][2], out[e][3]);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_rmsnorm_add(const RmsBlockParams& p, const DeviceCtx&, cudaStream_t s) {
-  const RowLaunch l = row_launch(p.d);
-  if (l.v == 1) k_rmsnorm_add<1><<<p.rows, l.threads, 0, s>>>(p);
-  else if (l.v == 2) k_rmsnorm_add<2><<<p.rows, l.threads, 0, s>>>(p);
-  else k_rmsnorm_add<4><<<p.rows, l.threads, 0, s>>>(p);
+cudaError_t launch_rmsnorm_add(const RmsBlockParams& p, const DeviceCtx& ctx, cudaStream_t s) {
+  // More vectors than two fillings of the SMs' threads: four a thread, so that the registers hold as many rows' loads as
+  // they can.  Below that one a thread, the shortest path from load to store.
+  const int nv = p.d / 8;
+  const int v = nv > 1024 || static_cast<long long>(p.rows) * nv > 4096ll * ctx.sm_count ? 4 : nv > 512 ? 2 : 1;
+  int tw = 1;
+  while (32 * tw * v < nv) tw *= 2;
+  const int warps = tw < 4 ? 4 : tw, rows = warps / tw;
+  const int grid = (p.rows + rows - 1) / rows;
+  if (v == 1) k_rmsnorm_add<1><<<grid, 32 * warps, 0, s>>>(p, tw);
+  else if (v == 2) k_rmsnorm_add<2><<<grid, 32 * warps, 0, s>>>(p, tw);
+  else k_rmsnorm_add<4><<<grid, 32 * warps, 0, s>>>(p, tw);
   return cudaGetLastError();
 }
 
@@ -241,15 +533,44 @@ size_t rmsnorm_add_bwd_scratch_floats(int rows, int d) {
   return static_cast<size_t>(rows < kBwdMaxBlocks ? rows : kBwdMaxBlocks) * d;
 }
 
-cudaError_t launch_rmsnorm_add_bwd(const RmsBlockParams& p, float* dweight, const DeviceCtx&, cudaStream_t s) {
-  const RowLaunch l = row_launch(p.d);
-  const int blocks = p.rows < kBwdMaxBlocks ? p.rows : kBwdMaxBlocks;
-  if (l.v == 1) k_rmsnorm_add_bwd<1><<<blocks, l.threads, 0, s>>>(p);
-  else if (l.v == 2) k_rmsnorm_add_bwd<2><<<blocks, l.threads, 0, s>>>(p);
-  else k_rmsnorm_add_bwd<4><<<blocks, l.threads, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+cudaError_t launch_rmsnorm_add_bwd(const RmsBlockParams& p, float* dweight, const DeviceCtx& ctx, cudaStream_t s) {
+  int blocks = ctx.sm_count < kBwdMaxBlocks ? ctx.sm_count : kBwdMaxBlocks;
+  if (p.rows < blocks) blocks = p.rows;
+  const int nv = p.d / 8;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  if (p.d <= kBwdMaxD) {
+    int tw = 1;
+    while (32 * tw * 4 < nv) tw *= 2;
+    const int teams = kBwdConsumers / tw;
+    // as many slots as fit (two of the widest row), no more than rows come
+    const int slot = 3 * p.d * 2, most = (p.rows + blocks - 1) / blocks;
+    int slots = kBwdSmem / slot;
+    if (slots > 32) slots = 32;
+    if (slots > most) slots = most;
+    int smem = slots * slot;
+    if (smem < teams * p.d * 4) smem = teams * p.d * 4;
+    e = cudaFuncSetAttribute(k_rmsnorm_add_bwd, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+    if (e != cudaSuccess) return e;
+    cfg.blockDim = dim3(32 * (kBwdConsumers + 1));
+    cfg.dynamicSmemBytes = smem;
+    e = cudaLaunchKernelEx(&cfg, k_rmsnorm_add_bwd, p, tw, slots, ctx.err, ctx.timeout_ns);
+  } else {
+    k_rmsnorm_add_bwd_wide<4><<<blocks, (nv + 127) / 128 * 32, 0, s>>>(p);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
-  return launch_column_sum(p.partial, blocks, p.d, dweight, false, s);
+  cfg.gridDim = dim3((p.d + 31) / 32);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, k_dweight_sum, static_cast<const float*>(p.partial), blocks, p.d, dweight);
 }
 
 cudaError_t launch_quantize_block(const QuantBlockParams& p, cudaStream_t s) {
