@@ -117,11 +117,13 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_rmsnorm_add(const RmsBl
 
 // With xhat = s rstd and g = dy w:  dx = rstd (g - xhat mean(g xhat)) + ds,  dweight = sum over rows of dy xhat.
 //
-// One persistent block an SM.  Warp 0 keeps the next rows of s, dy and ds coming into a ring in shared memory (bulk
-// copies; about 190 KB in flight an SM), teams of TW of the 16 consumer warps take a row each: thread j of a team has
-// the vectors j + 32 TW k (k < 4), reads them once for the two sums and once for the output (shared memory is cheap
-// here, registers are not), and keeps the weights and its dweight sums in registers.  Row i of the block belongs to team
-// i % teams, so the order of every sum is fixed.
+// One persistent block an SM.  Warp 0 keeps the next groups of rows of s, dy and ds coming into a ring in shared memory
+// (bulk copies of about 8 KB, so a group has several rows where rows are short; up to 190 KB in flight an SM), teams of
+// TW of the 16 consumer warps take a row each: thread j of a team has the vectors j + 32 TW k (k < 4), reads them once
+// for the two sums and once for the output (shared memory is cheap here, registers are not), and keeps the weights and
+// its dweight sums in registers.  Row i of the block belongs to team i % teams, so the order of every sum is fixed.
+constexpr int kBwdSmem = 196608;    // most shared memory of the ring; the teams' sums take 64 KB at most
+constexpr int kBwdMaxBlocks = 160;  // dweight partial rows at most (one block an SM)
 constexpr int kBwdConsumers = 16;
 constexpr int kBwdMaxD = 256 * 4 * kBwdConsumers;
 constexpr uint32_t kSiteRmsProducer = 32, kSiteRmsConsumer = 33;
@@ -131,7 +133,8 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
 }
 
 __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
-    k_rmsnorm_add_bwd(const RmsBlockParams p, int tw, int slots, unsigned int* err, unsigned long long timeout_ns) {
+    k_rmsnorm_add_bwd(const RmsBlockParams p, int tw, int group, int slots, unsigned int* err,
+                      unsigned long long timeout_ns) {
   extern __shared__ __align__(128) uint8_t bwd_smem[];
   __shared__ float2 red[2][kBwdConsumers];
   __shared__ int vote[2][kBwdConsumers];
@@ -139,11 +142,12 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool has_r = p.r.p[0] != nullptr;
-  const uint32_t row_bytes = static_cast<uint32_t>(p.d) * 2u, slot_bytes = row_bytes * 3u;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.d) * 2u, part_bytes = row_bytes * static_cast<uint32_t>(group);
+  const uint32_t slot_bytes = part_bytes * 3u;  // [s | dy | ds] of a group
   if (threadIdx.x == 0) {
     for (int s = 0; s < slots; ++s) {
       mbar_init(full + s, 1);
-      mbar_init(empty + s, tw);
+      mbar_init(empty + s, tw * group);
     }
     abort_flag = 0;
     fence_barrier_init();
@@ -154,7 +158,7 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
   griddep_launch_dependents();
   const WaitCtx wc{&abort_flag, err, timeout_ns};
   const int grid = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
-  const int n_rows = (p.rows - first + grid - 1) / grid;
+  const int groups = (p.rows + group - 1) / group, n_groups = (groups - first + grid - 1) / grid;
   const int cw = warp - 1, team = cw / tw, teams = kBwdConsumers / tw;
   const int nv = p.d / 8, step = 32 * tw, j = (cw - team * tw) * 32 + lane;
   float2 dw[4][4];
@@ -166,16 +170,22 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
     if (lane == 0) {
       uint32_t phase = 0;
       int slot = 0, issued = 0;
-      for (int i = 0; i < n_rows; ++i) {
+      for (int i = 0; i < n_groups; ++i) {
         if (!wait_bounded(empty + slot, phase ^ 1u, wc, kSiteRmsProducer)) break;
-        const int row = first + i * grid, c = row / p.rows_per_chunk;
-        const long long off = static_cast<long long>(row - c * p.rows_per_chunk) * row_bytes;
+        const int r0 = (first + i * grid) * group, n = min(group, p.rows - r0);
         uint8_t* dst = bwd_smem + static_cast<long long>(slot) * slot_bytes;
-        mbar_arrive_expect_tx(full + slot, has_r ? slot_bytes : 2u * row_bytes);
-        bulk_load(dst, static_cast<const uint8_t*>(p.x.p[c]) + off, row_bytes, full + slot);
-        bulk_load(dst + row_bytes, static_cast<const uint8_t*>(p.dy) + static_cast<long long>(row) * row_bytes, row_bytes,
-                  full + slot);
-        if (has_r) bulk_load(dst + 2 * row_bytes, static_cast<const uint8_t*>(p.r.p[c]) + off, row_bytes, full + slot);
+        mbar_arrive_expect_tx(full + slot, static_cast<uint32_t>(n) * row_bytes * (has_r ? 3u : 2u));
+        bulk_load(dst + part_bytes, static_cast<const uint8_t*>(p.dy) + static_cast<long long>(r0) * row_bytes,
+                  static_cast<uint32_t>(n) * row_bytes, full + slot);
+        for (int r = 0; r < n;) {  // the group's rows of one chunk after the other
+          const int c = (r0 + r) / p.rows_per_chunk, in = r0 + r - c * p.rows_per_chunk;
+          const int m = min(n - r, p.rows_per_chunk - in);
+          const long long off = static_cast<long long>(in) * row_bytes;
+          const uint32_t bytes = static_cast<uint32_t>(m) * row_bytes, at = static_cast<uint32_t>(r) * row_bytes;
+          bulk_load(dst + at, static_cast<const uint8_t*>(p.x.p[c]) + off, bytes, full + slot);
+          if (has_r) bulk_load(dst + 2 * part_bytes + at, static_cast<const uint8_t*>(p.r.p[c]) + off, bytes, full + slot);
+          r += m;
+        }
         ++issued;
         if (++slot == slots) {
           slot = 0;
@@ -192,14 +202,18 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
     for (int k = 0; k < 4; ++k)
       w4[k] = j + k * step < nv ? __ldg(static_cast<const uint4*>(p.weight) + j + k * step) : make_uint4(0, 0, 0, 0);
     const float inv_d = 1.f / static_cast<float>(p.d);
-    int par = 0;
-    for (int i = team; i < n_rows; i += teams, par ^= 1) {
-      const int slot = i % slots;
+    // the team's next row: row `in` of the block's group gi, in slot `slot` (phase: how often the ring went round)
+    int gi = team / group, in = team - gi * group, slot = gi % slots;
+    uint32_t phase = static_cast<uint32_t>(gi / slots) & 1u;
+    const int dgi = teams / group, din = teams - dgi * group;
+    for (int par = 0;; par ^= 1) {
+      const int row = (first + gi * grid) * group + in;
+      if (gi >= n_groups || row >= p.rows) break;
       // every warp waits (bounded) on its own; the outcomes are voted on, so a team leaves the loop together
-      const bool ok = __all_sync(0xffffffffu, wait_bounded(full + slot, static_cast<uint32_t>(i / slots) & 1u, wc, kSiteRmsConsumer));
-      const uint4* xs = reinterpret_cast<const uint4*>(bwd_smem + static_cast<long long>(slot) * slot_bytes);
-      const uint4* ys = xs + nv;
-      const uint4* rs = ys + nv;
+      const bool ok = __all_sync(0xffffffffu, wait_bounded(full + slot, phase, wc, kSiteRmsConsumer));
+      const uint4* xs = reinterpret_cast<const uint4*>(bwd_smem + static_cast<long long>(slot) * slot_bytes) + in * nv;
+      const uint4* ys = xs + group * nv;
+      const uint4* rs = ys + group * nv;
       float2 sq = make_float2(0.f, 0.f), sg = sq;
       if (ok) {
 #pragma unroll
@@ -236,7 +250,7 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
       const float rstd = rsqrtf(t.x * inv_d + p.eps);
       const float c = t.y * rstd * rstd * rstd * inv_d;  // rstd mean(g xhat) rstd
       const float2 r2 = make_float2(rstd, rstd), nc2 = make_float2(-c, -c);
-      const int row = first + i * grid, ch = row / p.rows_per_chunk;
+      const int ch = row / p.rows_per_chunk;
       uint4* out = static_cast<uint4*>(p.s.p[ch]) + static_cast<long long>(row - ch * p.rows_per_chunk) * nv;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -258,6 +272,13 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + slot);
+      int ahead = dgi;
+      if ((in += din) >= group) {
+        in -= group;
+        ++ahead;
+      }
+      gi += ahead;
+      for (slot += ahead; slot >= slots; slot -= slots) phase ^= 1u;
     }
   }
   __syncthreads();  // the producer has drained its copies: the ring's memory is free for the teams' sums [teams][d]
@@ -280,25 +301,27 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
   }
 }
 
-// dweight[c] = the sum of the blocks' partial rows, in a fixed order: 32 columns a block, rows over its 8 warps.
-__global__ void __launch_bounds__(256) k_dweight_sum(const float* partial, int rows, int d, float* dweight) {
-  __shared__ float red[8][33];
+// dweight[c] = the sum of the blocks' partial rows, in a fixed order: 32 columns a block, the rows over its 32 warps, so
+// that all of a warp's loads are in flight together.
+__global__ void __launch_bounds__(1024) k_dweight_sum(const float* partial, int rows, int d, float* dweight) {
+  __shared__ float red[32][33];
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-  float a[4] = {0.f, 0.f, 0.f, 0.f};
-  if (c < d) {
-    int r = warp;
-    for (; r + 24 < rows; r += 32)
+  float a[(kBwdMaxBlocks + 31) / 32];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) a[u] += partial[static_cast<long long>(r + 8 * u) * d + c];
-    for (int u = 0; r < rows; r += 8, ++u) a[u & 3] += partial[static_cast<long long>(r) * d + c];
+  for (int u = 0; u < (kBwdMaxBlocks + 31) / 32; ++u) {
+    const int r = warp + 32 * u;
+    a[u] = c < d && r < rows ? partial[static_cast<long long>(r) * d + c] : 0.f;
   }
-  red[warp][lane] = (a[0] + a[1]) + (a[2] + a[3]);
+  float t = 0.f;
+#pragma unroll
+  for (int u = 0; u < (kBwdMaxBlocks + 31) / 32; ++u) t += a[u];
+  red[warp][lane] = t;
   __syncthreads();
   if (warp == 0 && c < d) {
-    float t = 0.f;
+    t = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t += red[w][lane];
+    for (int w = 0; w < 32; ++w) t += red[w][lane];
     dweight[c] = t;
   }
 }
@@ -366,9 +389,6 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_add_bwd_wide(const RmsBlockPar
     out[1] = make_float4(dw[k][4], dw[k][5], dw[k][6], dw[k][7]);
   }
 }
-
-constexpr int kBwdSmem = 196608;    // most shared memory of the ring; the teams' sums take 64 KB at most
-constexpr int kBwdMaxBlocks = 160;  // dweight partial rows at most (one block an SM)
 
 // ----------------------------------------------------------------------------- quantiser
 
@@ -550,8 +570,11 @@ cudaError_t launch_rmsnorm_add_bwd(const RmsBlockParams& p, float* dweight, cons
     int tw = 1;
     while (32 * tw * 4 < nv) tw *= 2;
     const int teams = kBwdConsumers / tw;
-    // as many slots as fit (two of the widest row), no more than rows come
-    const int slot = 3 * p.d * 2, most = (p.rows + blocks - 1) / blocks;
+    // groups of about 8 KB a tensor, but one for each block at least; as many slots as fit (two of the widest row)
+    int group = 8192 / (2 * p.d);
+    if (group > p.rows / blocks) group = p.rows / blocks;
+    if (group < 1) group = 1;
+    const int slot = 3 * p.d * 2 * group, groups = (p.rows + group - 1) / group, most = (groups + blocks - 1) / blocks;
     int slots = kBwdSmem / slot;
     if (slots > 32) slots = 32;
     if (slots > most) slots = most;
@@ -561,14 +584,14 @@ cudaError_t launch_rmsnorm_add_bwd(const RmsBlockParams& p, float* dweight, cons
     if (e != cudaSuccess) return e;
     cfg.blockDim = dim3(32 * (kBwdConsumers + 1));
     cfg.dynamicSmemBytes = smem;
-    e = cudaLaunchKernelEx(&cfg, k_rmsnorm_add_bwd, p, tw, slots, ctx.err, ctx.timeout_ns);
+    e = cudaLaunchKernelEx(&cfg, k_rmsnorm_add_bwd, p, tw, group, slots, ctx.err, ctx.timeout_ns);
   } else {
     k_rmsnorm_add_bwd_wide<4><<<blocks, (nv + 127) / 128 * 32, 0, s>>>(p);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((p.d + 31) / 32);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(1024);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, k_dweight_sum, static_cast<const float*>(p.partial), blocks, p.d, dweight);
 }
