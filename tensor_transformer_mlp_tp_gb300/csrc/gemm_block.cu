@@ -62,18 +62,37 @@ cudaError_t run_pair(const GemmBlockParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// CTAs that share a tile's k-blocks: as many (a power of two up to 8) as fill the SMs' slots, which keeps the most bytes
+// in flight, with two k-blocks each at least.
+int few_ranks(int tiles, int k_blocks, int slots) {
+  int ranks = 1;
+  while (ranks < 8 && 2ll * ranks * tiles <= slots && 4 * ranks <= k_blocks) ranks *= 2;
+  return ranks;
+}
+
+// Which kernel: up to 128 rows the one that streams B once.  Above, whichever has fewer k-blocks one after the other: a
+// pair's k-block (256 x 256) takes about 0.40 us and a 128 x 128 one 0.45 us, measured on GB300 with tiles for a single
+// wave (M = 256, N = 4096, K = 16384: 32 us split over two CTAs a tile, 53 us on pairs; M = 384: 58 and 53 us;
+// M = 1024, N = 1024, K = 4096: 12.9 and 16.6 us; M = 192, N = 16384, K = 4096: 38 and 18.5 us).
+bool few_rows(const GemmBlockLaunch& g, int k_blocks, int sms) {
+  if (g.M <= 128) return true;
+  const long long few_tiles = static_cast<long long>((g.M + 127) / 128) * ((g.N + 127) / 128);
+  if (few_tiles > 4ll * sms) return false;
+  const long long ranks = few_ranks(static_cast<int>(few_tiles), k_blocks, sms);
+  const long long few = (few_tiles * ranks + sms - 1) / sms * ((k_blocks + ranks - 1) / ranks);
+  const long long pairs = sms / 2, pair_tiles = static_cast<long long>((g.M + 255) / 256) * ((g.N + 255) / 256);
+  const long long pair = (pair_tiles + pairs - 1) / pairs * k_blocks;
+  return 9 * few <= 8 * pair;
+}
+
 template <int BT, int OUT, bool BVEC>
 cudaError_t run_few(GemmBlockParams p, const DeviceCtx& ctx, cudaStream_t s) {
   using S = BlockFewShape<BT, BVEC>;
   auto kern = k_gemm_block_few<BT, OUT, BVEC>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  // Split K until the CTAs fill the SMs' slots (two an SM up to BT = 64): what bounds the launch is how many bytes are
-  // in flight.  A CTA keeps at least two k-blocks.
   const int tiles = (p.g.N + 127) / 128, row_tiles = (p.g.M + BT - 1) / BT;
-  const int slots = ctx.sm_count * (BT == 128 ? 1 : 2);
-  int ranks = 1;
-  while (ranks < 8 && 2 * ranks * tiles * row_tiles <= slots && 4 * ranks <= p.k_blocks) ranks *= 2;
+  const int ranks = few_ranks(tiles * row_tiles, p.k_blocks, ctx.sm_count * (BT == 128 ? 1 : 2));
   p.group_m = ranks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks * tiles, row_tiles);
@@ -106,8 +125,6 @@ cudaError_t launch_few(GemmBlockParams& p, const DeviceCtx& ctx, cudaStream_t s)
   return g.c_fp32 ? run_few<BT, kOutFp32, false>(p, ctx, s) : run_few<BT, kOutBf16, false>(p, ctx, s);
 }
 
-constexpr int kFewRows = 128;
-
 }  // namespace
 
 cudaError_t launch_gemm_block(const GemmBlockLaunch& g, const DeviceCtx& ctx, cudaStream_t s) {
@@ -119,7 +136,8 @@ cudaError_t launch_gemm_block(const GemmBlockLaunch& g, const DeviceCtx& ctx, cu
   p.k_blocks = (g.K + kBlock - 1) / kBlock;
   p.err = ctx.err;
   p.timeout_ns = ctx.timeout_ns;
-  if (g.M <= kFewRows) return g.M <= 16 ? launch_few<16>(p, ctx, s) : g.M <= 32 ? launch_few<32>(p, ctx, s)
+  if (few_rows(g, p.k_blocks, ctx.sm_count))
+    return g.M <= 16 ? launch_few<16>(p, ctx, s) : g.M <= 32 ? launch_few<32>(p, ctx, s)
                               : g.M <= 64 ? launch_few<64>(p, ctx, s) : launch_few<128>(p, ctx, s);
   p.m_blocks = (g.M + 255) / 256;
   p.n_blocks = (g.N + 255) / 256;

@@ -3,8 +3,8 @@
 // of A as its N (128 x BT x 32 UMMAs, cta_group::1), and the K blocks are split over a cluster of CTAs, whose fp32 sums
 // are joined through distributed shared memory in rank order -- no workspace, no atomics, one launch.
 //
-// Warp 0 copies (TMA ring), warp 1 issues, warps 2-5 promote: a thread holds one output column's BT sums, scaled per
-// k-block by its own row scale of B and the BT scales of A.  With BT columns a partial sum, several fit in TMEM, so the
+// Warp 0 copies (TMA ring), warp 1 issues, the others promote: a thread holds BT (or BT / 2) sums of one output column,
+// scaled per k-block by its own row scale of B and the scales of A.  With BT columns a partial sum, several fit in TMEM, so the
 // promotion's latency is hidden.  In the end each CTA of the cluster finishes BT / C of the rows: a warp per row, four
 // consecutive columns a lane, which makes a 1 x 128 block of an 8-bit output one warp's.
 #pragma once
@@ -17,12 +17,15 @@ template <int BT, bool BVEC>
 struct BlockFewShape {
   static_assert(BT == 16 || BT == 32 || BT == 64 || BT == 128, "BT");
   // two CTAs share an SM up to BT = 64
-  static constexpr int kStages = BT <= 32 ? 5 : BT == 64 ? 4 : 6;
+  static constexpr int kStages = BT <= 64 ? 4 : 6;
   static constexpr int kWTile = 128 * 128, kTTile = BT * 128;
   static constexpr int kStage = kWTile + kTTile;
   static constexpr int kBufs = BT == 128 ? 2 : 4;  // partial sums in TMEM
   static constexpr int kTmemCols = kBufs * BT;
-  static constexpr int kThreads = 192;
+  // Promotion warps: four (one a TMEM lane quadrant), or eight that halve the columns where there are many.
+  static constexpr int kPromoteWarps = BT >= 64 ? 8 : 4;
+  static constexpr int kCols = BT / (kPromoteWarps / 4);  // of one warp
+  static constexpr int kThreads = 64 + 32 * kPromoteWarps;
   // Slots of the k-blocks' scales, rewritten 16 blocks later (see BlockPairShape): the producer is at most kStages
   // blocks ahead of the UMMAs, those at most kBufs ahead of the promotion.
   static constexpr int kScaleSlots = 16;
@@ -47,7 +50,8 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
 // grid: (cluster size x column tiles, row tiles).  p.tmA: A [M x K], boxes of 128 bytes x BT rows; p.tmB: B [N x K],
 // 128 bytes x 128 rows; p.tmSA boxes of BT scales, p.tmSB (BVEC) of 128.
 template <int BT, int OUT, bool BVEC>
-__global__ void __launch_bounds__(192, BT == 128 ? 1 : 2) k_gemm_block_few(const __grid_constant__ GemmBlockParams p) {
+__global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ? 1 : 2)
+    k_gemm_block_few(const __grid_constant__ GemmBlockParams p) {
   using S = BlockFewShape<BT, BVEC>;
   constexpr int STAGES = S::kStages, BUFS = S::kBufs;
   extern __shared__ uint8_t smem_raw[];
@@ -77,7 +81,7 @@ __global__ void __launch_bounds__(192, BT == 128 ? 1 : 2) k_gemm_block_few(const
     }
     for (int a = 0; a < BUFS; ++a) {
       mbar_init(tfull + a, 1);
-      mbar_init(tempty + a, 4);
+      mbar_init(tempty + a, S::kPromoteWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -101,7 +105,8 @@ __global__ void __launch_bounds__(192, BT == 128 ? 1 : 2) k_gemm_block_few(const
   griddep_launch_dependents();
   const WaitCtx wc{abort_flag, p.err, p.timeout_ns};
 
-  float acc[BT];
+  constexpr int CW = S::kCols;
+  float2 acc[CW / 2];
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol = policy_evict_normal();
@@ -148,8 +153,8 @@ __global__ void __launch_bounds__(192, BT == 128 ? 1 : 2) k_gemm_block_few(const
       wait_drain(drain, 0, p.timeout_ns);
     }
   } else {
-    const int quad = warp & 3;
-    const uint32_t trow = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t trow = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half * CW);
     const float* sb = p.g.b_scales + (BVEC ? 0 : static_cast<long long>(n0 >> 7) * p.k_blocks + kb0);
     float sb_cur = 0.f, sb_next = 0.f;  // weight scales: lane l holds that of block 32 j + l
     if (!BVEC) {
@@ -157,36 +162,45 @@ __global__ void __launch_bounds__(192, BT == 128 ? 1 : 2) k_gemm_block_few(const
       if (32 + static_cast<int>(lane) < kbs) sb_next = __ldg(sb + 32 + lane);
     }
 #pragma unroll
-    for (int j = 0; j < BT; ++j) acc[j] = 0.f;
+    for (int j = 0; j < CW / 2; ++j) acc[j] = make_float2(0.f, 0.f);
     for (int b = 0; b < kbs; ++b) {
       const int buf = b % BUFS;
       if (!warp_wait(tfull + buf, static_cast<uint32_t>(b / BUFS) & 1u, wc, kSiteBlockPromote)) break;
       tc_fence_after_sync();
+      constexpr int kChunks = CW / 16, kAhead = kChunks < 3 ? kChunks : 3;  // 16-column loads in flight
+      uint32_t r[kAhead][16];
+#pragma unroll
+      for (int c = 0; c < kAhead; ++c) tmem_load_16cols_async(trow + buf * BT + c * 16, r[c]);
       const float* slot = scale_ring + (b & (S::kScaleSlots - 1)) * S::kSlotFloats;
       const float sr = BVEC ? slot[S::kRowFloats + quad * 32 + lane] : __shfl_sync(0xffffffffu, sb_cur, b & 31);
+      const float2 sr2 = make_float2(sr, sr);
       if (!BVEC && (b & 31) == 31) {
         sb_cur = sb_next;
         const int next = b + 33 + static_cast<int>(lane);
         sb_next = next < kbs ? __ldg(sb + next) : 0.f;
       }
 #pragma unroll
-      for (int c = 0; c < BT; c += 16) {
-        uint32_t r[16];
-        tmem_load_16cols_async(trow + buf * BT + c, r);
-        tmem_wait_ld(r);
-        if (c + 16 == BT) {
+      for (int c = 0; c < kChunks; ++c) {
+        uint32_t(&v)[16] = r[c % kAhead];
+        float2 w[8];  // the chunk's products of scales, while its columns come
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float4 s = *reinterpret_cast<const float4*>(slot + half * CW + c * 16 + 2 * j);
+          w[j] = __fmul2_rn(make_float2(s.x, s.y), sr2);
+          w[j + 1] = __fmul2_rn(make_float2(s.z, s.w), sr2);
+        }
+        tmem_wait_ld(v);
+        if (c == kChunks - kAhead) {  // every load has returned: the buffer is free before the last sums, not after them
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) tmem_wait_ld(r[i]);
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(tempty + buf);
         }
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 s = *reinterpret_cast<const float4*>(slot + c + j);
-          acc[c + j] = fmaf(__uint_as_float(r[j]), sr * s.x, acc[c + j]);
-          acc[c + j + 1] = fmaf(__uint_as_float(r[j + 1]), sr * s.y, acc[c + j + 1]);
-          acc[c + j + 2] = fmaf(__uint_as_float(r[j + 2]), sr * s.z, acc[c + j + 2]);
-          acc[c + j + 3] = fmaf(__uint_as_float(r[j + 3]), sr * s.w, acc[c + j + 3]);
-        }
+        for (int j = 0; j < 8; ++j)
+          acc[c * 8 + j] = __ffma2_rn(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), w[j], acc[c * 8 + j]);
+        if (c + kAhead < kChunks) tmem_load_16cols_async(trow + buf * BT + (c + kAhead) * 16, v);
       }
     }
   }
@@ -194,7 +208,11 @@ __global__ void __launch_bounds__(192, BT == 128 ? 1 : 2) k_gemm_block_few(const
   float* red = reinterpret_cast<float*>(smem);
   if (warp >= 2) {
 #pragma unroll
-    for (int j = 0; j < BT; ++j) red[j * 128 + (warp & 3) * 32 + lane] = acc[j];
+    for (int j = 0; j < CW / 2; ++j) {
+      float* at = red + (((warp - 2) >> 2) * CW + 2 * j) * 128 + (warp & 3) * 32 + lane;
+      at[0] = acc[j].x;
+      at[128] = acc[j].y;
+    }
   }
   if (warp == 1) {
     __syncwarp();
@@ -212,7 +230,7 @@ __global__ void __launch_bounds__(192, BT == 128 ? 1 : 2) k_gemm_block_few(const
   }
   const uint32_t red_addr = smem_u32(red) + lane * 16;
   const int rows = min(BT, p.g.M - m0);
-  for (int j = rank + ranks * warp; j < rows; j += ranks * 6) {
+  for (int j = rank + ranks * warp; j < rows; j += ranks * (S::kThreads / 32)) {
     const int row = m0 + j;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     for (int r = 0; r < ranks; ++r) {
