@@ -11,6 +11,7 @@ raises; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -184,9 +185,12 @@ def _opt_ptrs(ts):
     return (None, None) if ts is None else _ptrs(ts)
 
 
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream(stream):
     if stream is None:  # the current stream's handle without building a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -662,12 +666,17 @@ def _scales(t, rows, cols, block_rows, fn):
 def _chunk_array(chunks, n, numel, fn):
     if chunks is None:
         return None
-    if len(chunks) != n:
-        _refuse(fn)
     kind = _ARRAYS.get(n)
     if kind is None:
         kind = _ARRAYS[n] = ctypes.c_void_p * n
-    return kind(*[_typed(t, _BF16, numel, fn) for t in chunks])
+    at = []
+    for t in chunks:
+        if t.dtype is not _BF16 or t.numel() < numel or not t.is_contiguous():
+            _refuse(fn)
+        at.append(t.data_ptr())
+    if len(at) != n:
+        _refuse(fn)
+    return kind(*at)
 
 
 def tpmlp_rmsnorm_add_gather(X_chunks, weight, N, R_chunks=None, S_chunks=None, Xg=None, Xq=None, x_scales=None,
@@ -684,6 +693,7 @@ def tpmlp_rmsnorm_add_gather(X_chunks, weight, N, R_chunks=None, S_chunks=None, 
         raise TpMlpError(fn, st)
 
 
+@functools.lru_cache(maxsize=256)
 def tpmlp_rmsnorm_add_backward_workspace_size(T, d, N) -> int:
     n = ctypes.c_size_t(0)
     _check("tpmlp_rmsnorm_add_backward_workspace_size", lib().tpmlp_rmsnorm_add_backward_workspace_size(
