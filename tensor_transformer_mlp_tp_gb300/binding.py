@@ -735,19 +735,23 @@ def tpmlp_quantize_block(src, block_rows=1, fmt=E4M3, q=None, scales=None, qT=No
 def tpmlp_gemm_fp8_block(A8, a_scales, B8, b_scales, C, bias=None, b_block_rows=128, a_fmt=E4M3, b_fmt=E4M3,
                          stream=None):
     """C [M x N] (bf16 or fp32, rows may be strided) = A8 [M x K] . B8 [N x K]^T with their block scales, + bias."""
-    fn = "tpmlp_gemm_fp8_block"
     M, K = A8.shape
     N, k = B8.shape
     ldc, step = C.stride()
     c_type = C.dtype
-    if k != K or C.shape != (M, N) or (step != 1 and N > 1) or (c_type is not _BF16 and c_type is not _FP32):
-        _refuse(fn)
+    kb = (K + 127) >> 7
+    nb = kb * ((N + 127) & -128) if b_block_rows == 1 else kb * ((N + 127) >> 7)
+    if (k != K or C.shape != (M, N) or (step != 1 and N > 1) or (c_type is not _BF16 and c_type is not _FP32) or
+            A8.element_size() != 1 or not A8.is_contiguous() or B8.element_size() != 1 or not B8.is_contiguous() or
+            a_scales.dtype is not _FP32 or a_scales.numel() < kb * ((M + 127) & -128) or not a_scales.is_contiguous() or
+            b_scales.dtype is not _FP32 or b_scales.numel() < nb or not b_scales.is_contiguous()):
+        _refuse("tpmlp_gemm_fp8_block")
     st = (_lib or lib()).tpmlp_gemm_fp8_block(
-        _bytes(A8, M * K, fn), a_fmt, _scales(a_scales, M, K, 1, fn), _bytes(B8, N * K, fn), b_fmt,
-        _scales(b_scales, N, K, b_block_rows, fn), b_block_rows, M, N, K, _typed(bias, _BF16, N, fn), C.data_ptr(),
+        A8.data_ptr(), a_fmt, a_scales.data_ptr(), B8.data_ptr(), b_fmt, b_scales.data_ptr(), b_block_rows, M, N, K,
+        None if bias is None else _typed(bias, _BF16, N, "tpmlp_gemm_fp8_block"), C.data_ptr(),
         FP32 if c_type is _FP32 else BF16, ldc if M > 1 else N, _stream(stream))
     if st:
-        raise TpMlpError(fn, st)
+        raise TpMlpError("tpmlp_gemm_fp8_block", st)
 
 
 def tpmlp_gemm1_fp8_block(Xq, x_scales, AqT, a_scales, bias, N, Hq, h_scales, Hpre=None, stream=None):

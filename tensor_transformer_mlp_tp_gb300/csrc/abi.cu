@@ -73,6 +73,8 @@ tpmlp_status device_ctx(DeviceCtx* out) {
     st.ctx.sm_count = sms;
     st.ctx.timeout_ns = timeout_ns_from_env();
     st.ctx_id = current_context_id();  // the lookup above made the device's context current
+    st.ctx.device = dev;
+    st.ctx.ctx_id = st.ctx_id;
     st.init = true;
   }
   *out = st.ctx;

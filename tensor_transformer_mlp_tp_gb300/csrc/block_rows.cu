@@ -580,7 +580,8 @@ cudaError_t launch_rmsnorm_add_bwd(const RmsBlockParams& p, float* dweight, cons
     if (slots > most) slots = most;
     int smem = slots * slot;
     if (smem < teams * p.d * 4) smem = teams * p.d * 4;
-    e = cudaFuncSetAttribute(k_rmsnorm_add_bwd, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+    static std::atomic<unsigned long long> set[64] = {};
+    e = raise_smem_once(k_rmsnorm_add_bwd, kBwdSmem, ctx, set);
     if (e != cudaSuccess) return e;
     cfg.blockDim = dim3(32 * (kBwdConsumers + 1));
     cfg.dynamicSmemBytes = smem;

@@ -37,11 +37,12 @@ int max_clusters(K kern, int cluster, int smem, int threads, std::atomic<int>* c
 }
 
 template <int OUT, bool BVEC>
-cudaError_t run_pair(const GemmBlockParams& p, cudaStream_t s) {
+cudaError_t run_pair(const GemmBlockParams& p, const DeviceCtx& ctx, cudaStream_t s) {
   using S = BlockPairShape<BVEC>;
   auto kern = k_gemm_block_pair<OUT, BVEC>;
   static std::atomic<int> cache[64] = {};
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  static std::atomic<unsigned long long> set[64] = {};
+  const cudaError_t e = raise_smem_once(kern, S::kSmem, ctx, set);
   if (e != cudaSuccess) return e;
   const int pairs = max_clusters(kern, 2, S::kSmem, S::kThreads, cache);
   const int tiles = p.m_blocks * p.n_blocks;
@@ -89,7 +90,8 @@ template <int BT, int OUT, bool BVEC>
 cudaError_t run_few(GemmBlockParams p, const DeviceCtx& ctx, cudaStream_t s) {
   using S = BlockFewShape<BT, BVEC>;
   auto kern = k_gemm_block_few<BT, OUT, BVEC>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  static std::atomic<unsigned long long> set[64] = {};
+  const cudaError_t e = raise_smem_once(kern, S::kSmem, ctx, set);
   if (e != cudaSuccess) return e;
   const int tiles = (p.g.N + 127) / 128, row_tiles = (p.g.M + BT - 1) / BT;
   const int ranks = few_ranks(tiles * row_tiles, p.k_blocks, ctx.sm_count * (BT == 128 ? 1 : 2));
@@ -100,14 +102,14 @@ cudaError_t run_few(GemmBlockParams p, const DeviceCtx& ctx, cudaStream_t s) {
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ranks;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = ranks;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = ranks > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
@@ -156,9 +158,9 @@ cudaError_t launch_gemm_block(const GemmBlockLaunch& g, const DeviceCtx& ctx, cu
   if (g.hq != nullptr)
     ok = ok && encode_tile_map(&p.tmH, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.hq, g.N, g.M, g.N, 128, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return cudaErrorInvalidValue;
-  if (g.hq != nullptr) return run_pair<kOutGelu8, false>(p, s);  // weights have 128-row tiles
-  if (g.b_block_rows == 1) return g.c_fp32 ? run_pair<kOutFp32, true>(p, s) : run_pair<kOutBf16, true>(p, s);
-  return g.c_fp32 ? run_pair<kOutFp32, false>(p, s) : run_pair<kOutBf16, false>(p, s);
+  if (g.hq != nullptr) return run_pair<kOutGelu8, false>(p, ctx, s);  // weights have 128-row tiles
+  if (g.b_block_rows == 1) return g.c_fp32 ? run_pair<kOutFp32, true>(p, ctx, s) : run_pair<kOutBf16, true>(p, ctx, s);
+  return g.c_fp32 ? run_pair<kOutFp32, false>(p, ctx, s) : run_pair<kOutBf16, false>(p, ctx, s);
 }
 
 }  // namespace tpmlp

@@ -3,6 +3,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "common.h"
 
 namespace tpmlp {
@@ -63,7 +65,20 @@ struct DeviceCtx {
   unsigned int* err;           // device error words
   unsigned long long timeout_ns;
   int sm_count;
+  int device;
+  unsigned long long ctx_id;   // the context the error words belong to (current_context_id)
 };
+
+// Raise `kern`'s dynamic shared memory to `bytes`, once for each context: `set` is the kernel's own array, one entry a
+// device, of the context it was last set in (concurrent callers store the same value).
+template <typename K>
+cudaError_t raise_smem_once(K kern, int bytes, const DeviceCtx& ctx, std::atomic<unsigned long long>* set) {
+  std::atomic<unsigned long long>& id = set[ctx.device & 63];
+  if (ctx.ctx_id != 0 && id.load(std::memory_order_relaxed) == ctx.ctx_id) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) id.store(ctx.ctx_id, std::memory_order_relaxed);
+  return e;
+}
 
 // Bounds-check violations counted by the row kernels' / the GEMMs' translation units since the last call
 // (zero in release builds, which check nothing), and the first site; both cleared.

@@ -348,6 +348,11 @@ __device__ __forceinline__ void tmem_load_16x32_async(uint32_t taddr, uint32_t (
       : "r"(taddr)
       : "memory");
 }
+// Wait for every tcgen05.ld of this warp where all that uses the loaded registers also uses `dep`: the value passes
+// through the statement, which orders the uses behind it without naming the registers.
+__device__ __forceinline__ void tmem_wait_ld_before(float2& dep) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(dep.x), "+f"(dep.y) : : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
