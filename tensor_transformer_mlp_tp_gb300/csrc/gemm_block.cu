@@ -67,7 +67,7 @@ cudaError_t run_pair(const GemmBlockParams& p, const DeviceCtx& ctx, cudaStream_
 // in flight, with two k-blocks each at least.
 int few_ranks(int tiles, int k_blocks, int slots) {
   int ranks = 1;
-  while (ranks < 8 && 2ll * ranks * tiles <= slots && 4 * ranks <= k_blocks) ranks *= 2;
+  while (ranks < kFewMaxRanks && 2ll * ranks * tiles <= slots && 4 * ranks <= k_blocks) ranks *= 2;
   return ranks;
 }
 

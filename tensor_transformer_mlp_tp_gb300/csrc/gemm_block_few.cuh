@@ -13,6 +13,8 @@
 
 namespace tpmlp {
 
+constexpr int kFewMaxRanks = 8;  // CTAs of a cluster
+
 template <int BT, bool BVEC>
 struct BlockFewShape {
   static_assert(BT == 16 || BT == 32 || BT == 64 || BT == 128, "BT");
@@ -233,9 +235,13 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
   for (int j = rank + ranks * warp; j < rows; j += ranks * (S::kThreads / 32)) {
     const int row = m0 + j;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int r = 0; r < ranks; ++r) {
-      const float4 q = ld_cluster_f4(mapa_shared(red_addr + j * 512, static_cast<uint32_t>(r)));
-      v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w;
+    float4 q[kFewMaxRanks];  // all in flight together, added in rank order
+#pragma unroll
+    for (int r = 0; r < kFewMaxRanks; ++r)
+      q[r] = r < ranks ? ld_cluster_f4(mapa_shared(red_addr + j * 512, static_cast<uint32_t>(r))) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < kFewMaxRanks; ++r) {
+      v[0] += q[r].x; v[1] += q[r].y; v[2] += q[r].z; v[3] += q[r].w;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += b4[i];

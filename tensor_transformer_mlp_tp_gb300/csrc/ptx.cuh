@@ -84,6 +84,19 @@ __device__ __forceinline__ bool mbar_try_wait_short(uint64_t* bar, uint32_t pari
   return ok != 0;
 }
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -347,11 +360,6 @@ __device__ __forceinline__ void tmem_load_16x32_async(uint32_t taddr, uint32_t (
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
-}
-// Wait for every tcgen05.ld of this warp where all that uses the loaded registers also uses `dep`: the value passes
-// through the statement, which orders the uses behind it without naming the registers.
-__device__ __forceinline__ void tmem_wait_ld_before(float2& dep) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(dep.x), "+f"(dep.y) : : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
