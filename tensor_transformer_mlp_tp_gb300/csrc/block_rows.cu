@@ -25,12 +25,6 @@ __device__ __forceinline__ float block_add(float v, float* red) {
   return t;
 }
 
-template <typename T>
-__device__ __forceinline__ T* chunk_at(T* const* chunks, int rows_per_chunk, int row, long long elems_per_row) {
-  const int j = row / rows_per_chunk;
-  return chunks[j] + static_cast<long long>(row - j * rows_per_chunk) * elems_per_row;
-}
-
 // s = bf16(x + r), y = s rsqrt(mean(s^2) + eps) w.  A team of TW warps per row; thread t of the team holds the 16-byte
 // vectors t + 32 TW k (k < V) in registers, so the row is read once, all its loads in flight together, and the 16 vectors
 // of a 1 x 128 block sit on the 16 lanes of a half warp.  The statistics are of the stored (rounded) sum, the value the
@@ -38,6 +32,8 @@ __device__ __forceinline__ T* chunk_at(T* const* chunks, int rows_per_chunk, int
 template <int V>
 __global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_rmsnorm_add(const RmsBlockParams p, int tw) {
   __shared__ float red[32];
+  griddep_wait();
+  griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, team = warp / tw, nv = p.d / 8;
   const int step = 32 * tw, j0 = threadIdx.x - team * step;
   const int row = blockIdx.x * (static_cast<int>(blockDim.x >> 5) / tw) + team;
@@ -132,9 +128,11 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+template <int VT>
 __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
     k_rmsnorm_add_bwd(const RmsBlockParams p, int tw, int group, int slots, unsigned int* err,
                       unsigned long long timeout_ns) {
+  constexpr bool kKeep = VT == 2;  // s and dy stay in registers between the two passes
   extern __shared__ __align__(128) uint8_t bwd_smem[];
   __shared__ float2 red[2][kBwdConsumers];
   __shared__ int vote[2][kBwdConsumers];
@@ -161,9 +159,9 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
   const int groups = (p.rows + group - 1) / group, n_groups = (groups - first + grid - 1) / grid;
   const int cw = warp - 1, team = cw / tw, teams = kBwdConsumers / tw;
   const int nv = p.d / 8, step = 32 * tw, j = (cw - team * tw) * 32 + lane;
-  float2 dw[4][4];
+  float2 dw[VT][4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < VT; ++k)
 #pragma unroll
     for (int w = 0; w < 4; ++w) dw[k][w] = make_float2(0.f, 0.f);
   if (warp == 0) {
@@ -197,9 +195,9 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
         wait_drain(full + i % slots, static_cast<uint32_t>(i / slots) & 1u, timeout_ns);
     }
   } else {
-    uint4 w4[4];
+    uint4 w4[VT];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < VT; ++k)
       w4[k] = j + k * step < nv ? __ldg(static_cast<const uint4*>(p.weight) + j + k * step) : make_uint4(0, 0, 0, 0);
     const float inv_d = 1.f / static_cast<float>(p.d);
     // the team's next row: row `in` of the block's group gi, in slot `slot` (phase: how often the ring went round)
@@ -214,13 +212,18 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
       const uint4* xs = reinterpret_cast<const uint4*>(bwd_smem + static_cast<long long>(slot) * slot_bytes) + in * nv;
       const uint4* ys = xs + group * nv;
       const uint4* rs = ys + group * nv;
+      uint4 x4[kKeep ? VT : 1], y4[kKeep ? VT : 1];
       float2 sq = make_float2(0.f, 0.f), sg = sq;
       if (ok) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < VT; ++k) {
           const int v = j + k * step;
           if (v >= nv) continue;
           const uint4 x = xs[v], y = ys[v];
+          if (kKeep) {
+            x4[kKeep ? k : 0] = x;
+            y4[kKeep ? k : 0] = y;
+          }
           const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w};
           const uint32_t wa[4] = {w4[k].x, w4[k].y, w4[k].z, w4[k].w};
 #pragma unroll
@@ -253,10 +256,10 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
       const int ch = row / p.rows_per_chunk;
       uint4* out = static_cast<uint4*>(p.s.p[ch]) + static_cast<long long>(row - ch * p.rows_per_chunk) * nv;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < VT; ++k) {
         const int v = j + k * step;
         if (v >= nv) continue;
-        const uint4 x = xs[v], y = ys[v];
+        const uint4 x = kKeep ? x4[kKeep ? k : 0] : xs[v], y = kKeep ? y4[kKeep ? k : 0] : ys[v];
         const uint4 r = has_r ? rs[v] : make_uint4(0, 0, 0, 0);
         const uint32_t xa[4] = {x.x, x.y, x.z, x.w}, ya[4] = {y.x, y.y, y.z, y.w}, ra[4] = {r.x, r.y, r.z, r.w};
         const uint32_t wa[4] = {w4[k].x, w4[k].y, w4[k].z, w4[k].w};
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
   float* acc = reinterpret_cast<float*>(bwd_smem);
   if (warp > 0) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < VT; ++k) {
       const int v = j + k * step;
       if (v >= nv) continue;
       float4* a = reinterpret_cast<float4*>(acc + static_cast<long long>(team) * p.d + v * 8);
@@ -403,6 +406,8 @@ template <int FMT, bool TILE>
 __global__ void __launch_bounds__(256) k_quantize_block(const QuantBlockParams p) {
   __shared__ __align__(16) uint32_t tile[kBlock * kBlock / 4];
   __shared__ float red[8][kBlock];  // column amaxes of the warps; row 0: the columns' factors.  TILE: red[0][warp]
+  griddep_wait();
+  griddep_launch_dependents();
   const int r0 = blockIdx.y * kBlock, c0 = blockIdx.x * kBlock;
   const int t = threadIdx.x, vc = t & 15, vr = t >> 4, warp = t >> 5;
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.src);
@@ -534,6 +539,27 @@ __global__ void __launch_bounds__(256) k_quantize_block(const QuantBlockParams p
 
 }  // namespace
 
+namespace {
+
+// Launch with programmatic stream serialisation: the kernel may be set up while the previous one ends (each waits for
+// that one, griddep_wait, before its first global access).
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
+}  // namespace
+
 cudaError_t launch_rmsnorm_add(const RmsBlockParams& p, const DeviceCtx& ctx, cudaStream_t s) {
   // More vectors than two fillings of the SMs' threads: four a thread, so that the registers hold as many rows' loads as
   // they can.  Below that one a thread, the shortest path from load to store.
@@ -543,10 +569,8 @@ cudaError_t launch_rmsnorm_add(const RmsBlockParams& p, const DeviceCtx& ctx, cu
   while (32 * tw * v < nv) tw *= 2;
   const int warps = tw < 4 ? 4 : tw, rows = warps / tw;
   const int grid = (p.rows + rows - 1) / rows;
-  if (v == 1) k_rmsnorm_add<1><<<grid, 32 * warps, 0, s>>>(p, tw);
-  else if (v == 2) k_rmsnorm_add<2><<<grid, 32 * warps, 0, s>>>(p, tw);
-  else k_rmsnorm_add<4><<<grid, 32 * warps, 0, s>>>(p, tw);
-  return cudaGetLastError();
+  auto kern = v == 1 ? k_rmsnorm_add<1> : v == 2 ? k_rmsnorm_add<2> : k_rmsnorm_add<4>;
+  return launch_overlapped(kern, dim3(grid), dim3(32 * warps), 0, s, p, tw);
 }
 
 size_t rmsnorm_add_bwd_scratch_floats(int rows, int d) {
@@ -557,18 +581,11 @@ cudaError_t launch_rmsnorm_add_bwd(const RmsBlockParams& p, float* dweight, cons
   int blocks = ctx.sm_count < kBwdMaxBlocks ? ctx.sm_count : kBwdMaxBlocks;
   if (p.rows < blocks) blocks = p.rows;
   const int nv = p.d / 8;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   cudaError_t e;
   if (p.d <= kBwdMaxD) {
+    const int vt = p.d <= kBwdMaxD / 2 ? 2 : 4;
     int tw = 1;
-    while (32 * tw * 4 < nv) tw *= 2;
+    while (32 * tw * vt < nv) tw *= 2;
     const int teams = kBwdConsumers / tw;
     // groups of about 8 KB a tensor, but one for each block at least; as many slots as fit (two of the widest row)
     int group = 8192 / (2 * p.d);
@@ -580,30 +597,26 @@ cudaError_t launch_rmsnorm_add_bwd(const RmsBlockParams& p, float* dweight, cons
     if (slots > most) slots = most;
     int smem = slots * slot;
     if (smem < teams * p.d * 4) smem = teams * p.d * 4;
-    static std::atomic<unsigned long long> set[64] = {};
-    e = raise_smem_once(k_rmsnorm_add_bwd, kBwdSmem, ctx, set);
+    static std::atomic<unsigned long long> set[2][64] = {};
+    auto kern = vt == 2 ? k_rmsnorm_add_bwd<2> : k_rmsnorm_add_bwd<4>;
+    e = raise_smem_once(kern, kBwdSmem, ctx, set[vt == 2 ? 0 : 1]);
     if (e != cudaSuccess) return e;
-    cfg.blockDim = dim3(32 * (kBwdConsumers + 1));
-    cfg.dynamicSmemBytes = smem;
-    e = cudaLaunchKernelEx(&cfg, k_rmsnorm_add_bwd, p, tw, group, slots, ctx.err, ctx.timeout_ns);
+    e = launch_overlapped(kern, dim3(blocks), dim3(32 * (kBwdConsumers + 1)), smem, s, p, tw, group, slots, ctx.err,
+                          ctx.timeout_ns);
   } else {
     k_rmsnorm_add_bwd_wide<4><<<blocks, (nv + 127) / 128 * 32, 0, s>>>(p);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((p.d + 31) / 32);
-  cfg.blockDim = dim3(1024);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, k_dweight_sum, static_cast<const float*>(p.partial), blocks, p.d, dweight);
+  return launch_overlapped(k_dweight_sum, dim3((p.d + 31) / 32), dim3(1024), 0, s, static_cast<const float*>(p.partial),
+                           blocks, p.d, dweight);
 }
 
 cudaError_t launch_quantize_block(const QuantBlockParams& p, cudaStream_t s) {
   const dim3 grid((p.cols + kBlock - 1) / kBlock, (p.rows + kBlock - 1) / kBlock);
-  if (p.fmt == 0 && p.block_rows == 1) k_quantize_block<0, false><<<grid, 256, 0, s>>>(p);
-  else if (p.fmt == 0) k_quantize_block<0, true><<<grid, 256, 0, s>>>(p);
-  else if (p.block_rows == 1) k_quantize_block<1, false><<<grid, 256, 0, s>>>(p);
-  else k_quantize_block<1, true><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  auto kern = p.block_rows == 1 ? (p.fmt == 0 ? k_quantize_block<0, false> : k_quantize_block<1, false>)
+                                : (p.fmt == 0 ? k_quantize_block<0, true> : k_quantize_block<1, true>);
+  return launch_overlapped(kern, grid, dim3(256), 0, s, p);
 }
 
 }  // namespace tpmlp
