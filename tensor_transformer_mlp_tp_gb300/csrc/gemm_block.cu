@@ -5,6 +5,7 @@
 #include <cuda_fp8.h>
 
 #include <atomic>
+#include <climits>
 #include <cstring>
 
 #include "gemm_block_few.cuh"
@@ -141,6 +142,7 @@ cudaError_t launch_gemm_block(const GemmBlockLaunch& g, const DeviceCtx& ctx, cu
   if (few_rows(g, p.k_blocks, ctx.sm_count))
     return g.M <= 16 ? launch_few<16>(p, ctx, s) : g.M <= 32 ? launch_few<32>(p, ctx, s)
                               : g.M <= 64 ? launch_few<64>(p, ctx, s) : launch_few<128>(p, ctx, s);
+  if (static_cast<long long>((g.M + 255) / 256) * ((g.N + 255) / 256) > INT_MAX) return cudaErrorNotSupported;
   p.m_blocks = (g.M + 255) / 256;
   p.n_blocks = (g.N + 255) / 256;
   p.group_m = 8;

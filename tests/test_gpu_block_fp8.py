@@ -389,3 +389,130 @@ def test_empty_batches_leave_outputs_alone():
     binding.tpmlp_quantize_block(e, q=torch.empty(0, 64, dtype=U8, device="cuda"), scales=torch.empty(1, 0, device="cuda"))
     torch.cuda.synchronize()
     assert (dw == 7).all()
+
+
+# ----------------------------------------------------------------------------- offsets past 2^31, threads, layouts
+
+def _sample(n, k, seed):
+    return torch.randint(0, n, (k,), generator=torch.Generator().manual_seed(seed)).tolist() + [0, n - 1]
+
+
+def test_norm_and_backward_past_two_to_the_31():
+    T, d, N = (1 << 19) + 256, 4096, 2
+    g = gen(31)
+    x = torch.empty(T, d, dtype=BF16, device="cuda").normal_(generator=g)
+    r = torch.empty(T, d, dtype=BF16, device="cuda").normal_(generator=g)
+    w = (1 + 0.3 * torch.randn(d, generator=g, device="cuda")).to(BF16)
+    S, q, sc = torch.empty_like(x), torch.empty(T, d, dtype=U8, device="cuda"), torch.empty(32, u.up(T, 128), device="cuda")
+    rows = T // N
+    binding.tpmlp_rmsnorm_add_gather(list(x.split(rows)), w, N, R_chunks=list(r.split(rows)),
+                                     S_chunks=list(S.split(rows)), Xq=q, x_scales=sc)
+    at = _sample(T, 40, 1)
+    s = S[at].to(F64)
+    total = x[at].to(F64) + r[at].to(F64)
+    within(S[at], total, 2.0 ** -8 * (1 + 2.0 ** -15) * total.abs(), "sum")
+    y = s * torch.rsqrt((s * s).mean(1, keepdim=True) + 1e-5) * w.to(F64)
+    scale = sc[:, at].t()
+    each = scale.to(F64).repeat_interleave(128, 1)
+    within(u.values(q[at], scale, 1, 0), y, (2.0 ** -4 + 2 * STAT) * y.abs() + 2.0 ** -10 * each, "e4m3")
+    dX, dw = x, torch.empty(d, device="cuda")
+    binding.tpmlp_rmsnorm_add_backward(list(S.split(rows)), w, r, N, list(dX.split(rows)), dw)
+    device_ok()
+    ref, _ = u.norm_grad(s, w.to(F64), r[at].to(F64), torch.zeros_like(s))
+    rstd = torch.rsqrt((s * s).mean(1, keepdim=True) + 1e-5)
+    size = (rstd * r[at].to(F64) * w.to(F64)).abs() + s.abs() * rstd ** 3 * (r[at].to(F64) * w.to(F64) * s).abs().sum(1, keepdim=True) / d
+    within(dX[at], ref, 2.0 ** -8 * ref.abs() + 2 * STAT * size, "dx")
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_block_past_two_to_the_31(block_rows):
+    rows, cols = 131328, 16400
+    src = torch.empty(rows, cols, dtype=BF16, device="cuda").normal_(generator=gen(32))
+    q, qt = torch.empty(rows, cols, dtype=U8, device="cuda"), torch.empty(cols, rows, dtype=U8, device="cuda")
+    sc = torch.empty(binding.block_scales_shape(rows, cols, block_rows), device="cuda")
+    st = torch.empty(binding.block_scales_shape(cols, rows, block_rows), device="cuda")
+    binding.tpmlp_quantize_block(src, block_rows, 0, q=q, scales=sc, qT=qt, scalesT=st)
+    device_ok()
+    for i, j in ((0, 0), (rows // 128 - 1, cols // 128), (rows // 128 - 1, 0), (700, 100)):
+        a, b = slice(128 * i, 128 * (i + 1)), slice(128 * j, min(cols, 128 * (j + 1)))
+        want, scale = u.quantize(src[a, b], block_rows, 0)
+        assert torch.equal(q[a, b], want)
+        assert torch.equal(sc[i, j:j + 1] if block_rows == 128 else sc[j, a], scale.reshape(-1))
+        want, scale = u.quantize(src[a, b].t(), block_rows, 0)
+        assert torch.equal(qt[b, a], want)
+        assert torch.equal(st[j, i:i + 1] if block_rows == 128 else st[i, b], scale.reshape(-1))
+
+
+@pytest.mark.parametrize("gelu", [False, True])
+def test_products_past_two_to_the_31(gelu):
+    M, N, K = 131328, 16400, 144
+    g = gen(33)
+    a, sa, av = u.operand(g, M, K, 1, 0)
+    b, sb, bv = u.operand(g, N, K, 128, 0, 0.02)
+    at = _sample(M, 30, 2)
+    ref, tol = av[at] @ bv.t(), u.gemm_bound(av[at], bv, K)
+    if not gelu:
+        C = torch.empty(M, N, dtype=BF16, device="cuda")
+        binding.tpmlp_gemm_fp8_block(a, sa, b, sb, C)
+        device_ok()
+        within(C[at], ref, tol + 2.0 ** -8 * (ref.abs() + tol), "C")
+        return
+    hq, hs = torch.empty(M, N, dtype=U8, device="cuda"), torch.empty(binding.block_scales_shape(M, N), device="cuda")
+    pre = torch.empty(M, N, dtype=BF16, device="cuda")
+    binding.tpmlp_gemm1_fp8_block(a, sa, b, sb, None, 1, hq, hs, Hpre=pre)
+    device_ok()
+    within(pre[at], ref, tol + 2.0 ** -8 * (ref.abs() + tol), "Hpre")
+    H, scale = u.gelu64(ref), hs[:, at].t()
+    dev = 1.13 * tol + 2e-7 * ref.abs() + 2.0 ** -21 * H.abs()
+    each = scale.to(F64).repeat_interleave(128, 1)[:, :N]
+    within(u.values(hq[at], scale, 1, 0), H, dev + (2.0 ** -4 + 2.0 ** -20) * (H.abs() + dev) + 2.0 ** -10 * each, "H")
+
+
+def test_calls_from_several_threads():
+    """Each thread on its own stream with its own buffers, shapes that take both product kernels."""
+    import threading
+
+    sets = [mlp(T, d, F, N, 40 + i) for i, (T, d, F, N) in enumerate([(96, 256, 1024, 4), (300, 512, 768, 3), (2, 128, 512, 2)])]
+    for m in sets:
+        mlp_step(m)
+    torch.cuda.synchronize()
+    want = [{k: m[k].clone() for k in OUTPUTS} for m in sets]
+    for m in sets:
+        for k in OUTPUTS:
+            m[k].zero_()
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(m):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(10):
+                mlp_step(m, s)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(m,)) for m in sets]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    for m, w in zip(sets, want):
+        assert all(torch.equal(m[k], w[k]) for k in OUTPUTS)
+
+
+def test_weight_gradient_over_padded_tokens_equals_the_unpadded_sum():
+    """dA with K = tokens rounded up to 16: the zero bytes behind the last token add nothing, whatever their scale."""
+    T, d, F = 37, 144, 272
+    g = gen(50)
+    X, dH = (torch.randn(T, n, generator=g, device="cuda").to(BF16) for n in (d, F))
+    P = u.up(T, 16)
+    xt, ht = torch.empty(d, P, dtype=U8, device="cuda"), torch.empty(F, P, dtype=U8, device="cuda")
+    xs, hs = (torch.empty(binding.block_scales_shape(n, T), device="cuda") for n in (d, F))
+    binding.tpmlp_quantize_block(X, 1, 0, qT=xt, scalesT=xs)
+    binding.tpmlp_quantize_block(dH, 1, 1, qT=ht, scalesT=hs)
+    dA = torch.empty(d, F, device="cuda")
+    binding.tpmlp_gemm_fp8_block(xt, xs, ht, hs, dA, b_block_rows=1, b_fmt=1)
+    l = u.values(xt[:, :T], u.scales_from_layout(xs, d, 1), 1, 0)
+    r = u.values(ht[:, :T], u.scales_from_layout(hs, F, 1), 1, 1)
+    ref, tol = l @ r.t(), u.gemm_bound(l, r, T)
+    within(dA, ref, tol + 2.0 ** -23 * ref.abs(), "dA")
