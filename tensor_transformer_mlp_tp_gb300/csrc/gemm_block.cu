@@ -64,11 +64,28 @@ cudaError_t run_pair(const GemmBlockParams& p, const DeviceCtx& ctx, cudaStream_
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// CTAs that share a tile's k-blocks: as many (a power of two up to 8) as fill the SMs' slots, which keeps the most bytes
-// in flight, with two k-blocks each at least.
-int few_ranks(int tiles, int k_blocks, int slots) {
+// Stands for the few-row kernel in occupancy queries and is never launched: for a kernel that uses tensor memory the
+// query answers one block an SM, while two are resident (their TMEM is half of it each).
+__global__ void __launch_bounds__(320) k_slot() {}
+
+// Clusters of `ranks` CTAs of the BT kernel that the device holds at once.  (Clusters of eight with a CTA an SM leave a
+// fifth of the SMs unused: 15 fit, 120 CTAs of 152.)
+template <int BT>
+int few_clusters(int ranks, const DeviceCtx& ctx) {
+  using S = BlockFewShape<BT, true>;  // the larger of the two
+  static std::atomic<int> cache[4][64] = {};
+  static std::atomic<unsigned long long> set[64] = {};
+  if (raise_smem_once(k_slot, 227 * 1024, ctx, set) != cudaSuccess) return 1;
+  const int slot = ranks == 1 ? 0 : ranks == 2 ? 1 : ranks == 4 ? 2 : 3;
+  return max_clusters(k_slot, ranks, S::kSmem, S::kThreads, cache[slot]);
+}
+
+// CTAs that share a tile's k-blocks: as many (a power of two up to 8) as the device holds for all tiles at once, which
+// keeps the most bytes in flight, with two k-blocks each at least.
+template <int BT>
+int few_ranks(long long tiles, int k_blocks, const DeviceCtx& ctx) {
   int ranks = 1;
-  while (ranks < kFewMaxRanks && 2ll * ranks * tiles <= slots && 4 * ranks <= k_blocks) ranks *= 2;
+  while (ranks < kFewMaxRanks && 4 * ranks <= k_blocks && tiles <= few_clusters<BT>(2 * ranks, ctx)) ranks *= 2;
   return ranks;
 }
 
@@ -76,11 +93,12 @@ int few_ranks(int tiles, int k_blocks, int slots) {
 // pair's k-block (256 x 256) takes about 0.40 us and a 128 x 128 one 0.45 us, measured on GB300 with tiles for a single
 // wave (M = 256, N = 4096, K = 16384: 32 us split over two CTAs a tile, 53 us on pairs; M = 384: 58 and 53 us;
 // M = 1024, N = 1024, K = 4096: 12.9 and 16.6 us; M = 192, N = 16384, K = 4096: 38 and 18.5 us).
-bool few_rows(const GemmBlockLaunch& g, int k_blocks, int sms) {
+bool few_rows(const GemmBlockLaunch& g, int k_blocks, const DeviceCtx& ctx) {
+  const int sms = ctx.sm_count;
   if (g.M <= 128) return true;
   const long long few_tiles = static_cast<long long>((g.M + 127) / 128) * ((g.N + 127) / 128);
   if (few_tiles > 4ll * sms) return false;
-  const long long ranks = few_ranks(static_cast<int>(few_tiles), k_blocks, sms);
+  const long long ranks = few_ranks<128>(few_tiles, k_blocks, ctx);
   const long long few = (few_tiles * ranks + sms - 1) / sms * ((k_blocks + ranks - 1) / ranks);
   const long long pairs = sms / 2, pair_tiles = static_cast<long long>((g.M + 255) / 256) * ((g.N + 255) / 256);
   const long long pair = (pair_tiles + pairs - 1) / pairs * k_blocks;
@@ -95,7 +113,7 @@ cudaError_t run_few(GemmBlockParams p, const DeviceCtx& ctx, cudaStream_t s) {
   const cudaError_t e = raise_smem_once(kern, S::kSmem, ctx, set);
   if (e != cudaSuccess) return e;
   const int tiles = (p.g.N + 127) / 128, row_tiles = (p.g.M + BT - 1) / BT;
-  const int ranks = few_ranks(tiles * row_tiles, p.k_blocks, ctx.sm_count * (BT == 128 ? 1 : 2));
+  const int ranks = few_ranks<BT>(static_cast<long long>(tiles) * row_tiles, p.k_blocks, ctx);
   p.group_m = ranks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks * tiles, row_tiles);
@@ -139,7 +157,7 @@ cudaError_t launch_gemm_block(const GemmBlockLaunch& g, const DeviceCtx& ctx, cu
   p.k_blocks = (g.K + kBlock - 1) / kBlock;
   p.err = ctx.err;
   p.timeout_ns = ctx.timeout_ns;
-  if (few_rows(g, p.k_blocks, ctx.sm_count))
+  if (few_rows(g, p.k_blocks, ctx))
     return g.M <= 16 ? launch_few<16>(p, ctx, s) : g.M <= 32 ? launch_few<32>(p, ctx, s)
                               : g.M <= 64 ? launch_few<64>(p, ctx, s) : launch_few<128>(p, ctx, s);
   if (static_cast<long long>((g.M + 255) / 256) * ((g.N + 255) / 256) > INT_MAX) return cudaErrorNotSupported;

@@ -107,6 +107,16 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
   griddep_launch_dependents();
   const WaitCtx wc{abort_flag, p.err, p.timeout_ns};
 
+  // the epilogue's four columns of a lane and their bias, on its way during the product
+  const int col = n0 + static_cast<int>(lane) * 4;
+  const bool col_in = col < p.g.N;
+  float b4[4] = {0.f, 0.f, 0.f, 0.f};
+  if (p.g.bias != nullptr && col_in) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.g.bias) + col));
+    const float2 lo = unpack_bf16x2(u.x), hi = unpack_bf16x2(u.y);
+    b4[0] = lo.x; b4[1] = lo.y; b4[2] = hi.x; b4[3] = hi.y;
+  }
+
   constexpr int CW = S::kCols;
   float2 acc[CW / 2];
   if (warp == 0) {
@@ -222,14 +232,6 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
     tmem_dealloc(tmem_base, S::kTmemCols);
   }
   cluster_sync_all();  // every CTA's sums are written (a cluster of one: a block barrier)
-  const int col = n0 + static_cast<int>(lane) * 4;
-  const bool col_in = col < p.g.N;
-  float b4[4] = {0.f, 0.f, 0.f, 0.f};
-  if (p.g.bias != nullptr && col_in) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.g.bias) + col));
-    const float2 lo = unpack_bf16x2(u.x), hi = unpack_bf16x2(u.y);
-    b4[0] = lo.x; b4[1] = lo.y; b4[2] = hi.x; b4[3] = hi.y;
-  }
   const uint32_t red_addr = smem_u32(red) + lane * 16;
   const int rows = min(BT, p.g.M - m0);
   for (int j = rank + ranks * warp; j < rows; j += ranks * (S::kThreads / 32)) {
