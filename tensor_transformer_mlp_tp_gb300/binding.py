@@ -627,6 +627,7 @@ def tpmlp_attention_tp_backward(X, Wqkv, Wo, QKV, O, LSE, dY, S, B, H, N, dX, dW
 # addresses are passed as plain integers and the pointer-array types are made once.
 
 _ARRAYS = {}
+_ONE = ctypes.c_void_p * 1
 _BF16, _FP32 = torch.bfloat16, torch.float32
 
 
@@ -634,6 +635,11 @@ def block_scales_shape(rows, cols, block_rows=1):
     """Shape of the fp32 scales of an 8-bit operand [rows x cols] with blocks of block_rows x 128."""
     kb = (cols + 127) >> 7
     return (kb, (rows + 127) & -128) if block_rows == 1 else ((rows + 127) >> 7, kb)
+
+
+@functools.lru_cache(maxsize=1024)
+def _shape(tokens, d, ffn, n_shards):
+    return Shape(tokens, d, ffn, n_shards, BF16)  # the library only reads it
 
 
 def _refuse(fn):
@@ -666,6 +672,11 @@ def _scales(t, rows, cols, block_rows, fn):
 def _chunk_array(chunks, n, numel, fn):
     if chunks is None:
         return None
+    if n == 1 and len(chunks) == 1:
+        t = chunks[0]
+        if t.dtype is not _BF16 or t.numel() < numel or not t.is_contiguous():
+            _refuse(fn)
+        return _ONE(t.data_ptr())
     kind = _ARRAYS.get(n)
     if kind is None:
         kind = _ARRAYS[n] = ctypes.c_void_p * n
@@ -679,6 +690,27 @@ def _chunk_array(chunks, n, numel, fn):
     return kind(*at)
 
 
+_WORKSPACES = {}  # (device index, stream id) -> the stream's workspace
+
+
+def _stream_workspace(nbytes, device, stream):
+    """A workspace that the current stream keeps for its calls, which it runs one after the other: an allocation between
+    two launches costs as much host time as a launch.  Fresh, and the caller's stream's until its work is done, where that
+    order does not hold: for an explicit stream, in a capture (the graph may be replayed on any stream), and on streams
+    that are not torch's own (a handle may be used again for another stream)."""
+    sid = 2 if stream is not None else torch._C._cuda_getCurrentStream(device.index)[0]
+    if (sid == 0 or sid & 1) and not torch._C._cuda_isCurrentStreamCapturing():
+        ws = _WORKSPACES.get((device.index, sid))
+        if ws is None or ws.numel() < nbytes:
+            ws = _WORKSPACES[device.index, sid] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        return ws
+    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    if stream is not None:
+        own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
+        ws.record_stream(own)
+    return ws
+
+
 def tpmlp_rmsnorm_add_gather(X_chunks, weight, N, R_chunks=None, S_chunks=None, Xg=None, Xq=None, x_scales=None,
                              eps=1e-5, stream=None):
     """S_j = X_j + R_j; Xg and / or (Xq, x_scales) = the RMS norm of S, gathered, in bf16 and / or block-scaled E4M3."""
@@ -687,7 +719,7 @@ def tpmlp_rmsnorm_add_gather(X_chunks, weight, N, R_chunks=None, S_chunks=None, 
     T, n = rows * N, rows * d
     st = (_lib or lib()).tpmlp_rmsnorm_add_gather(
         _chunk_array(X_chunks, N, n, fn), _chunk_array(R_chunks, N, n, fn), _typed(weight, _BF16, d, fn), eps,
-        Shape(T, d, d * N, N, BF16), _chunk_array(S_chunks, N, n, fn), _typed(Xg, _BF16, T * d, fn),
+        _shape(T, d, d * N, N), _chunk_array(S_chunks, N, n, fn), _typed(Xg, _BF16, T * d, fn),
         _bytes(Xq, T * d, fn), _scales(x_scales, T, d, 1, fn), _stream(stream))
     if st:
         raise TpMlpError(fn, st)
@@ -707,11 +739,10 @@ def tpmlp_rmsnorm_add_backward(S_chunks, weight, dXg, N, dX_chunks, dweight, dS_
     rows, d = S_chunks[0].shape
     T, n = rows * N, rows * d
     if ws is None:
-        ws = torch.empty(max(tpmlp_rmsnorm_add_backward_workspace_size(T, d, N), 256), dtype=torch.uint8,
-                         device=weight.device)
+        ws = _stream_workspace(tpmlp_rmsnorm_add_backward_workspace_size(T, d, N), weight.device, stream)
     st = (_lib or lib()).tpmlp_rmsnorm_add_backward(
         _chunk_array(S_chunks, N, n, fn), _typed(weight, _BF16, d, fn), eps, _typed(dXg, _BF16, T * d, fn),
-        _chunk_array(dS_chunks, N, n, fn), Shape(T, d, d * N, N, BF16), _chunk_array(dX_chunks, N, n, fn),
+        _chunk_array(dS_chunks, N, n, fn), _shape(T, d, d * N, N), _chunk_array(dX_chunks, N, n, fn),
         _typed(dweight, _FP32, d, fn), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
     if st:
         raise TpMlpError(fn, st)
@@ -763,7 +794,7 @@ def tpmlp_gemm1_fp8_block(Xq, x_scales, AqT, a_scales, bias, N, Hq, h_scales, Hp
         _refuse(fn)
     st = (_lib or lib()).tpmlp_gemm1_fp8_block(
         _bytes(Xq, T * d, fn), _scales(x_scales, T, d, 1, fn), _bytes(AqT, F * d, fn),
-        _scales(a_scales, F, d, 128, fn), _typed(bias, _BF16, F, fn), Shape(T, d, F, N, BF16), _bytes(Hq, T * F, fn),
+        _scales(a_scales, F, d, 128, fn), _typed(bias, _BF16, F, fn), _shape(T, d, F, N), _bytes(Hq, T * F, fn),
         _scales(h_scales, T, F, 1, fn), _typed(Hpre, _BF16, T * F, fn), _stream(stream))
     if st:
         raise TpMlpError(fn, st)

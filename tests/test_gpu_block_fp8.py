@@ -516,3 +516,59 @@ def test_weight_gradient_over_padded_tokens_equals_the_unpadded_sum():
     r = u.values(ht[:, :T], u.scales_from_layout(hs, F, 1), 1, 1)
     ref, tol = l @ r.t(), u.gemm_bound(l, r, T)
     within(dA, ref, tol + 2.0 ** -23 * ref.abs(), "dA")
+
+
+def test_workspaces_kept_for_a_stream():
+    """Backward calls without a workspace: one kept for each of torch's streams, grown when needed, a fresh one for an
+    explicit stream and in a capture."""
+    def case(T, d, seed):
+        s, ds, w, _ = norm_inputs(gen(seed), T, d, 1)
+        dy = torch.randn(T, d, generator=gen(seed + 1), device="cuda").to(BF16)
+        return s, ds, w, dy, torch.empty_like(s), torch.empty(d, device="cuda")
+
+    def run(c, **kw):
+        binding.tpmlp_rmsnorm_add_backward([c[0]], c[2], c[3], 1, [c[4]], c[5], dS_chunks=[c[1]], **kw)
+        return c[4], c[5]
+
+    small, big = case(40, 64, 1), case(200, 8192, 3)
+    need = lambda c: torch.empty(binding.tpmlp_rmsnorm_add_backward_workspace_size(*c[0].shape, 1), dtype=U8, device="cuda")
+    want = [[t.clone() for t in run(c, ws=need(c))] for c in (small, big)]
+    check = lambda c, w: all(torch.equal(a, b) for a, b in zip((c[4], c[5]), w))
+    streams = [torch.cuda.current_stream(), torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    binding._WORKSPACES.clear()
+    for st in streams:
+        with torch.cuda.stream(st):
+            for c, w in ((small, want[0]), (big, want[1]), (small, want[0])):
+                for t in (c[4], c[5]):
+                    t.zero_()
+                run(c)
+                st.synchronize()
+                assert check(c, w)
+    kept = {k: v.data_ptr() for k, v in binding._WORKSPACES.items()}
+    assert len(kept) == 3 and len(set(kept.values())) == 3
+    # two streams at once, many times over, each with its own
+    a, b = case(300, 1024, 5), case(300, 1024, 7)
+    wa, wb = [[t.clone() for t in run(c)] for c in (a, b)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, st in ((a, streams[1]), (b, streams[2])):
+            with torch.cuda.stream(st):
+                run(c)
+    torch.cuda.synchronize()
+    assert check(a, wa) and check(b, wb)
+    before = dict(binding._WORKSPACES)
+    run(a, stream=streams[1])                       # an explicit stream, as an object and as a handle
+    run(b, stream=streams[2].cuda_stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(small)
+    assert {k: v.data_ptr() for k, v in binding._WORKSPACES.items()} == {k: v.data_ptr() for k, v in before.items()}
+    torch.cuda.synchronize()
+    assert check(a, wa) and check(b, wb)
+    small[4].zero_()
+    with torch.cuda.stream(streams[2]):             # the graph beside eager calls on the stream it was not captured on
+        graph.replay()
+    run(big)
+    torch.cuda.synchronize()
+    assert check(small, want[0]) and check(big, want[1])
