@@ -186,6 +186,7 @@ def _opt_ptrs(ts):
 
 
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+_current_stream, _capturing = torch._C._cuda_getCurrentStream, torch._C._cuda_isCurrentStreamCapturing
 
 
 def _stream(stream):
@@ -646,6 +647,14 @@ def _refuse(fn):
     raise TpMlpError(fn, ERR_INVALID_ARG)
 
 
+def _device_of(t, fn):
+    """The calls run on the current device's stream: refuse tensors of the host or of another device."""
+    d = t.get_device()
+    if d < 0 or d != _current_device():
+        _refuse(fn)
+    return d
+
+
 def _typed(t, dtype, numel, fn):
     """Address of a contiguous tensor of `dtype` with at least `numel` elements (None: NULL)."""
     if t is None:
@@ -693,17 +702,20 @@ def _chunk_array(chunks, n, numel, fn):
 _WORKSPACES = {}  # (device index, stream id) -> the stream's workspace
 
 
-def _stream_workspace(nbytes, device, stream):
+def _stream_workspace(nbytes, dev, stream):
     """A workspace that the current stream keeps for its calls, which it runs one after the other: an allocation between
     two launches costs as much host time as a launch.  Fresh, and the caller's stream's until its work is done, where that
     order does not hold: for an explicit stream, in a capture (the graph may be replayed on any stream), and on streams
     that are not torch's own (a handle may be used again for another stream)."""
-    sid = 2 if stream is not None else torch._C._cuda_getCurrentStream(device.index)[0]
-    if (sid == 0 or sid & 1) and not torch._C._cuda_isCurrentStreamCapturing():
-        ws = _WORKSPACES.get((device.index, sid))
-        if ws is None or ws.numel() < nbytes:
-            ws = _WORKSPACES[device.index, sid] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        return ws
+    if stream is None:
+        sid = _current_stream(dev)[0]
+        if (sid == 0 or sid & 1) and not _capturing():
+            ws = _WORKSPACES.get((dev, sid))
+            if ws is None or ws.numel() < nbytes:
+                ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=torch.device("cuda", dev))
+                _WORKSPACES[dev, sid] = ws
+            return ws
+    device = torch.device("cuda", dev)
     ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     if stream is not None:
         own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
@@ -717,10 +729,11 @@ def tpmlp_rmsnorm_add_gather(X_chunks, weight, N, R_chunks=None, S_chunks=None, 
     fn = "tpmlp_rmsnorm_add_gather"
     rows, d = X_chunks[0].shape
     T, n = rows * N, rows * d
-    st = (_lib or lib()).tpmlp_rmsnorm_add_gather(
-        _chunk_array(X_chunks, N, n, fn), _chunk_array(R_chunks, N, n, fn), _typed(weight, _BF16, d, fn), eps,
-        _shape(T, d, d * N, N), _chunk_array(S_chunks, N, n, fn), _typed(Xg, _BF16, T * d, fn),
-        _bytes(Xq, T * d, fn), _scales(x_scales, T, d, 1, fn), _stream(stream))
+    args = (_chunk_array(X_chunks, N, n, fn), _chunk_array(R_chunks, N, n, fn), _typed(weight, _BF16, d, fn), eps,
+            _shape(T, d, d * N, N), _chunk_array(S_chunks, N, n, fn), _typed(Xg, _BF16, T * d, fn),
+            _bytes(Xq, T * d, fn), _scales(x_scales, T, d, 1, fn))
+    dev = _device_of(weight, fn)
+    st = (_lib or lib()).tpmlp_rmsnorm_add_gather(*args, _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise TpMlpError(fn, st)
 
@@ -738,12 +751,14 @@ def tpmlp_rmsnorm_add_backward(S_chunks, weight, dXg, N, dX_chunks, dweight, dS_
     fn = "tpmlp_rmsnorm_add_backward"
     rows, d = S_chunks[0].shape
     T, n = rows * N, rows * d
+    args = (_chunk_array(S_chunks, N, n, fn), _typed(weight, _BF16, d, fn), eps, _typed(dXg, _BF16, T * d, fn),
+            _chunk_array(dS_chunks, N, n, fn), _shape(T, d, d * N, N), _chunk_array(dX_chunks, N, n, fn),
+            _typed(dweight, _FP32, d, fn))
+    dev = _device_of(weight, fn)
     if ws is None:
-        ws = _stream_workspace(tpmlp_rmsnorm_add_backward_workspace_size(T, d, N), weight.device, stream)
-    st = (_lib or lib()).tpmlp_rmsnorm_add_backward(
-        _chunk_array(S_chunks, N, n, fn), _typed(weight, _BF16, d, fn), eps, _typed(dXg, _BF16, T * d, fn),
-        _chunk_array(dS_chunks, N, n, fn), _shape(T, d, d * N, N), _chunk_array(dX_chunks, N, n, fn),
-        _typed(dweight, _FP32, d, fn), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
+        ws = _stream_workspace(tpmlp_rmsnorm_add_backward_workspace_size(T, d, N), dev, stream)
+    st = (_lib or lib()).tpmlp_rmsnorm_add_backward(*args, ws.data_ptr(), ws.nbytes, _raw_stream(dev) if stream is None
+                                                    else _stream(stream))
     if st:
         raise TpMlpError(fn, st)
 
@@ -755,10 +770,11 @@ def tpmlp_quantize_block(src, block_rows=1, fmt=E4M3, q=None, scales=None, qT=No
     ld, step = src.stride()
     if src.dtype is not _BF16 or (step != 1 and cols > 1):
         _refuse(fn)
-    st = (_lib or lib()).tpmlp_quantize_block(
-        src.data_ptr(), ld if rows > 1 else cols, rows, cols, block_rows, fmt, _bytes(q, rows * cols, fn),
-        _scales(scales, rows, cols, block_rows, fn), _bytes(qT, cols * ((rows + 15) & -16), fn),
-        _scales(scalesT, cols, rows, block_rows, fn), _stream(stream))
+    args = (src.data_ptr(), ld if rows > 1 else cols, rows, cols, block_rows, fmt, _bytes(q, rows * cols, fn),
+            _scales(scales, rows, cols, block_rows, fn), _bytes(qT, cols * ((rows + 15) & -16), fn),
+            _scales(scalesT, cols, rows, block_rows, fn))
+    dev = _device_of(src, fn)
+    st = (_lib or lib()).tpmlp_quantize_block(*args, _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise TpMlpError(fn, st)
 
@@ -777,10 +793,12 @@ def tpmlp_gemm_fp8_block(A8, a_scales, B8, b_scales, C, bias=None, b_block_rows=
             a_scales.dtype is not _FP32 or a_scales.numel() < kb * ((M + 127) & -128) or not a_scales.is_contiguous() or
             b_scales.dtype is not _FP32 or b_scales.numel() < nb or not b_scales.is_contiguous()):
         _refuse("tpmlp_gemm_fp8_block")
+    dev = _device_of(C, "tpmlp_gemm_fp8_block")
     st = (_lib or lib()).tpmlp_gemm_fp8_block(
         A8.data_ptr(), a_fmt, a_scales.data_ptr(), B8.data_ptr(), b_fmt, b_scales.data_ptr(), b_block_rows, M, N, K,
         None if bias is None else _typed(bias, _BF16, N, "tpmlp_gemm_fp8_block"), C.data_ptr(),
-        FP32 if c_type is _FP32 else BF16, ldc if M > 1 else N, _stream(stream))
+        FP32 if c_type is _FP32 else BF16, ldc if M > 1 else N,
+        _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise TpMlpError("tpmlp_gemm_fp8_block", st)
 
@@ -792,10 +810,11 @@ def tpmlp_gemm1_fp8_block(Xq, x_scales, AqT, a_scales, bias, N, Hq, h_scales, Hp
     F, k = AqT.shape
     if k != d:
         _refuse(fn)
-    st = (_lib or lib()).tpmlp_gemm1_fp8_block(
-        _bytes(Xq, T * d, fn), _scales(x_scales, T, d, 1, fn), _bytes(AqT, F * d, fn),
-        _scales(a_scales, F, d, 128, fn), _typed(bias, _BF16, F, fn), _shape(T, d, F, N), _bytes(Hq, T * F, fn),
-        _scales(h_scales, T, F, 1, fn), _typed(Hpre, _BF16, T * F, fn), _stream(stream))
+    args = (_bytes(Xq, T * d, fn), _scales(x_scales, T, d, 1, fn), _bytes(AqT, F * d, fn),
+            _scales(a_scales, F, d, 128, fn), _typed(bias, _BF16, F, fn), _shape(T, d, F, N), _bytes(Hq, T * F, fn),
+            _scales(h_scales, T, F, 1, fn), _typed(Hpre, _BF16, T * F, fn))
+    dev = _device_of(Hq, fn)
+    st = (_lib or lib()).tpmlp_gemm1_fp8_block(*args, _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise TpMlpError(fn, st)
 

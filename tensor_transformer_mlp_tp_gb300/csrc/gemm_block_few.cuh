@@ -7,6 +7,11 @@
 // scaled per k-block by its own row scale of B and the scales of A.  With BT columns a partial sum, several fit in TMEM, so the
 // promotion's latency is hidden.  In the end each CTA of the cluster finishes BT / C of the rows: a warp per row, four
 // consecutive columns a lane, which makes a 1 x 128 block of an 8-bit output one warp's.
+//
+// What bounds it: HBM, and a fixed part of about 3 us (set-up, the first bytes, the join).  Measured on GB300: one row,
+// N = 4096, K = 16384 (67 MB) 13.3 us, 5.0 TB/s, with 256 CTAs in 32 clusters of eight (15.3 us with four CTAs a tile);
+// N = 16384, K = 4096: 13.8 us; 64 rows 16.7 us; 128 rows 20 us (one CTA an SM, 128 x 128 tiles, then the promotion's
+// 450 ns a k-block counts).
 #pragma once
 
 #include "gemm_block_pair.cuh"

@@ -1,13 +1,26 @@
-// The block-scaled product on CTA pairs (tcgen05, cta_group::2): a cluster of two CTAs computes a 256 x 256 tile.
+// The block-scaled product on CTA pairs (tcgen05, cta_group::2): a cluster of two CTAs computes a 256 x 256 tile of
+//   C[m, n] = sum_kb sA[kb, m] sB[kb, n] sum_{k in kb} A8[m, k] B8[n, k].
 //
 // Each k-block of 128 is summed by the tensor cores into a partial sum in TMEM (four 256 x 256 x 32 UMMAs, the first
 // of them overwriting), and eight promotion warps per CTA add it, scaled, to fp32 sums in registers: warp w owns the
-// 32 rows of TMEM quadrant w % 4 and 128 of the tile's 256 columns, so a thread keeps 128 sums of one row -- one 1 x 128
-// block of an 8-bit output, whose amax needs no exchange.  The partial sums are double-buffered (2 x 256 TMEM columns),
-// so the UMMAs of k-block i + 1 run while block i is promoted.
+// 32 rows of TMEM quadrant w % 4 and 128 of the tile's 256 columns, so a thread keeps 128 sums -- with weight scales, of
+// one row: one 1 x 128 block of an 8-bit output, whose amax needs no exchange.  The partial sums are double-buffered
+// (2 x 256 TMEM columns), so the UMMAs of k-block i + 1 run while block i is promoted.
+//
+// Why a whole 256 x 256 tile: with N = 128 an UMMA takes 131 cycles against 163 for N = 256 (measured; shared memory
+// feeds both operands and takes the next copies), so four half-width buffers, which would hide the hand-over, lose more.
+//
+// What bounds it (clock64 on GB300, cycles a k-block): the UMMAs 650; but a buffer is in turn filled (650), committed and
+// seen (320), read (370 to 440: eight 16-column loads with the products between them, a packed FMA of three registers
+// taking three cycles) and handed back (100 in the even CTA, 230 from the odd one), and two buffers make that 740 to 800.
+// A sustained run is at the power limit besides (1360 W at 1.67 GHz).  Measured at 8192 x 4096 x 16384: 370 us in a
+// burst, 430 us sustained (2550 TFLOP/s; the per-tensor kernel, which promotes nothing, 306 and 351 us on the same
+// codes).  With both operands scaled by rows (BVEC) the products double and the loads are the slower fragment form: 590
+// us at 4096 x 16384 x 8192, about 1350 cycles a k-block.
 //
 // Synchronisation as in the per-tensor pair kernel: full / empty of the TMA ring, tfull / tempty of the partial sums,
-// the barriers that count both CTAs in the even one.  All waits are bounded.
+// the barriers that count both CTAs in the even one.  All waits are bounded.  An arrive on tempty publishes nothing, so
+// it is relaxed: a release at cluster scope waits for the thread's copies in flight and cost half the kernel's time.
 #pragma once
 
 #include "block_fp8.cuh"
@@ -175,85 +188,85 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
   };
 
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kIssueRegs));
-  if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------------ producer (both CTAs)
-      const uint64_t pol_a = policy_evict_normal(), pol_b = policy_evict_last();
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, issued_parity = 0, blk = 0;
-      bool ok = true;
-      for (int t = cluster_id; ok && t < num_tiles; t += num_clusters) {
-        int mb, nb;
-        tile_at(t, mb, nb);
-        const int m0 = mb * 256 + static_cast<int>(rank) * 128, n0 = nb * 256 + static_cast<int>(rank) * 128;
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++blk) {
-          if (!wait_bounded(empty + stage, phase ^ 1u, wc, kSiteBlockProducer)) {
-            ok = false;
-            break;
-          }
-          if (leader) mbar_arrive_expect_tx(full + stage, 2 * S::kStageBytes);
-          const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
-          tma_load_2d_pair(sA + stage * S::kATile, &p.tmA, bar, kb * 128, m0, pol_a);
-          tma_load_2d_pair(sB + stage * S::kBTile, &p.tmB, bar, kb * 128, n0, pol_b);
-          float* slot = scale_ring + (blk & (S::kScaleSlots - 1)) * S::kSlotFloats;
-          tma_load_2d_pair(slot, &p.tmSA, bar, m0, kb, pol_a);
-          if (BVEC) tma_load_2d_pair(slot + 128, &p.tmSB, bar, nb * 256, kb, pol_a);
-          issued |= 1u << stage;
-          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kIssueRegs));
+    if (warp == 0) {
+      if (lane == 0) {
+        // ------------------------------------------------------------------ producer (both CTAs)
+        const uint64_t pol_a = policy_evict_normal(), pol_b = policy_evict_last();
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, issued_parity = 0, blk = 0;
+        bool ok = true;
+        for (int t = cluster_id; ok && t < num_tiles; t += num_clusters) {
+          int mb, nb;
+          tile_at(t, mb, nb);
+          const int m0 = mb * 256 + static_cast<int>(rank) * 128, n0 = nb * 256 + static_cast<int>(rank) * 128;
+          for (int kb = 0; kb < p.k_blocks; ++kb, ++blk) {
+            if (!wait_bounded(empty + stage, phase ^ 1u, wc, kSiteBlockProducer)) {
+              ok = false;
+              break;
+            }
+            if (leader) mbar_arrive_expect_tx(full + stage, 2 * S::kStageBytes);
+            const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
+            tma_load_2d_pair(sA + stage * S::kATile, &p.tmA, bar, kb * 128, m0, pol_a);
+            tma_load_2d_pair(sB + stage * S::kBTile, &p.tmB, bar, kb * 128, n0, pol_b);
+            float* slot = scale_ring + (blk & (S::kScaleSlots - 1)) * S::kSlotFloats;
+            tma_load_2d_pair(slot, &p.tmSA, bar, m0, kb, pol_a);
+            if (BVEC) tma_load_2d_pair(slot + 128, &p.tmSB, bar, nb * 256, kb, pol_a);
+            issued |= 1u << stage;
+            issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
+        // copies in flight land before shared memory is released (the odd CTA is held at the closing cluster barrier)
+        if (leader)
+          for (int s = 0; s < STAGES; ++s)
+            if (issued & (1u << s)) wait_drain(full + s, (issued_parity >> s) & 1u, p.timeout_ns);
       }
-      // copies in flight land before shared memory is released (the odd CTA is held at the closing cluster barrier)
-      if (leader)
-        for (int s = 0; s < STAGES; ++s)
-          if (issued & (1u << s)) wait_drain(full + s, (issued_parity >> s) & 1u, p.timeout_ns);
-    }
-  } else if (warp == 1) {
-    if (leader) {
-      // ------------------------------------------------------------------ MMA issuer (even CTA)
-      // The whole warp walks the loop and one elected lane issues: descriptors are then warp-uniform, and an issue
-      // costs a few cycles where a loop of one lane alone took about 75 for each (measured, clock64).
-      const uint32_t idesc = idesc_f8_f32(256, 256, static_cast<uint32_t>(p.g.a_fmt), static_cast<uint32_t>(p.g.b_fmt),
-                                          false, false);
-      const bool elected = elect_one();
-      int stage = 0;
-      uint32_t phase = 0, blk = 0;
-      bool ok = true;
-      for (int t = cluster_id; ok && t < num_tiles; t += num_clusters) {
-        for (int kb = 0; kb < p.k_blocks; ++kb, ++blk) {
-          const uint32_t acc = blk & 1u;
-          if (!warp_wait(full + stage, phase, wc, kSiteBlockMmaFull) ||
-              !warp_wait(tempty + acc, ((blk >> 1) & 1u) ^ 1u, wc, kSiteBlockMmaEmpty)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const uint32_t a_base = smem_u32(sA + stage * S::kATile), b_base = smem_u32(sB + stage * S::kBTile);
-          if (elected) {
+    } else if (warp == 1) {
+      if (leader) {
+        // ------------------------------------------------------------------ MMA issuer (even CTA)
+        // The whole warp walks the loop and one elected lane issues: descriptors are then warp-uniform, and an issue
+        // costs a few cycles where a loop of one lane alone took about 75 for each (measured, clock64).
+        const uint32_t idesc = idesc_f8_f32(256, 256, static_cast<uint32_t>(p.g.a_fmt), static_cast<uint32_t>(p.g.b_fmt),
+                                            false, false);
+        const bool elected = elect_one();
+        int stage = 0;
+        uint32_t phase = 0, blk = 0;
+        bool ok = true;
+        for (int t = cluster_id; ok && t < num_tiles; t += num_clusters) {
+          for (int kb = 0; kb < p.k_blocks; ++kb, ++blk) {
+            const uint32_t acc = blk & 1u;
+            if (!warp_wait(full + stage, phase, wc, kSiteBlockMmaFull) ||
+                !warp_wait(tempty + acc, ((blk >> 1) & 1u) ^ 1u, wc, kSiteBlockMmaEmpty)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint32_t a_base = smem_u32(sA + stage * S::kATile), b_base = smem_u32(sB + stage * S::kBTile);
+            if (elected) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_f8_pair(tmem_base + acc * 256, sdesc_sw128(a_base + k * 32, 16, 1024),
-                           sdesc_sw128(b_base + k * 32, 16, 1024), idesc, k != 0 ? 1u : 0u);
-            umma_commit_pair_multicast(tfull + acc, 0x3);
-            umma_commit_pair_multicast(empty + stage, 0x3);
-          }
-          __syncwarp();
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+              for (int k = 0; k < 4; ++k)
+                umma_f8_pair(tmem_base + acc * 256, sdesc_sw128(a_base + k * 32, 16, 1024),
+                             sdesc_sw128(b_base + k * 32, 16, 1024), idesc, k != 0 ? 1u : 0u);
+              umma_commit_pair_multicast(tfull + acc, 0x3);
+              umma_commit_pair_multicast(empty + stage, 0x3);
+            }
+            __syncwarp();
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
-      }
-      if (elected) {
-        umma_commit_pair(drain);
-        wait_drain(drain, 0, p.timeout_ns);
+        if (elected) {
+          umma_commit_pair(drain);
+          wait_drain(drain, 0, p.timeout_ns);
+        }
       }
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kPromoteRegs));
     // -------------------------------------------------------------------- promotion and epilogue (both CTAs)

@@ -129,6 +129,20 @@ def test_binding_refuses_what_the_abi_cannot_express(L):
                                       torch.zeros(4, 64, dtype=u8), sc)
 
 
+def test_binding_refuses_host_tensors(L):
+    """Well-formed tensors of the host: refused before the library sees their addresses."""
+    bf, u8 = torch.bfloat16, torch.uint8
+    x, w, xq, sc = torch.zeros(4, 64, dtype=bf), torch.ones(64, dtype=bf), torch.zeros(4, 64, dtype=u8), torch.zeros(1, 128)
+    for call in (lambda: binding.tpmlp_rmsnorm_add_gather([x], w, 1, Xq=xq, x_scales=sc),
+                 lambda: binding.tpmlp_rmsnorm_add_backward([x], w, x, 1, [x], torch.zeros(64)),
+                 lambda: binding.tpmlp_quantize_block(x, q=xq, scales=sc),
+                 lambda: binding.tpmlp_gemm_fp8_block(xq, sc, xq[:, :].repeat(2, 1), torch.zeros(1, 1), torch.zeros(4, 8)),
+                 lambda: binding.tpmlp_gemm1_fp8_block(xq, sc, torch.zeros(16, 64, dtype=u8), torch.zeros(1, 1), None, 1,
+                                                       torch.zeros(4, 16, dtype=u8), sc)):
+        with pytest.raises(binding.TpMlpError):
+            call()
+
+
 def test_scale_shapes():
     assert binding.block_scales_shape(300, 144) == (2, 384)
     assert binding.block_scales_shape(300, 144, 128) == (3, 2)
