@@ -114,7 +114,7 @@ cudaError_t run_few(GemmBlockParams p, const DeviceCtx& ctx, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int tiles = (p.g.N + 127) / 128, row_tiles = (p.g.M + BT - 1) / BT;
   const int ranks = few_ranks<BT>(static_cast<long long>(tiles) * row_tiles, p.k_blocks, ctx);
-  p.group_m = ranks;
+  p.ranks = ranks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks * tiles, row_tiles);
   cfg.blockDim = dim3(S::kThreads);
@@ -163,7 +163,10 @@ cudaError_t launch_gemm_block(const GemmBlockLaunch& g, const DeviceCtx& ctx, cu
   if (static_cast<long long>((g.M + 255) / 256) * ((g.N + 255) / 256) > INT_MAX) return cudaErrorNotSupported;
   p.m_blocks = (g.M + 255) / 256;
   p.n_blocks = (g.N + 255) / 256;
-  p.group_m = 8;
+  // the factor of a division by d for dividends below 2^31: floor(2^32 (2^s - d) / d) + 1 with 2^s >= d
+  const unsigned long long d = static_cast<unsigned long long>(kGroupM) * p.n_blocks;
+  while ((1ull << p.group_shift) < d) ++p.group_shift;
+  p.group_factor = static_cast<uint32_t>((((1ull << p.group_shift) - d) << 32) / d + 1);
   bool ok = encode_tile_map(&p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.a, g.K, g.M, g.K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
             encode_tile_map(&p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.b, g.K, g.N, g.K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
   ok = ok && encode_tile_map(&p.tmSA, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.a_scales, p.m_pad, p.k_blocks, p.m_pad, 128, 1, CU_TENSOR_MAP_SWIZZLE_NONE);

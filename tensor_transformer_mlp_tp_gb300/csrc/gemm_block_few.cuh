@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
 
   const int warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31u;
-  const int rank = static_cast<int>(cluster_ctarank()), ranks = p.group_m;  // CTAs of the cluster
+  const int rank = static_cast<int>(cluster_ctarank()), ranks = p.ranks;  // CTAs of the cluster
   const int n0 = static_cast<int>(blockIdx.x) / ranks * 128, m0 = static_cast<int>(blockIdx.y) * BT;
   const int kb0 = static_cast<int>(static_cast<long long>(p.k_blocks) * rank / ranks);
   const int kbs = static_cast<int>(static_cast<long long>(p.k_blocks) * (rank + 1) / ranks) - kb0;

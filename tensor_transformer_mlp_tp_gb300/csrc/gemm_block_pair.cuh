@@ -33,11 +33,15 @@ struct GemmBlockParams {
   CUtensorMap tmC;        // C (bf16 / fp32) or the pre-activation (bf16), 32 x 32 boxes
   CUtensorMap tmH;        // 8-bit output, boxes of 128 bytes x 32 rows
   GemmBlockLaunch g;
-  int m_blocks, n_blocks, k_blocks, group_m;
+  int m_blocks, n_blocks, k_blocks;
+  int ranks;                        // few-row kernel: CTAs of a cluster
+  uint32_t group_factor, group_shift;  // pair kernel: t / (kGroupM n_blocks) = (umulhi(t, factor) + t) >> shift, t < 2^31
   long long m_pad, n_pad;
   unsigned int* err;
   unsigned long long timeout_ns;
 };
+
+constexpr int kGroupM = 8;  // row blocks of a raster group
 
 enum BlockOut : int { kOutBf16 = 0, kOutFp32 = 1, kOutGelu8 = 2 };
 
@@ -179,12 +183,18 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
   const int num_tiles = p.m_blocks * p.n_blocks;
   const int cluster_id = blockIdx.x >> 1;
   const int num_clusters = gridDim.x >> 1;
-  const int group = p.group_m * p.n_blocks;
+  // Tile t: groups of kGroupM row blocks, column by column.  The quotient by a whole group comes from the host's factor
+  // (a division of unknown operands is over a hundred cycles, on every warp's way into a tile).
   auto tile_at = [&](int t, int& mb, int& nb) {
-    const int first = t / group * p.group_m;
-    const int gm = min(p.m_blocks - first, p.group_m);
-    mb = first + t % group % gm;
-    nb = t % group / gm;
+    const int g = static_cast<int>((__umulhi(static_cast<uint32_t>(t), p.group_factor) + static_cast<uint32_t>(t)) >> p.group_shift);
+    const int first = g * kGroupM, rest = t - first * p.n_blocks, gm = p.m_blocks - first;
+    if (gm >= kGroupM) {
+      mb = first + rest % kGroupM;
+      nb = rest / kGroupM;
+    } else {
+      mb = first + rest % gm;
+      nb = rest / gm;
+    }
   };
 
   if (warp < 4) {

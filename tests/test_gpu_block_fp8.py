@@ -236,6 +236,23 @@ def test_gemm_fp8_block(M, N, K, b_block_rows, dtype):
     assert torch.equal(C2, C.t[:, :N])
 
 
+# shapes with more than a wave of 128 x 128 tiles, which run on CTA pairs: rows, columns and k-blocks that end inside
+PAIR_SHAPES = [(700, 2312, 272), (1030, 1160, 400), (4104, 264, 144), (300, 5000, 16), (2050, 4104, 1040)]
+
+
+@pytest.mark.parametrize("M,N,K", PAIR_SHAPES)
+@pytest.mark.parametrize("b_block_rows", [1, 128])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gemm_fp8_block_many_tiles(M, N, K, b_block_rows, dtype):
+    test_gemm_fp8_block(M, N, K, b_block_rows, dtype)
+
+
+@pytest.mark.parametrize("T,d,F", [(1030, 400, 1168), (700, 272, 2320), (4104, 144, 272), (2050, 1040, 4112)])
+@pytest.mark.parametrize("pre", [True, False])
+def test_gemm1_fp8_block_many_tiles(T, d, F, pre):
+    test_gemm1_fp8_block(T, d, F, 1, pre)
+
+
 @pytest.mark.parametrize("M", [2, 200])
 def test_gemm_fp8_block_infinities_and_nan_stay_in_their_rows(M):
     """A NaN code spoils its row of C alone; scales of rows behind the last are not used."""
