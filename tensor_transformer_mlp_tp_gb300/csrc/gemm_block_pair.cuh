@@ -336,23 +336,14 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
             sb_next = next < p.k_blocks ? __ldg(sb + next) : 0.f;
           }
         }
-        float2 c2[kFrag ? 4 : 8];
+        constexpr int kPairs = kFrag ? 4 : 1;  // of columns in a chunk of the fragment layout, each with its scales
+        float2 c2[kPairs];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           uint32_t(&v)[16] = r[c % 3];
-          if constexpr (BVEC && kFrag) {
-            if ((c & 1) == 0) {
+          if (kFrag && (c & 1) == 0) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) c2[g] = *reinterpret_cast<const float2*>(cs + (c >> 1) * 32 + 8 * g);
-            }
-          }
-          if constexpr (BVEC && !kFrag) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const float4 f = *reinterpret_cast<const float4*>(cs + c * 16 + 4 * g);
-              c2[2 * g] = make_float2(f.x, f.y);
-              c2[(2 * g + 1) & (kFrag ? 3 : 7)] = make_float2(f.z, f.w);
-            }
+            for (int g = 0; g < kPairs; ++g) c2[g] = *reinterpret_cast<const float2*>(cs + (c >> 1) * 32 + 8 * g);
           }
           tmem_wait_ld(v);
           // Every load has returned: the buffer is free before the last sums, not after them.  (The fragment loads are
@@ -370,7 +361,7 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float2 q = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            if constexpr (BVEC) q = __fmul2_rn(q, c2[kFrag ? i >> 1 : i]);
+            if constexpr (kFrag) q = __fmul2_rn(q, c2[(i >> 1) % kPairs]);
             acc[c * 8 + i] = __ffma2_rn(q, rs[kFrag ? (c & 1) * 2 + (i & 1) : 0], acc[c * 8 + i]);
           }
           if (c < 5) load(c + 3, v);
