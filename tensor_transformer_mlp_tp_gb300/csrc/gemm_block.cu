@@ -135,7 +135,8 @@ cudaError_t run_few(GemmBlockParams p, const DeviceCtx& ctx, cudaStream_t s) {
 template <int BT>
 cudaError_t launch_few(GemmBlockParams& p, const DeviceCtx& ctx, cudaStream_t s) {
   const GemmBlockLaunch& g = p.g;
-  bool ok = encode_tile_map(&p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.a, g.K, g.M, g.K, 128, BT, CU_TENSOR_MAP_SWIZZLE_128B) &&
+  p.box_rows = g.M < BT ? g.M : BT;
+  bool ok = encode_tile_map(&p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.a, g.K, g.M, g.K, 128, p.box_rows, CU_TENSOR_MAP_SWIZZLE_128B) &&
             encode_tile_map(&p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.b, g.K, g.N, g.K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
             encode_tile_map(&p.tmSA, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, g.a_scales, p.m_pad, p.k_blocks, p.m_pad, BT, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
   if (g.b_block_rows == 1)

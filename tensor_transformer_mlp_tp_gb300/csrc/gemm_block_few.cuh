@@ -10,7 +10,7 @@
 //
 // What bounds it: HBM, and a fixed part of about 3 us (set-up, the first bytes, the join).  Measured on GB300: one row,
 // N = 4096, K = 16384 (67 MB) 13.3 us, 5.0 TB/s, with 256 CTAs in 32 clusters of eight (15.3 us with four CTAs a tile);
-// N = 16384, K = 4096: 13.8 us; 64 rows 16.7 us; 128 rows 20 us (one CTA an SM, 128 x 128 tiles, then the promotion's
+// N = 16384, K = 4096: 13.3 us; 64 rows 16.9 us; 128 rows 20 us (one CTA an SM, 128 x 128 tiles, then the promotion's
 // 450 ns a k-block counts).
 #pragma once
 
@@ -38,7 +38,7 @@ struct BlockFewShape {
   static constexpr int kScaleSlots = 16;
   static constexpr int kRowFloats = BT < 32 ? 32 : BT;  // a copy starts on a 128-byte boundary
   static constexpr int kSlotFloats = kRowFloats + (BVEC ? 128 : 0);
-  static constexpr int kStageBytes = kStage + (BT + (BVEC ? 128 : 0)) * 4;
+  static constexpr int kStageBytes = kStage + (BT + (BVEC ? 128 : 0)) * 4;  // copied for a k-block of BT rows
   static constexpr int kSmem = 1024 + kStages * kStage + kScaleSlots * kSlotFloats * 4 + 256;
   static_assert(kStages + kBufs + 2 < kScaleSlots, "see kScaleSlots");
   static_assert(kStages * kStage >= BT * 128 * 4, "the sums are joined in the ring's memory");
@@ -54,8 +54,11 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
   return v;
 }
 
-// grid: (cluster size x column tiles, row tiles).  p.tmA: A [M x K], boxes of 128 bytes x BT rows; p.tmB: B [N x K],
-// 128 bytes x 128 rows; p.tmSA boxes of BT scales, p.tmSB (BVEC) of 128.
+// grid: (cluster size x column tiles, row tiles).  p.tmA: A [M x K], boxes of 128 bytes x p.box_rows rows, the M there are
+// up to BT: with boxes of BT rows the copies' zero rows past A's end cost more than real ones, as if every CTA read one
+// line for them (N = 16384, K = 4096: one row 16.3 us, now 13.3; 17 rows 17.5, now 14.6).  The rest of a tile stays unwritten and
+// makes columns of partial sums that nothing reads.  p.tmB: B [N x K], 128 bytes x 128 rows; p.tmSA boxes of BT scales,
+// p.tmSB (BVEC) of 128.
 template <int BT, int OUT, bool BVEC>
 __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ? 1 : 2)
     k_gemm_block_few(const __grid_constant__ GemmBlockParams p) {
@@ -127,12 +130,13 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol = policy_evict_normal();
+      const uint32_t stage_bytes = S::kStageBytes - (BT - p.box_rows) * 128;
       uint32_t issued = 0, issued_parity = 0;
       for (int b = 0; b < kbs; ++b) {
         const int stage = b % STAGES;
         const uint32_t phase = static_cast<uint32_t>(b / STAGES) & 1u;
         if (!wait_bounded(empty + stage, phase ^ 1u, wc, kSiteBlockProducer)) break;
-        mbar_arrive_expect_tx(full + stage, S::kStageBytes);
+        mbar_arrive_expect_tx(full + stage, stage_bytes);
         tma_load_2d(sW + stage * S::kWTile, &p.tmB, full + stage, (kb0 + b) * 128, n0, pol);
         tma_load_2d(sT + stage * S::kTTile, &p.tmA, full + stage, (kb0 + b) * 128, m0, pol);
         float* slot = scale_ring + (b & (S::kScaleSlots - 1)) * S::kSlotFloats;

@@ -34,7 +34,7 @@ struct GemmBlockParams {
   CUtensorMap tmH;        // 8-bit output, boxes of 128 bytes x 32 rows
   GemmBlockLaunch g;
   int m_blocks, n_blocks, k_blocks;
-  int ranks;                        // few-row kernel: CTAs of a cluster
+  int ranks, box_rows;                 // few-row kernel: CTAs of a cluster, rows of a box of A
   uint32_t group_factor, group_shift;  // pair kernel: t / (kGroupM n_blocks) = (umulhi(t, factor) + t) >> shift, t < 2^31
   long long m_pad, n_pad;
   unsigned int* err;

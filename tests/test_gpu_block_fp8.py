@@ -267,6 +267,34 @@ def test_gemm_fp8_block_infinities_and_nan_stay_in_their_rows(M):
     assert C[1].isnan().all() and torch.equal(C[0], clean[0]) and torch.equal(C[2:], clean[2:])
 
 
+@pytest.mark.parametrize("rows", [1, 7, 17, 23, 33, 40, 65, 127])
+def test_products_of_few_rows_after_a_product_of_nan(rows):
+    """Nothing that an earlier call left on the device reaches the rows or scales of a call with fewer rows."""
+    g = gen(rows)
+    K, N = 2048, 2048
+    a, sa, av = u.operand(g, rows, K, 1, 0)
+    b, sb, bv = u.operand(g, N, K, 128, 0, 0.02)
+    full = 16 if rows <= 16 else 32 if rows <= 32 else 64 if rows <= 64 else 128
+    nan = torch.full((full, K), 0x7F, dtype=U8, device="cuda")
+    s_nan = torch.full(binding.block_scales_shape(full, K), float("nan"), device="cuda")
+    C = torch.empty(full, N, device="cuda")
+    Hq, hs = torch.empty(full, N, dtype=U8, device="cuda"), torch.empty(binding.block_scales_shape(full, N), device="cuda")
+    outs = []
+    for spoil in (False, True):
+        if spoil:
+            binding.tpmlp_gemm_fp8_block(nan, s_nan, b, sb, C)
+        binding.tpmlp_gemm_fp8_block(a, sa, b, sb, C[:rows])
+        if spoil:
+            binding.tpmlp_gemm1_fp8_block(nan, s_nan, b, sb, None, 1, Hq, hs)
+        binding.tpmlp_gemm1_fp8_block(a, sa, b, sb, None, 1, Hq[:rows], hs)
+        outs.append((C[:rows].clone(), Hq[:rows].clone(), hs[:, :rows].clone()))
+    device_ok()
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+    ref = av @ bv.t()
+    tol = u.gemm_bound(av, bv, K)
+    within(outs[1][0], ref, tol + 2.0 ** -23 * (ref.abs() + tol), "C")
+
+
 @pytest.mark.parametrize("T,d,F,N", [(1, 16, 16, 1), (1, 4096, 1024, 8), (5, 144, 272, 1), (37, 512, 1040, 1),
                                      (64, 256, 128, 1), (130, 272, 400, 1), (257, 1024, 4096, 8), (520, 384, 656, 1)])
 @pytest.mark.parametrize("pre", [True, False])
