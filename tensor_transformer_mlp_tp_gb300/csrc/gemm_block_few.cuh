@@ -10,7 +10,7 @@
 //
 // What bounds it: HBM, and a fixed part of about 3 us (set-up, the first bytes, the join).  Measured on GB300: one row,
 // N = 4096, K = 16384 (67 MB) 13.3 us, 5.0 TB/s, with 256 CTAs in 32 clusters of eight (15.3 us with four CTAs a tile);
-// N = 16384, K = 4096: 13.3 us; 64 rows 16.9 us; 128 rows 20 us (one CTA an SM, 128 x 128 tiles, then the promotion's
+// N = 16384, K = 4096: 13.3 us; 48 rows 15.9 us; 64 rows 16.8 us; 128 rows 20 us (one CTA an SM, 128 x 128 tiles, then the promotion's
 // 450 ns a k-block counts).
 #pragma once
 
@@ -22,21 +22,22 @@ constexpr int kFewMaxRanks = 8;  // CTAs of a cluster
 
 template <int BT, bool BVEC>
 struct BlockFewShape {
-  static_assert(BT == 16 || BT == 32 || BT == 64 || BT == 128, "BT");
-  // two CTAs share an SM up to BT = 64
+  static_assert(BT == 16 || BT == 32 || BT == 48 || BT == 64 || BT == 128, "BT");
+  // Two CTAs share an SM up to BT = 64.  (Three with three stages, BT = 16: 13.1 -> 13.7 us; five stages: 13.3.)
   static constexpr int kStages = BT <= 64 ? 4 : 6;
   static constexpr int kWTile = 128 * 128, kTTile = BT * 128;
   static constexpr int kStage = kWTile + kTTile;
   static constexpr int kBufs = BT == 128 ? 2 : 4;  // partial sums in TMEM
-  static constexpr int kTmemCols = kBufs * BT;
-  // Promotion warps: four (one a TMEM lane quadrant), or eight that halve the columns where there are many.
-  static constexpr int kPromoteWarps = BT >= 64 ? 8 : 4;
+  static constexpr int kTmemCols = BT == 48 ? 256 : kBufs * BT;  // allocated in powers of two
+  // Promotion warps: four (one a TMEM lane quadrant); eight that halve the columns where a thread would hold 128 sums
+  // (at 64 four measure 16.8 us where eight take 17.4: 64 rows, N = 4096, K = 16384).
+  static constexpr int kPromoteWarps = BT > 64 ? 8 : 4;
   static constexpr int kCols = BT / (kPromoteWarps / 4);  // of one warp
   static constexpr int kThreads = 64 + 32 * kPromoteWarps;
   // Slots of the k-blocks' scales, rewritten 16 blocks later (see BlockPairShape): the producer is at most kStages
   // blocks ahead of the UMMAs, those at most kBufs ahead of the promotion.
   static constexpr int kScaleSlots = 16;
-  static constexpr int kRowFloats = BT < 32 ? 32 : BT;  // a copy starts on a 128-byte boundary
+  static constexpr int kRowFloats = (BT + 31) & -32;  // a copy starts on a 128-byte boundary
   static constexpr int kSlotFloats = kRowFloats + (BVEC ? 128 : 0);
   static constexpr int kStageBytes = kStage + (BT + (BVEC ? 128 : 0)) * 4;  // copied for a k-block of BT rows
   static constexpr int kSmem = 1024 + kStages * kStage + kScaleSlots * kSlotFloats * 4 + 256;

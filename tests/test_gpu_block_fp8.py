@@ -253,6 +253,13 @@ def test_gemm1_fp8_block_many_tiles(T, d, F, pre):
     test_gemm1_fp8_block(T, d, F, 1, pre)
 
 
+@pytest.mark.parametrize("M,N,K", [(33, 16, 16), (41, 272, 912), (48, 4096, 1040), (47, 520, 16384), (49, 1000, 2048)])
+@pytest.mark.parametrize("b_block_rows", [1, 128])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gemm_fp8_block_between_32_and_64_rows(M, N, K, b_block_rows, dtype):
+    test_gemm_fp8_block(M, N, K, b_block_rows, dtype)
+
+
 @pytest.mark.parametrize("M", [2, 200])
 def test_gemm_fp8_block_infinities_and_nan_stay_in_their_rows(M):
     """A NaN code spoils its row of C alone; scales of rows behind the last are not used."""
@@ -267,14 +274,14 @@ def test_gemm_fp8_block_infinities_and_nan_stay_in_their_rows(M):
     assert C[1].isnan().all() and torch.equal(C[0], clean[0]) and torch.equal(C[2:], clean[2:])
 
 
-@pytest.mark.parametrize("rows", [1, 7, 17, 23, 33, 40, 65, 127])
+@pytest.mark.parametrize("rows", [1, 7, 17, 23, 33, 40, 57, 127])
 def test_products_of_few_rows_after_a_product_of_nan(rows):
     """Nothing that an earlier call left on the device reaches the rows or scales of a call with fewer rows."""
     g = gen(rows)
     K, N = 2048, 2048
     a, sa, av = u.operand(g, rows, K, 1, 0)
     b, sb, bv = u.operand(g, N, K, 128, 0, 0.02)
-    full = 16 if rows <= 16 else 32 if rows <= 32 else 64 if rows <= 64 else 128
+    full = 16 if rows <= 16 else 32 if rows <= 32 else 48 if rows <= 48 else 64 if rows <= 64 else 128
     nan = torch.full((full, K), 0x7F, dtype=U8, device="cuda")
     s_nan = torch.full(binding.block_scales_shape(full, K), float("nan"), device="cuda")
     C = torch.empty(full, N, device="cuda")
