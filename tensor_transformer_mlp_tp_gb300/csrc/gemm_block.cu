@@ -89,10 +89,11 @@ int few_ranks(long long tiles, int k_blocks, const DeviceCtx& ctx) {
   return ranks;
 }
 
-// Which kernel: up to 128 rows the one that streams B once.  Above, whichever has fewer k-blocks one after the other: a
-// pair's k-block (256 x 256) takes about 0.40 us and a 128 x 128 one 0.45 us, measured on GB300 with tiles for a single
-// wave (M = 256, N = 4096, K = 16384: 32 us split over two CTAs a tile, 53 us on pairs; M = 384: 58 and 53 us;
-// M = 1024, N = 1024, K = 4096: 12.9 and 16.6 us; M = 192, N = 16384, K = 4096: 38 and 18.5 us).
+// Which kernel: up to 128 rows the one that streams B once.  Above, whichever has fewer k-blocks one after the other, and
+// at as many the same: a pair's k-block (256 x 256) takes about 0.41 us (0.65 with column scales) and a 128 x 128 one 0.37
+// (0.41), measured on GB300 with tiles for a single wave (M = 256, N = 8192, K = 8192: 30.2 us on pairs, 27.1 with this rule;
+// with column scales 45.3 and 30.2.  M = 300, N = 4096, K = 4096: 17.0 and 15.2 us.  M = 640: 17.3 us on pairs, 29.1 in two
+// waves of the other).
 bool few_rows(const GemmBlockLaunch& g, int k_blocks, const DeviceCtx& ctx) {
   const int sms = ctx.sm_count;
   if (g.M <= 128) return true;
@@ -102,7 +103,7 @@ bool few_rows(const GemmBlockLaunch& g, int k_blocks, const DeviceCtx& ctx) {
   const long long few = (few_tiles * ranks + sms - 1) / sms * ((k_blocks + ranks - 1) / ranks);
   const long long pairs = sms / 2, pair_tiles = static_cast<long long>((g.M + 255) / 256) * ((g.N + 255) / 256);
   const long long pair = (pair_tiles + pairs - 1) / pairs * k_blocks;
-  return 9 * few <= 8 * pair;
+  return few <= pair;
 }
 
 template <int BT, int OUT, bool BVEC>

@@ -1,18 +1,22 @@
 // The block-scaled product for few rows of A (decoded tokens): every weight byte is read once, so the time is that of
 // streaming B.  The operands change sides: a CTA takes 128 rows of B (output columns) as the UMMA's M and up to BT rows
-// of A as its N (128 x BT x 32 UMMAs, cta_group::1), and the K blocks are split over a cluster of CTAs, whose fp32 sums
-// are joined through distributed shared memory in rank order -- no workspace, no atomics, one launch.
+// of A as its N (128 x BT x 32 UMMAs, cta_group::1); with 128 rows of A they stay on theirs.  The K blocks are split over
+// a cluster of CTAs, whose fp32 sums are joined through distributed shared memory in rank order -- no workspace, no
+// atomics, one launch.
 //
-// Warp 0 copies (TMA ring), warp 1 issues, the others promote: a thread holds BT (or BT / 2) sums of one output column,
-// scaled per k-block by its own row scale of B and the scales of A.  With BT columns a partial sum, several fit in TMEM, so the
-// promotion's latency is hidden.  In the end each CTA of the cluster finishes BT / C of the rows: a warp per row, four
-// consecutive columns a lane, which makes a 1 x 128 block of an 8-bit output one warp's.
+// Warp 0 copies (TMA ring), warp 1 issues, the others promote: a thread holds BT sums of one output column, scaled per
+// k-block by its own row scale of B and the scales of A (BT = 128: 64 sums of one row, or of one column).  With BT columns
+// a partial sum, several fit in TMEM, so the promotion's latency is hidden.  In the end each CTA of the cluster finishes
+// BT / C of the rows: a warp a few rows at a time, four consecutive columns a lane, which makes a 1 x 128 block of an
+// 8-bit output one warp's.
 //
 // What bounds it: HBM, and a fixed part of about 3 us (set-up, the first bytes, the join).  Measured on GB300: one row,
-// N = 4096, K = 16384 (67 MB) 13.3 us, 5.0 TB/s, with 256 CTAs in 32 clusters of eight (15.3 us with four CTAs a tile);
-// N = 16384, K = 4096: 13.3 us; 48 rows 15.9 us; 64 rows 16.8 us; 128 rows 20 us (one CTA an SM, 128 x 128 tiles, then the promotion's
-// 450 ns a k-block counts).
+// N = 4096, K = 16384 (67 MB) 13.2 us, 5.1 TB/s, with 256 CTAs in 32 clusters of eight (15.3 us with four CTAs a tile);
+// 48 rows 15.9 us; 64 rows 16.8 us; 128 rows 17.8 us (one CTA an SM; a k-block of operands for all of them is 0.37 us, as
+// fast as L2 gives them).  N = 16384, K = 4096: one row 13.3 us, 64 rows 16.3, 128 rows 18.0.
 #pragma once
+
+#include <type_traits>
 
 #include "gemm_block_pair.cuh"
 
@@ -28,6 +32,10 @@ struct BlockFewShape {
   static constexpr int kWTile = 128 * 128, kTTile = BT * 128;
   static constexpr int kStage = kWTile + kTTile;
   static constexpr int kBufs = BT == 128 ? 2 : 4;  // partial sums in TMEM
+  // A's rows as the UMMA's M: a thread's sums are of one row of A, and the scale of all of them in a k-block is one number.
+  // With columns of A every lane reads the scales of 64 of them from shared memory: 0.45 us a k-block, now 0.37
+  // (128 rows, N = 4096, K = 16384: 20.0 -> 17.9 us).  Column scales would cost the same reads in this order.
+  static constexpr bool kRows = BT == 128 && !BVEC;
   static constexpr int kTmemCols = BT == 48 ? 256 : kBufs * BT;  // allocated in powers of two
   // Promotion warps: four (one a TMEM lane quadrant); eight that halve the columns where a thread would hold 128 sums
   // (at 64 four measure 16.8 us where eight take 17.4: 64 rows, N = 4096, K = 16384).
@@ -65,6 +73,7 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
     k_gemm_block_few(const __grid_constant__ GemmBlockParams p) {
   using S = BlockFewShape<BT, BVEC>;
   constexpr int STAGES = S::kStages, BUFS = S::kBufs;
+  constexpr bool kRows = S::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sW = smem;
@@ -150,8 +159,8 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
         if (issued & (1u << s)) wait_drain(full + s, (issued_parity >> s) & 1u, p.timeout_ns);
     }
   } else if (warp == 1) {
-    const uint32_t idesc = idesc_f8_f32(128, BT, static_cast<uint32_t>(p.g.b_fmt), static_cast<uint32_t>(p.g.a_fmt),
-                                        false, false);
+    const uint32_t fmt_a = static_cast<uint32_t>(p.g.a_fmt), fmt_b = static_cast<uint32_t>(p.g.b_fmt);
+    const uint32_t idesc = idesc_f8_f32(128, BT, kRows ? fmt_a : fmt_b, kRows ? fmt_b : fmt_a, false, false);
     const bool elected = elect_one();
     for (int b = 0; b < kbs; ++b) {
       const int stage = b % STAGES, buf = b % BUFS;
@@ -160,10 +169,11 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
         break;
       tc_fence_after_sync();
       const uint32_t w_base = smem_u32(sW + stage * S::kWTile), t_base = smem_u32(sT + stage * S::kTTile);
+      const uint32_t m_base = kRows ? t_base : w_base, n_base = kRows ? w_base : t_base;
       if (elected) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          umma_f8(tmem_base + buf * BT, sdesc_sw128(w_base + k * 32, 16, 1024), sdesc_sw128(t_base + k * 32, 16, 1024),
+          umma_f8(tmem_base + buf * BT, sdesc_sw128(m_base + k * 32, 16, 1024), sdesc_sw128(n_base + k * 32, 16, 1024),
                   idesc, k != 0 ? 1u : 0u);
         umma_commit(tfull + buf);
         umma_commit(empty + stage);
@@ -194,7 +204,8 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
 #pragma unroll
       for (int c = 0; c < kAhead; ++c) tmem_load_16cols_async(trow + buf * BT + c * 16, r[c]);
       const float* slot = scale_ring + (b & (S::kScaleSlots - 1)) * S::kSlotFloats;
-      const float sr = BVEC ? slot[S::kRowFloats + quad * 32 + lane] : __shfl_sync(0xffffffffu, sb_cur, b & 31);
+      float sr = BVEC ? slot[S::kRowFloats + quad * 32 + lane] : __shfl_sync(0xffffffffu, sb_cur, b & 31);
+      if (kRows) sr *= slot[quad * 32 + lane];
       const float2 sr2 = make_float2(sr, sr);
       if (!BVEC && (b & 31) == 31) {
         sb_cur = sb_next;
@@ -204,12 +215,16 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         uint32_t(&v)[16] = r[c % kAhead];
-        float2 w[8];  // the chunk's products of scales, while its columns come
+        float2 w[kRows ? 1 : 8];  // the chunk's products of scales, while its columns come
+        if constexpr (kRows) {
+          w[0] = sr2;
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float4 s = *reinterpret_cast<const float4*>(slot + half * CW + c * 16 + 2 * j);
-          w[j] = __fmul2_rn(make_float2(s.x, s.y), sr2);
-          w[j + 1] = __fmul2_rn(make_float2(s.z, s.w), sr2);
+          for (int j = 0; j < 8; j += 2) {
+            const float4 s = *reinterpret_cast<const float4*>(slot + half * CW + c * 16 + 2 * j);
+            w[j] = __fmul2_rn(make_float2(s.x, s.y), sr2);
+            w[j + 1] = __fmul2_rn(make_float2(s.z, s.w), sr2);
+          }
         }
         tmem_wait_ld(v);
         if (c == kChunks - kAhead) {  // every load has returned: the buffer is free before the last sums, not after them
@@ -221,19 +236,30 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          acc[c * 8 + j] = __ffma2_rn(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), w[j], acc[c * 8 + j]);
+          acc[c * 8 + j] = __ffma2_rn(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), w[kRows ? 0 : j],
+                                      acc[c * 8 + j]);
         if (c + kAhead < kChunks) tmem_load_16cols_async(trow + buf * BT + (c + kAhead) * 16, v);
       }
     }
   }
-  __syncthreads();  // the ring is drained: its memory holds the CTA's sums [BT][128] from here on
+  // The ring is drained: its memory holds the CTA's sums [BT][128] from here on, with kRows the 16-byte pieces of row r at
+  // places XOR r % 32 (a row a thread would hit one bank otherwise).
+  __syncthreads();
   float* red = reinterpret_cast<float*>(smem);
   if (warp >= 2) {
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    if constexpr (kRows) {
 #pragma unroll
-    for (int j = 0; j < CW / 2; ++j) {
-      float* at = red + (((warp - 2) >> 2) * CW + 2 * j) * 128 + (warp & 3) * 32 + lane;
-      at[0] = acc[j].x;
-      at[128] = acc[j].y;
+      for (int j = 0; j < CW / 4; ++j)
+        *reinterpret_cast<float4*>(red + (quad * 32 + lane) * 128 + ((half * (CW / 4) + j) ^ lane) * 4) =
+            make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
+    } else {
+#pragma unroll
+      for (int j = 0; j < CW / 2; ++j) {
+        float* at = red + (half * CW + 2 * j) * 128 + quad * 32 + lane;
+        at[0] = acc[j].x;
+        at[128] = acc[j].y;
+      }
     }
   }
   if (warp == 1) {
@@ -242,40 +268,91 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
     tmem_dealloc(tmem_base, S::kTmemCols);
   }
   cluster_sync_all();  // every CTA's sums are written (a cluster of one: a block barrier)
-  const uint32_t red_addr = smem_u32(red) + lane * 16;
+  const uint32_t red_addr = smem_u32(red);
   const int rows = min(BT, p.g.M - m0);
-  for (int j = rank + ranks * warp; j < rows; j += ranks * (S::kThreads / 32)) {
-    const int row = m0 + j;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    float4 q[kFewMaxRanks];  // all in flight together, added in rank order
+  // Several rows of a warp go through each step together: a read of another SM, the reduction of a block's largest value
+  // and the divisions of its scale are long chains (128 rows, N = 16384, K = 4096: 19.9 -> 18.0 us, with GeLU 22.6 -> 20.1).
+  const int step = ranks * (S::kThreads / 32);
+  auto join = [&](auto rows_const, auto ranks_const) {
+    constexpr int R = decltype(rows_const)::value, RANKS = decltype(ranks_const)::value;
+    for (int j0 = rank + ranks * warp; j0 < rows; j0 += R * step) {
+      float4 q[R][RANKS];
+      float v[R][4];
 #pragma unroll
-    for (int r = 0; r < kFewMaxRanks; ++r)
-      q[r] = r < ranks ? ld_cluster_f4(mapa_shared(red_addr + j * 512, static_cast<uint32_t>(r))) : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < R; ++i) {
+        const int j = j0 + i * step;
+        const uint32_t at = red_addr + j * 512 + (kRows ? lane ^ (j & 31) : lane) * 16;
 #pragma unroll
-    for (int r = 0; r < kFewMaxRanks; ++r) {
-      v[0] += q[r].x; v[1] += q[r].y; v[2] += q[r].z; v[3] += q[r].w;
-    }
+        for (int r = 0; r < RANKS; ++r)
+          q[i][r] = r < ranks && j < rows ? ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(r))) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += b4[i];
-    if constexpr (OUT == kOutFp32) {
-      if (col_in) *reinterpret_cast<float4*>(static_cast<float*>(p.g.c) + row * p.g.ldc + col) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-      const uint2 u = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-      if constexpr (OUT == kOutBf16) {
-        if (col_in) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.g.c) + row * p.g.ldc + col) = u;
+      for (int i = 0; i < R; ++i) {
+        v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+#pragma unroll
+        for (int r = 0; r < RANKS; ++r) {  // in rank order
+          v[i][0] += q[i][r].x; v[i][1] += q[i][r].y; v[i][2] += q[i][r].z; v[i][3] += q[i][r].w;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[i][c] += b4[c];
+      }
+      if constexpr (OUT == kOutGelu8) {
+        float2 h[R][2];
+        float amax[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          h[i][0] = gelu2(make_float2(v[i][0], v[i][1]));
+          h[i][1] = gelu2(make_float2(v[i][2], v[i][3]));
+          amax[i] = col_in ? fmaxf(fmaxf(fabsf(h[i][0].x), fabsf(h[i][0].y)), fmaxf(fabsf(h[i][1].x), fabsf(h[i][1].y))) : 0.f;
+        }
+        // Each exchange halves the rows that a lane holds: 32 / R lanes end with the largest value of one row and form its
+        // scale, R rows' divisions at once.
+        int o = 16;
+#pragma unroll
+        for (int n = R / 2; n >= 1; n /= 2, o /= 2)
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            const bool high = lane & o;
+            const float keep = high ? amax[i + n] : amax[i], send = high ? amax[i] : amax[i + n];
+            amax[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, o));
+          }
+#pragma unroll
+        for (; o >= 1; o /= 2) amax[0] = fmaxf(amax[0], __shfl_xor_sync(0xffffffffu, amax[0], o));
+        constexpr int kLanes = 32 / R;
+        const BlockScale b = block_scale(amax[0], 448.f);
+        const int jl = j0 + static_cast<int>(lane / kLanes) * step;
+        if (lane % kLanes == 0 && jl < rows) p.g.h_scales[(n0 >> 7) * p.m_pad + m0 + jl] = b.scale;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const int j = j0 + i * step, row = m0 + j;
+          const float inv = __shfl_sync(0xffffffffu, b.inv, i * kLanes);
+          const long long at = static_cast<long long>(row) * p.g.N + col;
+          if (col_in && j < rows) {
+            if (p.g.pre != nullptr)
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.g.pre) + at) =
+                  make_uint2(pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]));
+            *reinterpret_cast<uint32_t*>(p.g.hq + at) = e4m3x4(h[i][0].x, h[i][0].y, h[i][1].x, h[i][1].y, inv);
+          }
+        }
       } else {
-        const long long at = static_cast<long long>(row) * p.g.N + col;
-        if (p.g.pre != nullptr && col_in) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.g.pre) + at) = u;
-        const float2 h0 = gelu2(make_float2(v[0], v[1])), h1 = gelu2(make_float2(v[2], v[3]));
-        float amax = col_in ? fmaxf(fmaxf(fabsf(h0.x), fabsf(h0.y)), fmaxf(fabsf(h1.x), fabsf(h1.y))) : 0.f;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const BlockScale b = block_scale(amax, 448.f);
-        if (col_in) *reinterpret_cast<uint32_t*>(p.g.hq + at) = e4m3x4(h0.x, h0.y, h1.x, h1.y, b.inv);
-        if (lane == 0) p.g.h_scales[(n0 >> 7) * p.m_pad + row] = b.scale;
+        for (int i = 0; i < R; ++i) {
+          const int j = j0 + i * step;
+          if (j >= rows || !col_in) continue;
+          const long long at = static_cast<long long>(m0 + j) * p.g.ldc + col;
+          if constexpr (OUT == kOutFp32)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.g.c) + at) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+          else
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.g.c) + at) =
+                make_uint2(pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]));
+        }
       }
     }
-  }
+  };
+  // as many rows as there are reads in flight for, and one where a warp has no second (with GeLU: 14.2 -> 14.0 us, one row)
+  if (OUT == kOutGelu8 && rows <= step) join(std::integral_constant<int, 1>{}, std::integral_constant<int, kFewMaxRanks>{});
+  else if (ranks <= 2) join(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+  else join(std::integral_constant<int, 2>{}, std::integral_constant<int, kFewMaxRanks>{});
   cluster_sync_all();  // the cluster has read this CTA's sums
 }
 
