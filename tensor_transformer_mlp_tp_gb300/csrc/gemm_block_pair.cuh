@@ -15,8 +15,8 @@
 // taking three cycles) and handed back (100 in the even CTA, 230 from the odd one), and two buffers make that 740 to 800.
 // A sustained run is at the power limit besides (1360 W at 1.67 GHz).  Measured at 8192 x 4096 x 16384: 370 us in a
 // burst, 430 us sustained (2550 TFLOP/s; the per-tensor kernel, which promotes nothing, 306 and 351 us on the same
-// codes).  With both operands scaled by rows (BVEC) the products double and the loads are the slower fragment form: 590
-// us at 4096 x 16384 x 8192, about 1350 cycles a k-block.
+// codes).  With both operands scaled by rows (BVEC) the products double and the loads are the slower fragment form: 570
+// us at 4096 x 16384 x 8192, about 1300 cycles a k-block.
 //
 // Synchronisation as in the per-tensor pair kernel: full / empty of the TMA ring, tfull / tempty of the partial sums,
 // the barriers that count both CTAs in the even one.  All waits are bounded.  An arrive on tempty publishes nothing, so
@@ -308,63 +308,88 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
         ok = warp_wait(tfull + ab, (blk >> 1) & 1u, wc, kSiteBlockPromote);
         if (!ok) break;
         tc_fence_after_sync();
-        uint32_t r[3][16];
         const uint32_t tcol = trow + ab * 256;
-        auto load = [&](int c, uint32_t (&v)[16]) {
-          if constexpr (kFrag)
-            tmem_load_16x32_async(tcol + (static_cast<uint32_t>((c & 1) * 16) << 16) + (c >> 1) * 32, v);
-          else
-            tmem_load_16cols_async(tcol + c * 16, v);
+        auto release = [&] {  // every load has returned: the buffer is free before the last sums, not after them
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader) mbar_arrive(tempty + ab);
+            else mbar_arrive_remote_relaxed(ab ? tempty1 : tempty0);
+          }
         };
-#pragma unroll
-        for (int c = 0; c < 3; ++c) load(c, r[c]);
-        float2 rs[kFrag ? 4 : 1];
-        const float* cs = slot + 128 + half * 128 + (kFrag ? 2 * (lane & 3) : 0);
         if constexpr (kFrag) {
+          // The products are what this path waits for (without them 366 us at 4096 x 16384 x 8192, without the loads 509,
+          // with both 570), and a packed instruction takes longer the more registers it reads: rows first, one scale for four
+          // products in a row, then columns, one scale for four sums (columns first: 593; a row's two steps after each other:
+          // 593; scalar: 691).
+          uint32_t r[4][16];
+          auto load = [&](int u) {  // rows 0 to 15 and 16 to 31 of columns 32 u to 32 u + 31
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              tmem_load_16x32_async(tcol + (static_cast<uint32_t>(h * 16) << 16) + u * 32, r[2 * (u & 1) + h]);
+          };
+          load(0);
+          float2 rs[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float f = slot[quad * 32 + 8 * i + (lane >> 2)];
             rs[i] = make_float2(f, f);
           }
+          const float* cs = slot + 128 + half * 128 + 2 * (lane & 3);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float2 c2[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) c2[g] = *reinterpret_cast<const float2*>(cs + u * 32 + 8 * g);
+            tmem_wait_ld(r[2 * (u & 1)]);
+            tmem_wait_ld(r[2 * (u & 1) + 1]);
+            if (u == 3) release();
+            else load(u + 1);
+            float2 q[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const uint32_t* v = r[2 * (u & 1) + (i >> 1)] + 4 * g + 2 * (i & 1);
+                q[i][g] = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+              }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int g = 0; g < 4; ++g) q[i][g] = __fmul2_rn(q[i][g], rs[i]);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float2& a = acc[16 * u + 8 * (i >> 1) + 2 * g + (i & 1)];
+                a = __ffma2_rn(q[i][g], c2[g], a);
+              }
+          }
         } else {
-          float f = slot[quad * 32 + lane];
-          if constexpr (!BVEC) f *= __shfl_sync(0xffffffffu, sb_cur, kb & 31);
-          rs[0] = make_float2(f, f);
-          if (!BVEC && (kb & 31) == 31) {
+          uint32_t r[3][16];
+#pragma unroll
+          for (int c = 0; c < 3; ++c) tmem_load_16cols_async(tcol + c * 16, r[c]);
+          const float f = slot[quad * 32 + lane] * __shfl_sync(0xffffffffu, sb_cur, kb & 31);
+          const float2 rs = make_float2(f, f);
+          if ((kb & 31) == 31) {
             sb_cur = sb_next;
             const int next = kb + 33 + static_cast<int>(lane);
             sb_next = next < p.k_blocks ? __ldg(sb + next) : 0.f;
           }
-        }
-        constexpr int kPairs = kFrag ? 4 : 1;  // of columns in a chunk of the fragment layout, each with its scales
-        float2 c2[kPairs];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t(&v)[16] = r[c % 3];
-          if (kFrag && (c & 1) == 0) {
-#pragma unroll
-            for (int g = 0; g < kPairs; ++g) c2[g] = *reinterpret_cast<const float2*>(cs + (c >> 1) * 32 + 8 * g);
-          }
-          tmem_wait_ld(v);
-          // Every load has returned: the buffer is free before the last sums, not after them.  (The fragment loads are
-          // slower: a chunk later costs them nothing and saves waiting, 615 -> 587 us at 4096 x 16384 x 8192.)
-          if (c == (kFrag ? 6 : 5)) {
-            tmem_wait_ld(r[0]);
-            tmem_wait_ld(r[1]);
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-              if (leader) mbar_arrive(tempty + ab);
-              else mbar_arrive_remote_relaxed(ab ? tempty1 : tempty0);
+          for (int c = 0; c < 8; ++c) {
+            uint32_t(&v)[16] = r[c % 3];
+            tmem_wait_ld(v);
+            if (c == 5) {
+              tmem_wait_ld(r[0]);
+              tmem_wait_ld(r[1]);
+              release();
             }
-          }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float2 q = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            if constexpr (kFrag) q = __fmul2_rn(q, c2[(i >> 1) % kPairs]);
-            acc[c * 8 + i] = __ffma2_rn(q, rs[kFrag ? (c & 1) * 2 + (i & 1) : 0], acc[c * 8 + i]);
+            for (int i = 0; i < 8; ++i)
+              acc[c * 8 + i] = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), rs, acc[c * 8 + i]);
+            if (c < 5) tmem_load_16cols_async(tcol + (c + 3) * 16, v);
           }
-          if (c < 5) load(c + 3, v);
         }
       }
       if (!ok) break;
