@@ -236,7 +236,7 @@ def test_gemm_fp8_block(M, N, K, b_block_rows, dtype):
     assert torch.equal(C2, C.t[:, :N])
 
 
-# shapes with more than a wave of 128 x 128 tiles, which run on CTA pairs: rows, columns and k-blocks that end inside
+# many tiles, of either kernel: rows, columns and k-blocks that end inside
 PAIR_SHAPES = [(700, 2312, 272), (1030, 1160, 400), (4104, 264, 144), (300, 5000, 16), (2050, 4104, 1040)]
 
 
@@ -250,6 +250,21 @@ def test_gemm_fp8_block_many_tiles(M, N, K, b_block_rows, dtype):
 @pytest.mark.parametrize("T,d,F", [(1030, 400, 1168), (700, 272, 2320), (4104, 144, 272), (2050, 1040, 4112)])
 @pytest.mark.parametrize("pre", [True, False])
 def test_gemm1_fp8_block_many_tiles(T, d, F, pre):
+    test_gemm1_fp8_block(T, d, F, 1, pre)
+
+
+# more than a wave of 128 x 128 tiles and no more waves of pairs: on pairs whatever a k-block takes in either kernel
+@pytest.mark.parametrize("M,N,K", [(1300, 2312, 272), (2300, 1160, 400), (8200, 264, 144), (300, 7000, 16), (513, 4104, 528),
+                                   (1300, 2312, 8464), (1285, 2568, 4112)])
+@pytest.mark.parametrize("b_block_rows", [1, 128])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gemm_fp8_block_on_pairs(M, N, K, b_block_rows, dtype):
+    test_gemm_fp8_block(M, N, K, b_block_rows, dtype)
+
+
+@pytest.mark.parametrize("T,d,F", [(1300, 272, 2320), (2300, 400, 1168), (8200, 144, 272), (513, 4112, 4112)])
+@pytest.mark.parametrize("pre", [True, False])
+def test_gemm1_fp8_block_on_pairs(T, d, F, pre):
     test_gemm1_fp8_block(T, d, F, 1, pre)
 
 
