@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 
 #include "block_fp8.cuh"
+#include "bwd_ring.h"
 
 namespace tpmlp {
 namespace {
@@ -119,12 +120,9 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_rmsnorm_add(const RmsBl
 // TW of the 16 consumer warps take a row each: thread j of a team has the vectors j + 32 TW k (k < VT), takes them from
 // the ring once (VT = 2, rows up to 8192) or once for the two sums and once for the output (VT = 4), and keeps the
 // weights and its dweight sums in registers.  Row i of the block belongs to team i % teams, so the order of every sum is
-// fixed.  Measured: 8192 x 4096 47 us with the final sum's 2.3 (5.7 TB/s, 0.85 of the copy rate; 58 us with VT = 4, 83
-// us with rows in registers and no ring), 65536 x 128 37 us (148 us with a row a copy), 320 x 1024 5.3 us.
-constexpr int kBwdSmem = 196608;    // most shared memory of the ring; the teams' sums take 64 KB at most
-constexpr int kBwdMaxBlocks = 160;  // dweight partial rows at most (one block an SM)
-constexpr int kBwdConsumers = 16;
-constexpr int kBwdMaxD = 256 * 4 * kBwdConsumers;
+// fixed; which rings are safe with that, and the check at the kernel's entry: bwd_ring_ok.  Measured: 8192 x 4096 47 us
+// with the final sum's 2.3 (5.7 TB/s, 0.85 of the copy rate; 58 us with VT = 4, 83 us with rows in registers and no
+// ring), 65536 x 128 37 us (148 us with a row a copy), 320 x 1024 5.3 us.
 constexpr uint32_t kSiteRmsProducer = 32, kSiteRmsConsumer = 33;
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
@@ -139,12 +137,23 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
   extern __shared__ __align__(128) uint8_t bwd_smem[];
   __shared__ float2 red[2][kBwdConsumers];
   __shared__ int vote[2][kBwdConsumers];
-  __shared__ __align__(8) uint64_t full[32], empty[32];
+  __shared__ __align__(8) uint64_t full[kBwdMaxSlots], empty[kBwdMaxSlots];
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool has_r = p.r.p[0] != nullptr;
   const uint32_t row_bytes = static_cast<uint32_t>(p.d) * 2u, part_bytes = row_bytes * static_cast<uint32_t>(group);
   const uint32_t slot_bytes = part_bytes * 3u;  // [s | dy | ds] of a group
+  const int grid = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
+  const int groups = (p.rows + group - 1) / group, n_groups = (groups - first + grid - 1) / grid;
+  const int cw = warp - 1, team = cw / tw, teams = kBwdConsumers / tw;
+  if (!bwd_ring_ok(n_groups, group, slots, teams)) {  // uniform over the block: no barrier is left waiting
+    griddep_wait();
+    if (threadIdx.x == 0) {
+      atomicOr(err, kErrConfig);
+      atomicCAS(err + 1, 0u, kSiteRowConfig);
+    }
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < slots; ++s) {
       mbar_init(full + s, 1);
@@ -158,9 +167,6 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
   griddep_wait();
   griddep_launch_dependents();
   const WaitCtx wc{&abort_flag, err, timeout_ns};
-  const int grid = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
-  const int groups = (p.rows + group - 1) / group, n_groups = (groups - first + grid - 1) / grid;
-  const int cw = warp - 1, team = cw / tw, teams = kBwdConsumers / tw;
   const int nv = p.d / 8, step = 32 * tw, j = (cw - team * tw) * 32 + lane;
   float2 dw[VT][4];
 #pragma unroll
@@ -581,33 +587,18 @@ size_t rmsnorm_add_bwd_scratch_floats(int rows, int d) {
 }
 
 cudaError_t launch_rmsnorm_add_bwd(const RmsBlockParams& p, float* dweight, const DeviceCtx& ctx, cudaStream_t s) {
-  int blocks = ctx.sm_count < kBwdMaxBlocks ? ctx.sm_count : kBwdMaxBlocks;
-  if (p.rows < blocks) blocks = p.rows;
-  const int nv = p.d / 8;
+  const int sms = ctx.sm_count < kBwdMaxBlocks ? ctx.sm_count : kBwdMaxBlocks, blocks = p.rows < sms ? p.rows : sms;
   cudaError_t e;
   if (p.d <= kBwdMaxD) {
-    const int vt = p.d <= kBwdMaxD / 2 ? 2 : 4;
-    int tw = 1;
-    while (32 * tw * vt < nv) tw *= 2;
-    const int teams = kBwdConsumers / tw;
-    // groups of about 8 KB a tensor, but one for each block at least; as many slots as fit (two of the widest row)
-    int group = 8192 / (2 * p.d);
-    if (group > p.rows / blocks) group = p.rows / blocks;
-    if (group < 1) group = 1;
-    const int slot = 3 * p.d * 2 * group, groups = (p.rows + group - 1) / group, most = (groups + blocks - 1) / blocks;
-    int slots = kBwdSmem / slot;
-    if (slots > 32) slots = 32;
-    if (slots > most) slots = most;
-    int smem = slots * slot;
-    if (smem < teams * p.d * 4) smem = teams * p.d * 4;
+    const BwdRing r = bwd_ring(p.rows, p.d, ctx.sm_count);
     static std::atomic<unsigned long long> set[2][64] = {};
-    auto kern = vt == 2 ? k_rmsnorm_add_bwd<2> : k_rmsnorm_add_bwd<4>;
-    e = raise_smem_once(kern, kBwdSmem, ctx, set[vt == 2 ? 0 : 1]);
+    auto kern = r.vt == 2 ? k_rmsnorm_add_bwd<2> : k_rmsnorm_add_bwd<4>;
+    e = raise_smem_once(kern, kBwdSmem, ctx, set[r.vt == 2 ? 0 : 1]);
     if (e != cudaSuccess) return e;
-    e = launch_overlapped(kern, dim3(blocks), dim3(32 * (kBwdConsumers + 1)), smem, s, p, tw, group, slots, ctx.err,
-                          ctx.timeout_ns);
+    e = launch_overlapped(kern, dim3(r.blocks), dim3(32 * (kBwdConsumers + 1)), r.smem, s, p, r.team_warps, r.group,
+                          r.slots, ctx.err, ctx.timeout_ns);
   } else {
-    k_rmsnorm_add_bwd_wide<4><<<blocks, (nv + 127) / 128 * 32, 0, s>>>(p);
+    k_rmsnorm_add_bwd_wide<4><<<blocks, (p.d / 8 + 127) / 128 * 32, 0, s>>>(p);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
