@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import threading
 
 import torch
 
@@ -700,6 +701,10 @@ def _chunk_array(chunks, n, numel, fn):
 
 
 _WORKSPACES = {}  # (device index, stream id) -> the stream's workspace
+# Held from taking a workspace to the end of the call that uses it: a call is two launches, and another host thread's
+# between them, on the same stream and so the same workspace, would have its partial sums added up.  (Reentrant: a
+# finaliser may run a call of its own.)
+_WORKSPACE_LOCK = threading.RLock()
 
 
 def _stream_workspace(nbytes, dev, stream):
@@ -755,10 +760,13 @@ def tpmlp_rmsnorm_add_backward(S_chunks, weight, dXg, N, dX_chunks, dweight, dS_
             _chunk_array(dS_chunks, N, n, fn), _shape(T, d, d * N, N), _chunk_array(dX_chunks, N, n, fn),
             _typed(dweight, _FP32, d, fn))
     dev = _device_of(weight, fn)
+    call, to = (_lib or lib()).tpmlp_rmsnorm_add_backward, _raw_stream(dev) if stream is None else _stream(stream)
     if ws is None:
-        ws = _stream_workspace(tpmlp_rmsnorm_add_backward_workspace_size(T, d, N), dev, stream)
-    st = (_lib or lib()).tpmlp_rmsnorm_add_backward(*args, ws.data_ptr(), ws.nbytes, _raw_stream(dev) if stream is None
-                                                    else _stream(stream))
+        with _WORKSPACE_LOCK:
+            ws = _stream_workspace(tpmlp_rmsnorm_add_backward_workspace_size(T, d, N), dev, stream)
+            st = call(*args, ws.data_ptr(), ws.nbytes, to)
+    else:
+        st = call(*args, ws.data_ptr(), ws.nbytes, to)
     if st:
         raise TpMlpError(fn, st)
 
