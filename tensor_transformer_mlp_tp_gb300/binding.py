@@ -709,9 +709,10 @@ _WORKSPACE_LOCK = threading.RLock()
 
 def _stream_workspace(nbytes, dev, stream):
     """A workspace that the current stream keeps for its calls, which it runs one after the other: an allocation between
-    two launches costs as much host time as a launch.  Fresh, and the caller's stream's until its work is done, where that
-    order does not hold: for an explicit stream, in a capture (the graph may be replayed on any stream), and on streams
-    that are not torch's own (a handle may be used again for another stream)."""
+    two launches costs as much host time as a launch.  Fresh where that order does not hold: for an explicit stream, in a
+    capture (the graph may be replayed on any stream), and on streams that are not torch's own (a handle may be used
+    again for another stream).  Fresh memory comes from the pool of the stream that runs the call: a block that another
+    stream has freed may still be written by that stream's queued work."""
     if stream is None:
         sid = _current_stream(dev)[0]
         if (sid == 0 or sid & 1) and not _capturing():
@@ -721,11 +722,21 @@ def _stream_workspace(nbytes, dev, stream):
                 _WORKSPACES[dev, sid] = ws
             return ws
     device = torch.device("cuda", dev)
-    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    if stream is not None:
-        own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
-        ws.record_stream(own)
-    return ws
+    if stream is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(_stream_object(stream, device)):  # from that stream's own memory, in the order of its work
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def _stream_object(stream, device):
+    """The torch stream of a stream argument; 0 and 1 are the handles of the legacy default stream, which is torch's.
+    The handle 2 is another stream in every thread, and torch keeps one pool for it: refused, it needs the caller's ws."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream)
+    if handle == 2:
+        _refuse("tpmlp_rmsnorm_add_backward")
+    return torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
 
 
 def tpmlp_rmsnorm_add_gather(X_chunks, weight, N, R_chunks=None, S_chunks=None, Xg=None, Xq=None, x_scales=None,

@@ -1,5 +1,6 @@
 """The Python side of the block-scaled FP8 calls without a GPU: stand-ins for device tensors and for the library, so that
 nothing reaches CUDA whatever gets past the checks."""
+import math
 import threading
 import time
 
@@ -17,7 +18,7 @@ class Fake:
 
     def __init__(self, *shape, dtype=BF16, dev=DEV, ptr=1 << 20, stride=None):
         self.shape, self.dtype, self._dev, self._ptr = torch.Size(shape), dtype, dev, ptr
-        self._stride = stride or tuple(torch.empty(shape, device="meta").stride())
+        self._stride = stride or tuple(math.prod(shape[i + 1:]) for i in range(len(shape)))
         self._plain = stride is None
 
     def numel(self):
@@ -116,3 +117,39 @@ def test_a_failed_call_leaves_the_kept_workspace_free(library, monkeypatch):
     t.start()
     t.join(10)
     assert done == [1]
+
+
+def test_a_fresh_workspace_comes_from_the_stream_that_runs_the_call(library, monkeypatch):
+    """Which stream is current where the memory is taken (the allocator's blocks are ordered by their own stream)."""
+    current, taken = [None], []
+
+    class Stream:
+        def __init__(self, name):
+            self.name = name
+
+    class Use:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.s.name
+
+        def __exit__(self, *a):
+            current[0] = self.before
+
+    def empty(n, dtype=None, device=None):
+        taken.append((current[0], n))
+        return Fake(n, dtype=U8, ptr=1 << 24)
+
+    monkeypatch.setattr(binding.torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(binding.torch.cuda, "stream", Use)
+    monkeypatch.setattr(binding.torch.cuda, "ExternalStream", lambda h, device: Stream(h))
+    monkeypatch.setattr(binding.torch.cuda, "default_stream", lambda device: Stream("default"))
+    monkeypatch.setattr(binding.torch, "empty", empty)
+    monkeypatch.setattr(Fake, "record_stream", lambda self, s: None, raising=False)
+    for stream, want in ((Stream("side"), "side"), (1 << 30, 1 << 30), (0, "default"), (1, "default"), (None, None)):
+        taken.clear()
+        assert binding._stream_workspace(4096, DEV, stream) is not None
+        assert [t[0] for t in taken] == [want] and taken[0][1] >= 4096
+    with pytest.raises(binding.TpMlpError):
+        binding._stream_workspace(4096, DEV, 2)

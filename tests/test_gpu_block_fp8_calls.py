@@ -51,3 +51,62 @@ def test_norm_backwards_of_several_threads_on_one_stream():
     [t.join() for t in threads]
     torch.cuda.synchronize()
     assert not errors and not wrong
+
+
+def test_workspace_of_an_explicit_stream_is_that_streams_memory():
+    """A block that the current stream has just freed, its work perhaps still queued, is not the workspace of a call on
+    another stream; the stream given as an object, as a handle, and as the default stream's handle."""
+    n = 5 << 20
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for cur, stream in ((torch.cuda.default_stream(), side), (torch.cuda.default_stream(), other.cuda_stream), (side, 0)):
+        with torch.cuda.stream(cur):
+            t = torch.empty(n, dtype=U8, device="cuda")
+            freed = t.data_ptr()
+            del t
+            assert torch.empty(n, dtype=U8, device="cuda").data_ptr() == freed  # what the current stream would be given
+            ws = binding._stream_workspace(n, torch.cuda.current_device(), stream)
+            assert ws.data_ptr() != freed
+            del ws
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("form", ["object", "handle", "default", "legacy"])
+def test_norm_backward_on_an_explicit_stream(form):
+    c = case(300, 1024, 70)
+    run(c, ws=own_workspace(c))
+    want = c[4].clone(), c[5].clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    stream = {"object": side, "handle": side.cuda_stream, "default": 0, "legacy": 1}[form]
+    for t in c[4:]:
+        t.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for _ in range(20):
+            run(c, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(c[4], want[0]) and torch.equal(c[5], want[1])
+
+
+def test_norm_backward_captured_with_its_stream_given():
+    """The graph keeps its workspace: replays beside eager calls on the captured stream and on another."""
+    cases = [case(200, 2048, 71 + i) for i in range(3)]
+    want = []
+    for c in cases:
+        run(c, ws=own_workspace(c))
+        want.append((c[4].clone(), c[5].clone()))
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run(cases[0], stream=side)
+    for c in cases:
+        c[4].zero_()
+        c[5].zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        graph.replay()
+        run(cases[1], stream=side)
+        run(cases[2])
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        assert torch.equal(c[4], w[0]) and torch.equal(c[5], w[1])
