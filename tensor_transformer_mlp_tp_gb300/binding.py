@@ -649,52 +649,46 @@ def _refuse(fn):
 
 
 def _device_of(t, fn):
-    """The calls run on the current device's stream: refuse tensors of the host or of another device."""
+    """The calls run on the current device's stream: refuse tensors of the host or of another device (the other operands
+    are compared with this one's device)."""
     d = t.get_device()
     if d < 0 or d != _current_device():
         _refuse(fn)
     return d
 
 
-def _typed(t, dtype, numel, fn):
-    """Address of a contiguous tensor of `dtype` with at least `numel` elements (None: NULL)."""
+def _typed(t, dtype, numel, dev, fn):
+    """Address of a contiguous tensor of `dtype` with at least `numel` elements on device `dev` (None: NULL)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.numel() < numel or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() < numel or not t.is_contiguous() or t.get_device() != dev:
         _refuse(fn)
     return t.data_ptr()
 
 
-def _bytes(t, numel, fn):
-    """Address of a contiguous tensor of 8-bit elements (uint8 or a float8 type)."""
+def _bytes(t, numel, dev, fn):
+    """Address of a contiguous tensor of 8-bit elements (uint8 or a float8 type) on device `dev`."""
     if t is None:
         return None
-    if t.element_size() != 1 or t.numel() < numel or not t.is_contiguous():
+    if t.element_size() != 1 or t.numel() < numel or not t.is_contiguous() or t.get_device() != dev:
         _refuse(fn)
     return t.data_ptr()
 
 
-def _scales(t, rows, cols, block_rows, fn):
+def _scales(t, rows, cols, block_rows, dev, fn):
     a, b = block_scales_shape(rows, cols, block_rows)
-    return _typed(t, _FP32, a * b, fn)
+    return _typed(t, _FP32, a * b, dev, fn)
 
 
-def _chunk_array(chunks, n, numel, fn):
+def _chunk_array(chunks, n, numel, dev, fn):
     if chunks is None:
         return None
     if n == 1 and len(chunks) == 1:
-        t = chunks[0]
-        if t.dtype is not _BF16 or t.numel() < numel or not t.is_contiguous():
-            _refuse(fn)
-        return _ONE(t.data_ptr())
+        return _ONE(_typed(chunks[0], _BF16, numel, dev, fn))
     kind = _ARRAYS.get(n)
     if kind is None:
         kind = _ARRAYS[n] = ctypes.c_void_p * n
-    at = []
-    for t in chunks:
-        if t.dtype is not _BF16 or t.numel() < numel or not t.is_contiguous():
-            _refuse(fn)
-        at.append(t.data_ptr())
+    at = [_typed(t, _BF16, numel, dev, fn) for t in chunks]
     if len(at) != n:
         _refuse(fn)
     return kind(*at)
@@ -745,10 +739,10 @@ def tpmlp_rmsnorm_add_gather(X_chunks, weight, N, R_chunks=None, S_chunks=None, 
     fn = "tpmlp_rmsnorm_add_gather"
     rows, d = X_chunks[0].shape
     T, n = rows * N, rows * d
-    args = (_chunk_array(X_chunks, N, n, fn), _chunk_array(R_chunks, N, n, fn), _typed(weight, _BF16, d, fn), eps,
-            _shape(T, d, d * N, N), _chunk_array(S_chunks, N, n, fn), _typed(Xg, _BF16, T * d, fn),
-            _bytes(Xq, T * d, fn), _scales(x_scales, T, d, 1, fn))
     dev = _device_of(weight, fn)
+    args = (_chunk_array(X_chunks, N, n, dev, fn), _chunk_array(R_chunks, N, n, dev, fn),
+            _typed(weight, _BF16, d, dev, fn), eps, _shape(T, d, d * N, N), _chunk_array(S_chunks, N, n, dev, fn),
+            _typed(Xg, _BF16, T * d, dev, fn), _bytes(Xq, T * d, dev, fn), _scales(x_scales, T, d, 1, dev, fn))
     st = (_lib or lib()).tpmlp_rmsnorm_add_gather(*args, _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise TpMlpError(fn, st)
@@ -767,16 +761,18 @@ def tpmlp_rmsnorm_add_backward(S_chunks, weight, dXg, N, dX_chunks, dweight, dS_
     fn = "tpmlp_rmsnorm_add_backward"
     rows, d = S_chunks[0].shape
     T, n = rows * N, rows * d
-    args = (_chunk_array(S_chunks, N, n, fn), _typed(weight, _BF16, d, fn), eps, _typed(dXg, _BF16, T * d, fn),
-            _chunk_array(dS_chunks, N, n, fn), _shape(T, d, d * N, N), _chunk_array(dX_chunks, N, n, fn),
-            _typed(dweight, _FP32, d, fn))
     dev = _device_of(weight, fn)
+    args = (_chunk_array(S_chunks, N, n, dev, fn), _typed(weight, _BF16, d, dev, fn), eps,
+            _typed(dXg, _BF16, T * d, dev, fn), _chunk_array(dS_chunks, N, n, dev, fn), _shape(T, d, d * N, N),
+            _chunk_array(dX_chunks, N, n, dev, fn), _typed(dweight, _FP32, d, dev, fn))
     call, to = (_lib or lib()).tpmlp_rmsnorm_add_backward, _raw_stream(dev) if stream is None else _stream(stream)
     if ws is None:
         with _WORKSPACE_LOCK:
             ws = _stream_workspace(tpmlp_rmsnorm_add_backward_workspace_size(T, d, N), dev, stream)
             st = call(*args, ws.data_ptr(), ws.nbytes, to)
     else:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            _refuse(fn)
         st = call(*args, ws.data_ptr(), ws.nbytes, to)
     if st:
         raise TpMlpError(fn, st)
@@ -789,10 +785,10 @@ def tpmlp_quantize_block(src, block_rows=1, fmt=E4M3, q=None, scales=None, qT=No
     ld, step = src.stride()
     if src.dtype is not _BF16 or (step != 1 and cols > 1):
         _refuse(fn)
-    args = (src.data_ptr(), ld if rows > 1 else cols, rows, cols, block_rows, fmt, _bytes(q, rows * cols, fn),
-            _scales(scales, rows, cols, block_rows, fn), _bytes(qT, cols * ((rows + 15) & -16), fn),
-            _scales(scalesT, cols, rows, block_rows, fn))
     dev = _device_of(src, fn)
+    args = (src.data_ptr(), ld if rows > 1 else cols, rows, cols, block_rows, fmt, _bytes(q, rows * cols, dev, fn),
+            _scales(scales, rows, cols, block_rows, dev, fn), _bytes(qT, cols * ((rows + 15) & -16), dev, fn),
+            _scales(scalesT, cols, rows, block_rows, dev, fn))
     st = (_lib or lib()).tpmlp_quantize_block(*args, _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise TpMlpError(fn, st)
@@ -813,9 +809,12 @@ def tpmlp_gemm_fp8_block(A8, a_scales, B8, b_scales, C, bias=None, b_block_rows=
             b_scales.dtype is not _FP32 or b_scales.numel() < nb or not b_scales.is_contiguous()):
         _refuse("tpmlp_gemm_fp8_block")
     dev = _device_of(C, "tpmlp_gemm_fp8_block")
+    if (A8.get_device() != dev or a_scales.get_device() != dev or B8.get_device() != dev or
+            b_scales.get_device() != dev):
+        _refuse("tpmlp_gemm_fp8_block")
     st = (_lib or lib()).tpmlp_gemm_fp8_block(
         A8.data_ptr(), a_fmt, a_scales.data_ptr(), B8.data_ptr(), b_fmt, b_scales.data_ptr(), b_block_rows, M, N, K,
-        None if bias is None else _typed(bias, _BF16, N, "tpmlp_gemm_fp8_block"), C.data_ptr(),
+        None if bias is None else _typed(bias, _BF16, N, dev, "tpmlp_gemm_fp8_block"), C.data_ptr(),
         FP32 if c_type is _FP32 else BF16, ldc if M > 1 else N,
         _raw_stream(dev) if stream is None else _stream(stream))
     if st:
@@ -829,10 +828,10 @@ def tpmlp_gemm1_fp8_block(Xq, x_scales, AqT, a_scales, bias, N, Hq, h_scales, Hp
     F, k = AqT.shape
     if k != d:
         _refuse(fn)
-    args = (_bytes(Xq, T * d, fn), _scales(x_scales, T, d, 1, fn), _bytes(AqT, F * d, fn),
-            _scales(a_scales, F, d, 128, fn), _typed(bias, _BF16, F, fn), _shape(T, d, F, N), _bytes(Hq, T * F, fn),
-            _scales(h_scales, T, F, 1, fn), _typed(Hpre, _BF16, T * F, fn))
     dev = _device_of(Hq, fn)
+    args = (_bytes(Xq, T * d, dev, fn), _scales(x_scales, T, d, 1, dev, fn), _bytes(AqT, F * d, dev, fn),
+            _scales(a_scales, F, d, 128, dev, fn), _typed(bias, _BF16, F, dev, fn), _shape(T, d, F, N),
+            _bytes(Hq, T * F, dev, fn), _scales(h_scales, T, F, 1, dev, fn), _typed(Hpre, _BF16, T * F, dev, fn))
     st = (_lib or lib()).tpmlp_gemm1_fp8_block(*args, _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise TpMlpError(fn, st)

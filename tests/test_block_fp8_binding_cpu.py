@@ -153,3 +153,57 @@ def test_a_fresh_workspace_comes_from_the_stream_that_runs_the_call(library, mon
         assert [t[0] for t in taken] == [want] and taken[0][1] >= 4096
     with pytest.raises(binding.TpMlpError):
         binding._stream_workspace(4096, DEV, 2)
+
+
+def gather(**kw):
+    a = dict(X=Fake(4, 64), R=Fake(4, 64), S=Fake(4, 64), X2=Fake(4, 64), w=Fake(64), Xg=Fake(8, 64), Xq=Fake(8, 64, dtype=U8),
+             xs=Fake(1, 128, dtype=F32))
+    a.update(kw)
+    binding.tpmlp_rmsnorm_add_gather([a["X"], a["X2"]], a["w"], 2, R_chunks=[a["R"], a["R"]], S_chunks=[a["S"], a["S"]],
+                                     Xg=a["Xg"], Xq=a["Xq"], x_scales=a["xs"])
+
+
+def quantize(**kw):
+    a = dict(src=Fake(40, 64), q=Fake(40, 64, dtype=U8), s=Fake(1, 128, dtype=F32), qT=Fake(64, 48, dtype=U8),
+             sT=Fake(1, 128, dtype=F32))
+    a.update(kw)
+    binding.tpmlp_quantize_block(a["src"], 1, 0, q=a["q"], scales=a["s"], qT=a["qT"], scalesT=a["sT"])
+
+
+def gemm(**kw):
+    a = dict(A=Fake(5, 64, dtype=U8), sa=Fake(1, 128, dtype=F32), B=Fake(16, 64, dtype=U8), sb=Fake(1, 1, dtype=F32),
+             C=Fake(5, 16), bias=Fake(16), a_fmt=0, b_fmt=0)
+    a.update(kw)
+    binding.tpmlp_gemm_fp8_block(a["A"], a["sa"], a["B"], a["sb"], a["C"], bias=a["bias"], a_fmt=a["a_fmt"], b_fmt=a["b_fmt"])
+
+
+def gemm1(**kw):
+    a = dict(X=Fake(5, 64, dtype=U8), sx=Fake(1, 128, dtype=F32), A=Fake(16, 64, dtype=U8), sa=Fake(1, 1, dtype=F32),
+             bias=Fake(16), H=Fake(5, 16, dtype=U8), sh=Fake(1, 128, dtype=F32), pre=Fake(5, 16))
+    a.update(kw)
+    binding.tpmlp_gemm1_fp8_block(a["X"], a["sx"], a["A"], a["sa"], a["bias"], 1, a["H"], a["sh"], Hpre=a["pre"])
+
+
+OPERANDS = {gather: dict(X=(4, 64), X2=(4, 64), R=(4, 64), S=(4, 64), w=(64,), Xg=(8, 64), Xq=(8, 64, U8), xs=(1, 128, F32)),
+            backward: dict(S=(64, 256), w=(256,), dXg=(64, 256), dX=(64, 256), dw=(256, F32), dS=(64, 256), ws=(1 << 20, U8)),
+            quantize: dict(src=(40, 64), q=(40, 64, U8), s=(1, 128, F32), qT=(64, 48, U8), sT=(1, 128, F32)),
+            gemm: dict(A=(5, 64, U8), sa=(1, 128, F32), B=(16, 64, U8), sb=(1, 1, F32), C=(5, 16), bias=(16,)),
+            gemm1: dict(X=(5, 64, U8), sx=(1, 128, F32), A=(16, 64, U8), sa=(1, 1, F32), bias=(16,), H=(5, 16, U8),
+                        sh=(1, 128, F32), pre=(5, 16))}
+
+
+def fake(spec, **kw):
+    dtype = spec[-1] if isinstance(spec[-1], torch.dtype) else BF16
+    return Fake(*[n for n in spec if isinstance(n, int)], dtype=dtype, **kw)
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c in OPERANDS for n in OPERANDS[c]],
+                         ids=lambda v: v if isinstance(v, str) else v.__name__)
+@pytest.mark.parametrize("dev", [-1, 1])
+def test_each_operand_elsewhere_is_refused(library, call, name, dev):
+    """One operand of the host or of another device among operands of this one: the library is not called."""
+    call(**{name: fake(OPERANDS[call][name])})
+    assert len(library.calls) == 1
+    with pytest.raises(binding.TpMlpError) as e:
+        call(**{name: fake(OPERANDS[call][name], dev=dev)})
+    assert e.value.status == binding.ERR_INVALID_ARG and len(library.calls) == 1
