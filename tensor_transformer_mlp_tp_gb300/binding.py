@@ -666,11 +666,16 @@ def _typed(t, dtype, numel, dev, fn):
     return t.data_ptr()
 
 
-def _bytes(t, numel, dev, fn):
-    """Address of a contiguous tensor of 8-bit elements (uint8 or a float8 type) on device `dev`."""
+_U8 = torch.uint8
+_FLOAT8 = {E4M3: torch.float8_e4m3fn, E5M2: torch.float8_e5m2}
+
+
+def _codes(t, fmt, numel, dev, fn):
+    """Address of a contiguous tensor of 8-bit codes, as plain bytes (uint8) or in the float8 type of `fmt`."""
     if t is None:
         return None
-    if t.element_size() != 1 or t.numel() < numel or not t.is_contiguous() or t.get_device() != dev:
+    if ((t.dtype is not _U8 and t.dtype is not _FLOAT8.get(fmt)) or t.numel() < numel or not t.is_contiguous() or
+            t.get_device() != dev):
         _refuse(fn)
     return t.data_ptr()
 
@@ -742,7 +747,7 @@ def tpmlp_rmsnorm_add_gather(X_chunks, weight, N, R_chunks=None, S_chunks=None, 
     dev = _device_of(weight, fn)
     args = (_chunk_array(X_chunks, N, n, dev, fn), _chunk_array(R_chunks, N, n, dev, fn),
             _typed(weight, _BF16, d, dev, fn), eps, _shape(T, d, d * N, N), _chunk_array(S_chunks, N, n, dev, fn),
-            _typed(Xg, _BF16, T * d, dev, fn), _bytes(Xq, T * d, dev, fn), _scales(x_scales, T, d, 1, dev, fn))
+            _typed(Xg, _BF16, T * d, dev, fn), _codes(Xq, E4M3, T * d, dev, fn), _scales(x_scales, T, d, 1, dev, fn))
     st = (_lib or lib()).tpmlp_rmsnorm_add_gather(*args, _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise TpMlpError(fn, st)
@@ -786,8 +791,8 @@ def tpmlp_quantize_block(src, block_rows=1, fmt=E4M3, q=None, scales=None, qT=No
     if src.dtype is not _BF16 or (step != 1 and cols > 1):
         _refuse(fn)
     dev = _device_of(src, fn)
-    args = (src.data_ptr(), ld if rows > 1 else cols, rows, cols, block_rows, fmt, _bytes(q, rows * cols, dev, fn),
-            _scales(scales, rows, cols, block_rows, dev, fn), _bytes(qT, cols * ((rows + 15) & -16), dev, fn),
+    args = (src.data_ptr(), ld if rows > 1 else cols, rows, cols, block_rows, fmt, _codes(q, fmt, rows * cols, dev, fn),
+            _scales(scales, rows, cols, block_rows, dev, fn), _codes(qT, fmt, cols * ((rows + 15) & -16), dev, fn),
             _scales(scalesT, cols, rows, block_rows, dev, fn))
     st = (_lib or lib()).tpmlp_quantize_block(*args, _raw_stream(dev) if stream is None else _stream(stream))
     if st:
@@ -804,7 +809,8 @@ def tpmlp_gemm_fp8_block(A8, a_scales, B8, b_scales, C, bias=None, b_block_rows=
     kb = (K + 127) >> 7
     nb = kb * ((N + 127) & -128) if b_block_rows == 1 else kb * ((N + 127) >> 7)
     if (k != K or C.shape != (M, N) or (step != 1 and N > 1) or (c_type is not _BF16 and c_type is not _FP32) or
-            A8.element_size() != 1 or not A8.is_contiguous() or B8.element_size() != 1 or not B8.is_contiguous() or
+            (A8.dtype is not _U8 and A8.dtype is not _FLOAT8.get(a_fmt)) or not A8.is_contiguous() or
+            (B8.dtype is not _U8 and B8.dtype is not _FLOAT8.get(b_fmt)) or not B8.is_contiguous() or
             a_scales.dtype is not _FP32 or a_scales.numel() < kb * ((M + 127) & -128) or not a_scales.is_contiguous() or
             b_scales.dtype is not _FP32 or b_scales.numel() < nb or not b_scales.is_contiguous()):
         _refuse("tpmlp_gemm_fp8_block")
@@ -829,9 +835,9 @@ def tpmlp_gemm1_fp8_block(Xq, x_scales, AqT, a_scales, bias, N, Hq, h_scales, Hp
     if k != d:
         _refuse(fn)
     dev = _device_of(Hq, fn)
-    args = (_bytes(Xq, T * d, dev, fn), _scales(x_scales, T, d, 1, dev, fn), _bytes(AqT, F * d, dev, fn),
+    args = (_codes(Xq, E4M3, T * d, dev, fn), _scales(x_scales, T, d, 1, dev, fn), _codes(AqT, E4M3, F * d, dev, fn),
             _scales(a_scales, F, d, 128, dev, fn), _typed(bias, _BF16, F, dev, fn), _shape(T, d, F, N),
-            _bytes(Hq, T * F, dev, fn), _scales(h_scales, T, F, 1, dev, fn), _typed(Hpre, _BF16, T * F, dev, fn))
+            _codes(Hq, E4M3, T * F, dev, fn), _scales(h_scales, T, F, 1, dev, fn), _typed(Hpre, _BF16, T * F, dev, fn))
     st = (_lib or lib()).tpmlp_gemm1_fp8_block(*args, _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise TpMlpError(fn, st)

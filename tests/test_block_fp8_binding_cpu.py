@@ -207,3 +207,31 @@ def test_each_operand_elsewhere_is_refused(library, call, name, dev):
     with pytest.raises(binding.TpMlpError) as e:
         call(**{name: fake(OPERANDS[call][name], dev=dev)})
     assert e.value.status == binding.ERR_INVALID_ARG and len(library.calls) == 1
+
+
+E4M3T, E5M2T, OTHER = torch.float8_e4m3fn, torch.float8_e5m2, (torch.float8_e4m3fnuz, torch.float8_e5m2fnuz, torch.int8, torch.bool)
+CODES = [(gather, "Xq", (8, 64)), (gemm, "A", (5, 64)), (gemm, "B", (16, 64)), (gemm1, "X", (5, 64)), (gemm1, "A", (16, 64)),
+         (gemm1, "H", (5, 16)), (quantize, "q", (40, 64)), (quantize, "qT", (64, 48))]
+
+
+@pytest.mark.parametrize("call,name,shape", CODES, ids=lambda v: getattr(v, "__name__", str(v)))
+def test_codes_of_another_format_are_refused(library, call, name, shape):
+    """Bytes pass as what the call's format says they are; a float8 type has to be that format's."""
+    call(**{name: Fake(*shape, dtype=U8)})
+    call(**{name: Fake(*shape, dtype=E4M3T)})
+    assert len(library.calls) == 2
+    for dtype in (E5M2T,) + OTHER:
+        with pytest.raises(binding.TpMlpError) as e:
+            call(**{name: Fake(*shape, dtype=dtype)})
+        assert e.value.status == binding.ERR_INVALID_ARG
+    assert len(library.calls) == 2
+
+
+def test_products_take_the_format_that_they_are_told(library):
+    gemm(A=Fake(5, 64, dtype=E5M2T), a_fmt=1)
+    gemm(B=Fake(16, 64, dtype=E5M2T), b_fmt=1)
+    assert len(library.calls) == 2
+    for kw in (dict(A=Fake(5, 64, dtype=E4M3T), a_fmt=1), dict(B=Fake(16, 64, dtype=E4M3T), b_fmt=1)):
+        with pytest.raises(binding.TpMlpError):
+            gemm(**kw)
+    assert len(library.calls) == 2
