@@ -113,6 +113,10 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_rmsnorm_add(const RmsBl
   }
 }
 
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // With xhat = s rstd and g = dy w:  dx = rstd (g - xhat mean(g xhat)) + ds,  dweight = sum over rows of dy xhat.
 //
 // One persistent block an SM.  Warp 0 keeps the next groups of rows of s, dy and ds coming into a ring in shared memory
@@ -123,12 +127,6 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_rmsnorm_add(const RmsBl
 // fixed; which rings are safe with that, and the check at the kernel's entry: bwd_ring_ok.  Measured: 8192 x 4096 47 us
 // with the final sum's 2.3 (5.7 TB/s, 0.85 of the copy rate; 58 us with VT = 4, 83 us with rows in registers and no
 // ring), 65536 x 128 37 us (148 us with a row a copy), 320 x 1024 5.3 us.
-constexpr uint32_t kSiteRmsProducer = 32, kSiteRmsConsumer = 33;
-
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 template <int VT>
 __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
     k_rmsnorm_add_bwd(const RmsBlockParams p, int tw, int group, int slots, unsigned int* err,

@@ -139,5 +139,7 @@ struct RowParams {
 constexpr uint32_t kSiteRowProducer = 16;
 constexpr uint32_t kSiteRowConsumer = 17;
 constexpr uint32_t kSiteRowConfig = 18;
+constexpr uint32_t kSiteRmsProducer = 19;
+constexpr uint32_t kSiteRmsConsumer = 20;
 
 }  // namespace tpmlp
