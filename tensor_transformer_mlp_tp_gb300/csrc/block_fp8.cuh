@@ -21,10 +21,6 @@ __device__ __forceinline__ BlockScale block_scale(float amax, float fmax) {
 
 __host__ __device__ constexpr float fp8_max(int fmt) { return fmt == 0 ? 448.f : 57344.f; }
 
-__device__ __forceinline__ uint2 fp8x8_dyn(const float (&f)[8], float s, int fmt) {
-  return fmt == 0 ? fp8x8<0>(f, s) : fp8x8<1>(f, s);
-}
-
 __device__ __forceinline__ void unpack_vec8(const uint4& u, float (&f)[8]) {
   const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y), c = unpack_bf16x2(u.z), d = unpack_bf16x2(u.w);
   f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y; f[4] = c.x; f[5] = c.y; f[6] = d.x; f[7] = d.y;
