@@ -144,8 +144,8 @@ TPMLP_API tpmlp_status tpmlp_get_device_status(tpmlp_stream_t stream, uint32_t* 
 
 /* Debug builds (compiled with -DTPMLP_DEBUG_BOUNDS; the tests build one
  * beside the release library) check the hand-computed global indices of the
- * row kernels and of the GEMM epilogues' direct stores against the extents of
- * their buffers, count every index found outside, record the site of the
+ * row kernels and of the GEMM epilogues' direct stores, the block-scaled ones
+ * among them, against the extents of their buffers, count every index found outside, record the site of the
  * first one, and skip (stores) or redirect to the first row (loads) that
  * access.  This call synchronises the device, sets *checked to 1 in such a
  * build and 0 in a release build (which checks nothing), and returns the

@@ -623,17 +623,19 @@ tpmlp_status tpmlp_get_device_status(tpmlp_stream_t stream, uint32_t* site) {
 
 tpmlp_status tpmlp_debug_bounds_status(int32_t* checked, uint32_t* violations, uint32_t* first_site) {
   if (checked == nullptr || violations == nullptr || first_site == nullptr) return TPMLP_ERR_INVALID_ARG;
-  unsigned int c[2] = {0, 0}, site[2] = {0, 0};
+  unsigned int c[4] = {0, 0, 0, 0}, site[4] = {0, 0, 0, 0};
   if (cudaDeviceSynchronize() != cudaSuccess) return TPMLP_ERR_CUDA;
-  if (rowwise_bounds_status(&c[0], &site[0]) != cudaSuccess || gemm_bounds_status(&c[1], &site[1]) != cudaSuccess)
+  if (rowwise_bounds_status(&c[0], &site[0]) != cudaSuccess || gemm_bounds_status(&c[1], &site[1]) != cudaSuccess ||
+      block_rows_bounds_status(&c[2], &site[2]) != cudaSuccess ||
+      gemm_block_bounds_status(&c[3], &site[3]) != cudaSuccess)
     return TPMLP_ERR_CUDA;
 #ifdef TPMLP_DEBUG_BOUNDS
   *checked = 1;
 #else
   *checked = 0;
 #endif
-  *violations = c[0] + c[1];
-  *first_site = site[0] != 0 ? site[0] : site[1];
+  *violations = c[0] + c[1] + c[2] + c[3];
+  *first_site = site[0] != 0 ? site[0] : site[1] != 0 ? site[1] : site[2] != 0 ? site[2] : site[3];
   return TPMLP_OK;
 }
 

@@ -4,6 +4,7 @@
 
 #include "block_fp8.cuh"
 #include "bwd_ring.h"
+#include "debug_bounds.cuh"
 
 namespace tpmlp {
 namespace {
@@ -26,6 +27,15 @@ __device__ __forceinline__ float block_add(float v, float* red) {
   return t;
 }
 
+// Debug builds: are the chunk of row `row`, and vectors v of that row, inside their tensors?
+__device__ __forceinline__ bool chunk_ok(const RmsBlockParams& p, int row, int chunk, uint32_t site) {
+  return TPMLP_IN_BOUNDS(row, p.rows, site) && TPMLP_IN_BOUNDS(chunk, p.n_chunks, site) &&
+         TPMLP_IN_BOUNDS(row - chunk * p.rows_per_chunk, p.rows_per_chunk, site);
+}
+__device__ __forceinline__ bool row_ok(const RmsBlockParams& p, int row, int v, uint32_t site) {
+  return TPMLP_IN_BOUNDS(row, p.rows, site) && TPMLP_IN_BOUNDS(v, p.d / 8, site);
+}
+
 // s = bf16(x + r), y = s rsqrt(mean(s^2) + eps) w.  A team of TW warps per row; thread t of the team holds the 16-byte
 // vectors t + 32 TW k (k < V) in registers, so the row is read once, all its loads in flight together, and the 16 vectors
 // of a 1 x 128 block sit on the 16 lanes of a half warp.  The statistics are of the stored (rounded) sum, the value the
@@ -40,8 +50,9 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_rmsnorm_add(const RmsBl
   const int step = 32 * tw, j0 = threadIdx.x - team * step;
   const int row = blockIdx.x * (static_cast<int>(blockDim.x >> 5) / tw) + team;
   const bool valid = row < p.rows;
-  const int j = valid ? row / p.rows_per_chunk : 0;
-  const long long off = valid ? static_cast<long long>(row - j * p.rows_per_chunk) * nv : 0;
+  int j = valid ? row / p.rows_per_chunk : 0;
+  long long off = valid ? static_cast<long long>(row - j * p.rows_per_chunk) * nv : 0;
+  if (valid && !chunk_ok(p, row, j, kBoundsInChunk)) off = j = 0;
   const uint4* x4 = static_cast<const uint4*>(p.x.p[j]) + off;
   const uint4* r4 = static_cast<const uint4*>(p.r.p[j]) + off;
   const bool has_r = p.r.p[0] != nullptr;
@@ -70,7 +81,8 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_rmsnorm_add(const RmsBl
       for (int e = 0; e < 8; ++e) f[e] += g[e];
       x[k] = pack_vec8(f);
       const int v = j0 + k * step;
-      if (p.s.p[0] != nullptr && valid && v < nv) (static_cast<uint4*>(p.s.p[j]) + off)[v] = x[k];
+      if (p.s.p[0] != nullptr && valid && v < nv && row_ok(p, row, v, kBoundsOutChunk))
+        (static_cast<uint4*>(p.s.p[j]) + off)[v] = x[k];
       unpack_vec8(x[k], f);
     }
 #pragma unroll
@@ -94,7 +106,8 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_rmsnorm_add(const RmsBl
     unpack_vec8(v < nv ? __ldg(static_cast<const uint4*>(p.weight) + v) : make_uint4(0, 0, 0, 0), w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[k][e] = f[e] * rstd * w[e];
-    if (p.xg != nullptr && valid && v < nv) (static_cast<uint4*>(p.xg) + row_off)[v] = pack_vec8(y[k]);
+    if (p.xg != nullptr && valid && v < nv && row_ok(p, row, v, kBoundsRowStore))
+      (static_cast<uint4*>(p.xg) + row_off)[v] = pack_vec8(y[k]);
     if (p.xq != nullptr) {
       const float a = half_warp_max(abs_max8(y[k]));
       if ((threadIdx.x & (V - 1)) == k) amax = a;
@@ -104,12 +117,15 @@ __global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_rmsnorm_add(const RmsBl
   // the divisions of the thread's V blocks are shared out: lane k of each half warp makes those of block k
   const BlockScale b = block_scale(amax, 448.f);
   const int kl = threadIdx.x & 15, block = (j0 + kl * step) >> 4;
-  if (kl < V && valid && block * 16 < nv) p.scales[block * p.rows_pad + row] = b.scale;
+  if (kl < V && valid && block * 16 < nv && TPMLP_IN_BOUNDS(row, p.rows_pad, kBoundsBlockScales) &&
+      TPMLP_IN_BOUNDS(block, (p.d + kBlock - 1) / kBlock, kBoundsBlockScales))
+    p.scales[block * p.rows_pad + row] = b.scale;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int v = j0 + k * step;
     const float inv = __shfl_sync(0xffffffffu, b.inv, k, 16);
-    if (valid && v < nv) (reinterpret_cast<uint2*>(p.xq) + row_off)[v] = fp8x8<0>(y[k], inv);
+    if (valid && v < nv && row_ok(p, row, v, kBoundsBlockCodes))
+      (reinterpret_cast<uint2*>(p.xq) + row_off)[v] = fp8x8<0>(y[k], inv);
   }
 }
 
@@ -177,13 +193,16 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
       int slot = 0, issued = 0;
       for (int i = 0; i < n_groups; ++i) {
         if (!wait_bounded(empty + slot, phase ^ 1u, wc, kSiteRmsProducer)) break;
-        const int r0 = (first + i * grid) * group, n = min(group, p.rows - r0);
+        int r0 = (first + i * grid) * group;
+        const int n = min(group, p.rows - r0);
+        if (!TPMLP_IN_BOUNDS(r0, p.rows, kBoundsRowLoad) || !TPMLP_IN_BOUNDS(r0 + n - 1, p.rows, kBoundsRowLoad)) r0 = 0;
         uint8_t* dst = bwd_smem + static_cast<long long>(slot) * slot_bytes;
         mbar_arrive_expect_tx(full + slot, static_cast<uint32_t>(n) * row_bytes * (has_r ? 3u : 2u));
         bulk_load(dst + part_bytes, static_cast<const uint8_t*>(p.dy) + static_cast<long long>(r0) * row_bytes,
                   static_cast<uint32_t>(n) * row_bytes, full + slot);
         for (int r = 0; r < n;) {  // the group's rows of one chunk after the other
-          const int c = (r0 + r) / p.rows_per_chunk, in = r0 + r - c * p.rows_per_chunk;
+          int c = (r0 + r) / p.rows_per_chunk, in = r0 + r - c * p.rows_per_chunk;
+          if (!chunk_ok(p, r0 + r, c, kBoundsInChunk)) c = in = 0;
           const int m = min(n - r, p.rows_per_chunk - in);
           const long long off = static_cast<long long>(in) * row_bytes;
           const uint32_t bytes = static_cast<uint32_t>(m) * row_bytes, at = static_cast<uint32_t>(r) * row_bytes;
@@ -261,6 +280,7 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
       const float c = t.y * rstd * rstd * rstd * inv_d;  // rstd mean(g xhat) rstd
       const float2 r2 = make_float2(rstd, rstd), nc2 = make_float2(-c, -c);
       const int ch = row / p.rows_per_chunk;
+      const bool out_ok = chunk_ok(p, row, ch, kBoundsOutChunk);
       uint4* out = static_cast<uint4*>(p.s.p[ch]) + static_cast<long long>(row - ch * p.rows_per_chunk) * nv;
 #pragma unroll
       for (int k = 0; k < VT; ++k) {
@@ -278,7 +298,7 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
           const float2 dx = __fadd2_rn(__ffma2_rn(xf, nc2, __fmul2_rn(yr, unpack_bf16x2(wa[w]))), unpack_bf16x2(ra[w]));
           o[w] = pack_bf16x2(dx.x, dx.y);
         }
-        out[v] = make_uint4(o[0], o[1], o[2], o[3]);
+        if (out_ok && row_ok(p, row, v, kBoundsOutChunk)) out[v] = make_uint4(o[0], o[1], o[2], o[3]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + slot);
@@ -307,7 +327,8 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
   for (int c = threadIdx.x; c < p.d; c += blockDim.x) {
     float t = 0.f;
     for (int tm = 0; tm < teams; ++tm) t += acc[static_cast<long long>(tm) * p.d + c];
-    p.partial[static_cast<long long>(first) * p.d + c] = t;
+    if (TPMLP_IN_BOUNDS(first, min(p.rows, kBwdMaxBlocks), kBoundsPartial))
+      p.partial[static_cast<long long>(first) * p.d + c] = t;
   }
 }
 
@@ -332,7 +353,7 @@ __global__ void __launch_bounds__(1024) k_dweight_sum(const float* partial, int 
     t = 0.f;
 #pragma unroll
     for (int w = 0; w < 32; ++w) t += red[w][lane];
-    dweight[c] = t;
+    if (TPMLP_IN_BOUNDS(c, d, kBoundsPartial)) dweight[c] = t;
   }
 }
 
@@ -349,8 +370,9 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_add_bwd_wide(const RmsBlockPar
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[k][e] = 0.f;
   for (int row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const int j = row / p.rows_per_chunk;
-    const long long off = static_cast<long long>(row - j * p.rows_per_chunk) * nv;
+    int j = row / p.rows_per_chunk;
+    long long off = static_cast<long long>(row - j * p.rows_per_chunk) * nv;
+    if (!chunk_ok(p, row, j, kBoundsInChunk)) off = j = 0;
     const uint4* x4 = static_cast<const uint4*>(p.x.p[j]) + off;
     const uint4* y4 = static_cast<const uint4*>(p.dy) + static_cast<long long>(row) * nv;
     float x[V][8], dy[V][8], sq = 0.f, sgx = 0.f;
@@ -387,13 +409,13 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_add_bwd_wide(const RmsBlockPar
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] += r[e];
       }
-      (static_cast<uint4*>(p.s.p[j]) + off)[v] = pack_vec8(o);
+      if (row_ok(p, row, v, kBoundsOutChunk)) (static_cast<uint4*>(p.s.p[j]) + off)[v] = pack_vec8(o);
     }
   }
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int v = threadIdx.x + k * blockDim.x;
-    if (v >= nv) continue;
+    if (v >= nv || !TPMLP_IN_BOUNDS(blockIdx.x, min(p.rows, kBwdMaxBlocks), kBoundsPartial)) continue;
     float4* out = reinterpret_cast<float4*>(p.partial + static_cast<long long>(blockIdx.x) * p.d + v * 8);
     out[0] = make_float4(dw[k][0], dw[k][1], dw[k][2], dw[k][3]);
     out[1] = make_float4(dw[k][4], dw[k][5], dw[k][6], dw[k][7]);
@@ -423,7 +445,8 @@ __global__ void __launch_bounds__(256) k_quantize_block(const QuantBlockParams p
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + vr + 16 * i;
-    u[i] = r < p.rows && c < p.cols ? __ldg(reinterpret_cast<const uint4*>(src + r * p.ld + c)) : make_uint4(0, 0, 0, 0);
+    u[i] = r < p.rows && c < p.cols && TPMLP_IN_BOUNDS(r * p.ld + c + 7, (p.rows - 1) * p.ld + p.cols, kBoundsBlockSource)
+               ? __ldg(reinterpret_cast<const uint4*>(src + r * p.ld + c)) : make_uint4(0, 0, 0, 0);
   }
   constexpr float kF = fp8_max(FMT);
   BlockScale b{};
@@ -443,8 +466,12 @@ __global__ void __launch_bounds__(256) k_quantize_block(const QuantBlockParams p
     for (int w = 0; w < 8; ++w) m = fmaxf(m, red[0][w]);
     b = block_scale(m, kF);
     if (t == 0) {
-      if (p.scales != nullptr) p.scales[static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x] = b.scale;
-      if (p.scales_t != nullptr) p.scales_t[static_cast<long long>(blockIdx.x) * gridDim.y + blockIdx.y] = b.scale;
+      if (p.scales != nullptr && TPMLP_IN_BOUNDS(c0, p.cols, kBoundsBlockScales) &&
+          TPMLP_IN_BOUNDS(r0, p.rows, kBoundsBlockScales))
+        p.scales[static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x] = b.scale;
+      if (p.scales_t != nullptr && TPMLP_IN_BOUNDS(c0, p.cols, kBoundsBlockScales) &&
+          TPMLP_IN_BOUNDS(r0, p.rows, kBoundsBlockScales))
+        p.scales_t[static_cast<long long>(blockIdx.x) * gridDim.y + blockIdx.y] = b.scale;
     }
   } else if (p.qt != nullptr) {
     float m[8] = {};
@@ -468,7 +495,8 @@ __global__ void __launch_bounds__(256) k_quantize_block(const QuantBlockParams p
       for (int w = 0; w < 8; ++w) a = fmaxf(a, red[w][t]);
       const BlockScale col = block_scale(a, kF);
       red[0][t] = col.inv;
-      if (c0 + t < p.cols)
+      if (c0 + t < p.cols && TPMLP_IN_BOUNDS(blockIdx.y, (p.rows + kBlock - 1) / kBlock, kBoundsBlockScales) &&
+          TPMLP_IN_BOUNDS(c0 + t, gridDim.x * kBlock, kBoundsBlockScales))
         p.scales_t[blockIdx.y * (static_cast<long long>(gridDim.x) * kBlock) + c0 + t] = col.scale;
     }
     __syncthreads();
@@ -479,6 +507,10 @@ __global__ void __launch_bounds__(256) k_quantize_block(const QuantBlockParams p
     for (int e = 0; e < 8; ++e) inv[e] = TILE ? b.inv : red[0][vc * 8 + e];
   }
   const long long rows_pad = static_cast<long long>(gridDim.y) * kBlock;
+  auto code_ok = [&](int r, int c) {  // debug builds
+    return TPMLP_IN_BOUNDS(static_cast<long long>(r) * p.cols + c + 7, static_cast<long long>(p.rows) * p.cols,
+                           kBoundsBlockCodes);
+  };
   float row_inv = 0.f;  // lane vc < 8 of a half warp: of row vr + 16 vc
   if (!TILE && p.q != nullptr) {
     float m = 0.f;
@@ -492,7 +524,9 @@ __global__ void __launch_bounds__(256) k_quantize_block(const QuantBlockParams p
     const BlockScale row = block_scale(m, kF);
     row_inv = row.inv;
     const int r = r0 + vr + 16 * (vc & 7);
-    if (vc < 8 && r < p.rows) p.scales[blockIdx.x * rows_pad + r] = row.scale;
+    if (vc < 8 && r < p.rows && TPMLP_IN_BOUNDS(blockIdx.x, (p.cols + kBlock - 1) / kBlock, kBoundsBlockScales) &&
+        TPMLP_IN_BOUNDS(r, rows_pad, kBoundsBlockScales))
+      p.scales[blockIdx.x * rows_pad + r] = row.scale;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -501,13 +535,13 @@ __global__ void __launch_bounds__(256) k_quantize_block(const QuantBlockParams p
     unpack_vec8(u[i], f);
     if constexpr (TILE) {
       const uint2 codes = fp8x8<FMT>(f, b.inv);
-      if (p.q != nullptr && r < p.rows && c < p.cols)
+      if (p.q != nullptr && r < p.rows && c < p.cols && code_ok(r, c))
         *reinterpret_cast<uint2*>(p.q + static_cast<long long>(r) * p.cols + c) = codes;
       if (p.qt != nullptr) *reinterpret_cast<uint2*>(tile + (vr + 16 * i) * 32 + ((2 * vc) ^ (4 * i))) = codes;
     } else {
       if (p.q != nullptr) {
         const float row = __shfl_sync(0xffffffffu, row_inv, i, 16);
-        if (r < p.rows && c < p.cols)
+        if (r < p.rows && c < p.cols && code_ok(r, c))
           *reinterpret_cast<uint2*>(p.q + static_cast<long long>(r) * p.cols + c) = fp8x8<FMT>(f, row);
       }
       if (p.qt != nullptr) {
@@ -539,7 +573,7 @@ __global__ void __launch_bounds__(256) k_quantize_block(const QuantBlockParams p
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int oc = c0 + 4 * w + e;
-    if (oc < p.cols && r < pitch)
+    if (oc < p.cols && r < pitch && TPMLP_IN_BOUNDS(oc * pitch + r + 15, p.cols * pitch, kBoundsBlockCodes))
       *reinterpret_cast<uint4*>(p.qt + oc * pitch + r) = make_uint4(out[e][0], out[e][1], out[e][2], out[e][3]);
   }
 }
@@ -602,6 +636,15 @@ cudaError_t launch_rmsnorm_add_bwd(const RmsBlockParams& p, float* dweight, cons
   if (e != cudaSuccess) return e;
   return launch_overlapped(k_dweight_sum, dim3((p.d + 31) / 32), dim3(1024), 0, s, static_cast<const float*>(p.partial),
                            blocks, p.d, dweight);
+}
+
+cudaError_t block_rows_bounds_status(unsigned int* count, unsigned int* site) {
+#ifdef TPMLP_DEBUG_BOUNDS
+  return bounds_read_and_clear(count, site);
+#else
+  *count = *site = 0;
+  return cudaSuccess;
+#endif
 }
 
 cudaError_t launch_quantize_block(const QuantBlockParams& p, cudaStream_t s) {

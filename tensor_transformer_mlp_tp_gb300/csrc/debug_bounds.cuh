@@ -25,6 +25,11 @@ enum BoundsSite : uint32_t {
   kBoundsGemmChunk = 120,    // the GEMM's chunked store: chunk index
   kBoundsGemmShard = 121,    // the GEMM's per-shard partial store: shard index
   kBoundsGemmColsum = 122,   // the GEMM's column partial sums: partial row
+  kBoundsBlockScales = 130,  // an entry of block scales
+  kBoundsBlockCodes = 131,   // 8-bit codes of a block-scaled operand
+  kBoundsBlockSource = 132,  // the block quantiser's source
+  kBoundsBlockGemm = 133,    // the block-scaled GEMM's direct stores of C or the pre-activation
+  kBoundsBlockBias = 134,    // its bias
 };
 
 #ifdef TPMLP_DEBUG_BOUNDS

@@ -150,6 +150,15 @@ cudaError_t launch_few(GemmBlockParams& p, const DeviceCtx& ctx, cudaStream_t s)
 
 }  // namespace
 
+cudaError_t gemm_block_bounds_status(unsigned int* count, unsigned int* site) {
+#ifdef TPMLP_DEBUG_BOUNDS
+  return bounds_read_and_clear(count, site);
+#else
+  *count = *site = 0;
+  return cudaSuccess;
+#endif
+}
+
 cudaError_t launch_gemm_block(const GemmBlockLaunch& g, const DeviceCtx& ctx, cudaStream_t s) {
   GemmBlockParams p;
   memset(&p, 0, sizeof(p));

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
   const int col = n0 + static_cast<int>(lane) * 4;
   const bool col_in = col < p.g.N;
   float b4[4] = {0.f, 0.f, 0.f, 0.f};
-  if (p.g.bias != nullptr && col_in) {
+  if (p.g.bias != nullptr && col_in && TPMLP_IN_BOUNDS(col + 3, p.g.N, kBoundsBlockBias)) {
     const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.g.bias) + col));
     const float2 lo = unpack_bf16x2(u.x), hi = unpack_bf16x2(u.y);
     b4[0] = lo.x; b4[1] = lo.y; b4[2] = hi.x; b4[3] = hi.y;
@@ -321,13 +321,14 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
         constexpr int kLanes = 32 / R;
         const BlockScale b = block_scale(amax[0], 448.f);
         const int jl = j0 + static_cast<int>(lane / kLanes) * step;
-        if (lane % kLanes == 0 && jl < rows) p.g.h_scales[(n0 >> 7) * p.m_pad + m0 + jl] = b.scale;
+        if (lane % kLanes == 0 && jl < rows && scale_ok(p, n0 >> 7, m0 + jl))
+          p.g.h_scales[(n0 >> 7) * p.m_pad + m0 + jl] = b.scale;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           const int j = j0 + i * step, row = m0 + j;
           const float inv = __shfl_sync(0xffffffffu, b.inv, i * kLanes);
           const long long at = static_cast<long long>(row) * p.g.N + col;
-          if (col_in && j < rows) {
+          if (col_in && j < rows && TPMLP_IN_BOUNDS(at + 3, static_cast<long long>(p.g.M) * p.g.N, kBoundsBlockGemm)) {
             if (p.g.pre != nullptr)
               *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.g.pre) + at) =
                   make_uint2(pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]));
@@ -340,6 +341,7 @@ __global__ void __launch_bounds__(BlockFewShape<BT, BVEC>::kThreads, BT == 128 ?
           const int j = j0 + i * step;
           if (j >= rows || !col_in) continue;
           const long long at = static_cast<long long>(m0 + j) * p.g.ldc + col;
+          if (!TPMLP_IN_BOUNDS(at + 3, (p.g.M - 1) * p.g.ldc + p.g.N, kBoundsBlockGemm)) continue;
           if constexpr (OUT == kOutFp32)
             *reinterpret_cast<float4*>(static_cast<float*>(p.g.c) + at) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
           else

@@ -24,6 +24,7 @@
 #pragma once
 
 #include "block_fp8.cuh"
+#include "debug_bounds.cuh"
 
 namespace tpmlp {
 
@@ -67,6 +68,11 @@ struct BlockPairShape {
   static constexpr int kIssueRegs = 40, kPromoteRegs = 232;
   static_assert(128 * kIssueRegs + 32 * kPromoteWarps * kPromoteRegs <= 168 * kThreads, "setmaxnreg split");
 };
+
+// Debug builds: is the scale of row `row` and 128-column block `block` of an 8-bit output inside its buffer?
+__device__ __forceinline__ bool scale_ok(const GemmBlockParams& p, int block, int row) {
+  return TPMLP_IN_BOUNDS(block, p.n_pad / kBlock, kBoundsBlockScales) && TPMLP_IN_BOUNDS(row, p.m_pad, kBoundsBlockScales);
+}
 
 // Where a warp's promotion leaves its 32 x 128 sums: float2 i of a thread.
 //   rows (BVEC = false, tcgen05.ld 32x32b): row = lane, columns 2 i, 2 i + 1;
@@ -401,7 +407,7 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
 #pragma unroll
           for (int g = 0; g < 16; ++g) {
             const int c = 8 * g + 2 * static_cast<int>(lane & 3);
-            const float2 b = col0 + c < p.g.N ? unpack_bf16x2(__ldg(reinterpret_cast<const uint32_t*>(bias + c)))
+            const float2 b = col0 + c < p.g.N && TPMLP_IN_BOUNDS(col0 + c + 1, p.g.N, kBoundsBlockBias) ? unpack_bf16x2(__ldg(reinterpret_cast<const uint32_t*>(bias + c)))
                                               : make_float2(0.f, 0.f);
 #pragma unroll
             for (int hj = 0; hj < 4; ++hj) {
@@ -412,7 +418,7 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const uint4 u = col0 + 8 * j < p.g.N ? __ldg(reinterpret_cast<const uint4*>(bias) + j) : make_uint4(0, 0, 0, 0);
+            const uint4 u = col0 + 8 * j < p.g.N && TPMLP_IN_BOUNDS(col0 + 8 * j + 7, p.g.N, kBoundsBlockBias) ? __ldg(reinterpret_cast<const uint4*>(bias) + j) : make_uint4(0, 0, 0, 0);
             acc[4 * j] = __fadd2_rn(acc[4 * j], unpack_bf16x2(u.x));
             acc[4 * j + 1] = __fadd2_rn(acc[4 * j + 1], unpack_bf16x2(u.y));
             acc[4 * j + 2] = __fadd2_rn(acc[4 * j + 2], unpack_bf16x2(u.z));
@@ -443,7 +449,8 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
           amax = fmaxf(amax, fmaxf(fabsf(acc[i].x), fabsf(acc[i].y)));
         }
         const BlockScale b = block_scale(amax, 448.f);
-        if (row < p.g.M && col0 < p.g.N) p.g.h_scales[(col0 >> 7) * p.m_pad + row] = b.scale;
+        if (row < p.g.M && col0 < p.g.N && scale_ok(p, col0 >> 7, row))
+          p.g.h_scales[(col0 >> 7) * p.m_pad + row] = b.scale;
         if (lane == 0) bulk_wait_read_all();
         __syncwarp();
 #pragma unroll
