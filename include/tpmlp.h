@@ -453,7 +453,9 @@ TPMLP_API tpmlp_status tpmlp_quantize_block(const void* src, int64_t ld, int64_t
  *   A8 [M x K] (a_fmt) with a_scales of block_rows = 1; B8 [N x K] (b_fmt) with
  *   b_scales of b_block_rows 1 (a weight gradient, K = tokens) or 128 (weights);
  *   bias [N] bf16 or NULL; C [M x N] in c_dtype (TPMLP_BF16 or TPMLP_FP32) with ldc
- *   elements between rows.  K % 16 == 0, N % 8 == 0, ldc % 8 == 0, ldc >= N. */
+ *   elements between rows.  K % 16 == 0, N % 8 == 0, ldc % 8 == 0, ldc >= N.  M or
+ *   N == 0 is an empty call; K == 0 is an error: a caller with a weight gradient over
+ *   no tokens leaves the call out (its gradient is the caller's zeros). */
 TPMLP_API tpmlp_status tpmlp_gemm_fp8_block(const void* A8, int a_fmt, const float* a_scales, const void* B8, int b_fmt,
                                             const float* b_scales, int b_block_rows, int64_t M, int64_t N, int64_t K,
                                             const void* bias, void* C, int c_dtype, int64_t ldc,

@@ -801,7 +801,9 @@ def tpmlp_quantize_block(src, block_rows=1, fmt=E4M3, q=None, scales=None, qT=No
 
 def tpmlp_gemm_fp8_block(A8, a_scales, B8, b_scales, C, bias=None, b_block_rows=128, a_fmt=E4M3, b_fmt=E4M3,
                          stream=None):
-    """C [M x N] (bf16 or fp32, rows may be strided) = A8 [M x K] . B8 [N x K]^T with their block scales, + bias."""
+    """C [M x N] (bf16 or fp32, rows may be strided) = A8 [M x K] . B8 [N x K]^T with their block scales, + bias.
+    K = 0, a weight gradient over no tokens, is an empty batch as in the other calls: nothing is launched, C is left
+    alone (the ABI itself refuses it)."""
     M, K = A8.shape
     N, k = B8.shape
     ldc, step = C.stride()
@@ -818,6 +820,8 @@ def tpmlp_gemm_fp8_block(A8, a_scales, B8, b_scales, C, bias=None, b_block_rows=
     if (A8.get_device() != dev or a_scales.get_device() != dev or B8.get_device() != dev or
             b_scales.get_device() != dev):
         _refuse("tpmlp_gemm_fp8_block")
+    if K == 0:
+        return
     st = (_lib or lib()).tpmlp_gemm_fp8_block(
         A8.data_ptr(), a_fmt, a_scales.data_ptr(), B8.data_ptr(), b_fmt, b_scales.data_ptr(), b_block_rows, M, N, K,
         None if bias is None else _typed(bias, _BF16, N, dev, "tpmlp_gemm_fp8_block"), C.data_ptr(),

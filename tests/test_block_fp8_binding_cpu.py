@@ -235,3 +235,13 @@ def test_products_take_the_format_that_they_are_told(library):
         with pytest.raises(binding.TpMlpError):
             gemm(**kw)
     assert len(library.calls) == 2
+
+
+def test_a_weight_gradient_over_no_tokens_is_an_empty_call(library):
+    """As every empty batch: nothing is launched and the output is left alone; what is wrong besides is still refused."""
+    kw = dict(A=Fake(5, 0, dtype=U8), sa=Fake(0, 128, dtype=F32), B=Fake(16, 0, dtype=U8), sb=Fake(0, 1, dtype=F32), bias=None)
+    gemm(**kw)
+    assert library.calls == []
+    for wrong in (dict(B=Fake(16, 32, dtype=U8)), dict(C=Fake(5, 24)), dict(A=Fake(5, 0, dtype=U8, dev=-1)), dict(sb=Fake(0, 1))):
+        with pytest.raises(binding.TpMlpError):
+            gemm(**{**kw, **wrong})

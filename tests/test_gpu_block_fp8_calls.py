@@ -110,3 +110,20 @@ def test_norm_backward_captured_with_its_stream_given():
     torch.cuda.synchronize()
     for c, w in zip(cases, want):
         assert torch.equal(c[4], w[0]) and torch.equal(c[5], w[1])
+
+
+def test_a_step_over_no_tokens_leaves_the_gradients_alone():
+    """Quantiser, products and norm backward of an empty batch in a row, as a step of a rank without tokens makes them."""
+    d, F = 64, 128
+    e = lambda *s, dt=U8: torch.empty(*s, dtype=dt, device="cuda")
+    sc = lambda r, c, b=1: e(*binding.block_scales_shape(r, c, b), dt=F32)
+    w, X, dH = torch.ones(d, dtype=BF16, device="cuda"), e(0, d, dt=BF16), e(0, F, dt=BF16)
+    dA, dw = torch.full((d, F), 7.0, device="cuda"), torch.full((d,), 7.0, device="cuda")
+    XT, xs, HT, hs = e(d, 0), sc(d, 0), e(F, 0), sc(F, 0)
+    binding.tpmlp_rmsnorm_add_gather([X], w, 1, Xq=e(0, d), x_scales=sc(0, d))
+    binding.tpmlp_quantize_block(X, 1, 0, qT=XT, scalesT=xs)
+    binding.tpmlp_quantize_block(dH, 1, 1, qT=HT, scalesT=hs)
+    binding.tpmlp_gemm_fp8_block(XT, xs, HT, hs, dA, b_block_rows=1, b_fmt=1)
+    binding.tpmlp_rmsnorm_add_backward([X], w, X, 1, [X], dw)
+    assert (dA == 7).all() and (dw == 7).all()
+    assert binding.tpmlp_get_device_status() == (binding.OK, 0)
