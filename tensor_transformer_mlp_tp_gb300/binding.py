@@ -212,9 +212,31 @@ def tpmlp_workspace_size(shape: Shape, op: int) -> int:
     return n.value
 
 
-def workspace(shape: Shape, op: int, device=None) -> torch.Tensor:
-    """A device buffer large enough for `op` (torch allocation; contents undefined)."""
-    return torch.empty(max(tpmlp_workspace_size(shape, op), 256), dtype=torch.uint8, device=device or "cuda")
+def _scratch(nbytes, device, stream=None):
+    """Device memory for a call on `stream` (None: the current one), from the pool of the stream that runs the call and
+    so in the order of its work: another stream's block, freed before or after, may still be written by queued work."""
+    nbytes = max(nbytes, 256)
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    handle = None if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if handle is None:
+        own = stream
+    elif handle in (0, 1):  # the legacy default stream, which is torch's
+        own = torch.cuda.default_stream(device)
+    else:
+        own = torch.cuda.ExternalStream(handle, device)
+    if handle == 2:  # the per-thread default stream: one handle for many streams, so its pool has no order
+        own.wait_stream(torch.cuda.current_stream(device))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws.record_stream(own)
+        return ws
+    with torch.cuda.stream(own):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def workspace(shape: Shape, op: int, device=None, stream=None) -> torch.Tensor:
+    """A device buffer large enough for `op` on `stream` (torch allocation; contents undefined)."""
+    return _scratch(tpmlp_workspace_size(shape, op), device or torch.device("cuda", torch.cuda.current_device()), stream)
 
 
 def tpmlp_debug_bounds_status():
@@ -237,7 +259,7 @@ def tpmlp_get_device_status(stream=None):
 def tpmlp_forward(X, A, B, bias, N, Y, Hpre_out=None, H_out=None, ws=None, stream=None):
     T, d = X.shape
     shape = make_shape(T, d, A.shape[1], N, _dtype_code(X))
-    ws = workspace(shape, OP_FWD, X.device) if ws is None else ws
+    ws = workspace(shape, OP_FWD, X.device, stream) if ws is None else ws
     _check("tpmlp_forward", lib().tpmlp_forward(_ptr(X), _ptr(A), _ptr(B), _ptr(bias), ctypes.byref(shape), _ptr(Y),
                                                 _ptr(Hpre_out), _ptr(H_out), _ptr(ws), ws.numel(), _stream(stream)))
     return Y
@@ -248,7 +270,7 @@ def tpmlp_sp_forward(X_chunks, gamma, beta, A, B, N, Y_chunks, bias=None, eps=1e
     rows, d = X_chunks[0].shape
     shape = make_shape(rows * N, d, A.shape[1], N)
     op = OP_SP_FWD if rs_mode == RS_FUSED else OP_SP_FWD_PARTIALS
-    ws = workspace(shape, op, A.device) if ws is None else ws
+    ws = workspace(shape, op, A.device, stream) if ws is None else ws
     xp, _xa = _ptrs(X_chunks)
     yp, _ya = _ptrs(Y_chunks)
     _check("tpmlp_sp_forward", lib().tpmlp_sp_forward(xp, _ptr(gamma), _ptr(beta), eps, _ptr(A), _ptr(B), _ptr(bias),
@@ -260,7 +282,7 @@ def tpmlp_sp_forward(X_chunks, gamma, beta, A, B, N, Y_chunks, bias=None, eps=1e
 def tpmlp_backward(X, A, B, bias, Hpre, dY, N, dX, dA, dB, dbias=None, H=None, ws=None, stream=None):
     T, d = X.shape
     shape = make_shape(T, d, A.shape[1], N)
-    ws = workspace(shape, OP_BWD, X.device) if ws is None else ws
+    ws = workspace(shape, OP_BWD, X.device, stream) if ws is None else ws
     _check("tpmlp_backward", lib().tpmlp_backward(_ptr(X), _ptr(A), _ptr(B), _ptr(bias), _ptr(Hpre), _ptr(H), _ptr(dY),
                                                   ctypes.byref(shape), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(dbias),
                                                   _ptr(ws), ws.numel(), _stream(stream)))
@@ -270,7 +292,7 @@ def tpmlp_sp_backward(X_chunks, gamma, beta, A, B, Hpre, dY_chunks, N, dX_chunks
                       bias=None, dbias=None, eps=1e-5, H=None, Xg=None, ws=None, stream=None):
     rows, d = X_chunks[0].shape
     shape = make_shape(rows * N, d, A.shape[1], N)
-    ws = workspace(shape, OP_SP_BWD, A.device) if ws is None else ws
+    ws = workspace(shape, OP_SP_BWD, A.device, stream) if ws is None else ws
     xp, _xa = _ptrs(X_chunks)
     dyp, _dya = _ptrs(dY_chunks)
     dxp, _dxa = _ptrs(dX_chunks)
@@ -286,7 +308,7 @@ def tpmlp_sp_block_forward(X_chunks, gamma, beta, A, B, N, Y_chunks, bias=None, 
     rows, d = X_chunks[0].shape
     shape = make_shape(rows * N, d, A.shape[1], N)
     op = OP_SP_FWD if rs_mode == RS_FUSED else OP_SP_FWD_PARTIALS
-    ws = workspace(shape, op, A.device) if ws is None else ws
+    ws = workspace(shape, op, A.device, stream) if ws is None else ws
     xp, _xa = _ptrs(X_chunks)
     yp, _ya = _ptrs(Y_chunks)
     _check("tpmlp_sp_block_forward", lib().tpmlp_sp_block_forward(
@@ -301,7 +323,7 @@ def tpmlp_sp_block_backward(X_chunks, gamma, beta, A, B, Hpre, dY_chunks, N, dX_
                             ws=None, keep_mask=None, stream=None):
     rows, d = X_chunks[0].shape
     shape = make_shape(rows * N, d, A.shape[1], N)
-    ws = workspace(shape, OP_SP_BLOCK_BWD, A.device) if ws is None else ws
+    ws = workspace(shape, OP_SP_BLOCK_BWD, A.device, stream) if ws is None else ws
     xp, _xa = _ptrs(X_chunks)
     dyp, _dya = _ptrs(dY_chunks)
     dxp, _dxa = _ptrs(dX_chunks)
@@ -365,7 +387,7 @@ def tpmlp_dropout_backward(dY_chunks, N, dZ, dbias2=None, p=None, seed=0, offset
     rows, d = dY_chunks[0].shape
     shape = make_shape(rows * N, d, 8 * N, N)  # ffn unused by this step
     if dbias2 is not None and ws is None:
-        ws = workspace(shape, OP_DROPOUT_BWD, dZ.device)
+        ws = workspace(shape, OP_DROPOUT_BWD, dZ.device, stream)
     dyp, _dya = _ptrs(dY_chunks)
     _check("tpmlp_dropout_backward", lib().tpmlp_dropout_backward(
         dyp, _dropout(p, seed, offset, keep_mask), ctypes.byref(shape), _ptr(dZ), _ptr(dbias2), _ptr(ws),
@@ -391,7 +413,7 @@ def tpmlp_rmsnorm_gather(X_chunks, weight, N, Xg, eps=1e-5, stream=None):
 def tpmlp_gemm_dh_geluprime(dY, B, Hpre, N, dHpre, H=None, dbias=None, ws=None, stream=None):
     shape = make_shape(dY.shape[0], dY.shape[1], B.shape[0], N)
     if dbias is not None and ws is None:
-        ws = workspace(shape, OP_DH_GELUPRIME, dY.device)
+        ws = workspace(shape, OP_DH_GELUPRIME, dY.device, stream)
     _check("tpmlp_gemm_dh_geluprime", lib().tpmlp_gemm_dh_geluprime(
         _ptr(dY), _ptr(B), _ptr(Hpre), ctypes.byref(shape), _ptr(dHpre), _ptr(H), _ptr(dbias), _ptr(ws),
         0 if ws is None else ws.numel(), _stream(stream)))
@@ -418,7 +440,7 @@ def tpmlp_gemm_dx_shard_accum(dHpre, A, N, dX, stream=None):
 def tpmlp_layernorm_backward(X_chunks, gamma, dXg, N, dX_chunks, dgamma, dbeta, eps=1e-5, ws=None, stream=None):
     rows, d = X_chunks[0].shape
     shape = make_shape(rows * N, d, 8 * N, N)  # ffn unused by this step
-    ws = workspace(shape, OP_LN_BWD, dXg.device) if ws is None else ws
+    ws = workspace(shape, OP_LN_BWD, dXg.device, stream) if ws is None else ws
     xp, _xa = _ptrs(X_chunks)
     dxp, _dxa = _ptrs(dX_chunks)
     _check("tpmlp_layernorm_backward", lib().tpmlp_layernorm_backward(
@@ -430,7 +452,7 @@ def tpmlp_layernorm_backward_add(X_chunks, gamma, dXg, R_chunks, N, dX_chunks, d
                                  stream=None):
     rows, d = X_chunks[0].shape
     shape = make_shape(rows * N, d, 8 * N, N)  # ffn unused by this step
-    ws = workspace(shape, OP_LN_BWD, dXg.device) if ws is None else ws
+    ws = workspace(shape, OP_LN_BWD, dXg.device, stream) if ws is None else ws
     xp, _xa = _ptrs(X_chunks)
     rp, _ra = _ptrs(R_chunks)
     dxp, _dxa = _ptrs(dX_chunks)
@@ -446,7 +468,7 @@ def tpmlp_layernorm_backward_blocks(X_chunks, gamma, dXg, N, dX_chunks, dgamma, 
     rows, d = X_chunks[0].shape
     shape = make_shape(rows * N, d, 8 * N, N)  # ffn unused by this step
     if ws is None:
-        ws = torch.empty(max(1, max_blocks) * 2 * d * 4, dtype=torch.uint8, device=dXg.device)
+        ws = _scratch(max(1, max_blocks) * 2 * d * 4, dXg.device, stream)
     xp, _xa = _ptrs(X_chunks)
     dxp, _dxa = _ptrs(dX_chunks)
     _check("tpmlp_layernorm_backward_blocks", lib().tpmlp_layernorm_backward_blocks(
@@ -512,7 +534,7 @@ def tpmlp_sp_forward_fp8(X_chunks, gamma, beta, A, B, N, Y_chunks, state, bias=N
     """The E4M3 block forward; the scales are updated by tpmlp_fp8_update_scales once the step is over."""
     rows, d = X_chunks[0].shape
     shape = make_shape(rows * N, d, A.shape[1], N)
-    ws = workspace(shape, OP_SP_FWD_FP8, A.device) if ws is None else ws
+    ws = workspace(shape, OP_SP_FWD_FP8, A.device, stream) if ws is None else ws
     xp, _xa = _ptrs(X_chunks)
     yp, _ya = _ptrs(Y_chunks)
     _check("tpmlp_sp_forward_fp8", lib().tpmlp_sp_forward_fp8(
@@ -536,7 +558,7 @@ def tpmlp_gemm_dh_geluprime_e5m2(dYq, Bq, Hpre, N, scale_dy, scale_b, scale_g, d
                                  stream=None):
     shape = make_shape(dYq.shape[0], dYq.shape[1], Bq.shape[0], N)
     if dbias is not None and ws is None:
-        ws = workspace(shape, OP_DH_GELUPRIME, dYq.device)
+        ws = workspace(shape, OP_DH_GELUPRIME, dYq.device, stream)
     _check("tpmlp_gemm_dh_geluprime_e5m2", lib().tpmlp_gemm_dh_geluprime_e5m2(
         _ptr(dYq), _ptr(Bq), _ptr(Hpre), ctypes.byref(shape), _ptr(scale_dy), _ptr(scale_b), _ptr(scale_g), _ptr(dHq),
         _ptr(amax_g), _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream)))
@@ -554,7 +576,7 @@ def tpmlp_sp_backward_fp8(X_chunks, gamma, A, B, Hpre, Xq, Hq, dY_chunks, N, fwd
                           dgamma, dbeta, dbias=None, eps=1e-5, dHq_out=None, ws=None, stream=None):
     rows, d = X_chunks[0].shape
     shape = make_shape(rows * N, d, A.shape[1], N)
-    ws = workspace(shape, OP_SP_BWD_FP8, A.device) if ws is None else ws
+    ws = workspace(shape, OP_SP_BWD_FP8, A.device, stream) if ws is None else ws
     xp, _xa = _ptrs(X_chunks)
     dyp, _dya = _ptrs(dY_chunks)
     dxp, _dxa = _ptrs(dX_chunks)
@@ -591,8 +613,7 @@ def tpmlp_attention_backward_workspace_size(S, B, H, head_dim=128):
 
 def tpmlp_attention_core_backward(QKV, O, dO, LSE, S, B, H, dQKV, causal=False, head_dim=128, ws=None, stream=None):
     if ws is None:
-        ws = torch.empty(max(tpmlp_attention_backward_workspace_size(S, B, H), 256), dtype=torch.uint8,
-                         device=QKV.device)
+        ws = _scratch(tpmlp_attention_backward_workspace_size(S, B, H), QKV.device, stream)
     _check("tpmlp_attention_core_backward", lib().tpmlp_attention_core_backward(
         _ptr(QKV), _ptr(O), _ptr(dO), _ptr(LSE), S, B, H, head_dim, 1 if causal else 0, _ptr(dQKV), _ptr(ws),
         ws.numel(), _stream(stream)))
@@ -602,7 +623,7 @@ def tpmlp_attention_core_backward(QKV, O, dO, LSE, S, B, H, dQKV, causal=False, 
 def tpmlp_attention_tp_forward(X, Wqkv, Wo, S, B, H, N, Y, bqkv=None, bo=None, causal=False, QKV_out=None,
                                O_out=None, LSE_out=None, ws=None, stream=None):
     if ws is None:
-        ws = torch.empty(max(tpmlp_attention_workspace_size(S, B, H), 256), dtype=torch.uint8, device=X.device)
+        ws = _scratch(tpmlp_attention_workspace_size(S, B, H), X.device, stream)
     _check("tpmlp_attention_tp_forward", lib().tpmlp_attention_tp_forward(
         _ptr(X), _ptr(Wqkv), _ptr(bqkv), _ptr(Wo), _ptr(bo), S, B, H, N, 1 if causal else 0, _ptr(Y), _ptr(QKV_out),
         _ptr(O_out), _ptr(LSE_out), _ptr(ws), ws.numel(), _stream(stream)))
@@ -612,8 +633,7 @@ def tpmlp_attention_tp_forward(X, Wqkv, Wo, S, B, H, N, Y, bqkv=None, bo=None, c
 def tpmlp_attention_tp_backward(X, Wqkv, Wo, QKV, O, LSE, dY, S, B, H, N, dX, dWqkv, dWo, dbqkv=None, dbo=None,
                                 causal=False, dQKV_out=None, ws=None, stream=None):
     if ws is None:
-        ws = torch.empty(max(tpmlp_attention_backward_workspace_size(S, B, H), 256), dtype=torch.uint8,
-                         device=X.device)
+        ws = _scratch(tpmlp_attention_backward_workspace_size(S, B, H), X.device, stream)
     _check("tpmlp_attention_tp_backward", lib().tpmlp_attention_tp_backward(
         _ptr(X), _ptr(Wqkv), _ptr(Wo), _ptr(QKV), _ptr(O), _ptr(LSE), _ptr(dY), S, B, H, N, 1 if causal else 0,
         _ptr(dX), _ptr(dWqkv), _ptr(dbqkv), _ptr(dWo), _ptr(dbo), _ptr(dQKV_out), _ptr(ws), ws.numel(),
@@ -710,8 +730,7 @@ def _stream_workspace(nbytes, dev, stream):
     """A workspace that the current stream keeps for its calls, which it runs one after the other: an allocation between
     two launches costs as much host time as a launch.  Fresh where that order does not hold: for an explicit stream, in a
     capture (the graph may be replayed on any stream), and on streams that are not torch's own (a handle may be used
-    again for another stream).  Fresh memory comes from the pool of the stream that runs the call: a block that another
-    stream has freed may still be written by that stream's queued work."""
+    again for another stream)."""
     if stream is None:
         sid = _current_stream(dev)[0]
         if (sid == 0 or sid & 1) and not _capturing():
@@ -720,22 +739,7 @@ def _stream_workspace(nbytes, dev, stream):
                 ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=torch.device("cuda", dev))
                 _WORKSPACES[dev, sid] = ws
             return ws
-    device = torch.device("cuda", dev)
-    if stream is None:
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    with torch.cuda.stream(_stream_object(stream, device)):  # from that stream's own memory, in the order of its work
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-
-
-def _stream_object(stream, device):
-    """The torch stream of a stream argument; 0 and 1 are the handles of the legacy default stream, which is torch's.
-    The handle 2 is another stream in every thread, and torch keeps one pool for it: refused, it needs the caller's ws."""
-    if isinstance(stream, torch.cuda.Stream):
-        return stream
-    handle = int(stream)
-    if handle == 2:
-        _refuse("tpmlp_rmsnorm_add_backward")
-    return torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
+    return _scratch(nbytes, torch.device("cuda", dev), stream)
 
 
 def tpmlp_rmsnorm_add_gather(X_chunks, weight, N, R_chunks=None, S_chunks=None, Xg=None, Xq=None, x_scales=None,

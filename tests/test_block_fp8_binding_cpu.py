@@ -121,11 +121,14 @@ def test_a_failed_call_leaves_the_kept_workspace_free(library, monkeypatch):
 
 def test_a_fresh_workspace_comes_from_the_stream_that_runs_the_call(library, monkeypatch):
     """Which stream is current where the memory is taken (the allocator's blocks are ordered by their own stream)."""
-    current, taken = [None], []
+    current, taken, waits, recorded = [None], [], [], []
 
     class Stream:
         def __init__(self, name):
             self.name = name
+
+        def wait_stream(self, other):
+            waits.append((self.name, other.name))
 
     class Use:
         def __init__(self, s):
@@ -146,13 +149,32 @@ def test_a_fresh_workspace_comes_from_the_stream_that_runs_the_call(library, mon
     monkeypatch.setattr(binding.torch.cuda, "ExternalStream", lambda h, device: Stream(h))
     monkeypatch.setattr(binding.torch.cuda, "default_stream", lambda device: Stream("default"))
     monkeypatch.setattr(binding.torch, "empty", empty)
-    monkeypatch.setattr(Fake, "record_stream", lambda self, s: None, raising=False)
+    monkeypatch.setattr(binding.torch.cuda, "current_stream", lambda device: Stream("current"))
+    monkeypatch.setattr(Fake, "record_stream", lambda self, s: recorded.append(s.name), raising=False)
     for stream, want in ((Stream("side"), "side"), (1 << 30, 1 << 30), (0, "default"), (1, "default"), (None, None)):
         taken.clear()
         assert binding._stream_workspace(4096, DEV, stream) is not None
         assert [t[0] for t in taken] == [want] and taken[0][1] >= 4096
-    with pytest.raises(binding.TpMlpError):
-        binding._stream_workspace(4096, DEV, 2)
+        taken.clear()  # the other calls' workspaces
+        binding.workspace(binding.make_shape(256, 64, 256, 2), binding.OP_FWD, torch.device("cuda", DEV), stream)
+        assert [t[0] for t in taken] == [want] and taken[0][1] >= 256 * 256 * 2
+    # the per-thread default stream's handle has no pool of its own: the current stream's memory, ordered on both sides
+    taken.clear()
+    binding._stream_workspace(4096, DEV, 2)
+    assert taken == [(None, 4096)] and waits == [(2, "current")] and recorded == [2]
+
+
+def test_every_call_passes_its_stream_to_its_workspace():
+    import inspect
+    import re
+
+    n = 0
+    for name, f in inspect.getmembers(binding, inspect.isfunction):
+        if {"ws", "stream"} <= set(inspect.signature(f).parameters):
+            made = re.findall(r"ws = (?:_scratch|workspace|_stream_workspace|torch\.empty)\([^=]*?stream\)", inspect.getsource(f))
+            assert len(made) == 1 and "torch.empty" not in made[0], name
+            n += 1
+    assert n >= 16
 
 
 def gather(**kw):

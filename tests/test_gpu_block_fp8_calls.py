@@ -70,14 +70,14 @@ def test_workspace_of_an_explicit_stream_is_that_streams_memory():
     torch.cuda.synchronize()
 
 
-@pytest.mark.parametrize("form", ["object", "handle", "default", "legacy"])
+@pytest.mark.parametrize("form", ["object", "handle", "default", "legacy", "per-thread"])
 def test_norm_backward_on_an_explicit_stream(form):
     c = case(300, 1024, 70)
     run(c, ws=own_workspace(c))
     want = c[4].clone(), c[5].clone()
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    stream = {"object": side, "handle": side.cuda_stream, "default": 0, "legacy": 1}[form]
+    stream = {"object": side, "handle": side.cuda_stream, "default": 0, "legacy": 1, "per-thread": 2}[form]
     for t in c[4:]:
         t.zero_()
     torch.cuda.synchronize()
@@ -127,3 +127,24 @@ def test_a_step_over_no_tokens_leaves_the_gradients_alone():
     binding.tpmlp_rmsnorm_add_backward([X], w, X, 1, [X], dw)
     assert (dA == 7).all() and (dw == 7).all()
     assert binding.tpmlp_get_device_status() == (binding.OK, 0)
+
+
+@pytest.mark.parametrize("form", ["object", "handle", "default", "legacy", "per-thread"])
+def test_layernorm_backward_on_an_explicit_stream(form):
+    """The other calls' workspaces: the same bits on a stream that is not the current one, whose memory it is."""
+    T, d, N = 512, 1024, 4
+    g = torch.Generator(device="cuda").manual_seed(80)
+    x, dy = (torch.randn(T, d, generator=g, device="cuda").to(BF16) for _ in range(2))
+    gamma = torch.ones(d, dtype=BF16, device="cuda")
+    side = torch.cuda.Stream()
+    stream = {"object": side, "handle": side.cuda_stream, "default": 0, "legacy": 1, "per-thread": 2}[form]
+    outs = []
+    for s in (None, stream):
+        dx, dg, db = torch.zeros_like(x), torch.zeros(d, device="cuda"), torch.zeros(d, device="cuda")
+        torch.cuda.synchronize()
+        with torch.cuda.stream(torch.cuda.Stream()):
+            binding.tpmlp_layernorm_backward(list(x.split(T // N)), gamma, dy, N, list(dx.split(T // N)), dg, db, stream=s)
+            assert s is None or torch.empty(1 << 22, dtype=U8, device="cuda").fill_(255).sum() > 0  # what it may be given
+        torch.cuda.synchronize()
+        outs.append((dx, dg, db))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
