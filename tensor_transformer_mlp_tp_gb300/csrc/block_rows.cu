@@ -140,9 +140,9 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
 // TW of the 16 consumer warps take a row each: thread j of a team has the vectors j + 32 TW k (k < VT), takes them from
 // the ring once (VT = 2, rows up to 8192) or once for the two sums and once for the output (VT = 4), and keeps the
 // weights and its dweight sums in registers.  Row i of the block belongs to team i % teams, so the order of every sum is
-// fixed; which rings are safe with that, and the check at the kernel's entry: bwd_ring_ok.  Measured: 8192 x 4096 47 us
-// with the final sum's 2.3 (5.7 TB/s, 0.85 of the copy rate; 58 us with VT = 4, 83 us with rows in registers and no
-// ring), 65536 x 128 37 us (148 us with a row a copy), 320 x 1024 5.3 us.
+// fixed; which rings are safe with that: bwd_ring_ok.  Measured: 8192 x 4096 46.4 us with the final sum's 2.3 (5.8 TB/s,
+// 0.86 of the copy rate; 58 us with VT = 4, 83 us with rows in registers and no ring), 65536 x 128 37 us (148 us with a
+// row a copy), 320 x 1024 5.5 us.
 template <int VT>
 __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
     k_rmsnorm_add_bwd(const RmsBlockParams p, int tw, int group, int slots, unsigned int* err,
@@ -157,17 +157,6 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
   const bool has_r = p.r.p[0] != nullptr;
   const uint32_t row_bytes = static_cast<uint32_t>(p.d) * 2u, part_bytes = row_bytes * static_cast<uint32_t>(group);
   const uint32_t slot_bytes = part_bytes * 3u;  // [s | dy | ds] of a group
-  const int grid = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
-  const int groups = (p.rows + group - 1) / group, n_groups = (groups - first + grid - 1) / grid;
-  const int cw = warp - 1, team = cw / tw, teams = kBwdConsumers / tw;
-  if (!bwd_ring_ok(n_groups, group, slots, teams)) {  // uniform over the block: no barrier is left waiting
-    griddep_wait();
-    if (threadIdx.x == 0) {
-      atomicOr(err, kErrConfig);
-      atomicCAS(err + 1, 0u, kSiteRowConfig);
-    }
-    return;
-  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < slots; ++s) {
       mbar_init(full + s, 1);
@@ -181,6 +170,9 @@ __global__ void __launch_bounds__(32 * (kBwdConsumers + 1), 1)
   griddep_wait();
   griddep_launch_dependents();
   const WaitCtx wc{&abort_flag, err, timeout_ns};
+  const int grid = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
+  const int groups = (p.rows + group - 1) / group, n_groups = (groups - first + grid - 1) / grid;
+  const int cw = warp - 1, team = cw / tw, teams = kBwdConsumers / tw;
   const int nv = p.d / 8, step = 32 * tw, j = (cw - team * tw) * 32 + lane;
   float2 dw[VT][4];
 #pragma unroll
@@ -623,6 +615,9 @@ cudaError_t launch_rmsnorm_add_bwd(const RmsBlockParams& p, float* dweight, cons
   cudaError_t e;
   if (p.d <= kBwdMaxD) {
     const BwdRing r = bwd_ring(p.rows, p.d, ctx.sm_count);
+    // Asked here and not at the kernel's entry: a return or an empty loop for such blocks there makes the compiler's code
+    // for the others slower (8192 x 4096: 46.4 -> 47.4 to 48.3 us).
+    if (!bwd_ring_ok(r.most, r.group, r.slots, r.teams)) return cudaErrorInvalidConfiguration;
     static std::atomic<unsigned long long> set[2][64] = {};
     auto kern = r.vt == 2 ? k_rmsnorm_add_bwd<2> : k_rmsnorm_add_bwd<4>;
     e = raise_smem_once(kern, kBwdSmem, ctx, set[r.vt == 2 ? 0 : 1]);

@@ -29,9 +29,6 @@ struct BwdRing {
 // before that for its own, reads old rows and frees the slot early, and the producer then re-arms a barrier with copies in
 // flight.  So every team with a row in a group must have had one in the slot's previous group: all teams have rows in
 // every whole group, or a row `in` of a slot always belongs to the same team, or no slot is used twice.
-#ifdef __CUDACC__
-__host__ __device__
-#endif
 inline bool bwd_ring_ok(int groups, int group, int slots, int teams) {
   if (group < 1 || slots < 1 || slots > kBwdMaxSlots) return false;
   return groups <= slots || group >= teams || slots * group % teams == 0;

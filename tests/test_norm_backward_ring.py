@@ -81,8 +81,8 @@ def test_every_team_of_a_group_knows_the_slots_previous_group(layouts, rows):
     assert not bad, f"{len(bad)} layouts, the first {bad[0]}"
 
 
-def test_the_kernels_own_check_agrees(layouts):
-    """bwd_ring_ok, which the kernel asks at its entry, against the condition itself."""
+def test_the_launchers_own_check_agrees(layouts):
+    """bwd_ring_ok, which the launcher asks before it launches, against the condition itself."""
     cases = [(groups, group, slots, teams) for teams in (1, 2, 4, 8, 16) for group in range(1, 20)
              for slots in range(1, 33) for groups in (slots, slots + 1, 10 * slots + teams)]
     for case, r in zip(cases, layouts(cases, "check")):
