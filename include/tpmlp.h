@@ -438,7 +438,8 @@ TPMLP_API tpmlp_status tpmlp_rmsnorm_add_backward(const void* const* S_chunks, c
 
 /* Block quantiser, the block-scaled counterpart of tpmlp_cast_e4m3 / _e5m2: src
  * [rows x cols] bf16 with ld elements between rows (ld % 8 == 0, ld >= cols,
- * cols % 16 == 0), as it stands, transposed, or both from one read of src:
+ * cols % 16 == 0, rows <= 128 * 65535: TPMLP_ERR_UNSUPPORTED beyond), as it stands,
+ * transposed, or both from one read of src:
  *   q [rows x cols] with scales (R = rows, K = cols), or both NULL;
  *   qT [cols x P], P = 16 ceil(rows / 16), with scalesT (R = cols, K = rows), or
  *   both NULL; its bytes r >= rows are zero, so that P serves as a K.
@@ -463,7 +464,8 @@ TPMLP_API tpmlp_status tpmlp_gemm_fp8_block(const void* A8, int a_fmt, const flo
 
 /* Column-parallel GEMM on block-scaled E4M3 operands with its activation:
  * P = Xq AqT^T + bias, Hq / h_scales = GeLU(P) in E4M3 with 1 x 128 blocks (R = T,
- * K = F), Hpre (NULL or [T x F] bf16) = P.  Xq [T x d] with x_scales (block_rows =
+ * K = F), Hpre (NULL or [T x F] bf16) = P; GeLU in fp32, off by 1e-7 |P| and, far
+ * below zero, by 1% of itself at most where P > -8.  Xq [T x d] with x_scales (block_rows =
  * 1), AqT [F x d] with a_scales (block_rows = 128), bias [F] bf16 or NULL, Hq
  * [T x F].  d % 16 == 0, F % 16 == 0.  (Xq, x_scales) are
  * tpmlp_rmsnorm_add_gather's outputs, (AqT, a_scales) the transposed ones of

@@ -93,7 +93,8 @@ int few_ranks(long long tiles, int k_blocks, const DeviceCtx& ctx) {
 // at as many the same: a pair's k-block (256 x 256) takes about 0.41 us (0.65 with column scales) and a 128 x 128 one 0.37
 // (0.41), measured on GB300 with tiles for a single wave (M = 256, N = 8192, K = 8192: 30.2 us on pairs, 27.1 with this rule;
 // with column scales 45.3 and 30.2.  M = 300, N = 4096, K = 4096: 17.0 and 15.2 us.  M = 640: 17.3 us on pairs, 29.1 in two
-// waves of the other).
+// waves of the other).  The counts alone are compared: where three waves of the small kernel with column scales (1.23 us a
+// k-block) meet two of pairs (1.30), pairs are taken.
 bool few_rows(const GemmBlockLaunch& g, int k_blocks, const DeviceCtx& ctx) {
   const int sms = ctx.sm_count;
   if (g.M <= 128) return true;

@@ -324,10 +324,11 @@ __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_bloc
           }
         };
         if constexpr (kFrag) {
-          // The products are what this path waits for (without them 366 us at 4096 x 16384 x 8192, without the loads 509,
-          // with both 570), and a packed instruction takes longer the more registers it reads: rows first, one scale for four
-          // products in a row, then columns, one scale for four sums (columns first: 593; a row's two steps after each other:
-          // 593; scalar: 691).
+          // 4096 x 16384 x 8192: 570 us, without the products 366, without the loads 509.  Both of the latter hand the buffer
+          // back where it is handed back now, so they do not tell the products' time from a buffer's stay with this warp;
+          // the FMA pipe is busy 42% of the time.  A packed instruction takes longer the more registers it reads: rows
+          // first, one scale for four products in a row, then columns, one scale for four sums (columns first: 593; a
+          // row's two steps after each other: 593; scalar: 691).
           uint32_t r[4][16];
           auto load = [&](int u) {  // rows 0 to 15 and 16 to 31 of columns 32 u to 32 u + 31
 #pragma unroll
