@@ -96,7 +96,10 @@ enum {
   TPMLP_OP_SP_BLOCK_BWD = 7,   /* tpmlp_sp_block_backward */
   TPMLP_OP_DROPOUT_BWD = 8,    /* tpmlp_dropout_backward with a dbias2 output */
   TPMLP_OP_SP_FWD_FP8 = 9,     /* tpmlp_sp_forward_fp8 */
-  TPMLP_OP_SP_BWD_FP8 = 10     /* tpmlp_sp_backward_fp8 */
+  TPMLP_OP_SP_BWD_FP8 = 10,    /* tpmlp_sp_backward_fp8 */
+  TPMLP_OP_GATED_FWD = 11,     /* tpmlp_gated_forward */
+  TPMLP_OP_GATED_BWD = 12,     /* tpmlp_gated_backward */
+  TPMLP_OP_DH_GATED = 13       /* tpmlp_gemm_dh_gated with a dbg or dbu output */
 };
 
 /* Dropout of the sequence-parallel region.  The pages name Dropout in the
@@ -474,6 +477,59 @@ TPMLP_API tpmlp_status tpmlp_gemm_fp8_block(const void* A8, int a_fmt, const flo
 TPMLP_API tpmlp_status tpmlp_gemm1_fp8_block(const void* Xq, const float* x_scales, const void* AqT,
                                              const float* a_scales, const void* bias, const tpmlp_shape* shape,
                                              void* Hq, float* h_scales, void* Hpre, tpmlp_stream_t stream);
+
+/* ------------------------------------------------------------------ gated feed-forward block
+ * The block with a second column-parallel projection that gates the first:
+ *   G = X Ag + bg,  U = X Au + bu,  H = act(G) * U,  Y = sum_i H_i B_i,
+ * Ag, Au [d x F] split by columns and B [F x d] by rows exactly as A and B of
+ * tpmlp_forward.  (The pages' MLP has one projection; the gated form has no
+ * counterpart there.)  bf16, fp32 sums; act and the product are formed in fp32
+ * from the unrounded sums, and H, Gpre = G, Upre = U are rounded once each.
+ * act: TPMLP_ACT_SILU, x / (1 + exp(-x)), or TPMLP_ACT_GELU, the exact x Phi(x).
+ * Outputs must not overlap inputs or one another. */
+enum { TPMLP_ACT_SILU = 0, TPMLP_ACT_GELU = 1 };
+
+/* The whole block.  X [T x d], Y [T x d], bg, bu [F] or NULL.  Gpre_out,
+ * Upre_out: both NULL, or [T x F] each, what tpmlp_gated_backward needs.
+ * H_out: NULL, or [T x F] (otherwise H lives in the workspace).  Workspace:
+ * size of TPMLP_OP_GATED_FWD. */
+TPMLP_API tpmlp_status tpmlp_gated_forward(const void* X, const void* Ag, const void* Au, const void* B, const void* bg,
+                                           const void* bu, int act, const tpmlp_shape* shape, void* Y, void* Gpre_out,
+                                           void* Upre_out, void* H_out, void* workspace, size_t workspace_bytes,
+                                           tpmlp_stream_t stream);
+
+/* Its backward, by the chain rule:
+ *   dH = dY B^T, dU = dH * act(G), dG = dH * U * act'(G), dB = H^T dY,
+ *   dAg = X^T dG, dAu = X^T dU, dbg, dbu = column sums of dG, dU (or NULL),
+ *   dX = sum_i dG_i Ag_i^T + dU_i Au_i^T, one K loop over both.
+ * Gpre, Upre: the forward's, or both NULL (recomputed from X; bg and bu are
+ * read only then).  H: the forward's H when not NULL (and Gpre given), else
+ * formed here from Gpre and Upre.  dG, dU and H are rounded to bf16 before the
+ * products that read them.  Outputs dX [T x d], dAg, dAu [d x F], dB [F x d],
+ * dbg, dbu [F] bf16.  Deterministic.  Workspace: size of TPMLP_OP_GATED_BWD. */
+TPMLP_API tpmlp_status tpmlp_gated_backward(const void* X, const void* Ag, const void* Au, const void* B, const void* bg,
+                                            const void* bu, int act, const void* Gpre, const void* Upre, const void* H,
+                                            const void* dY, const tpmlp_shape* shape, void* dX, void* dAg, void* dAu,
+                                            void* dB, void* dbg, void* dbu, void* workspace, size_t workspace_bytes,
+                                            tpmlp_stream_t stream);
+
+/* The steps of the block.  Both projections with their activation and product:
+ * H = act(X Ag + bg) * (X Au + bu); Gpre, Upre NULL or [T x F] each, together. */
+TPMLP_API tpmlp_status tpmlp_gemm1_gated(const void* X, const void* Ag, const void* Au, const void* bg, const void* bu,
+                                         int act, const tpmlp_shape* shape, void* H, void* Gpre, void* Upre,
+                                         tpmlp_stream_t stream);
+
+/* dG = dH * Upre * act'(Gpre), dU = dH * act(Gpre) with dH = dY B^T; H (NULL or
+ * [T x F]) = act(Gpre) * Upre; dbg, dbu (NULL or [F]) = column sums of dG, dU before their rounding
+ * (workspace: size of TPMLP_OP_DH_GATED). */
+TPMLP_API tpmlp_status tpmlp_gemm_dh_gated(const void* dY, const void* B, const void* Gpre, const void* Upre, int act,
+                                           const tpmlp_shape* shape, void* dG, void* dU, void* H, void* dbg, void* dbu,
+                                           void* workspace, size_t workspace_bytes, tpmlp_stream_t stream);
+
+/* dX = sum_i dG_i Ag_i^T + dU_i Au_i^T.  The other gradients are tpmlp_gemm_wgrad_b (dB from H) and tpmlp_gemm_wgrad_a
+ * (dAg from dG, dAu from dU). */
+TPMLP_API tpmlp_status tpmlp_gemm_dx_gated(const void* dG, const void* dU, const void* Ag, const void* Au,
+                                           const tpmlp_shape* shape, void* dX, tpmlp_stream_t stream);
 
 /* ------------------------------------------------------------------ single steps (bf16)
  * Each step is one kernel launch (plus a small fixed-order reduction where

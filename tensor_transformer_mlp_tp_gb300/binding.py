@@ -25,7 +25,8 @@ _lib = None
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE = range(6)
 BF16, FP32 = 0, 1
 (OP_FWD, OP_SP_FWD, OP_SP_FWD_PARTIALS, OP_BWD, OP_SP_BWD, OP_DH_GELUPRIME, OP_LN_BWD, OP_SP_BLOCK_BWD,
- OP_DROPOUT_BWD, OP_SP_FWD_FP8, OP_SP_BWD_FP8) = range(11)
+ OP_DROPOUT_BWD, OP_SP_FWD_FP8, OP_SP_BWD_FP8, OP_GATED_FWD, OP_GATED_BWD, OP_DH_GATED) = range(14)
+ACT_SILU, ACT_GELU = 0, 1
 E4M3, E5M2 = 0, 1
 RS_FUSED, RS_PARTIALS = 0, 1
 
@@ -130,6 +131,14 @@ _SIGS = {
     "tpmlp_gemm_fp8_block": ([_P, ctypes.c_int, _P, _P, ctypes.c_int, _P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
                               ctypes.c_int64, _P, _P, ctypes.c_int, ctypes.c_int64, _P], ctypes.c_int),
     "tpmlp_gemm1_fp8_block": ([_P, _P, _P, _P, _P, _SP, _P, _P, _P, _P], ctypes.c_int),
+    "tpmlp_gemm1_gated": ([_P, _P, _P, _P, _P, ctypes.c_int, _SP, _P, _P, _P, _P], ctypes.c_int),
+    "tpmlp_gemm_dh_gated": ([_P, _P, _P, _P, ctypes.c_int, _SP, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+                            ctypes.c_int),
+    "tpmlp_gemm_dx_gated": ([_P, _P, _P, _P, _SP, _P, _P], ctypes.c_int),
+    "tpmlp_gated_forward": ([_P, _P, _P, _P, _P, _P, ctypes.c_int, _SP, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+                            ctypes.c_int),
+    "tpmlp_gated_backward": ([_P, _P, _P, _P, _P, _P, ctypes.c_int, _P, _P, _P, _P, _SP, _P, _P, _P, _P, _P, _P, _P,
+                              ctypes.c_size_t, _P], ctypes.c_int),
 }
 
 
@@ -849,6 +858,121 @@ def tpmlp_gemm1_fp8_block(Xq, x_scales, AqT, a_scales, bias, N, Hq, h_scales, Hp
     st = (_lib or lib()).tpmlp_gemm1_fp8_block(*args, _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise TpMlpError(fn, st)
+
+
+# ----------------------------------------------------------------------------- gated feed-forward block
+#
+# Checked like the block-scaled calls: contiguous bf16 tensors of the current device whose sizes fit one another.
+
+_KEPT_BYTES = 16 << 20  # a larger workspace is not kept for a stream: its call is long beside an allocation
+
+
+@functools.lru_cache(maxsize=256)
+def _op_workspace_size(tokens, d, ffn, n_shards, op) -> int:
+    return tpmlp_workspace_size(_shape(tokens, d, ffn, n_shards), op)
+
+
+def _call_with_workspace(fn, call, args, nbytes, dev, ws, stream):
+    """Runs call(*args, workspace, its size, stream) on the workspace that is given, or else on one of nbytes."""
+    to = _raw_stream(dev) if stream is None else _stream(stream)
+    if ws is None and nbytes <= _KEPT_BYTES:
+        with _WORKSPACE_LOCK:
+            ws = _stream_workspace(nbytes, dev, stream)
+            st = call(*args, ws.data_ptr(), ws.nbytes, to)
+    else:
+        if ws is None:
+            ws = _scratch(nbytes, torch.device("cuda", dev), stream)
+        elif ws.get_device() != dev or not ws.is_contiguous():
+            _refuse(fn)
+        st = call(*args, ws.data_ptr(), ws.nbytes, to)
+    if st:
+        raise TpMlpError(fn, st)
+
+
+def _matrix(t, rows, cols, dev, fn):
+    """Address of a contiguous bf16 matrix [rows x cols] on device `dev` (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not _BF16 or t.shape != (rows, cols) or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(fn)
+    return t.data_ptr()
+
+
+def tpmlp_gemm1_gated(X, Ag, Au, N, H, act=ACT_SILU, bg=None, bu=None, Gpre=None, Upre=None, stream=None):
+    """H = act(X Ag + bg) * (X Au + bu); Gpre, Upre = the two factors before the activation."""
+    fn = "tpmlp_gemm1_gated"
+    T, d = X.shape
+    F = Ag.shape[1]
+    dev = _device_of(X, fn)
+    args = (_matrix(X, T, d, dev, fn), _matrix(Ag, d, F, dev, fn), _matrix(Au, d, F, dev, fn),
+            _typed(bg, _BF16, F, dev, fn), _typed(bu, _BF16, F, dev, fn), act, _shape(T, d, F, N),
+            _matrix(H, T, F, dev, fn), _matrix(Gpre, T, F, dev, fn), _matrix(Upre, T, F, dev, fn))
+    st = (_lib or lib()).tpmlp_gemm1_gated(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise TpMlpError(fn, st)
+
+
+def tpmlp_gemm_dh_gated(dY, B, Gpre, Upre, N, dG, dU, act=ACT_SILU, H=None, dbg=None, dbu=None, ws=None, stream=None):
+    fn = "tpmlp_gemm_dh_gated"
+    T, d = dY.shape
+    F = B.shape[0]
+    dev = _device_of(dY, fn)
+    args = (_matrix(dY, T, d, dev, fn), _matrix(B, F, d, dev, fn), _matrix(Gpre, T, F, dev, fn),
+            _matrix(Upre, T, F, dev, fn), act, _shape(T, d, F, N), _matrix(dG, T, F, dev, fn),
+            _matrix(dU, T, F, dev, fn), _matrix(H, T, F, dev, fn), _typed(dbg, _BF16, F, dev, fn),
+            _typed(dbu, _BF16, F, dev, fn))
+    call = (_lib or lib()).tpmlp_gemm_dh_gated
+    if dbg is None and dbu is None:
+        st = call(*args, None, 0, _raw_stream(dev) if stream is None else _stream(stream))
+        if st:
+            raise TpMlpError(fn, st)
+    else:
+        _call_with_workspace(fn, call, args, _op_workspace_size(T, d, F, N, OP_DH_GATED), dev, ws, stream)
+
+
+def tpmlp_gemm_dx_gated(dG, dU, Ag, Au, N, dX, stream=None):
+    fn = "tpmlp_gemm_dx_gated"
+    T, F = dG.shape
+    d = Ag.shape[0]
+    dev = _device_of(dG, fn)
+    args = (_matrix(dG, T, F, dev, fn), _matrix(dU, T, F, dev, fn), _matrix(Ag, d, F, dev, fn),
+            _matrix(Au, d, F, dev, fn), _shape(T, d, F, N), _matrix(dX, T, d, dev, fn))
+    st = (_lib or lib()).tpmlp_gemm_dx_gated(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise TpMlpError(fn, st)
+
+
+def tpmlp_gated_forward(X, Ag, Au, B, N, Y, act=ACT_SILU, bg=None, bu=None, Gpre_out=None, Upre_out=None, H_out=None,
+                        ws=None, stream=None):
+    """Y = (act(X Ag + bg) * (X Au + bu)) B."""
+    fn = "tpmlp_gated_forward"
+    T, d = X.shape
+    F = Ag.shape[1]
+    dev = _device_of(X, fn)
+    args = (_matrix(X, T, d, dev, fn), _matrix(Ag, d, F, dev, fn), _matrix(Au, d, F, dev, fn),
+            _matrix(B, F, d, dev, fn), _typed(bg, _BF16, F, dev, fn), _typed(bu, _BF16, F, dev, fn), act,
+            _shape(T, d, F, N), _matrix(Y, T, d, dev, fn), _matrix(Gpre_out, T, F, dev, fn),
+            _matrix(Upre_out, T, F, dev, fn), _matrix(H_out, T, F, dev, fn))
+    _call_with_workspace(fn, (_lib or lib()).tpmlp_gated_forward, args, _op_workspace_size(T, d, F, N, OP_GATED_FWD),
+                         dev, ws, stream)
+    return Y
+
+
+def tpmlp_gated_backward(X, Ag, Au, B, Gpre, Upre, dY, N, dX, dAg, dAu, dB, act=ACT_SILU, bg=None, bu=None, dbg=None,
+                         dbu=None, H=None, ws=None, stream=None):
+    """The gradients of tpmlp_gated_forward; Gpre and Upre (both None: recomputed) and H (None: formed) are its own."""
+    fn = "tpmlp_gated_backward"
+    T, d = X.shape
+    F = Ag.shape[1]
+    dev = _device_of(X, fn)
+    args = (_matrix(X, T, d, dev, fn), _matrix(Ag, d, F, dev, fn), _matrix(Au, d, F, dev, fn),
+            _matrix(B, F, d, dev, fn), _typed(bg, _BF16, F, dev, fn), _typed(bu, _BF16, F, dev, fn), act,
+            _matrix(Gpre, T, F, dev, fn), _matrix(Upre, T, F, dev, fn), _matrix(H, T, F, dev, fn),
+            _matrix(dY, T, d, dev, fn), _shape(T, d, F, N), _matrix(dX, T, d, dev, fn), _matrix(dAg, d, F, dev, fn),
+            _matrix(dAu, d, F, dev, fn), _matrix(dB, F, d, dev, fn), _typed(dbg, _BF16, F, dev, fn),
+            _typed(dbu, _BF16, F, dev, fn))
+    _call_with_workspace(fn, (_lib or lib()).tpmlp_gated_backward, args, _op_workspace_size(T, d, F, N, OP_GATED_BWD),
+                         dev, ws, stream)
 
 
 def tpmlp_selftest_wait_timeout(budget_us: int, stream=None):

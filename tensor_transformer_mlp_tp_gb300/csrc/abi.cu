@@ -187,6 +187,9 @@ size_t ws_bytes(const tpmlp_shape* s, int op) {
     case TPMLP_OP_SP_BLOCK_BWD: return 3 * z.tf + z.colsum + 3 * z.td + z.lnbwd + z.dropcol;
     case TPMLP_OP_DROPOUT_BWD: return z.dropcol;
     case TPMLP_OP_SP_FWD_FP8: return 2 * z.df8 + z.td8 + z.tf8;
+    case TPMLP_OP_GATED_FWD: return z.tf;
+    case TPMLP_OP_GATED_BWD: return 5 * z.tf + 2 * z.colsum;
+    case TPMLP_OP_DH_GATED: return 2 * z.colsum;
     case TPMLP_OP_SP_BWD_FP8: return 2 * z.td + 3 * z.td8 + 2 * z.df8 + 3 * z.tf8 + z.colsum + z.lnbwd;
     default: return 0;
   }
@@ -573,6 +576,76 @@ cudaError_t backward_core(const DeviceCtx& c, const void* X, const void* A, cons
   return do_dx(c, dhpre, A, s, dX, st);
 }
 
+// The gated block's steps.
+cudaError_t do_gemm1_gated(const DeviceCtx& c, const void* X, const void* Ag, const void* Au, const void* bg,
+                           const void* bu, int act, const tpmlp_shape* s, void* H, void* Gpre, void* Upre,
+                           cudaStream_t st) {
+  GemmLaunch g;
+  g.M = static_cast<int>(s->tokens);
+  g.N = static_cast<int>(s->ffn);
+  g.K = static_cast<int>(s->d);
+  g.a = {X, s->d, false};
+  g.b = {Ag, s->ffn, true};
+  g.b2 = {Au, s->ffn, true};
+  g.epi = kEpiGated;
+  g.act = act;
+  g.out0 = H;
+  g.ld0 = s->ffn;
+  g.out1 = Gpre;
+  g.out2 = Upre;
+  g.ld1 = s->ffn;
+  g.bias = bg;
+  g.bias_u = bu;
+  return launch_gemm(g, c, st);
+}
+
+cudaError_t do_dh_gated(const DeviceCtx& c, const void* dY, const void* B, const void* Gpre, const void* Upre, int act,
+                        const tpmlp_shape* s, void* dG, void* dU, void* H, void* dbg, void* dbu, float* colsum_g,
+                        float* colsum_u, cudaStream_t st) {
+  GemmLaunch g;
+  g.M = static_cast<int>(s->tokens);
+  g.N = static_cast<int>(s->ffn);
+  g.K = static_cast<int>(s->d);
+  g.a = {dY, s->d, false};
+  g.b = {B, s->d, false};
+  g.epi = kEpiDGated;
+  g.act = act;
+  g.out0 = dG;
+  g.ld0 = s->ffn;
+  g.out1 = dU;
+  g.out2 = H;
+  g.ld1 = s->ffn;
+  g.aux = Gpre;
+  g.aux_u = Upre;
+  g.ld_aux = s->ffn;
+  g.colsum = dbg != nullptr ? colsum_g : nullptr;
+  g.colsum_u = dbu != nullptr ? colsum_u : nullptr;
+  cudaError_t e = launch_gemm(g, c, st);
+  const int rows = 4 * static_cast<int>((s->tokens + kBM - 1) / kBM), cols = static_cast<int>(s->ffn);
+  if (e == cudaSuccess && dbg != nullptr) e = launch_column_sum(colsum_g, rows, cols, dbg, true, st);
+  if (e == cudaSuccess && dbu != nullptr) e = launch_column_sum(colsum_u, rows, cols, dbu, true, st);
+  return e;
+}
+
+cudaError_t do_dx_gated(const DeviceCtx& c, const void* dG, const void* dU, const void* Ag, const void* Au,
+                        const tpmlp_shape* s, void* dX, cudaStream_t st) {
+  GemmLaunch g;
+  g.M = static_cast<int>(s->tokens);
+  g.N = static_cast<int>(s->d);
+  g.K = static_cast<int>(s->ffn);
+  g.a = {dG, s->ffn, false};
+  g.b = {Ag, s->ffn, false};
+  g.a2 = {dU, s->ffn, false};
+  g.b2 = {Au, s->ffn, false};
+  g.dual = true;
+  g.epi = kEpiStore;
+  g.out0 = dX;
+  g.ld0 = s->d;
+  return launch_gemm(g, c, st);
+}
+
+bool act_ok(int act) { return act == TPMLP_ACT_SILU || act == TPMLP_ACT_GELU; }
+
 }  // namespace
 }  // namespace tpmlp
 
@@ -601,7 +674,7 @@ tpmlp_status tpmlp_workspace_size(const tpmlp_shape* shape, int op, size_t* byte
   tpmlp_status st = check_shape(shape, sp, bf16_only);
   if (st != TPMLP_OK) return st;
   if (shape->tokens == 0) return TPMLP_OK;  // empty batch: nothing to launch, pointers may be NULL
-  if (op < TPMLP_OP_FWD || op > TPMLP_OP_SP_BWD_FP8) return TPMLP_ERR_INVALID_ARG;
+  if (op < TPMLP_OP_FWD || op > TPMLP_OP_DH_GATED) return TPMLP_ERR_INVALID_ARG;
   if ((op == TPMLP_OP_SP_FWD_FP8 || op == TPMLP_OP_SP_BWD_FP8) && (shape->d % 16 != 0 || shape->ffn % 16 != 0))
     return TPMLP_ERR_INVALID_ARG;
   if (op == TPMLP_OP_SP_BWD_FP8 && shape->tokens % 16 != 0) return TPMLP_ERR_INVALID_ARG;
@@ -1477,6 +1550,120 @@ tpmlp_status tpmlp_gemm1_fp8_block(const void* Xq, const float* x_scales, const 
   g.h_scales = h_scales;
   g.pre = Hpre;
   return cuda_status(launch_gemm_block(g, c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tpmlp_status tpmlp_gemm1_gated(const void* X, const void* Ag, const void* Au, const void* bg, const void* bu, int act,
+                               const tpmlp_shape* shape, void* H, void* Gpre, void* Upre, tpmlp_stream_t stream) {
+  tpmlp_status st = check_shape(shape, false, true);
+  if (st != TPMLP_OK) return st;
+  if (!act_ok(act)) return TPMLP_ERR_INVALID_ARG;
+  if (shape->tokens == 0) return TPMLP_OK;  // empty batch: nothing to launch, pointers may be NULL
+  if (!ptrs_ok({X, Ag, Au, H}) || !opt_ok(bg) || !opt_ok(bu) || !opt_ok(Gpre) || !opt_ok(Upre) ||
+      (Gpre == nullptr) != (Upre == nullptr))
+    return TPMLP_ERR_INVALID_ARG;
+  DeviceCtx c;
+  if ((st = device_ctx(&c)) != TPMLP_OK) return st;
+  return cuda_status(do_gemm1_gated(c, X, Ag, Au, bg, bu, act, shape, H, Gpre, Upre,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tpmlp_status tpmlp_gemm_dh_gated(const void* dY, const void* B, const void* Gpre, const void* Upre, int act,
+                                 const tpmlp_shape* shape, void* dG, void* dU, void* H, void* dbg, void* dbu,
+                                 void* workspace, size_t workspace_bytes, tpmlp_stream_t stream) {
+  tpmlp_status st = check_shape(shape, false, true);
+  if (st != TPMLP_OK) return st;
+  if (!act_ok(act)) return TPMLP_ERR_INVALID_ARG;
+  if (shape->tokens == 0) return TPMLP_OK;  // empty batch: nothing to launch, pointers may be NULL
+  if (!ptrs_ok({dY, B, Gpre, Upre, dG, dU}) || !opt_ok(H) || !opt_ok(dbg) || !opt_ok(dbu)) return TPMLP_ERR_INVALID_ARG;
+  if ((dbg != nullptr || dbu != nullptr) && (workspace == nullptr || !al16(workspace) ||
+                                             workspace_bytes < ws_bytes(shape, TPMLP_OP_DH_GATED)))
+    return TPMLP_ERR_WORKSPACE;
+  DeviceCtx c;
+  if ((st = device_ctx(&c)) != TPMLP_OK) return st;
+  const size_t colsum = sizes_of(shape).colsum;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  return cuda_status(do_dh_gated(c, dY, B, Gpre, Upre, act, shape, dG, dU, H, dbg, dbu, reinterpret_cast<float*>(w),
+                                 w == nullptr ? nullptr : reinterpret_cast<float*>(w + colsum),
+                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tpmlp_status tpmlp_gemm_dx_gated(const void* dG, const void* dU, const void* Ag, const void* Au,
+                                 const tpmlp_shape* shape, void* dX, tpmlp_stream_t stream) {
+  tpmlp_status st = check_shape(shape, false, true);
+  if (st != TPMLP_OK) return st;
+  if (shape->tokens == 0) return TPMLP_OK;  // empty batch: nothing to launch, pointers may be NULL
+  if (!ptrs_ok({dG, dU, Ag, Au, dX})) return TPMLP_ERR_INVALID_ARG;
+  DeviceCtx c;
+  if ((st = device_ctx(&c)) != TPMLP_OK) return st;
+  return cuda_status(do_dx_gated(c, dG, dU, Ag, Au, shape, dX, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tpmlp_status tpmlp_gated_forward(const void* X, const void* Ag, const void* Au, const void* B, const void* bg,
+                                 const void* bu, int act, const tpmlp_shape* shape, void* Y, void* Gpre_out,
+                                 void* Upre_out, void* H_out, void* workspace, size_t workspace_bytes,
+                                 tpmlp_stream_t stream) {
+  tpmlp_status st = check_shape(shape, false, true);
+  if (st != TPMLP_OK) return st;
+  if (!act_ok(act)) return TPMLP_ERR_INVALID_ARG;
+  if (shape->tokens == 0) return TPMLP_OK;  // empty batch: nothing to launch, pointers may be NULL
+  if (!ptrs_ok({X, Ag, Au, B, Y}) || !opt_ok(bg) || !opt_ok(bu) || !opt_ok(Gpre_out) || !opt_ok(Upre_out) ||
+      !opt_ok(H_out) || (Gpre_out == nullptr) != (Upre_out == nullptr))
+    return TPMLP_ERR_INVALID_ARG;
+  if (workspace == nullptr || !al16(workspace) || workspace_bytes < ws_bytes(shape, TPMLP_OP_GATED_FWD))
+    return TPMLP_ERR_WORKSPACE;
+  DeviceCtx c;
+  if ((st = device_ctx(&c)) != TPMLP_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  void* H = H_out != nullptr ? H_out : workspace;
+  cudaError_t e = do_gemm1_gated(c, X, Ag, Au, bg, bu, act, shape, H, Gpre_out, Upre_out, s);
+  if (e == cudaSuccess) e = do_gemm2(c, H, B, shape, Y, nullptr, s);
+  return cuda_status(e);
+}
+
+tpmlp_status tpmlp_gated_backward(const void* X, const void* Ag, const void* Au, const void* B, const void* bg,
+                                  const void* bu, int act, const void* Gpre, const void* Upre, const void* H,
+                                  const void* dY, const tpmlp_shape* shape, void* dX, void* dAg, void* dAu, void* dB,
+                                  void* dbg, void* dbu, void* workspace, size_t workspace_bytes,
+                                  tpmlp_stream_t stream) {
+  tpmlp_status st = check_shape(shape, false, true);
+  if (st != TPMLP_OK) return st;
+  if (!act_ok(act)) return TPMLP_ERR_INVALID_ARG;
+  if (shape->tokens == 0) return TPMLP_OK;  // empty batch: nothing to launch, pointers may be NULL
+  if (!ptrs_ok({X, Ag, Au, B, dY, dX, dAg, dAu, dB}) || !opt_ok(bg) || !opt_ok(bu) || !opt_ok(Gpre) || !opt_ok(Upre) ||
+      !opt_ok(H) || !opt_ok(dbg) || !opt_ok(dbu) || (Gpre == nullptr) != (Upre == nullptr))
+    return TPMLP_ERR_INVALID_ARG;
+  if (workspace == nullptr || !al16(workspace) || workspace_bytes < ws_bytes(shape, TPMLP_OP_GATED_BWD))
+    return TPMLP_ERR_WORKSPACE;
+  DeviceCtx c;
+  if ((st = device_ctx(&c)) != TPMLP_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const Sizes z = sizes_of(shape);
+  Carve ws(workspace);
+  void* dG = ws.take(z.tf);
+  void* dU = ws.take(z.tf);
+  void* h_ws = ws.take(z.tf);
+  void* g_ws = ws.take(z.tf);
+  void* u_ws = ws.take(z.tf);
+  float* colsum_g = static_cast<float*>(ws.take(z.colsum));
+  float* colsum_u = static_cast<float*>(ws.take(z.colsum));
+  cudaError_t e = cudaSuccess;
+  void* h_out = nullptr;  // H emitted by the derivatives' epilogue only when nobody supplied it
+  if (Gpre == nullptr) {
+    e = do_gemm1_gated(c, X, Ag, Au, bg, bu, act, shape, h_ws, g_ws, u_ws, s);
+    Gpre = g_ws;
+    Upre = u_ws;
+    H = h_ws;
+  } else if (H == nullptr) {
+    h_out = h_ws;
+    H = h_ws;
+  }
+  if (e == cudaSuccess)
+    e = do_dh_gated(c, dY, B, Gpre, Upre, act, shape, dG, dU, h_out, dbg, dbu, colsum_g, colsum_u, s);
+  if (e == cudaSuccess) e = do_wgrad_b(c, H, dY, shape, dB, s);
+  if (e == cudaSuccess) e = do_wgrad_a(c, X, dG, shape, dAg, s);
+  if (e == cudaSuccess) e = do_wgrad_a(c, X, dU, shape, dAu, s);
+  if (e == cudaSuccess) e = do_dx_gated(c, dG, dU, Ag, Au, shape, dX, s);
+  return cuda_status(e);
 }
 
 }  // extern "C"

@@ -44,7 +44,14 @@ enum Epilogue : int {
                       // out1 (optional) = bf16(acc + bias)
   kEpiDGeluQ = 5,     // g = acc * GeLU'(aux): out0 = E5M2(g * scale_out), amax_out = max |g|, optional
                       // column sums of g
+  kEpiGated = 6,      // two products G, U of one tile: out0 = bf16(act(G + bias) * (U + bias_u)); out1, out2
+                      // (optional) = bf16(G + bias), bf16(U + bias_u)
+  kEpiDGated = 7,     // d = acc, G = aux, U = aux_u: out0 = bf16(d * U * act'(G)), out1 = bf16(d * act(G)),
+                      // out2 (optional) = bf16(act(G) * U); optional column sums of the first two
 };
+
+// Activations of the gated epilogues.
+constexpr int kActSilu = 0, kActGelu = 1;
 
 struct ChunkPtrs {
   void* p[kMaxShards];
@@ -63,7 +70,10 @@ struct GemmParams {
   CUtensorMap tmC0;         // out0 / out1 as [M x N] bf16, 32 x 32 boxes, 64-byte swizzle (tma_out bits 0 / 1)
   CUtensorMap tmC1;
   CUtensorMap tmB_half;     // K-major B with boxes of a quarter tile's columns (half tiles of the pair kernel)
-  int tma_out;              // bit 0: out0 rows leave through TMA box stores, bit 1: out1 too
+  CUtensorMap tmA_2;        // the second product's operands: kEpiGated the up projection (tmB_2), a sum of two products
+  CUtensorMap tmB_2;        // both
+  CUtensorMap tmC2;         // out2
+  int tma_out;              // bits 0, 1, 2: out0, out1, out2 leave through TMA box stores
   int M, N, K;
   int m_blocks, n_blocks;
   int k_blocks_per_shard;   // k-blocks summed into one accumulator
@@ -99,6 +109,13 @@ struct GemmParams {
   const float* scale_out;
   float* amax_out;
   int a_fmt, b_fmt;           // 8-bit operand formats (0 = E4M3, 1 = E5M2)
+  // Gated epilogues.
+  int act;                    // kActSilu, kActGelu
+  void* out2;                 // row strides of out1 and out2 are ld1
+  const void* bias_u;         // [N] bf16 or nullptr
+  const void* aux_u;          // U; the row stride is ld_aux
+  float* colsum_u;            // column partial sums of out1, as colsum
+  int k_first;                // a sum of two products: k-blocks of the first
   unsigned int* err;
   unsigned long long timeout_ns;
 };

@@ -24,6 +24,7 @@ constexpr int kShortK = 2048;    // at or below: the GeLU epilogue runs balanced
 // warps equal, 6 warps 10% slower), 6 for the FP8 quantising epilogues (10 and 14 measured slower).
 constexpr int kBalWarps = 10;
 constexpr int kBalFp8 = 6;
+constexpr int kBalGated = 8;  // the gated epilogues: two warps a TMEM lane quadrant
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -103,10 +104,10 @@ bool half_map_ok(const GemmParams& p) {
   return false;
 }
 
-template <int BN, bool AMN, bool BMN, int EPI, bool FP8 = false, int BAL = 0>
+template <int BN, bool AMN, bool BMN, int EPI, bool FP8 = false, int BAL = 0, bool DUAL = false>
 cudaError_t run_pair(GemmParams p, cudaStream_t s) {
   using S = PairShape<BN, kPairStages, kEpiWarps, BAL>;
-  auto kern = k_gemm_tc2<BN, AMN, BMN, EPI, kPairStages, kEpiWarps, FP8, BAL>;
+  auto kern = k_gemm_tc2<BN, AMN, BMN, EPI, kPairStages, kEpiWarps, FP8, BAL, DUAL>;
   constexpr int kThreads = S::kThreads;
   static std::atomic<int> cache[64] = {};  // co-resident pairs per device (concurrent callers store the same value)
   int dev = 0;
@@ -121,7 +122,7 @@ cudaError_t run_pair(GemmParams p, cudaStream_t s) {
   // A last wave of whole tiles that would leave more than half of the pairs idle runs as one round of
   // half-width tiles instead (each pair then finishes its share in half a tile's time).
   const long long rem = tiles % pairs;
-  if (BN == kBN && p.shards == 1 && rem != 0 && 2 * rem <= pairs && (BMN || half_map_ok(p))) {
+  if (BN == kBN && EPI != kEpiGated && !DUAL && p.shards == 1 && rem != 0 && 2 * rem <= pairs && (BMN || half_map_ok(p))) {
     p.full_units = static_cast<int>(tiles - rem);
     units = tiles + rem;
   }
@@ -211,6 +212,59 @@ static cudaError_t launch_gemm_fp8(const GemmLaunch& g, const DeviceCtx& ctx, cu
   }
 }
 
+// The gated block's products, on CTA pairs whatever M is: G and U of one tile with their epilogue (kEpiGated), dH with
+// both derivatives (kEpiDGated), and the sum of two products (dual).
+static cudaError_t launch_gemm_gated(const GemmLaunch& g, const DeviceCtx& ctx, cudaStream_t s) {
+  GemmParams p;
+  memset(&p, 0, sizeof(p));
+  const bool gated = g.epi == kEpiGated;
+  const int tile_cols = gated ? kBN / 2 : kBN;
+  // the operands: X [M x K] and [K x N] weights (gated); rows of K both (the derivatives and the dual product)
+  bool ok = make_map(&p.tmA, g.a.ptr, g.K, g.M, g.a.ld, kBK, kBM);
+  if (gated) {
+    ok = ok && make_map(&p.tmB, g.b.ptr, g.N, g.K, g.b.ld, 64, kBK) && make_map(&p.tmB_2, g.b2.ptr, g.N, g.K, g.b2.ld, 64, kBK);
+  } else {
+    ok = ok && make_map(&p.tmB, g.b.ptr, g.K, g.N, g.b.ld, kBK, kBN / 2);
+    if (g.dual)
+      ok = ok && make_map(&p.tmA_2, g.a2.ptr, g.K, g.M, g.a2.ld, kBK, kBM) &&
+           make_map(&p.tmB_2, g.b2.ptr, g.K, g.N, g.b2.ld, kBK, kBN / 2);
+    else
+      ok = ok && make_map(&p.tmB_half, g.b.ptr, g.K, g.N, g.b.ld, kBK, kBN / 4);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  p.M = g.M;
+  p.N = g.N;
+  p.K = g.K;
+  p.m_blocks = (g.M + 2 * kBM - 1) / (2 * kBM);
+  p.n_blocks = (g.N + tile_cols - 1) / tile_cols;
+  p.shards = 1;
+  p.k_first = (g.K + kBK - 1) / kBK;
+  p.k_blocks_per_shard = (g.dual ? 2 : 1) * p.k_first;
+  p.group_m = kGroupM / 2;
+  p.out0 = g.out0;
+  p.ld0 = g.ld0;
+  p.out1 = g.out1;
+  p.out2 = g.out2;
+  p.ld1 = g.ld1;
+  p.bias = g.bias;
+  p.bias_u = g.bias_u;
+  p.aux = g.aux;
+  p.aux_u = g.aux_u;
+  p.ld_aux = g.ld_aux;
+  p.colsum = g.colsum;
+  p.colsum_u = g.colsum_u;
+  p.act = g.act;
+  p.err = ctx.err;
+  p.timeout_ns = ctx.timeout_ns;
+  constexpr CUtensorMapSwizzle kSw = CU_TENSOR_MAP_SWIZZLE_64B;
+  if (make_map(&p.tmC0, g.out0, g.N, g.M, g.ld0, 32, 32, false, kSw)) p.tma_out |= 1;
+  if (g.out1 != nullptr && make_map(&p.tmC1, g.out1, g.N, g.M, g.ld1, 32, 32, false, kSw)) p.tma_out |= 2;
+  if (g.out2 != nullptr && make_map(&p.tmC2, g.out2, g.N, g.M, g.ld1, 32, 32, false, kSw)) p.tma_out |= 4;
+  if (gated) return run_pair<kBN, false, true, kEpiGated, false, kBalGated>(p, s);
+  if (g.dual) return run_pair<kBN, false, false, kEpiStore, false, kBalWarps, true>(p, s);
+  return run_pair<kBN, false, false, kEpiDGated, false, kBalGated>(p, s);
+}
+
 cudaError_t gemm_bounds_status(unsigned int* count, unsigned int* site) {
 #ifdef TPMLP_DEBUG_BOUNDS
   return bounds_read_and_clear(count, site);
@@ -223,6 +277,7 @@ cudaError_t gemm_bounds_status(unsigned int* count, unsigned int* site) {
 cudaError_t launch_gemm(const GemmLaunch& g, const DeviceCtx& ctx, cudaStream_t s) {
   if (g.M <= 0 || g.N <= 0 || g.K <= 0) return cudaSuccess;
   if (g.fp8) return launch_gemm_fp8(g, ctx, s);
+  if (g.epi == kEpiGated || g.epi == kEpiDGated || g.dual) return launch_gemm_gated(g, ctx, s);
   GemmParams p;
   memset(&p, 0, sizeof(p));
   // A operand (the M side): box of 128 rows x 64 k (K-major) or 64 m x 64 k rows (MN-major).

@@ -35,6 +35,7 @@
 // first global access.
 #pragma once
 
+#include "gated.cuh"
 #include "gemm_tc.cuh"
 
 namespace tpmlp {
@@ -80,12 +81,19 @@ __device__ __forceinline__ void unit_of(const GemmParams& p, int u, int& tile, i
 // spread evenly over all four SM sub-partitions (for epilogue-bound launches: short K or the FP8 rate);
 // BAL = 0: the two warps on the TMA and MMA sub-partitions only copy TMEM to shared memory for the
 // two helper warps.
-template <int BN, bool A_MN, bool B_MN, int EPI, int STAGES, int EPI_WARPS, bool FP8 = false, int BAL = 0>
+// kEpiGated: a tile is BN / 2 output columns.  The UMMA's first BN / 2 columns are the gate projection's, loaded by the
+// even CTA, the others the up projection's, loaded by the odd one, so that each CTA's TMEM holds both factors of its 128
+// rows and the epilogue multiplies them.
+// DUAL: the k-blocks of a second product (tmA_2, tmB_2) follow the first one's into the same sums.
+template <int BN, bool A_MN, bool B_MN, int EPI, int STAGES, int EPI_WARPS, bool FP8 = false, int BAL = 0,
+          bool DUAL = false>
 __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS, 1)
     k_gemm_tc2(const __grid_constant__ GemmParams p) {
   static_assert(!FP8 || (!A_MN && !B_MN), "FP8 operands are K-major");
   static_assert(FP8 || (EPI != kEpiBiasGeluQ && EPI != kEpiDGeluQ), "the quantising epilogues follow FP8 operands");
-  constexpr bool kAux = EPI == kEpiDGelu || EPI == kEpiDGeluQ;  // reads the pre-activation tile
+  constexpr bool kGated = EPI == kEpiGated;
+  static_assert((!kGated && EPI != kEpiDGated) || (BAL > 0 && !FP8), "the gated epilogues are balanced ones, bf16");
+  constexpr bool kAux = EPI == kEpiDGelu || EPI == kEpiDGeluQ || EPI == kEpiDGated;  // reads the pre-activation tile
   // FP8 GEMMs with a GeLU / GeLU' epilogue are epilogue-bound at the doubled MMA rate: there every epilogue
   // warp reads TMEM itself and the math is spread over all four SM sub-partitions (see the epilogue).
   static_assert(BAL == 0 || (BAL >= 4 && BAL <= 14), "balanced epilogue: 4 to 14 warps");
@@ -135,9 +143,12 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&p.tmA);
     tma_prefetch_desc(&p.tmB);
-    if (!B_MN && p.full_units < p.m_blocks * p.n_blocks * p.shards) tma_prefetch_desc(&p.tmB_half);
+    if (kGated || DUAL) tma_prefetch_desc(&p.tmB_2);
+    if (DUAL) tma_prefetch_desc(&p.tmA_2);
+    if (!B_MN && !kGated && p.full_units < p.m_blocks * p.n_blocks * p.shards) tma_prefetch_desc(&p.tmB_half);
     if (p.tma_out & 1) tma_prefetch_desc(&p.tmC0);
     if (p.tma_out & 2) tma_prefetch_desc(&p.tmC1);
+    if (p.tma_out & 4) tma_prefetch_desc(&p.tmC2);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, S::kTmemCols);
@@ -176,7 +187,8 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
         tile_coords(p, tile, shard, mb, nb);
         const int kb0 = shard * p.k_blocks_per_shard;
         const int m0 = mb * 256 + static_cast<int>(rank) * 128;
-        const int n0 = nb * BN + col_off + static_cast<int>(rank) * (width / 2);  // this CTA's half of the columns
+        // this CTA's half of the columns
+        const int n0 = kGated ? nb * (BN / 2) : nb * BN + col_off + static_cast<int>(rank) * (width / 2);
         const uint32_t stage_bytes = static_cast<uint32_t>(S::kATile + (width / 2) * kBK * 2);
         for (int kb = 0; kb < p.k_blocks_per_shard; ++kb) {
           if (!wait_bounded(empty + stage, phase ^ 1u, wc, kSiteProducerEmpty)) {
@@ -185,20 +197,23 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
           }
           if (leader) mbar_arrive_expect_tx(full + stage, 2 * stage_bytes);
           const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
-          const int k0 = (kb0 + kb) * kKElems;
+          const bool second = DUAL && kb >= p.k_first;  // DUAL: one shard, kb0 = 0
+          const int k0 = (kb0 + kb - (second ? p.k_first : 0)) * kKElems;
           uint8_t* a_dst = sA + stage * S::kATile;
           uint8_t* b_dst = sB + stage * S::kBTile;
+          const CUtensorMap* map_a = second ? &p.tmA_2 : &p.tmA;
+          const CUtensorMap* map_b = second || (kGated && rank == 1) ? &p.tmB_2 : &p.tmB;
           if constexpr (!A_MN) {
-            tma_load_2d_pair(a_dst, &p.tmA, bar, k0, m0, pol_a);
+            tma_load_2d_pair(a_dst, map_a, bar, k0, m0, pol_a);
           } else {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) tma_load_2d_pair(a_dst + j * 64 * kBK * 2, &p.tmA, bar, m0 + 64 * j, k0, pol_a);
+            for (int j = 0; j < 2; ++j) tma_load_2d_pair(a_dst + j * 64 * kBK * 2, map_a, bar, m0 + 64 * j, k0, pol_a);
           }
           if constexpr (!B_MN) {
-            tma_load_2d_pair(b_dst, width == BN ? &p.tmB : &p.tmB_half, bar, k0, n0, pol_b);
+            tma_load_2d_pair(b_dst, DUAL || width == BN ? map_b : &p.tmB_half, bar, k0, n0, pol_b);
           } else {
             for (int j = 0; j < width / 128; ++j)  // 64-column boxes
-              tma_load_2d_pair(b_dst + j * 64 * kBK * 2, &p.tmB, bar, n0 + 64 * j, k0, pol_b);
+              tma_load_2d_pair(b_dst + j * 64 * kBK * 2, map_b, bar, n0 + 64 * j, k0, pol_b);
           }
           issued |= 1u << stage;
           issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -277,8 +292,9 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
     const int first = quad >= 2 ? quad : quad + 4;  // lowest epilogue warp of this quadrant
     const int n_quad = (BAL + 2 - first + 3) / 4;    // epilogue warps of this quadrant
     const int i_quad = (warp - first) / 4;
-    const int c_begin = 32 * (i_quad * (BN / 32) / n_quad);
-    const int c_end = 32 * ((i_quad + 1) * (BN / 32) / n_quad);
+    constexpr int kOutCols = kGated ? BN / 2 : BN;
+    const int c_begin = 32 * (i_quad * (kOutCols / 32) / n_quad);
+    const int c_end = 32 * ((i_quad + 1) * (kOutCols / 32) / n_quad);
     uint8_t* sbuf = store_bufs + (warp - 2) * S::kStoreBuf;
     EpiState est{1.f, 1.f, 0.f};
     if constexpr (FP8) est.descale = 1.f / (__ldg(p.scale_a) * __ldg(p.scale_b));
@@ -289,7 +305,7 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
       unit_of<BN>(p, u, tile, col_off, width);
       int shard, mb, nb;
       tile_coords(p, tile, shard, mb, nb);
-      const int n_base = nb * BN + col_off;     // the unit's first output column
+      const int n_base = nb * kOutCols + col_off;     // the unit's first output column
       const int c_stop = min(c_end, width);     // this warp's chunks within the unit
       const int acc = local & 1;
       const uint32_t acc_phase = (local >> 1) & 1;
@@ -303,6 +319,9 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
         const int ncols = min(c_stop - c_begin, p.N - pcol);
         if (row < p.M && ncols > 0)
           prefetch_l2_bulk(static_cast<const __nv_bfloat16*>(p.aux) + static_cast<long long>(row) * p.ld_aux + pcol,
+                           static_cast<uint32_t>(ncols) * 2u);
+        if (EPI == kEpiDGated && row < p.M && ncols > 0)
+          prefetch_l2_bulk(static_cast<const __nv_bfloat16*>(p.aux_u) + static_cast<long long>(row) * p.ld_aux + pcol,
                            static_cast<uint32_t>(ncols) * 2u);
       }
       int ok = 1;
@@ -325,7 +344,18 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
         }
         float v[32];
         tmem_load_32cols(trow + static_cast<uint32_t>(c), v);
-        epilogue_32<EPI>(p, v, aux_cur, row, n_base + c, shard, mb128, quad, lane, est, sbuf);
+        if constexpr (kGated) {
+          float u[32];
+          tmem_load_32cols(trow + static_cast<uint32_t>(BN / 2 + c), u);
+          gated_epilogue_32(p, v, u, row, n_base + c, lane, sbuf);
+        } else if constexpr (EPI == kEpiDGated) {
+          uint4 u_raw[4];
+          load_raw32(static_cast<const __nv_bfloat16*>(p.aux_u) + (aux_row - static_cast<const __nv_bfloat16*>(p.aux)),
+                     n_base + c, p.N, row < p.M, u_raw);
+          dgated_epilogue_32(p, v, aux_cur, u_raw, row, n_base + c, mb128, quad, lane, sbuf);
+        } else {
+          epilogue_32<EPI>(p, v, aux_cur, row, n_base + c, shard, mb128, quad, lane, est, sbuf);
+        }
       }
       tc_fence_before_sync();
       __syncwarp();

@@ -54,6 +54,15 @@ struct GemmLaunch {
   const float* scale_out = nullptr;  // kEpiBiasGeluQ, kEpiDGeluQ
   float* amax_out = nullptr;         // kEpiBiasGeluQ, kEpiDGeluQ
   int a_fmt = 0, b_fmt = 0;          // 0 = E4M3, 1 = E5M2
+  // Gated epilogues (out1, out2 share ld1; aux, aux_u share ld_aux), and a second product of the same M, N, K added into
+  // the first one's sum (kEpiStore, `dual`)
+  Operand a2{}, b2{};
+  bool dual = false;
+  int act = kActSilu;
+  void* out2 = nullptr;
+  const void* bias_u = nullptr;
+  const void* aux_u = nullptr;
+  float* colsum_u = nullptr;
 };
 
 // Tensor map of a row-major matrix of `outer` rows of `inner` elements, `ld` elements apart; copies fill zeros out of
