@@ -531,6 +531,48 @@ TPMLP_API tpmlp_status tpmlp_gemm_dh_gated(const void* dY, const void* B, const 
 TPMLP_API tpmlp_status tpmlp_gemm_dx_gated(const void* dG, const void* dU, const void* Ag, const void* Au,
                                            const tpmlp_shape* shape, void* dX, tpmlp_stream_t stream);
 
+/* ------------------------------------------------------------------ 4-bit weights
+ * For decoded tokens, whose time is that of reading the weights: a matrix W
+ * [K x N] (math layout, as A and B) stands for (q - z) s, with a code q in 0..15
+ * for each element and a bf16 scale s and a zero point z for each group of 32,
+ * 64 or 128 consecutive rows of a column (the last group may be shorter):
+ *   scales [G x N] bf16, zeros [G x N] bytes or NULL (z = 8), G = ceil(K / group).
+ * Codes Q: tiles of 16 columns x 64 rows, 512 bytes each, tile (nt, kt) at
+ * nt ceil(K / 64) + kt; in a tile, with column 8 c + g (g < 8) and row
+ * 16 j + 8 r + 2 t + h (t < 4, h < 2), the code is in 32-bit word
+ * 4 (4 g + t) + j, bits 4 (c + 2 r) + 16 h and up.  512 ceil(N / 16) ceil(K / 64)
+ * bytes; places past K or N hold 8.  (The pages have no counterpart.)
+ *   N % 8 == 0, K % 8 == 0, pointers 16-byte aligned. */
+
+/* Q, scales and (when not NULL) zeros of W [K x N] bf16, per group:
+ *   zeros == NULL:  s = bf16(a / 7), a the largest magnitude, z = 8;
+ *   zeros != NULL:  s = bf16((hi - lo) / 15) with lo = min(0, least value) and
+ *                   hi = max(0, largest), z = rint(-lo / s) within 0..15;
+ *   q = rint(w / s) + z within 0..15, halves to even.
+ * Range and quotients in fp32; a and hi - lo are kept within 2^-100 and bf16's
+ * largest number.  A NaN counts as 0; an infinity takes an end of the codes. */
+TPMLP_API tpmlp_status tpmlp_quantize_w4(const void* W, int64_t K, int64_t N, int group, void* Q, void* scales,
+                                         uint8_t* zeros, tpmlp_stream_t stream);
+
+/* The inverse: W = bf16((q - z) s), for the bf16 products of a long prompt. */
+TPMLP_API tpmlp_status tpmlp_dequantize_w4(const void* Q, const void* scales, const uint8_t* zeros, int64_t K, int64_t N,
+                                           int group, void* W, tpmlp_stream_t stream);
+
+/* Y [M x N] bf16 = X [M x K] W + bias (bias [N] bf16 or NULL): per group the sum
+ * of x (q - z), exact products in fp32, is scaled as a whole and added to an
+ * fp32 sum, so the weights are never rounded.  Any M; made for up to a few
+ * hundred tokens.  M or N == 0 is an empty call; K == 0 is an error. */
+TPMLP_API tpmlp_status tpmlp_gemm_w4(const void* X, const void* Q, const void* scales, const uint8_t* zeros,
+                                     const void* bias, int64_t M, int64_t N, int64_t K, int group, void* Y,
+                                     tpmlp_stream_t stream);
+
+/* tpmlp_gemm1_gated on 4-bit weights: H = act(X Wg + bg) * (X Wu + bu), Wg and Wu
+ * [d x F] with the same group and both with zero points or both without. */
+TPMLP_API tpmlp_status tpmlp_gemm1_gated_w4(const void* X, const void* Qg, const void* g_scales, const uint8_t* g_zeros,
+                                            const void* bg, const void* Qu, const void* u_scales,
+                                            const uint8_t* u_zeros, const void* bu, int act, int group,
+                                            const tpmlp_shape* shape, void* H, tpmlp_stream_t stream);
+
 /* ------------------------------------------------------------------ single steps (bf16)
  * Each step is one kernel launch (plus a small fixed-order reduction where
  * noted); the block calls above are sequences of these.  They take explicit

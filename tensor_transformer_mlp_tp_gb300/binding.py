@@ -139,6 +139,12 @@ _SIGS = {
                             ctypes.c_int),
     "tpmlp_gated_backward": ([_P, _P, _P, _P, _P, _P, ctypes.c_int, _P, _P, _P, _P, _SP, _P, _P, _P, _P, _P, _P, _P,
                               ctypes.c_size_t, _P], ctypes.c_int),
+    "tpmlp_quantize_w4": ([_P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, _P, _P, _P, _P], ctypes.c_int),
+    "tpmlp_dequantize_w4": ([_P, _P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, _P, _P], ctypes.c_int),
+    "tpmlp_gemm_w4": ([_P, _P, _P, _P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, _P, _P],
+                      ctypes.c_int),
+    "tpmlp_gemm1_gated_w4": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_int, _SP, _P, _P],
+                             ctypes.c_int),
 }
 
 
@@ -973,6 +979,80 @@ def tpmlp_gated_backward(X, Ag, Au, B, Gpre, Upre, dY, N, dX, dAg, dAu, dB, act=
             _typed(dbu, _BF16, F, dev, fn))
     _call_with_workspace(fn, (_lib or lib()).tpmlp_gated_backward, args, _op_workspace_size(T, d, F, N, OP_GATED_BWD),
                          dev, ws, stream)
+
+
+# ----------------------------------------------------------------------------- 4-bit weights
+
+def w4_codes_shape(K, N):
+    """Shape of the codes (uint8) of a 4-bit matrix [K x N]."""
+    return ((N + 15) >> 4, (K + 63) >> 6, 512)
+
+
+def w4_groups(K, group):
+    """Groups along K: scales (bf16) and zero points (uint8) are [groups x N]."""
+    return (K + group - 1) // group
+
+
+def _w4(Q, scales, zeros, K, N, group, dev, fn):
+    """Addresses of a 4-bit matrix's codes, scales and zero points."""
+    if group not in (32, 64, 128):
+        _refuse(fn)
+    n = (K + group - 1) // group * N
+    return (_typed(Q, _U8, ((N + 15) >> 4) * ((K + 63) >> 6) * 512, dev, fn), _typed(scales, _BF16, n, dev, fn),
+            _typed(zeros, _U8, n, dev, fn))
+
+
+def tpmlp_quantize_w4(W, group, Q, scales, zeros=None, stream=None):
+    """4-bit codes, scales and (optional) zero points of W [K x N] bf16."""
+    fn = "tpmlp_quantize_w4"
+    K, N = W.shape
+    dev = _device_of(W, fn)
+    st = (_lib or lib()).tpmlp_quantize_w4(_matrix(W, K, N, dev, fn), K, N, group,
+                                           *_w4(Q, scales, zeros, K, N, group, dev, fn),
+                                           _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise TpMlpError(fn, st)
+
+
+def tpmlp_dequantize_w4(Q, scales, group, W, zeros=None, stream=None):
+    """W [K x N] bf16 of a 4-bit matrix."""
+    fn = "tpmlp_dequantize_w4"
+    K, N = W.shape
+    dev = _device_of(W, fn)
+    st = (_lib or lib()).tpmlp_dequantize_w4(*_w4(Q, scales, zeros, K, N, group, dev, fn), K, N, group,
+                                             _matrix(W, K, N, dev, fn),
+                                             _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise TpMlpError(fn, st)
+
+
+def tpmlp_gemm_w4(X, Q, scales, group, Y, zeros=None, bias=None, stream=None):
+    """Y [M x N] = X [M x K] W + bias with a 4-bit W."""
+    fn = "tpmlp_gemm_w4"
+    M, K = X.shape
+    N = Y.shape[1]
+    dev = _device_of(X, fn)
+    q, s, z = _w4(Q, scales, zeros, K, N, group, dev, fn)
+    st = (_lib or lib()).tpmlp_gemm_w4(_matrix(X, M, K, dev, fn), q, s, z, _typed(bias, _BF16, N, dev, fn), M, N, K, group,
+                                       _matrix(Y, M, N, dev, fn),
+                                       _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise TpMlpError(fn, st)
+
+
+def tpmlp_gemm1_gated_w4(X, Qg, g_scales, Qu, u_scales, group, H, N=1, act=ACT_SILU, g_zeros=None, u_zeros=None, bg=None,
+                         bu=None, stream=None):
+    """H [T x F] = act(X Wg + bg) * (X Wu + bu) with 4-bit Wg, Wu [d x F]."""
+    fn = "tpmlp_gemm1_gated_w4"
+    T, d = X.shape
+    F = H.shape[1]
+    dev = _device_of(X, fn)
+    args = (_matrix(X, T, d, dev, fn), *_w4(Qg, g_scales, g_zeros, d, F, group, dev, fn), _typed(bg, _BF16, F, dev, fn),
+            *_w4(Qu, u_scales, u_zeros, d, F, group, dev, fn), _typed(bu, _BF16, F, dev, fn), act, group,
+            _shape(T, d, F, N), _matrix(H, T, F, dev, fn))
+    st = (_lib or lib()).tpmlp_gemm1_gated_w4(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise TpMlpError(fn, st)
 
 
 def tpmlp_selftest_wait_timeout(budget_us: int, stream=None):

@@ -12,6 +12,7 @@
 #include "block_fp8.h"
 #include "launch.h"
 #include "ptx.cuh"
+#include "w4.h"
 
 namespace tpmlp {
 
@@ -696,19 +697,22 @@ tpmlp_status tpmlp_get_device_status(tpmlp_stream_t stream, uint32_t* site) {
 
 tpmlp_status tpmlp_debug_bounds_status(int32_t* checked, uint32_t* violations, uint32_t* first_site) {
   if (checked == nullptr || violations == nullptr || first_site == nullptr) return TPMLP_ERR_INVALID_ARG;
-  unsigned int c[4] = {0, 0, 0, 0}, site[4] = {0, 0, 0, 0};
+  unsigned int c[5] = {}, site[5] = {};
   if (cudaDeviceSynchronize() != cudaSuccess) return TPMLP_ERR_CUDA;
   if (rowwise_bounds_status(&c[0], &site[0]) != cudaSuccess || gemm_bounds_status(&c[1], &site[1]) != cudaSuccess ||
       block_rows_bounds_status(&c[2], &site[2]) != cudaSuccess ||
-      gemm_block_bounds_status(&c[3], &site[3]) != cudaSuccess)
+      gemm_block_bounds_status(&c[3], &site[3]) != cudaSuccess || w4_bounds_status(&c[4], &site[4]) != cudaSuccess)
     return TPMLP_ERR_CUDA;
 #ifdef TPMLP_DEBUG_BOUNDS
   *checked = 1;
 #else
   *checked = 0;
 #endif
-  *violations = c[0] + c[1] + c[2] + c[3];
-  *first_site = site[0] != 0 ? site[0] : site[1] != 0 ? site[1] : site[2] != 0 ? site[2] : site[3];
+  *violations = *first_site = 0;
+  for (int i = 0; i < 5; ++i) {
+    *violations += c[i];
+    if (*first_site == 0) *first_site = site[i];
+  }
   return TPMLP_OK;
 }
 
@@ -1664,6 +1668,84 @@ tpmlp_status tpmlp_gated_backward(const void* X, const void* Ag, const void* Au,
   if (e == cudaSuccess) e = do_wgrad_a(c, X, dU, shape, dAu, s);
   if (e == cudaSuccess) e = do_dx_gated(c, dG, dU, Ag, Au, shape, dX, s);
   return cuda_status(e);
+}
+
+// Sizes and operands of the calls on 4-bit weights.
+static tpmlp_status check_w4(int64_t M, int64_t N, int64_t K, int group) {
+  if (M < 0 || N < 0 || K < 0 || N % 8 != 0 || K % 8 != 0 || (group != 32 && group != 64 && group != 128))
+    return TPMLP_ERR_INVALID_ARG;
+  if (M > INT_MAX / 2 || N > INT_MAX / 2 || K > INT_MAX / 2) return TPMLP_ERR_UNSUPPORTED;
+  return TPMLP_OK;
+}
+
+tpmlp_status tpmlp_quantize_w4(const void* W, int64_t K, int64_t N, int group, void* Q, void* scales, uint8_t* zeros,
+                               tpmlp_stream_t stream) {
+  const tpmlp_status st = check_w4(0, N, K, group);
+  if (st != TPMLP_OK) return st;
+  if (N == 0 || K == 0) return TPMLP_OK;
+  if (!ptrs_ok({W, Q, scales}) || !opt_ok(zeros)) return TPMLP_ERR_INVALID_ARG;
+  if ((K + kW4Rows - 1) / kW4Rows > 65535 / 2) return TPMLP_ERR_UNSUPPORTED;
+  const W4Pack p{const_cast<void*>(W), static_cast<uint4*>(Q), scales, zeros, static_cast<int>(K), static_cast<int>(N), group};
+  return cuda_status(launch_quantize_w4(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tpmlp_status tpmlp_dequantize_w4(const void* Q, const void* scales, const uint8_t* zeros, int64_t K, int64_t N, int group,
+                                 void* W, tpmlp_stream_t stream) {
+  const tpmlp_status st = check_w4(0, N, K, group);
+  if (st != TPMLP_OK) return st;
+  if (N == 0 || K == 0) return TPMLP_OK;
+  if (!ptrs_ok({W, Q, scales}) || !opt_ok(zeros)) return TPMLP_ERR_INVALID_ARG;
+  if ((K + kW4Rows - 1) / kW4Rows > 65535 / 2) return TPMLP_ERR_UNSUPPORTED;
+  const W4Pack p{W, static_cast<uint4*>(const_cast<void*>(Q)), const_cast<void*>(scales), const_cast<uint8_t*>(zeros),
+                 static_cast<int>(K), static_cast<int>(N), group};
+  return cuda_status(launch_dequantize_w4(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tpmlp_status tpmlp_gemm_w4(const void* X, const void* Q, const void* scales, const uint8_t* zeros, const void* bias,
+                           int64_t M, int64_t N, int64_t K, int group, void* Y, tpmlp_stream_t stream) {
+  tpmlp_status st = check_w4(M, N, K, group);
+  if (st != TPMLP_OK) return st;
+  if (M == 0 || N == 0) return TPMLP_OK;
+  if (!ptrs_ok({X, Q, scales, Y}) || !opt_ok(zeros) || !opt_ok(bias) || K == 0) return TPMLP_ERR_INVALID_ARG;
+  DeviceCtx c;
+  if ((st = device_ctx(&c)) != TPMLP_OK) return st;
+  W4Launch g{};
+  g.x = X;
+  g.w[0] = {static_cast<const uint4*>(Q), scales, zeros, bias};
+  g.y = Y;
+  g.M = static_cast<int>(M);
+  g.N = static_cast<int>(N);
+  g.K = static_cast<int>(K);
+  g.group = group;
+  return cuda_status(launch_gemm_w4(g, c, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tpmlp_status tpmlp_gemm1_gated_w4(const void* X, const void* Qg, const void* g_scales, const uint8_t* g_zeros,
+                                  const void* bg, const void* Qu, const void* u_scales, const uint8_t* u_zeros,
+                                  const void* bu, int act, int group, const tpmlp_shape* shape, void* H,
+                                  tpmlp_stream_t stream) {
+  tpmlp_status st = check_shape(shape, false, true);
+  if (st != TPMLP_OK) return st;
+  if ((st = check_w4(shape->tokens, shape->ffn, shape->d, group)) != TPMLP_OK) return st;
+  if (!act_ok(act)) return TPMLP_ERR_INVALID_ARG;
+  if (shape->tokens == 0) return TPMLP_OK;  // empty batch: nothing to launch, pointers may be NULL
+  if (!ptrs_ok({X, Qg, g_scales, Qu, u_scales, H}) || !opt_ok(g_zeros) || !opt_ok(u_zeros) || !opt_ok(bg) ||
+      !opt_ok(bu) || (g_zeros == nullptr) != (u_zeros == nullptr))
+    return TPMLP_ERR_INVALID_ARG;
+  DeviceCtx c;
+  if ((st = device_ctx(&c)) != TPMLP_OK) return st;
+  W4Launch g{};
+  g.x = X;
+  g.w[0] = {static_cast<const uint4*>(Qg), g_scales, g_zeros, bg};
+  g.w[1] = {static_cast<const uint4*>(Qu), u_scales, u_zeros, bu};
+  g.gated = true;
+  g.act = act;
+  g.y = H;
+  g.M = static_cast<int>(shape->tokens);
+  g.N = static_cast<int>(shape->ffn);
+  g.K = static_cast<int>(shape->d);
+  g.group = group;
+  return cuda_status(launch_gemm_w4(g, c, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -89,12 +89,13 @@ cudaError_t raise_smem_once(K kern, int bytes, const DeviceCtx& ctx, std::atomic
   return e;
 }
 
-// Bounds-check violations counted by the row kernels' / the GEMMs' / the block-scaled ones' translation units since the
+// Bounds-check violations counted by the row kernels' / the GEMMs' / the block-scaled / the 4-bit units since the
 // last call (zero in release builds, which check nothing), and the first site; both cleared.
 cudaError_t rowwise_bounds_status(unsigned int* count, unsigned int* site);
 cudaError_t gemm_bounds_status(unsigned int* count, unsigned int* site);
 cudaError_t block_rows_bounds_status(unsigned int* count, unsigned int* site);
 cudaError_t gemm_block_bounds_status(unsigned int* count, unsigned int* site);
+cudaError_t w4_bounds_status(unsigned int* count, unsigned int* site);
 
 // Returns cudaErrorNotSupported for operand/epilogue combinations without a kernel.
 cudaError_t launch_gemm(const GemmLaunch& g, const DeviceCtx& ctx, cudaStream_t s);
