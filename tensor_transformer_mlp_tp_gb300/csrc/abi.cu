@@ -581,6 +581,22 @@ cudaError_t backward_core(const DeviceCtx& c, const void* X, const void* A, cons
 cudaError_t do_gemm1_gated(const DeviceCtx& c, const void* X, const void* Ag, const void* Au, const void* bg,
                            const void* bu, int act, const tpmlp_shape* s, void* H, void* Gpre, void* Upre,
                            cudaStream_t st) {
+  if (s->tokens <= kFewRows) {
+    GemmFewLaunch f;
+    f.M = static_cast<int>(s->tokens);
+    f.N = static_cast<int>(s->ffn);
+    f.K = static_cast<int>(s->d);
+    f.x = X;
+    f.w[0] = Ag;
+    f.w[1] = Au;
+    f.bias[0] = bg;
+    f.bias[1] = bu;
+    f.out = H;
+    f.pre[0] = Gpre;
+    f.pre[1] = Upre;
+    f.act = act;
+    return launch_gemm_few(f, c, st);
+  }
   GemmLaunch g;
   g.M = static_cast<int>(s->tokens);
   g.N = static_cast<int>(s->ffn);
@@ -645,6 +661,21 @@ cudaError_t do_dx_gated(const DeviceCtx& c, const void* dG, const void* dU, cons
   return launch_gemm(g, c, st);
 }
 
+// The gated block's row-parallel product, right behind do_gemm1_gated.
+cudaError_t do_gemm2_gated(const DeviceCtx& c, const void* H, const void* B, const tpmlp_shape* s, void* Y,
+                           cudaStream_t st) {
+  if (s->tokens > kFewRows) return do_gemm2(c, H, B, s, Y, nullptr, st);
+  GemmFewLaunch f;
+  f.M = static_cast<int>(s->tokens);
+  f.N = static_cast<int>(s->d);
+  f.K = static_cast<int>(s->ffn);
+  f.x = H;
+  f.w[0] = B;
+  f.out = Y;
+  f.early_weights = true;
+  return launch_gemm_few(f, c, st);
+}
+
 bool act_ok(int act) { return act == TPMLP_ACT_SILU || act == TPMLP_ACT_GELU; }
 
 }  // namespace
@@ -697,11 +728,12 @@ tpmlp_status tpmlp_get_device_status(tpmlp_stream_t stream, uint32_t* site) {
 
 tpmlp_status tpmlp_debug_bounds_status(int32_t* checked, uint32_t* violations, uint32_t* first_site) {
   if (checked == nullptr || violations == nullptr || first_site == nullptr) return TPMLP_ERR_INVALID_ARG;
-  unsigned int c[5] = {}, site[5] = {};
+  unsigned int c[6] = {}, site[6] = {};
   if (cudaDeviceSynchronize() != cudaSuccess) return TPMLP_ERR_CUDA;
   if (rowwise_bounds_status(&c[0], &site[0]) != cudaSuccess || gemm_bounds_status(&c[1], &site[1]) != cudaSuccess ||
       block_rows_bounds_status(&c[2], &site[2]) != cudaSuccess ||
-      gemm_block_bounds_status(&c[3], &site[3]) != cudaSuccess || w4_bounds_status(&c[4], &site[4]) != cudaSuccess)
+      gemm_block_bounds_status(&c[3], &site[3]) != cudaSuccess || w4_bounds_status(&c[4], &site[4]) != cudaSuccess ||
+      gemm_few_bounds_status(&c[5], &site[5]) != cudaSuccess)
     return TPMLP_ERR_CUDA;
 #ifdef TPMLP_DEBUG_BOUNDS
   *checked = 1;
@@ -709,7 +741,7 @@ tpmlp_status tpmlp_debug_bounds_status(int32_t* checked, uint32_t* violations, u
   *checked = 0;
 #endif
   *violations = *first_site = 0;
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < 6; ++i) {
     *violations += c[i];
     if (*first_site == 0) *first_site = site[i];
   }
@@ -1620,7 +1652,7 @@ tpmlp_status tpmlp_gated_forward(const void* X, const void* Ag, const void* Au, 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   void* H = H_out != nullptr ? H_out : workspace;
   cudaError_t e = do_gemm1_gated(c, X, Ag, Au, bg, bu, act, shape, H, Gpre_out, Upre_out, s);
-  if (e == cudaSuccess) e = do_gemm2(c, H, B, shape, Y, nullptr, s);
+  if (e == cudaSuccess) e = do_gemm2_gated(c, H, B, shape, Y, s);
   return cuda_status(e);
 }
 

@@ -27,6 +27,9 @@ enum WaitSite : uint32_t {
   kSiteBlockMmaFull = 8,    // ring slot filled
   kSiteBlockMmaEmpty = 9,   // partial sums read
   kSiteBlockPromote = 10,   // partial sums written
+  kSiteFewProducer = 11,    // few-row bf16 GEMM: ring slot free
+  kSiteFewMma = 12,         // ring slot filled
+  kSiteFewEpilogue = 13,    // sums complete
 };
 
 // GEMM tile: BM x BN output, BK-deep k-blocks (64 bf16 = one 128-byte swizzle row).

@@ -30,6 +30,7 @@ enum BoundsSite : uint32_t {
   kBoundsBlockSource = 132,  // the block quantiser's source
   kBoundsBlockGemm = 133,    // the block-scaled GEMM's direct stores of C or the pre-activation
   kBoundsBlockBias = 134,    // its bias
+  kBoundsGemmFew = 135,      // the few-row bf16 GEMM's outputs
   kBoundsW4Out = 140,        // products with 4-bit weights: the output
 };
 

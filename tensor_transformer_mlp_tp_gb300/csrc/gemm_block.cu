@@ -8,34 +8,11 @@
 #include <climits>
 #include <cstring>
 
+#include "cluster_fit.cuh"
 #include "gemm_block_few.cuh"
 
 namespace tpmlp {
 namespace {
-
-// Largest number of co-resident clusters of `kern` on the current device (cached per device).
-template <typename K>
-int max_clusters(K kern, int cluster, int smem, int threads, std::atomic<int>* cache) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  const int known = cache[dev & 63].load(std::memory_order_relaxed);
-  if (known > 0) return known;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cluster);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) n = 1;
-  cache[dev & 63].store(n, std::memory_order_relaxed);
-  return n;
-}
 
 template <int OUT, bool BVEC>
 cudaError_t run_pair(const GemmBlockParams& p, const DeviceCtx& ctx, cudaStream_t s) {
@@ -64,29 +41,10 @@ cudaError_t run_pair(const GemmBlockParams& p, const DeviceCtx& ctx, cudaStream_
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// Stands for the few-row kernel in occupancy queries and is never launched: for a kernel that uses tensor memory the
-// query answers one block an SM, while two are resident (their TMEM is half of it each).
-__global__ void __launch_bounds__(320) k_slot() {}
-
-// Clusters of `ranks` CTAs of the BT kernel that the device holds at once.  (Clusters of eight with a CTA an SM leave a
-// fifth of the SMs unused: 15 fit, 120 CTAs of 152.)
+// CTAs that share a tile's k-blocks (the larger shape stands for both).
 template <int BT>
-int few_clusters(int ranks, const DeviceCtx& ctx) {
-  using S = BlockFewShape<BT, true>;  // the larger of the two
-  static std::atomic<int> cache[4][64] = {};
-  static std::atomic<unsigned long long> set[64] = {};
-  if (raise_smem_once(k_slot, 227 * 1024, ctx, set) != cudaSuccess) return 1;
-  const int slot = ranks == 1 ? 0 : ranks == 2 ? 1 : ranks == 4 ? 2 : 3;
-  return max_clusters(k_slot, ranks, S::kSmem, S::kThreads, cache[slot]);
-}
-
-// CTAs that share a tile's k-blocks: as many (a power of two up to 8) as the device holds for all tiles at once, which
-// keeps the most bytes in flight, with two k-blocks each at least.
-template <int BT>
-int few_ranks(long long tiles, int k_blocks, const DeviceCtx& ctx) {
-  int ranks = 1;
-  while (ranks < kFewMaxRanks && 4 * ranks <= k_blocks && tiles <= few_clusters<BT>(2 * ranks, ctx)) ranks *= 2;
-  return ranks;
+int block_few_ranks(long long tiles, int k_blocks, const DeviceCtx& ctx) {
+  return few_ranks<BlockFewShape<BT, true>>(tiles, k_blocks, kFewMaxRanks, ctx);
 }
 
 // Which kernel: up to 128 rows the one that streams B once.  Above, whichever has fewer k-blocks one after the other, and
@@ -100,7 +58,7 @@ bool few_rows(const GemmBlockLaunch& g, int k_blocks, const DeviceCtx& ctx) {
   if (g.M <= 128) return true;
   const long long few_tiles = static_cast<long long>((g.M + 127) / 128) * ((g.N + 127) / 128);
   if (few_tiles > 4ll * sms) return false;
-  const long long ranks = few_ranks<128>(few_tiles, k_blocks, ctx);
+  const long long ranks = block_few_ranks<128>(few_tiles, k_blocks, ctx);
   const long long few = (few_tiles * ranks + sms - 1) / sms * ((k_blocks + ranks - 1) / ranks);
   const long long pairs = sms / 2, pair_tiles = static_cast<long long>((g.M + 255) / 256) * ((g.N + 255) / 256);
   const long long pair = (pair_tiles + pairs - 1) / pairs * k_blocks;
@@ -115,7 +73,7 @@ cudaError_t run_few(GemmBlockParams p, const DeviceCtx& ctx, cudaStream_t s) {
   const cudaError_t e = raise_smem_once(kern, S::kSmem, ctx, set);
   if (e != cudaSuccess) return e;
   const int tiles = (p.g.N + 127) / 128, row_tiles = (p.g.M + BT - 1) / BT;
-  const int ranks = few_ranks<BT>(static_cast<long long>(tiles) * row_tiles, p.k_blocks, ctx);
+  const int ranks = block_few_ranks<BT>(static_cast<long long>(tiles) * row_tiles, p.k_blocks, ctx);
   p.ranks = ranks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks * tiles, row_tiles);

@@ -54,15 +54,6 @@ struct BlockFewShape {
   static_assert(kSmem <= 232448, "shared memory per block");
 };
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(cluster_addr)
-               : "memory");
-  return v;
-}
-
 // grid: (cluster size x column tiles, row tiles).  p.tmA: A [M x K], boxes of 128 bytes x p.box_rows rows, the M there are
 // up to BT: with boxes of BT rows the copies' zero rows past A's end cost more than real ones, as if every CTA read one
 // line for them (N = 16384, K = 4096: one row 16.3 us, now 13.3; 17 rows 17.5, now 14.6).  The rest of a tile stays unwritten and

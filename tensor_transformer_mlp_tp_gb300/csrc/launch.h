@@ -96,9 +96,27 @@ cudaError_t gemm_bounds_status(unsigned int* count, unsigned int* site);
 cudaError_t block_rows_bounds_status(unsigned int* count, unsigned int* site);
 cudaError_t gemm_block_bounds_status(unsigned int* count, unsigned int* site);
 cudaError_t w4_bounds_status(unsigned int* count, unsigned int* site);
+cudaError_t gemm_few_bounds_status(unsigned int* count, unsigned int* site);
 
 // Returns cudaErrorNotSupported for operand/epilogue combinations without a kernel.
 cudaError_t launch_gemm(const GemmLaunch& g, const DeviceCtx& ctx, cudaStream_t s);
+
+// out [M x N] bf16 = x [M x K] w[0] + bias[0], or with w[1] act(x w[0] + bias[0]) * (x w[1] + bias[1]), for up to kFewRows
+// rows; w [K x N] row-major.
+constexpr int kFewRows = 128;
+struct GemmFewLaunch {
+  int M = 0, N = 0, K = 0;
+  const void* x = nullptr;
+  const void* w[2] = {};
+  const void* bias[2] = {};
+  void* out = nullptr;
+  void* pre[2] = {};           // with w[1]: the factors before the activation
+  int act = 0;
+  // The kernel before on the stream is one of this library's that waits for its own predecessor before it lets this one
+  // start, and writes none of w: their first copies then need not wait for its end.
+  bool early_weights = false;
+};
+cudaError_t launch_gemm_few(const GemmFewLaunch& g, const DeviceCtx& ctx, cudaStream_t s);
 
 cudaError_t launch_layernorm_fwd(const RowParams& r, const DeviceCtx& ctx, cudaStream_t s);
 // The RMS norm of the SequenceParallelLayerNorm listing (gamma = the weight; beta unused).
