@@ -30,6 +30,8 @@ enum WaitSite : uint32_t {
   kSiteFewProducer = 11,    // few-row bf16 GEMM: ring slot free
   kSiteFewMma = 12,         // ring slot filled
   kSiteFewEpilogue = 13,    // sums complete
+  kSiteW4Producer = 14,     // products with 4-bit weights, few rows: ring slot free
+  kSiteW4Consumer = 15,     // ring slot filled
 };
 
 // GEMM tile: BM x BN output, BK-deep k-blocks (64 bf16 = one 128-byte swizzle row).

@@ -122,14 +122,6 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* buf, 
   }
 }
 
-// A warp's wait: short tries first, which cover the gaps of the pipeline's steady state, then the bounded wait.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, uint32_t site) {
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i)
-    if (__all_sync(0xffffffffu, mbar_try_wait_short(bar, parity))) return true;
-  return __all_sync(0xffffffffu, wait_bounded(bar, parity, w, site));
-}
-
 template <int OUT, bool BVEC>
 __global__ void __launch_bounds__(BlockPairShape<BVEC>::kThreads, 1) k_gemm_block_pair(const __grid_constant__ GemmBlockParams p) {
   using S = BlockPairShape<BVEC>;

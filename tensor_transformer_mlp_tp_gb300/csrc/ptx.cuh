@@ -116,6 +116,14 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, con
   }
 }
 
+// A warp's wait: short tries first, which cover the gaps of the pipeline's steady state, then the bounded wait.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, uint32_t site) {
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait_short(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, w, site));
+}
+
 // Teardown wait: same limit, but ignores the abort flag (used to drain
 // copies or MMAs still in flight before shared memory or TMEM is released).
 __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity, uint64_t budget_ns) {
@@ -173,6 +181,17 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                    smem_u32(dst)),
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
+}
+
+// Asynchronous copies of BYTES (8 or 16) by a thread, of which `have` are read and the rest become zeros, in groups.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void* dst, const void* src, int have) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES), "r"(have) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
 // Bring `bytes` (a multiple of 16) at a 16-byte aligned global address into L2, asynchronously.
@@ -466,6 +485,12 @@ __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr
 
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float ld_cluster_f1(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {

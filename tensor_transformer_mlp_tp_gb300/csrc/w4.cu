@@ -1,8 +1,10 @@
 // Products with 4-bit weights and group scales, their quantiser and its inverse.
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <climits>
 
+#include "cluster_fit.cuh"
 #include "debug_bounds.cuh"
 #include "gated.cuh"
 #include "w4.cuh"
@@ -14,80 +16,437 @@ constexpr float kW4Tiny = 7.8886090522101181e-31f;  // 2^-100, the least range a
 constexpr float kW4Big = 3.3895313892515355e38f;    // bf16's largest number, the largest
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                "{%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-constexpr int kWarps = 8;
+// Up to 16 tokens (TT tiles of eight, the m16n8k16 product's columns).  One block an SM, blocks in clusters of `ranks`; a
+// cluster takes every so many-th column tile (both matrices of the gated form), its blocks share K, and eight warps share
+// a block's part of it; up to eight tokens two such teams take turns with the tiles.  One lane of a warp of its own streams the
+// codes of one tile after the other into a ring by bulk copies of up to 32 KB, so that the bytes in flight cost neither
+// registers nor instructions.  What a weight costs is its unpacking, nine instructions for eight codes.
+//
+// The products are of fp16 numbers, for the unpacking's sake.  q - z is exact; what a warp reads of a token is brought
+// below 2^15 by a power of two, which loses nothing of a value within 2^-32 of the largest there.  A group's sum in fp32 is
+// scaled by s 2^-15 and added to an fp32 sum, and the power of two is taken back as the warps' sums are joined.
+//
+// X is staged once, so that a lane's B registers of a 64-row tile are 32 consecutive bytes, the rows a multiple of 128
+// bytes and 16 apart (conflict-free); lanes past the last token read a row of zeros.  The sums of a round of tiles are joined
+// in a fixed order, the warps' and then the blocks'.
+constexpr int kWarps = 8;        // of a team
+constexpr int kW4Ranks = 4;
+constexpr int kW4Stages = 4;      // copies in flight a team at most
 
-// Eight tokens (blockIdx.y) and 16 columns (blockIdx.x) a block; its warps share K and join their sums in shared memory.
-template <bool GATED>
-__global__ void __launch_bounds__(32 * kWarps) k_gemm_w4(const __grid_constant__ W4Launch p) {
-  constexpr int MATS = GATED ? 2 : 1;
-  __shared__ float red[kWarps][MATS][16][8];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * kW4Cols, m = blockIdx.y * 8 + g;
-  const int k_tiles = (p.K + kW4Rows - 1) / kW4Rows, groups = (p.K + p.group - 1) / p.group;
-  const int kt0 = static_cast<int>(static_cast<long long>(k_tiles) * warp / kWarps);
-  const int kt1 = static_cast<int>(static_cast<long long>(k_tiles) * (warp + 1) / kWarps);
-  const uint32_t* x = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.x) + static_cast<long long>(m < p.M ? m : 0) * p.K);
-  float sum[MATS][4] = {};
-  for (int kt = kt0; kt < kt1; ++kt) {
-    uint32_t b[4][2];
+struct W4FewParams {
+  W4Launch g;
+  int ranks, clusters;         // blocks of a cluster; clusters
+  int chunk, stages, round;    // row tiles a copy; a team's copies in flight; column tiles (of either matrix) between joins
+  int shift;                   // log2 of the group
+  int x_pitch;                 // bytes of a token's staged row
+  unsigned int* err;
+  unsigned long long timeout_ns;
+};
+
+template <int TT, bool G32, bool ZEROS>
+struct W4FewShape {
+  static constexpr int kTeams = TT == 1 ? 2 : 1;
+  static constexpr int kConsumers = 32 * kTeams * kWarps, kThreads = kConsumers + 32;
+  static constexpr int kSums = 8 * TT * 16;  // of a tile
+  // Scales and zero points of a warp's part of a chunk: 16 columns of each, for every row tile or half of one.
+  static constexpr int kParts = G32 ? 16 : 8, kPartBytes = ZEROS ? 48 : 32, kSlot = kParts * kPartBytes;
+  // rows of zeros, scales in flight, the tokens' powers of two, barriers
+  static constexpr int kFixed = 512 + kTeams * kWarps * 4 * kSlot + kWarps * 16 * 4 + 256;
+  static constexpr int kSmem = 232448;
+};
+
+// Row m, column col of the output from the sums (equal for a plain product).
+template <int MATS>
+__device__ __forceinline__ void w4_finish(const W4Launch& g, int m, int col, float first, float last) {
+  if (!TPMLP_IN_BOUNDS(static_cast<long long>(m) * g.N + col, static_cast<long long>(g.M) * g.N, kBoundsW4Out)) return;
+  float v[2] = {first, last};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+  for (int k = 0; k < MATS; ++k)
+    if (g.w[k].bias != nullptr) v[k] += __bfloat162float(static_cast<const __nv_bfloat16*>(g.w[k].bias)[col]);
+  if (MATS == 2) v[0] = act2(g.act, make_float2(v[0], v[0])).x * v[1];
+  static_cast<__nv_bfloat16*>(g.y)[static_cast<long long>(m) * g.N + col] = __float2bfloat16_rn(v[0]);
+}
+
+template <int THREADS>
+__device__ __forceinline__ void consumers_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
+// Two bf16 of X times f, in fp16.
+__device__ __forceinline__ uint32_t x_half2(uint32_t pair, float f) {
+  const float2 v = unpack_bf16x2(pair);
+  const __half2 h = __floats2half2_rn(v.x * f, v.y * f);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int MATS, int TT, bool G32, bool ZEROS>
+__global__ void __launch_bounds__(W4FewShape<TT, G32, ZEROS>::kThreads, 1) k_gemm_w4_few(const __grid_constant__ W4FewParams p) {
+  using S = W4FewShape<TT, G32, ZEROS>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int M = p.g.M, N = p.g.N, K = p.g.K, ranks = p.ranks;
+  const int rank = ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0, cluster = static_cast<int>(blockIdx.x) / ranks;
+  const int k_tiles = (K + kW4Rows - 1) / kW4Rows;
+  const int kt_a = static_cast<int>(static_cast<long long>(k_tiles) * rank / ranks);
+  const int kt_n = static_cast<int>(static_cast<long long>(k_tiles) * (rank + 1) / ranks) - kt_a;
+  const int chunks = (kt_n + p.chunk - 1) / p.chunk;  // of a column tile
+  const int tiles = ((N + kW4Cols - 1) / kW4Cols - cluster + p.clusters - 1) / p.clusters * MATS;
+
+  uint8_t* ring = smem;
+  float* red = reinterpret_cast<float*>(ring + S::kTeams * p.stages * p.chunk * 512);  // [tile of the round][warp][token][column]
+  uint8_t* zero_row = reinterpret_cast<uint8_t*>(red + p.round * kWarps * S::kSums);
+  uint8_t* slot_mem = zero_row + 512;  // [warp][slot]
+  uint8_t* sx = slot_mem + S::kTeams * kWarps * 4 * S::kSlot;
+  float* tok = reinterpret_cast<float*>(sx + M * p.x_pitch);  // [warp][token]: the power of two to take back
+  uint64_t* full = reinterpret_cast<uint64_t*>(tok + kWarps * 16);
+  uint64_t* empty = full + S::kTeams * p.stages;
+  int* abort_flag = reinterpret_cast<int*>(empty + S::kTeams * p.stages);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kTeams * p.stages; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, kWarps);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  const WaitCtx wc{abort_flag, p.err, p.timeout_ns};
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == S::kTeams * kWarps) {
+    // Each team has a ring of its own: a wait tells a phase from the one before it only, and a team that skipped the other's
+    // would miss some.
+    int stage[S::kTeams] = {};
+    uint32_t phase[S::kTeams] = {}, issued = 0, issued_parity = 0;
+    bool ok = true;
+    for (int round0 = 0; round0 < tiles; round0 += p.round) {
+      if (lane == 0) {
+        for (int tile0 = round0; ok && tile0 < min(tiles, round0 + p.round); tile0 += S::kTeams)
+          for (int c = 0; ok && c < chunks; ++c) {
+            const uint32_t bytes = static_cast<uint32_t>(min(p.chunk, kt_n - c * p.chunk)) * 512u;
+#pragma unroll
+            for (int of = 0; of < S::kTeams; ++of) {
+              const int tile = tile0 + of, i = of * p.stages + stage[of];
+              if (tile >= tiles) break;
+              const uint4* src = p.g.w[MATS == 1 ? 0 : tile & 1].q +
+                                 ((cluster + static_cast<long long>(tile / MATS) * p.clusters) * k_tiles + kt_a + c * p.chunk) * 32;
+              if (!wait_bounded(empty + i, phase[of] ^ 1u, wc, kSiteW4Producer)) {
+                ok = false;
+                break;
+              }
+              mbar_arrive_expect_tx(full + i, bytes);
+              bulk_load(ring + i * p.chunk * 512, src, bytes, full + i);
+              issued |= 1u << i;
+              issued_parity = (issued_parity & ~(1u << i)) | (phase[of] << i);
+              if (++stage[of] == p.stages) {
+                stage[of] = 0;
+                phase[of] ^= 1u;
+              }
+            }
+          }
+      }
+      __syncwarp();
+      if (ranks > 1) {
+        cluster_sync_all();
+        cluster_sync_all();
+      }
+    }
+    if (lane == 0)  // copies in flight land before the block's shared memory is released
+      for (int i = 0; i < S::kTeams * p.stages; ++i)
+        if (issued & (1u << i)) wait_drain(full + i, (issued_parity >> i) & 1u, p.timeout_ns);
+    return;
+  }
+
+  const int team = warp / kWarps, w = warp % kWarps;  // this warp takes the team's tiles, part w of each chunk
+  // A warp fetches the scales and zero points of what it reads of a chunk (eight row tiles at most) three chunks ahead into
+  // slots of its own, eight columns a lane.
+  uint8_t* slots = slot_mem + warp * 4 * S::kSlot;
+  int f_tile = team, f_chunk = 0, f_slot = 0, f_col = (cluster + team / MATS * p.clusters) * kW4Cols + 8 * (lane & 1);
+  long long f_row = 0;  // of scales, times N
+  auto fetch = [&]() {
+    if (f_tile < tiles && lane < 2 * S::kParts) {
+      if (f_tile < S::kTeams || chunks > 1) {
+        const int n = min(p.chunk, kt_n - f_chunk * p.chunk), w0 = n * w / kWarps;
+        const int row = (kt_a + f_chunk * p.chunk + w0) * kW4Rows + (G32 ? 32 : 64) * (lane >> 1);
+        f_row = static_cast<long long>(min(row, K - 1) >> p.shift) * N;
+      }
+      const W4Matrix& mat = p.g.w[MATS == 1 ? 0 : f_tile & 1];
+      const bool in = f_col < N;
+      const long long at = f_row + (in ? f_col : 0);
+      uint8_t* dst = slots + f_slot * S::kSlot + (lane >> 1) * S::kPartBytes;
+      cp_async<16>(dst + 16 * (lane & 1), static_cast<const __nv_bfloat16*>(mat.scales) + at, in ? 16 : 0);
+      if (ZEROS) cp_async<8>(dst + 32 + 8 * (lane & 1), mat.zeros + at, in ? 8 : 0);
+    }
+    cp_async_commit();
+    f_slot = (f_slot + 1) & 3;
+    if (++f_chunk == chunks) {
+      f_chunk = 0;
+      f_tile += S::kTeams;
+      if (MATS == 1) f_col += S::kTeams * p.clusters * kW4Cols;
+      else if (S::kTeams == 2 || (f_tile & 1) == 0) f_col += p.clusters * kW4Cols;
+    }
+  };
+
+  // X: part w of every chunk (eight row tiles at most, 32 bytes a lane) of the team's tokens, as it is, then each token
+  // scaled by its largest value there and turned into the products' order.
+  const __nv_bfloat16* xg = static_cast<const __nv_bfloat16*>(p.g.x);
+  auto part_of = [&](int c, int& first, int& pieces) {  // of chunk c: its first row tile in the block's part, 16-byte pieces
+    const int n = min(p.chunk, kt_n - c * p.chunk), w0 = n * w / kWarps;
+    first = c * p.chunk + w0;
+    pieces = (n * (w + 1) / kWarps - w0) * 8;
+  };
+  for (int c = 0; c < chunks; ++c) {
+    int first, pieces;
+    part_of(c, first, pieces);
+    for (int m = team; m < M; m += S::kTeams)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int k = kt * kW4Rows + 16 * j + 8 * h + 2 * t;
-        b[j][h] = m < p.M && k < p.K ? __ldg(x + k / 2) : 0u;
+        const int piece = lane + 32 * h, k = (kt_a + first) * kW4Rows + piece * 8;
+        if (piece < pieces)
+          cp_async<16>(sx + m * p.x_pitch + first * 128 + piece * 16, xg + static_cast<long long>(m) * K + (k < K ? k : 0), k < K ? 16 : 0);
       }
+  }
+  cp_async_commit();
 #pragma unroll
-    for (int i = 0; i < MATS; ++i) {
-      const W4Matrix& w = p.w[i];
-      const uint4 q4 = __ldg(w.q + (static_cast<long long>(blockIdx.x) * k_tiles + kt) * 32 + lane);
-      const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
-      const int steps = p.group == 32 ? 2 : 4;  // of 16 rows, with one scale
-      for (int j0 = 0; j0 < 4; j0 += steps) {
-        const int grp = min((kt * kW4Rows + 16 * j0) / p.group, groups - 1);
-        const long long at = static_cast<long long>(grp) * p.N + n0 + g;
-        const bool in0 = n0 + g < p.N, in1 = n0 + g + 8 < p.N;
-        const __nv_bfloat16* sc = static_cast<const __nv_bfloat16*>(w.scales) + at;
-        const float s0 = in0 ? __bfloat162float(sc[0]) : 0.f, s1 = in1 ? __bfloat162float(sc[8]) : 0.f;
-        const uint32_t z0 = w.zeros != nullptr && in0 ? w4_base(w.zeros[at]) : kW4Base8;
-        const uint32_t z1 = w.zeros != nullptr && in1 ? w4_base(w.zeros[at + 8]) : kW4Base8;
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int j = j0; j < j0 + steps; ++j) {
-          const uint32_t a[4] = {w4_minus(w4_pair<0>(q[j]), z0), w4_minus(w4_pair<1>(q[j]), z1),
-                                 w4_minus(w4_pair<2>(q[j]), z0), w4_minus(w4_pair<3>(q[j]), z1)};
-          mma_16816(c, a, b[j]);
+  for (int i = 0; i < 3; ++i) fetch();
+  if (threadIdx.x < 32) reinterpret_cast<uint4*>(zero_row)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+  cp_async_wait<3>();
+  __syncwarp();
+  for (int m = team; m < M; m += S::kTeams) {
+    uint8_t* row = sx + m * p.x_pitch;
+    uint32_t largest = 0;  // bits of bf16 without the sign
+    for (int c = 0; c < chunks; ++c) {
+      int first, pieces;
+      part_of(c, first, pieces);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (lane + 32 * h < pieces) {
+          const uint4 v = reinterpret_cast<const uint4*>(row + first * 128)[lane + 32 * h];
+          largest = __vmaxu2(__vmaxu2(largest, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu)),
+                             __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
         }
-        sum[i][0] = fmaf(c[0], s0, sum[i][0]);
-        sum[i][1] = fmaf(c[1], s0, sum[i][1]);
-        sum[i][2] = fmaf(c[2], s1, sum[i][2]);
-        sum[i][3] = fmaf(c[3], s1, sum[i][3]);
-      }
+    }
+    largest = __reduce_max_sync(0xffffffffu, max(largest >> 16, largest & 0xFFFFu));
+    // its exponent e (infinities and NaN count as the largest finite values); 2^(14 - e), and 2^(e + 1) back
+    const int e = min(max(static_cast<int>(largest >> 7) - 127, -112), 126);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+    if (lane == 0) tok[w * 16 + m] = __uint_as_float(static_cast<uint32_t>(127 + e + 1) << 23);
+    for (int c = 0; c < chunks; ++c) {
+      int first, pieces;
+      part_of(c, first, pieces);
+      uint4 v[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (lane + 32 * h < pieces) v[h] = reinterpret_cast<const uint4*>(row + first * 128)[lane + 32 * h];
+      __syncwarp();
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (lane + 32 * h < pieces) {
+          uint32_t* dst = reinterpret_cast<uint32_t*>(row + (first + 4 * h + (lane >> 3)) * 128) + (lane & 7);
+          dst[0] = x_half2(v[h].x, up);
+          dst[8] = x_half2(v[h].y, up);
+          dst[16] = x_half2(v[h].z, up);
+          dst[24] = x_half2(v[h].w, up);
+        }
     }
   }
+  // this lane's tokens: their rows, or the zeros, which do not advance
+  const uint8_t* x_row[TT];
+  int x_step[TT];
 #pragma unroll
-  for (int i = 0; i < MATS; ++i)
+  for (int tt = 0; tt < TT; ++tt) {
+    const bool in = 8 * tt + g < M;
+    x_row[tt] = in ? sx + (8 * tt + g) * p.x_pitch + t * 32 : zero_row + t * 32;
+    x_step[tt] = in ? 128 : 0;
+  }
+  consumers_sync<S::kConsumers>();  // both teams' tokens
+  int stage = team * p.stages, slot = 0;
+  uint32_t phase = 0;
+  for (int round0 = 0; round0 < tiles; round0 += p.round) {
+    const int nt = min(p.round, tiles - round0);
+    float* dst = red + (team * kWarps + w) * S::kSums + 2 * t * 16 + g;
+    for (int tile = team; tile < nt; tile += S::kTeams, dst += S::kTeams * kWarps * S::kSums) {
+      float sum[TT][4] = {};
+      for (int c = 0; c < chunks; ++c) {
+        int first, pieces;
+        part_of(c, first, pieces);
+        cp_async_wait<2>();
+        __syncwarp();  // this chunk's scales are there for all lanes, and the slot before has been read
+        const uint8_t* sl = slots + slot * S::kSlot;
+        slot = (slot + 1) & 3;
+        fetch();
+        (void)warp_wait(full + stage, phase, wc, kSiteW4Consumer);
+        const uint4* src = reinterpret_cast<const uint4*>(ring + (stage * p.chunk + first - c * p.chunk) * 512) + lane;
+        const uint8_t* xs[TT];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) red[warp][i][g + 8 * (r >> 1)][2 * t + (r & 1)] = sum[i][r];
-  __syncthreads();
-  if (threadIdx.x < 128) {
-    const int c = threadIdx.x & 15, row = blockIdx.y * 8 + (threadIdx.x >> 4), col = n0 + c;
-    if (row < p.M && col < p.N && TPMLP_IN_BOUNDS(static_cast<long long>(row) * p.N + col, static_cast<long long>(p.M) * p.N, kBoundsW4Out)) {
-      float v[MATS] = {};
+        for (int tt = 0; tt < TT; ++tt) xs[tt] = x_row[tt] + first * x_step[tt];
+#pragma unroll 4
+        for (int i = 0; i < pieces; i += 8, src += 32) {
+          const uint4 q4 = *src;
+          const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
+          uint4 b4[TT][2];
 #pragma unroll
-      for (int i = 0; i < MATS; ++i) {
-        for (int w = 0; w < kWarps; ++w) v[i] += red[w][i][c][threadIdx.x >> 4];
-        if (p.w[i].bias != nullptr) v[i] += __bfloat162float(static_cast<const __nv_bfloat16*>(p.w[i].bias)[col]);
+          for (int tt = 0; tt < TT; ++tt) {
+            b4[tt][0] = reinterpret_cast<const uint4*>(xs[tt])[0];
+            b4[tt][1] = reinterpret_cast<const uint4*>(xs[tt])[1];
+            xs[tt] += x_step[tt];
+          }
+          constexpr int kSteps = G32 ? 2 : 4;  // of 16 rows, with one scale
+#pragma unroll
+          for (int j0 = 0; j0 < 4; j0 += kSteps, sl += S::kPartBytes) {
+            // 2^-15 s for the first eight columns, 2^-19 s for the others, whose codes come out sixteen times as large
+            const float s0 = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sl)[g]) * 0x1p-15f;
+            const float s1 = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sl)[g + 8]) * 0x1p-19f;
+            const uint32_t z0 = w4_base0(ZEROS ? sl[32 + g] : 8u), z1 = w4_base1(ZEROS ? sl[40 + g] : 8u);
+            float c4[TT][4] = {};
+#pragma unroll
+            for (int j = j0; j < j0 + kSteps; ++j) {
+              uint32_t a[4];
+              w4_unpack(q[j], z0, z1, a);
+#pragma unroll
+              for (int tt = 0; tt < TT; ++tt) {
+                const uint4 v = b4[tt][j >> 1];
+                const uint32_t b[2] = {j & 1 ? v.z : v.x, j & 1 ? v.w : v.y};
+                mma_16816(c4[tt], a, b);
+              }
+            }
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+              sum[tt][0] = fmaf(c4[tt][0], s0, sum[tt][0]);
+              sum[tt][1] = fmaf(c4[tt][1], s0, sum[tt][1]);
+              sum[tt][2] = fmaf(c4[tt][2], s1, sum[tt][2]);
+              sum[tt][3] = fmaf(c4[tt][3], s1, sum[tt][3]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + stage);
+        if (++stage == (team + 1) * p.stages) {
+          stage = team * p.stages;
+          phase ^= 1u;
+        }
       }
-      if constexpr (GATED) v[0] = act2(p.act, make_float2(v[0], v[0])).x * v[1];
-      static_cast<__nv_bfloat16*>(p.y)[static_cast<long long>(row) * p.N + col] = __float2bfloat16_rn(v[0]);
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) dst[(8 * tt + (r & 1)) * 16 + 8 * (r >> 1)] = sum[tt][r];
+    }
+    consumers_sync<S::kConsumers>();
+    // the block's sums of tile i (column tile c, matrix k), token m, column n; ranks > 1: into the first warp's place
+    for (int c = threadIdx.x; c < nt * M * 16; c += S::kConsumers) {
+      const int tile = c / (M * 16), r = c - tile * M * 16, m = r >> 4;
+      if (MATS == 2 && ranks == 1 && (tile & 1)) continue;
+      float v[MATS];
+#pragma unroll
+      for (int k = 0; k < MATS; ++k) {
+        if (k > 0 && ranks > 1) break;
+        const float* at = red + (tile + k) * kWarps * S::kSums + r;
+        v[k] = 0.f;
+#pragma unroll
+        for (int o = 0; o < kWarps; ++o) v[k] = fmaf(at[o * S::kSums], tok[o * 16 + m], v[k]);
+      }
+      if (ranks > 1) {
+        red[tile * kWarps * S::kSums + r] = v[0];
+      } else {
+        const int col = (cluster + (round0 + tile) / MATS * p.clusters) * kW4Cols + (r & 15);
+        if (col < N) w4_finish<MATS>(p.g, m, col, v[0], v[MATS - 1]);
+      }
+    }
+    __syncwarp();
+    if (ranks > 1) {
+      cluster_sync_all();
+      for (int c = threadIdx.x; c < nt / MATS * M * 16; c += S::kConsumers) {
+        const int i = c / (M * 16), r = c - i * M * 16, m = r >> 4;
+        const int col = (cluster + (round0 / MATS + i) * p.clusters) * kW4Cols + (r & 15);
+        if ((i + m) % ranks != rank || col >= N) continue;
+        float v[MATS];
+#pragma unroll
+        for (int k = 0; k < MATS; ++k) {
+          v[k] = 0.f;
+          const uint32_t at = smem_u32(red + (i * MATS + k) * kWarps * S::kSums + r);
+          for (int o = 0; o < ranks; ++o) v[k] += ld_cluster_f1(mapa_shared(at, static_cast<uint32_t>(o)));
+        }
+        w4_finish<MATS>(p.g, m, col, v[0], v[MATS - 1]);
+      }
+      __syncwarp();
+      cluster_sync_all();  // the cluster has read this block's sums
+    } else {
+      consumers_sync<S::kConsumers>();  // the next round overwrites this one's scales and sums
     }
   }
+}
+
+template <int MATS, int TT, bool G32, bool ZEROS>
+cudaError_t run_w4_few(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t s) {
+  using S = W4FewShape<TT, G32, ZEROS>;
+  auto kern = k_gemm_w4_few<MATS, TT, G32, ZEROS>;
+  static std::atomic<unsigned long long> set[64] = {};
+  const cudaError_t e = raise_smem_once(kern, S::kSmem, ctx, set);
+  if (e != cudaSuccess) return e;
+  W4FewParams p{};
+  p.g = g;
+  p.shift = g.group == 32 ? 5 : g.group == 64 ? 6 : 7;
+  p.err = ctx.err;
+  p.timeout_ns = ctx.timeout_ns;
+  const int col_tiles = (g.N + kW4Cols - 1) / kW4Cols, k_tiles = (g.K + kW4Rows - 1) / kW4Rows;
+  // Blocks of a cluster: the number that leaves the busiest SM the least to read, with room for X, for 64 KB of codes in
+  // flight (or half of that, if none has room for it), and for two column tiles' sums.
+  double least = 0;
+  for (int ring_least = 65536; ring_least >= 32768 && p.clusters == 0; ring_least /= 2)
+    for (int r = 1; r <= kW4Ranks && k_tiles >= r; r *= 2) {
+      static std::atomic<int> cache[3][64] = {};
+      const int fit = r == 1 ? ctx.sm_count : max_clusters(kern, r, S::kSmem, S::kThreads, cache[r / 2]);
+      const double load = static_cast<double>((col_tiles + fit - 1) / fit) / r;
+      const int mine = (k_tiles + r - 1) / r, x_pitch = mine * 128 + 16;
+      constexpr int tile_bytes = kWarps * S::kSums * 4;
+      const long long left = S::kSmem - S::kFixed - static_cast<long long>(g.M) * x_pitch;
+      if (left < ring_least + 2 * tile_bytes || (p.clusters != 0 && load > 0.93 * least)) continue;
+      least = load;
+      p.ranks = r;
+      p.clusters = fit < col_tiles ? fit : col_tiles;
+      p.x_pitch = x_pitch;
+      // a round is all of the cluster's tiles, or as many as leave the ring its part
+      const int most = static_cast<int>((left - ring_least) / tile_bytes) / 2 * 2;
+      const int all = (col_tiles + p.clusters - 1) / p.clusters * MATS;
+      p.round = all < most ? all : most;
+      const int ring = static_cast<int>(left) - p.round * tile_bytes;
+      p.chunk = mine < 64 ? mine : 64;
+      while (p.chunk > 16 && ring / (S::kTeams * (p.chunk * 512 + 16)) < 2) p.chunk /= 2;
+      p.stages = ring / (S::kTeams * (p.chunk * 512 + 16));
+      if (p.stages > kW4Stages) p.stages = kW4Stages;
+    }
+  if (p.clusters == 0) return cudaErrorNotSupported;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.ranks * p.clusters);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = p.ranks;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.ranks > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int MATS, int TT>
+cudaError_t launch_w4_few(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t s) {
+  const bool z = g.w[0].zeros != nullptr;
+  if (g.group == 32) return z ? run_w4_few<MATS, TT, true, true>(g, ctx, s) : run_w4_few<MATS, TT, true, false>(g, ctx, s);
+  return z ? run_w4_few<MATS, TT, false, true>(g, ctx, s) : run_w4_few<MATS, TT, false, false>(g, ctx, s);
 }
 
 // One warp a group of a column tile: lane l < 16 takes column l.
@@ -155,11 +514,17 @@ cudaError_t w4_bounds_status(unsigned int* count, unsigned int* site) {
 #endif
 }
 
-cudaError_t launch_gemm_w4(const W4Launch& g, const DeviceCtx&, cudaStream_t s) {
-  const dim3 grid((g.N + kW4Cols - 1) / kW4Cols, (g.M + 7) / 8);
-  if (g.gated) k_gemm_w4<true><<<grid, 32 * kWarps, 0, s>>>(g);
-  else k_gemm_w4<false><<<grid, 32 * kWarps, 0, s>>>(g);
-  return cudaGetLastError();
+cudaError_t launch_gemm_w4(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t s) {
+  W4Launch part = g;
+  for (int m = 0; m < g.M; m += 16) {
+    part.M = g.M - m < 16 ? g.M - m : 16;
+    part.x = static_cast<const __nv_bfloat16*>(g.x) + static_cast<long long>(m) * g.K;
+    part.y = static_cast<__nv_bfloat16*>(g.y) + static_cast<long long>(m) * g.N;
+    const cudaError_t e = part.M <= 8 ? (g.gated ? launch_w4_few<2, 1>(part, ctx, s) : launch_w4_few<1, 1>(part, ctx, s))
+                                      : (g.gated ? launch_w4_few<2, 2>(part, ctx, s) : launch_w4_few<1, 2>(part, ctx, s));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_quantize_w4(const W4Pack& p, cudaStream_t s) {
