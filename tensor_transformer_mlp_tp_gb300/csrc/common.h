@@ -32,6 +32,13 @@ enum WaitSite : uint32_t {
   kSiteFewEpilogue = 13,    // sums complete
   kSiteW4Producer = 14,     // products with 4-bit weights, few rows: ring slot free
   kSiteW4Consumer = 15,     // ring slot filled
+  kSiteW4TcProducer = 41,   // on the UMMA: ring slot free
+  kSiteW4TcMmaX = 42,       // ring slot filled, at the issuer
+  kSiteW4TcMmaA = 43,       // weights unpacked
+  kSiteW4TcMmaD = 44,       // partial sums read
+  kSiteW4TcUnpack = 45,     // ring slot filled, at the unpacking warps
+  kSiteW4TcUnpackA = 46,    // unpacked weights read
+  kSiteW4TcScale = 47,      // partial sums written
 };
 
 // GEMM tile: BM x BN output, BK-deep k-blocks (64 bf16 = one 128-byte swizzle row).

@@ -329,6 +329,9 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
                : "memory");
 }
 
+// Wait for every tcgen05.st of this warp.
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // Shared-memory matrix descriptor (tcgen05 format), 128-byte swizzle.
 //  bits  0-13  start address >> 4
 //  bits 16-29  leading-dimension byte offset >> 4

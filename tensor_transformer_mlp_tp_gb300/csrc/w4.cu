@@ -3,11 +3,12 @@
 
 #include <atomic>
 #include <climits>
+#include <cstring>
 
 #include "cluster_fit.cuh"
 #include "debug_bounds.cuh"
 #include "gated.cuh"
-#include "w4.cuh"
+#include "w4_tc.cuh"
 
 namespace tpmlp {
 namespace {
@@ -36,6 +37,7 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 // bytes and 16 apart (conflict-free); lanes past the last token read a row of zeros.  The sums of a round of tiles are joined
 // in a fixed order, the warps' and then the blocks'.
 constexpr int kWarps = 8;        // of a team
+constexpr int kW4FewTokens = 16;
 constexpr int kW4Ranks = 4;
 constexpr int kW4Stages = 4;      // copies in flight a team at most
 
@@ -514,17 +516,61 @@ cudaError_t w4_bounds_status(unsigned int* count, unsigned int* site) {
 #endif
 }
 
+namespace {
+
+template <int BT, int STEPS, bool ZEROS>
+cudaError_t run_w4_tc(W4TcParams& p, const DeviceCtx& ctx, cudaStream_t s) {
+  using S = W4TcShape<BT>;
+  auto kern = k_gemm_w4_tc<BT, STEPS, ZEROS>;
+  static std::atomic<unsigned long long> set[64] = {};
+  const cudaError_t e = raise_smem_once(kern, S::kSmem, ctx, set);
+  if (e != cudaSuccess) return e;
+  const W4Launch& g = p.g;
+  p.box_rows = g.M < BT ? g.M : BT;
+  if (!encode_tile_map(&p.tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.x, g.K, g.M, g.K, kW4Rows, p.box_rows, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  const int cols = g.gated ? 128 : 256, blocks = (g.N + cols - 1) / cols, tiles = (g.M + BT - 1) / BT;
+  if (tiles > 65535) return cudaErrorNotSupported;
+  p.ranks = few_ranks<S>(static_cast<long long>(blocks) * tiles, (g.K + kW4TcRows - 1) / kW4TcRows, kW4TcRanks, ctx);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.ranks * blocks, tiles);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = p.ranks;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.ranks > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int BT>
+cudaError_t launch_w4_tc(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t s) {
+  W4TcParams p;
+  memset(&p, 0, sizeof(p));
+  p.g = g;
+  p.shift = g.group == 32 ? 5 : g.group == 64 ? 6 : 7;
+  p.err = ctx.err;
+  p.timeout_ns = ctx.timeout_ns;
+  const bool z = g.w[0].zeros != nullptr;
+  if (g.group == 32) return z ? run_w4_tc<BT, 2, true>(p, ctx, s) : run_w4_tc<BT, 2, false>(p, ctx, s);
+  if (g.group == 64) return z ? run_w4_tc<BT, 4, true>(p, ctx, s) : run_w4_tc<BT, 4, false>(p, ctx, s);
+  return z ? run_w4_tc<BT, 8, true>(p, ctx, s) : run_w4_tc<BT, 8, false>(p, ctx, s);
+}
+
+}  // namespace
+
 cudaError_t launch_gemm_w4(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t s) {
-  W4Launch part = g;
-  for (int m = 0; m < g.M; m += 16) {
-    part.M = g.M - m < 16 ? g.M - m : 16;
-    part.x = static_cast<const __nv_bfloat16*>(g.x) + static_cast<long long>(m) * g.K;
-    part.y = static_cast<__nv_bfloat16*>(g.y) + static_cast<long long>(m) * g.N;
-    const cudaError_t e = part.M <= 8 ? (g.gated ? launch_w4_few<2, 1>(part, ctx, s) : launch_w4_few<1, 1>(part, ctx, s))
-                                      : (g.gated ? launch_w4_few<2, 2>(part, ctx, s) : launch_w4_few<1, 2>(part, ctx, s));
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  cudaError_t e = cudaErrorNotSupported;
+  if (g.M <= 8) e = g.gated ? launch_w4_few<2, 1>(g, ctx, s) : launch_w4_few<1, 1>(g, ctx, s);
+  else if (g.M <= kW4FewTokens) e = g.gated ? launch_w4_few<2, 2>(g, ctx, s) : launch_w4_few<1, 2>(g, ctx, s);
+  if (e != cudaErrorNotSupported) return e;  // no room for X there
+  return g.M <= 32 ? launch_w4_tc<32>(g, ctx, s) : launch_w4_tc<64>(g, ctx, s);
 }
 
 cudaError_t launch_quantize_w4(const W4Pack& p, cudaStream_t s) {

@@ -1,0 +1,343 @@
+// Products with 4-bit weights on the UMMA, for more tokens than the m16n8k16 kernel takes: the unpacked weights never touch
+// shared memory.
+//
+// A CTA takes two blocks of 128 columns of W (256 columns, or the same 128 of both matrices of the gated form) as the
+// UMMA's rows and up to BT tokens as its columns; a cluster of CTAs shares K.  Warp 0 copies codes (bulk copies of a column
+// tile's rows) and X (TMA boxes), warp 1 issues, eight warps unpack: a lane's 16 bytes of a 16 x 64 tile are registers in
+// the order of the m16n8k16 product's A operand, which is that of tcgen05.st's 16x128b shape, so a tile goes to tensor memory
+// by one instruction as the UMMA's A operand.  Codes become bf16 q - z, exact.  Eight more warps scale: the UMMAs of a group
+// make a partial sum in TMEM, a thread has those of one column of W, one scale for all of them.  The cluster's sums are
+// joined through distributed shared memory in rank order.
+#pragma once
+
+#include "gated.cuh"
+#include "w4.cuh"
+
+namespace tpmlp {
+
+constexpr int kW4TcRanks = 8;  // CTAs of a cluster at most
+constexpr int kW4TcRows = 128;  // of W a stage: two row tiles
+
+struct W4TcParams {
+  CUtensorMap tmX;  // boxes of 64 x box_rows
+  W4Launch g;
+  int ranks, box_rows, shift;
+  unsigned int* err;
+  unsigned long long timeout_ns;
+};
+
+template <int BT>
+struct W4TcShape {
+  static_assert(BT == 32 || BT == 64, "BT");
+  static constexpr int kCodes = 2 * 8 * 2 * 512;       // two blocks of eight column tiles, two row tiles
+  static constexpr int kX = 2 * BT * 128;
+  static constexpr int kStage = kCodes + kX;
+  static constexpr int kStages = BT == 64 ? 6 : 8;
+  static constexpr int kABufs = 3;                     // unpacked row tiles in TMEM, 32 columns a block
+  static constexpr int kD = kABufs * 64;               // partial sums behind them: [buffer][block][BT]
+  static constexpr int kTmemCols = 512;
+  static constexpr int kWarps = 2 + 8 + 8, kThreads = 32 * kWarps;
+  static constexpr int kSmem = 1024 + kStages * kStage + 256;
+  static_assert(kD + 4 * BT <= kTmemCols, "tensor memory");
+  static_assert(kStages * kStage >= 2 * BT * 128 * 4, "the sums are joined in the ring's memory");
+  static_assert(kSmem <= 232448, "shared memory per block");
+};
+
+// 16 lanes x 32 columns into TMEM: registers 2 i and 2 i + 1 of lane 4 g + t are column 4 i + t of lanes g and g + 8.
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// STEPS: UMMAs (16 rows of W each) of a group.  grid: (cluster size x column blocks, token tiles)
+template <int BT, int STEPS, bool ZEROS>
+__global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const __grid_constant__ W4TcParams p) {
+  using S = W4TcShape<BT>;
+  constexpr int STAGES = S::kStages, ABUFS = S::kABufs;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * S::kStage);
+  uint64_t* empty = full + STAGES;
+  uint64_t* a_full = empty + STAGES;
+  uint64_t* a_empty = a_full + ABUFS;
+  uint64_t* tfull = a_empty + ABUFS;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31u;
+  const bool gated = p.g.gated;
+  const int rank = static_cast<int>(cluster_ctarank()), ranks = p.ranks;
+  const int N = p.g.N, K = p.g.K;
+  const int n0 = static_cast<int>(blockIdx.x) / ranks * (gated ? 128 : 256), m0 = static_cast<int>(blockIdx.y) * BT;
+  const int k_tiles = (K + kW4Rows - 1) / kW4Rows, all_stages = (k_tiles + 1) / 2;
+  const int st0 = static_cast<int>(static_cast<long long>(all_stages) * rank / ranks);
+  const int st1 = static_cast<int>(static_cast<long long>(all_stages) * (rank + 1) / ranks);
+  const int kt0 = 2 * st0, kts = min(2 * st1, k_tiles) - kt0;  // this CTA's row tiles
+  const int parts = (4 * kts + STEPS - 1) / STEPS;             // and groups
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 9);
+    }
+    for (int i = 0; i < ABUFS; ++i) {
+      mbar_init(a_full + i, 8);
+      mbar_init(a_empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tfull + i, 1);
+      mbar_init(tempty + i, 8);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) tma_prefetch_desc(&p.tmX);
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, S::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+  const WaitCtx wc{abort_flag, p.err, p.timeout_ns};
+
+  float acc[BT];
+  if (warp == 0) {
+    // Lanes 0..15 copy a column tile each, 16 and 17 the boxes of X.
+    const int block = static_cast<int>(lane) >> 3, tile = (n0 + (gated ? 0 : 128 * block)) / kW4Cols + (static_cast<int>(lane) & 7);
+    const int n_tiles = (N + kW4Cols - 1) / kW4Cols;
+    const bool have = lane < 16 && tile < n_tiles;
+    const int count = __popc(__ballot_sync(0xffffffffu, have));
+    const uint4* src = have ? p.g.w[gated ? block : 0].q + (static_cast<long long>(tile) * k_tiles + kt0) * 32 : nullptr;
+    const uint64_t pol = policy_evict_normal();
+    uint32_t issued = 0, issued_parity = 0;
+    for (int s = 0; s < st1 - st0; ++s) {
+      const int stage = s % STAGES, rows = min(2, kts - 2 * s);  // row tiles
+      const uint32_t phase = static_cast<uint32_t>(s / STAGES) & 1u;
+      if (!warp_wait(empty + stage, phase ^ 1u, wc, kSiteW4TcProducer)) break;
+      uint8_t* dst = smem + stage * S::kStage;
+      if (lane == 0) mbar_arrive_expect_tx(full + stage, static_cast<uint32_t>(rows * (count * 512 + p.box_rows * 128)));
+      __syncwarp();
+      if (have) bulk_load(dst + lane * 1024, src + s * 64, static_cast<uint32_t>(rows) * 512u, full + stage);
+      else if (lane >= 16 && lane < 16 + static_cast<uint32_t>(rows))
+        tma_load_2d(dst + S::kCodes + (lane - 16) * (BT * 128), &p.tmX, full + stage, (kt0 + 2 * s + static_cast<int>(lane) - 16) * kW4Rows, m0, pol);
+      __syncwarp();
+      issued |= 1u << stage;
+      issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+    }
+    if (lane == 0)  // copies in flight land before their memory is used again
+      for (int s = 0; s < STAGES; ++s)
+        if (issued & (1u << s)) wait_drain(full + s, (issued_parity >> s) & 1u, p.timeout_ns);
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, BT, false, false);
+    const bool elected = elect_one();
+    bool ok = true;
+    for (int kt = 0; ok && kt < kts; ++kt) {
+      const int stage = (kt >> 1) % STAGES, abuf = kt % ABUFS;
+      if (((kt & 1) == 0 && !warp_wait(full + stage, static_cast<uint32_t>((kt >> 1) / STAGES) & 1u, wc, kSiteW4TcMmaX)) ||
+          !warp_wait(a_full + abuf, static_cast<uint32_t>(kt / ABUFS) & 1u, wc, kSiteW4TcMmaA))
+        break;
+      const uint32_t x_base = smem_u32(smem + stage * S::kStage + S::kCodes + (kt & 1) * (BT * 128));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 4 * kt + j, part = i / STEPS;
+        if (i % STEPS == 0 && !warp_wait(tempty + (part & 1), (static_cast<uint32_t>(part >> 1) & 1u) ^ 1u, wc, kSiteW4TcMmaD)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        if (elected) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            umma_bf16_tmem_a(tmem_base + S::kD + ((part & 1) * 2 + b) * BT, tmem_base + (abuf * 2 + b) * 32 + 8 * j,
+                             sdesc_sw128(x_base + j * 32, 16, 1024), idesc, i % STEPS != 0 ? 1u : 0u);
+          if (i % STEPS == STEPS - 1 || i == 4 * kts - 1) umma_commit(tfull + (part & 1));
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (elected) {
+        umma_commit(a_empty + abuf);
+        if ((kt & 1) == 1 || kt == kts - 1) umma_commit(empty + stage);
+      }
+      __syncwarp();
+    }
+    if (elected) {
+      umma_commit(drain);
+      wait_drain(drain, 0, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp < 10) {
+    // -------------------------------------------------------------------- unpacking
+    const int quad = warp & 3, block = (warp - 2) >> 2, g = static_cast<int>(lane) >> 2;
+    const int col = n0 + (gated ? 0 : 128 * block) + 32 * quad + static_cast<int>(lane);
+    const uint8_t* zeros = p.g.w[gated ? block : 0].zeros;
+    constexpr int kHalves = STEPS == 2 ? 2 : 1;  // groups of a row tile
+    constexpr int kAhead = 4;                    // row tiles whose zero points are on their way, a column a lane
+    uint32_t zv[kAhead][kHalves];
+    auto load_z = [&](int kt, uint32_t (&z)[kHalves]) {
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        const int row = min((kt0 + kt) * kW4Rows + 32 * h, K - 1);
+        z[h] = ZEROS && col < N ? __ldg(zeros + static_cast<long long>(row >> p.shift) * N + col) & 15u : 8u;
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load_z(u, zv[u]);
+    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(block * 32);
+    bool ok = true;
+    for (int base = 0; ok && base < kts; base += kAhead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int kt = base + u;
+        if (kt >= kts) break;
+        const int stage = (kt >> 1) % STAGES, abuf = kt % ABUFS;
+        if ((kt & 1) == 0 && !warp_wait(full + stage, static_cast<uint32_t>((kt >> 1) / STAGES) & 1u, wc, kSiteW4TcUnpack)) {
+          ok = false;
+          break;
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(smem + stage * S::kStage + (block * 8 + 2 * quad) * 1024 + (kt & 1) * 512) + lane;
+        const uint4 q0 = src[0], q1 = src[64];  // two column tiles
+        __syncwarp();
+        if (lane == 0 && ((kt & 1) == 1 || kt == kts - 1)) mbar_arrive(empty + stage);
+        uint32_t a[2][16];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t q[4] = {c == 0 ? q0.x : q1.x, c == 0 ? q0.y : q1.y, c == 0 ? q0.z : q1.z, c == 0 ? q0.w : q1.w};
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
+            uint32_t b0 = kW4Base8, b1 = kW4Base8;
+            if (ZEROS) {
+              b0 = w4_base(__shfl_sync(0xffffffffu, zv[u][h], 16 * c + g));
+              b1 = w4_base(__shfl_sync(0xffffffffu, zv[u][h], 16 * c + g + 8));
+            }
+#pragma unroll
+            for (int j = h * 4 / kHalves; j < (h + 1) * 4 / kHalves; ++j) w4_unpack_bf16(q[j], b0, b1, a[c] + 4 * j);
+          }
+        }
+        load_z(kt + kAhead, zv[u]);
+        if (!warp_wait(a_empty + abuf, (static_cast<uint32_t>(kt / ABUFS) & 1u) ^ 1u, wc, kSiteW4TcUnpackA)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          tmem_st_16x32(a_lane + (static_cast<uint32_t>(16 * c) << 16) + static_cast<uint32_t>(abuf * 64), a[c]);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(a_full + abuf);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------------- scaling
+    const int quad = warp & 3, block = (warp - 10) >> 2;
+    const int col = n0 + (gated ? 0 : 128 * block) + 32 * quad + static_cast<int>(lane);
+    const __nv_bfloat16* scales = static_cast<const __nv_bfloat16*>(p.g.w[gated ? block : 0].scales);
+    constexpr int kAhead = 4;
+    float sv[kAhead];
+    auto load_s = [&](int part) {
+      const int row = min(kt0 * kW4Rows + part * (16 * STEPS), K - 1);
+      return col < N ? __bfloat162float(scales[static_cast<long long>(row >> p.shift) * N + col]) : 0.f;
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) sv[u] = load_s(u);
+#pragma unroll
+    for (int j = 0; j < BT; ++j) acc[j] = 0.f;
+    const uint32_t d_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(S::kD + block * BT);
+    bool ok = true;
+    for (int base = 0; ok && base < parts; base += kAhead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int part = base + u;
+        if (part >= parts) break;
+        if (!warp_wait(tfull + (part & 1), static_cast<uint32_t>(part >> 1) & 1u, wc, kSiteW4TcScale)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const float s = sv[u];
+        sv[u] = load_s(part + kAhead);
+        uint32_t r[2][16];
+        tmem_load_16cols_async(d_lane + (part & 1) * 2 * BT, r[0]);
+#pragma unroll
+        for (int c = 0; c < BT / 16; ++c) {
+          if (c + 1 < BT / 16) tmem_load_16cols_async(d_lane + (part & 1) * 2 * BT + (c + 1) * 16, r[(c + 1) & 1]);
+          tmem_wait_ld(r[c & 1]);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[c * 16 + j] = fmaf(__uint_as_float(r[c & 1][j]), s, acc[c * 16 + j]);
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty + (part & 1));
+      }
+    }
+  }
+  // The ring is drained: its memory holds the CTA's sums [block][token][128] from here on.
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(smem);
+  if (warp >= 10) {
+    float* at = red + ((warp - 10) >> 2) * (BT * 128) + (warp & 3) * 32 + lane;
+#pragma unroll
+    for (int j = 0; j < BT; ++j) at[j * 128] = acc[j];
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc(tmem_base, S::kTmemCols);
+  }
+  cluster_sync_all();  // every CTA's sums are written (a cluster of one: a block barrier)
+  const int rows = min(BT, p.g.M - m0);
+  const uint32_t red_addr = smem_u32(red);
+  // a token of a block of columns a warp; the gated form takes both blocks together
+  for (int i = rank + ranks * warp; i < (gated ? rows : 2 * rows); i += ranks * S::kWarps) {
+    const int j = gated ? i : i >> 1, first = gated ? 0 : i & 1;
+    const int col = n0 + 128 * first + static_cast<int>(lane) * 4;
+    float v[2][4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (b == 1 && !gated) break;
+      float4 q[kW4TcRanks];
+#pragma unroll
+      for (int r = 0; r < kW4TcRanks; ++r)
+        q[r] = r < ranks ? ld_cluster_f4(mapa_shared(red_addr + (((first + b) * BT + j) * 128 + lane * 4) * 4, static_cast<uint32_t>(r)))
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[b][0] = v[b][1] = v[b][2] = v[b][3] = 0.f;
+#pragma unroll
+      for (int r = 0; r < kW4TcRanks; ++r) {  // in rank order
+        v[b][0] += q[r].x; v[b][1] += q[r].y; v[b][2] += q[r].z; v[b][3] += q[r].w;
+      }
+      const void* bias = p.g.w[b].bias;
+      if (bias != nullptr && col < N) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(bias) + col));
+        const float2 lo = unpack_bf16x2(u.x), hi = unpack_bf16x2(u.y);
+        v[b][0] += lo.x; v[b][1] += lo.y; v[b][2] += hi.x; v[b][3] += hi.y;
+      }
+    }
+    const long long at = static_cast<long long>(m0 + j) * N + col;
+    if (col >= N || !TPMLP_IN_BOUNDS(at + 3, static_cast<long long>(p.g.M) * N, kBoundsW4Out)) continue;
+    if (gated) {
+      const float2 a = __fmul2_rn(act2(p.g.act, make_float2(v[0][0], v[0][1])), make_float2(v[1][0], v[1][1]));
+      const float2 b = __fmul2_rn(act2(p.g.act, make_float2(v[0][2], v[0][3])), make_float2(v[1][2], v[1][3]));
+      v[0][0] = a.x; v[0][1] = a.y; v[0][2] = b.x; v[0][3] = b.y;
+    }
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.g.y) + at) = make_uint2(pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]));
+  }
+  __syncwarp();
+  cluster_sync_all();  // the cluster has read this CTA's sums
+}
+
+}  // namespace tpmlp
