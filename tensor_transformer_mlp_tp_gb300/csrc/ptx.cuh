@@ -124,6 +124,25 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
   return __all_sync(0xffffffffu, wait_bounded(bar, parity, w, site));
 }
 
+// The same without suspending, and with the time asked for once in many tries only: reading the global timer takes about a
+// microsecond, which a pipeline whose stages hand over to one another every few hundred cycles would pay at every step.
+__device__ __forceinline__ bool warp_wait_spin(uint64_t* bar, uint32_t parity, const WaitCtx& w, uint32_t site) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait_short(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *w.abort != 0)) return false;
+    const uint64_t now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
+    if (t0 == 0) t0 = now;
+    if (now - t0 > w.budget_ns) {
+      record_error(w, kErrTimeout, site);
+      return false;
+    }
+  }
+}
+
 // Teardown wait: same limit, but ignores the abort flag (used to drain
 // copies or MMAs still in flight before shared memory or TMEM is released).
 __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity, uint64_t budget_ns) {

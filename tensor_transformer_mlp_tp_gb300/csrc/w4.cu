@@ -529,6 +529,10 @@ cudaError_t run_w4_tc(W4TcParams& p, const DeviceCtx& ctx, cudaStream_t s) {
   p.box_rows = g.M < BT ? g.M : BT;
   if (!encode_tile_map(&p.tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.x, g.K, g.M, g.K, kW4Rows, p.box_rows, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
+  const long long words = static_cast<long long>((g.K + kW4Rows - 1) / kW4Rows) * 128;
+  for (int i = 0; i < (g.gated ? 2 : 1); ++i)
+    if (!encode_tile_map(&p.tmQ[i], CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, g.w[i].q, words, (g.N + kW4Cols - 1) / kW4Cols, words, 256, 8, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorInvalidValue;
   const int cols = g.gated ? 128 : 256, blocks = (g.N + cols - 1) / cols, tiles = (g.M + BT - 1) / BT;
   if (tiles > 65535) return cudaErrorNotSupported;
   p.ranks = few_ranks<S>(static_cast<long long>(blocks) * tiles, (g.K + kW4TcRows - 1) / kW4TcRows, kW4TcRanks, ctx);

@@ -2,8 +2,7 @@
 // shared memory.
 //
 // A CTA takes two blocks of 128 columns of W (256 columns, or the same 128 of both matrices of the gated form) as the
-// UMMA's rows and up to BT tokens as its columns; a cluster of CTAs shares K.  Warp 0 copies codes (bulk copies of a column
-// tile's rows) and X (TMA boxes), warp 1 issues, eight warps unpack: a lane's 16 bytes of a 16 x 64 tile are registers in
+// UMMA's rows and up to BT tokens as its columns; a cluster of CTAs shares K.  Warp 0 copies codes and X (TMA boxes), warp 1 issues, eight warps unpack: a lane's 16 bytes of a 16 x 64 tile are registers in
 // the order of the m16n8k16 product's A operand, which is that of tcgen05.st's 16x128b shape, so a tile goes to tensor memory
 // by one instruction as the UMMA's A operand.  Codes become bf16 q - z, exact.  Eight more warps scale: the UMMAs of a group
 // make a partial sum in TMEM, a thread has those of one column of W, one scale for all of them.  The cluster's sums are
@@ -19,7 +18,8 @@ constexpr int kW4TcRanks = 8;  // CTAs of a cluster at most
 constexpr int kW4TcRows = 128;  // of W a stage: two row tiles
 
 struct W4TcParams {
-  CUtensorMap tmX;  // boxes of 64 x box_rows
+  CUtensorMap tmX;      // boxes of 64 x box_rows
+  CUtensorMap tmQ[2];   // codes as words, a column tile a row: boxes of two row tiles (256 words) x eight column tiles
   W4Launch g;
   int ranks, box_rows, shift;
   unsigned int* err;
@@ -33,8 +33,8 @@ struct W4TcShape {
   static constexpr int kX = 2 * BT * 128;
   static constexpr int kStage = kCodes + kX;
   static constexpr int kStages = BT == 64 ? 6 : 8;
-  static constexpr int kABufs = 3;                     // unpacked row tiles in TMEM, 32 columns a block
-  static constexpr int kD = kABufs * 64;               // partial sums behind them: [buffer][block][BT]
+  static constexpr int kABufs = 2;                     // unpacked stages in TMEM, 64 columns a block
+  static constexpr int kD = kABufs * 128;              // partial sums behind them: [buffer][block][BT]
   static constexpr int kTmemCols = 512;
   static constexpr int kWarps = 2 + 8 + 8, kThreads = 32 * kWarps;
   static constexpr int kSmem = 1024 + kStages * kStage + 256;
@@ -43,13 +43,15 @@ struct W4TcShape {
   static_assert(kSmem <= 232448, "shared memory per block");
 };
 
-// 16 lanes x 32 columns into TMEM: registers 2 i and 2 i + 1 of lane 4 g + t are column 4 i + t of lanes g and g + 8.
-__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
+// 16 lanes x 64 columns into TMEM: registers 2 i and 2 i + 1 of lane 4 g + t are column 4 i + t of lanes g and g + 8.
+__device__ __forceinline__ void tmem_st_16x64(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 
@@ -100,7 +102,11 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
     fence_barrier_init();
     fence_proxy_async_smem();
   }
-  if (warp == 0 && lane == 0) tma_prefetch_desc(&p.tmX);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.tmX);
+    tma_prefetch_desc(&p.tmQ[0]);
+    if (gated) tma_prefetch_desc(&p.tmQ[1]);
+  }
   if (warp == 1) {
     tmem_alloc(tmem_slot, S::kTmemCols);
     tmem_relinquish();
@@ -115,24 +121,23 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
 
   float acc[BT];
   if (warp == 0) {
-    // Lanes 0..15 copy a column tile each, 16 and 17 the boxes of X.
-    const int block = static_cast<int>(lane) >> 3, tile = (n0 + (gated ? 0 : 128 * block)) / kW4Cols + (static_cast<int>(lane) & 7);
-    const int n_tiles = (N + kW4Cols - 1) / kW4Cols;
-    const bool have = lane < 16 && tile < n_tiles;
-    const int count = __popc(__ballot_sync(0xffffffffu, have));
-    const uint4* src = have ? p.g.w[gated ? block : 0].q + (static_cast<long long>(tile) * k_tiles + kt0) * 32 : nullptr;
+    // four boxes a stage (past the matrix's ends they fill zeros): single column tiles by bulk copies of 1 KB, 16 of them, took
+    // longer to issue than to multiply
     const uint64_t pol = policy_evict_normal();
+    const int tile = n0 / kW4Cols;
     uint32_t issued = 0, issued_parity = 0;
     for (int s = 0; s < st1 - st0; ++s) {
-      const int stage = s % STAGES, rows = min(2, kts - 2 * s);  // row tiles
+      const int stage = s % STAGES, at = kt0 + 2 * s;  // row tile
       const uint32_t phase = static_cast<uint32_t>(s / STAGES) & 1u;
-      if (!warp_wait(empty + stage, phase ^ 1u, wc, kSiteW4TcProducer)) break;
+      if (!warp_wait_spin(empty + stage, phase ^ 1u, wc, kSiteW4TcProducer)) break;
       uint8_t* dst = smem + stage * S::kStage;
-      if (lane == 0) mbar_arrive_expect_tx(full + stage, static_cast<uint32_t>(rows * (count * 512 + p.box_rows * 128)));
-      __syncwarp();
-      if (have) bulk_load(dst + lane * 1024, src + s * 64, static_cast<uint32_t>(rows) * 512u, full + stage);
-      else if (lane >= 16 && lane < 16 + static_cast<uint32_t>(rows))
-        tma_load_2d(dst + S::kCodes + (lane - 16) * (BT * 128), &p.tmX, full + stage, (kt0 + 2 * s + static_cast<int>(lane) - 16) * kW4Rows, m0, pol);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(full + stage, static_cast<uint32_t>(S::kCodes + 2 * p.box_rows * 128));
+        for (int b = 0; b < 2; ++b)
+          tma_load_2d(dst + b * 8192, &p.tmQ[gated ? b : 0], full + stage, at * 128, tile + (gated ? 0 : 8 * b), pol);
+        for (int r = 0; r < 2; ++r)
+          tma_load_2d(dst + S::kCodes + r * (BT * 128), &p.tmX, full + stage, (at + r) * kW4Rows, m0, pol);
+      }
       __syncwarp();
       issued |= 1u << stage;
       issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -144,16 +149,17 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
     constexpr uint32_t idesc = idesc_bf16_f32(128, BT, false, false);
     const bool elected = elect_one();
     bool ok = true;
-    for (int kt = 0; ok && kt < kts; ++kt) {
-      const int stage = (kt >> 1) % STAGES, abuf = kt % ABUFS;
-      if (((kt & 1) == 0 && !warp_wait(full + stage, static_cast<uint32_t>((kt >> 1) / STAGES) & 1u, wc, kSiteW4TcMmaX)) ||
-          !warp_wait(a_full + abuf, static_cast<uint32_t>(kt / ABUFS) & 1u, wc, kSiteW4TcMmaA))
+    for (int st = 0; ok && st < st1 - st0; ++st) {
+      const int stage = st % STAGES, abuf = st % ABUFS, steps = 4 * min(2, kts - 2 * st);
+      if (!warp_wait_spin(full + stage, static_cast<uint32_t>(st / STAGES) & 1u, wc, kSiteW4TcMmaX) ||
+          !warp_wait_spin(a_full + abuf, static_cast<uint32_t>(st / ABUFS) & 1u, wc, kSiteW4TcMmaA))
         break;
-      const uint32_t x_base = smem_u32(smem + stage * S::kStage + S::kCodes + (kt & 1) * (BT * 128));
+      const uint32_t x_base = smem_u32(smem + stage * S::kStage + S::kCodes);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = 4 * kt + j, part = i / STEPS;
-        if (i % STEPS == 0 && !warp_wait(tempty + (part & 1), (static_cast<uint32_t>(part >> 1) & 1u) ^ 1u, wc, kSiteW4TcMmaD)) {
+      for (int j = 0; j < 8; ++j) {
+        if (j >= steps) break;
+        const int i = 8 * st + j, part = i / STEPS;
+        if (j % STEPS == 0 && !warp_wait_spin(tempty + (part & 1), (static_cast<uint32_t>(part >> 1) & 1u) ^ 1u, wc, kSiteW4TcMmaD)) {
           ok = false;
           break;
         }
@@ -161,16 +167,16 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
         if (elected) {
 #pragma unroll
           for (int b = 0; b < 2; ++b)
-            umma_bf16_tmem_a(tmem_base + S::kD + ((part & 1) * 2 + b) * BT, tmem_base + (abuf * 2 + b) * 32 + 8 * j,
-                             sdesc_sw128(x_base + j * 32, 16, 1024), idesc, i % STEPS != 0 ? 1u : 0u);
-          if (i % STEPS == STEPS - 1 || i == 4 * kts - 1) umma_commit(tfull + (part & 1));
+            umma_bf16_tmem_a(tmem_base + S::kD + ((part & 1) * 2 + b) * BT, tmem_base + (abuf * 2 + b) * 64 + 8 * j,
+                             sdesc_sw128(x_base + (j >> 2) * (BT * 128) + (j & 3) * 32, 16, 1024), idesc, j % STEPS != 0 ? 1u : 0u);
+          if (j % STEPS == STEPS - 1 || j == steps - 1) umma_commit(tfull + (part & 1));
         }
         __syncwarp();
       }
       if (!ok) break;
       if (elected) {
         umma_commit(a_empty + abuf);
-        if ((kt & 1) == 1 || kt == kts - 1) umma_commit(empty + stage);
+        umma_commit(empty + stage);
       }
       __syncwarp();
     }
@@ -184,58 +190,64 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
     const int quad = warp & 3, block = (warp - 2) >> 2, g = static_cast<int>(lane) >> 2;
     const int col = n0 + (gated ? 0 : 128 * block) + 32 * quad + static_cast<int>(lane);
     const uint8_t* zeros = p.g.w[gated ? block : 0].zeros;
-    constexpr int kHalves = STEPS == 2 ? 2 : 1;  // groups of a row tile
-    constexpr int kAhead = 4;                    // row tiles whose zero points are on their way, a column a lane
-    uint32_t zv[kAhead][kHalves];
-    auto load_z = [&](int kt, uint32_t (&z)[kHalves]) {
+    constexpr int kGroups = 8 / STEPS;  // of a stage
+    constexpr int kAhead = 2;           // stages whose zero points are on their way, a column a lane
+    uint32_t zv[kAhead][kGroups];
+    auto load_z = [&](int st, uint32_t (&z)[kGroups]) {
 #pragma unroll
-      for (int h = 0; h < kHalves; ++h) {
-        const int row = min((kt0 + kt) * kW4Rows + 32 * h, K - 1);
-        z[h] = ZEROS && col < N ? __ldg(zeros + static_cast<long long>(row >> p.shift) * N + col) & 15u : 8u;
+      for (int h = 0; h < kGroups; ++h) {
+        const int row = min((kt0 + 2 * st) * kW4Rows + 16 * STEPS * h, K - 1);
+        z[h] = ZEROS && col < N ? __ldg(zeros + static_cast<long long>(row >> p.shift) * N + col) : 8u;
       }
     };
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) load_z(u, zv[u]);
-    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(block * 32);
+    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(block * 64);
     bool ok = true;
-    for (int base = 0; ok && base < kts; base += kAhead) {
+    for (int base = 0; ok && base < st1 - st0; base += kAhead) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int kt = base + u;
-        if (kt >= kts) break;
-        const int stage = (kt >> 1) % STAGES, abuf = kt % ABUFS;
-        if ((kt & 1) == 0 && !warp_wait(full + stage, static_cast<uint32_t>((kt >> 1) / STAGES) & 1u, wc, kSiteW4TcUnpack)) {
+        const int st = base + u;
+        if (st >= st1 - st0) break;
+        const int stage = st % STAGES, abuf = st % ABUFS;
+        if (!warp_wait_spin(full + stage, static_cast<uint32_t>(st / STAGES) & 1u, wc, kSiteW4TcUnpack)) {
           ok = false;
           break;
         }
-        const uint4* src = reinterpret_cast<const uint4*>(smem + stage * S::kStage + (block * 8 + 2 * quad) * 1024 + (kt & 1) * 512) + lane;
-        const uint4 q0 = src[0], q1 = src[64];  // two column tiles
-        __syncwarp();
-        if (lane == 0 && ((kt & 1) == 1 || kt == kts - 1)) mbar_arrive(empty + stage);
-        uint32_t a[2][16];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t q[4] = {c == 0 ? q0.x : q1.x, c == 0 ? q0.y : q1.y, c == 0 ? q0.z : q1.z, c == 0 ? q0.w : q1.w};
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h) {
-            uint32_t b0 = kW4Base8, b1 = kW4Base8;
-            if (ZEROS) {
-              b0 = w4_base(__shfl_sync(0xffffffffu, zv[u][h], 16 * c + g));
-              b1 = w4_base(__shfl_sync(0xffffffffu, zv[u][h], 16 * c + g + 8));
-            }
-#pragma unroll
-            for (int j = h * 4 / kHalves; j < (h + 1) * 4 / kHalves; ++j) w4_unpack_bf16(q[j], b0, b1, a[c] + 4 * j);
-          }
-        }
-        load_z(kt + kAhead, zv[u]);
-        if (!warp_wait(a_empty + abuf, (static_cast<uint32_t>(kt / ABUFS) & 1u) ^ 1u, wc, kSiteW4TcUnpackA)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after_sync();
+        // two column tiles of two row tiles (what the second holds of a last, single one is not multiplied)
+        const uint4* src = reinterpret_cast<const uint4*>(smem + stage * S::kStage + (block * 8 + 2 * quad) * 1024) + lane;
+        uint4 q4[2][2];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          tmem_st_16x32(a_lane + (static_cast<uint32_t>(16 * c) << 16) + static_cast<uint32_t>(abuf * 64), a[c]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) q4[c][r] = src[c * 64 + r * 32];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + stage);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t q[8] = {q4[c][0].x, q4[c][0].y, q4[c][0].z, q4[c][0].w, q4[c][1].x, q4[c][1].y, q4[c][1].z, q4[c][1].w};
+          uint32_t a[32];
+#pragma unroll
+          for (int h = 0; h < kGroups; ++h) {
+            uint32_t b0 = kW4Base8, b1 = kW4Base8;
+            if (ZEROS) {
+              b0 = w4_base(__shfl_sync(0xffffffffu, zv[u][h], 16 * c + g) & 15u);
+              b1 = w4_base(__shfl_sync(0xffffffffu, zv[u][h], 16 * c + g + 8) & 15u);
+            }
+#pragma unroll
+            for (int j = h * STEPS; j < (h + 1) * STEPS; ++j) w4_unpack_bf16(q[j], b0, b1, a + 4 * j);
+          }
+          if (c == 0) {
+            if (!warp_wait_spin(a_empty + abuf, (static_cast<uint32_t>(st / ABUFS) & 1u) ^ 1u, wc, kSiteW4TcUnpackA)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+          }
+          tmem_st_16x64(a_lane + (static_cast<uint32_t>(16 * c) << 16) + static_cast<uint32_t>(abuf * 128), a);
+        }
+        if (!ok) break;
+        load_z(st + kAhead, zv[u]);
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
@@ -246,12 +258,12 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
     // -------------------------------------------------------------------- scaling
     const int quad = warp & 3, block = (warp - 10) >> 2;
     const int col = n0 + (gated ? 0 : 128 * block) + 32 * quad + static_cast<int>(lane);
-    const __nv_bfloat16* scales = static_cast<const __nv_bfloat16*>(p.g.w[gated ? block : 0].scales);
+    const uint16_t* scales = static_cast<const uint16_t*>(p.g.w[gated ? block : 0].scales);
     constexpr int kAhead = 4;
-    float sv[kAhead];
+    uint16_t sv[kAhead];  // as they are: a conversion here would wait for the load
     auto load_s = [&](int part) {
       const int row = min(kt0 * kW4Rows + part * (16 * STEPS), K - 1);
-      return col < N ? __bfloat162float(scales[static_cast<long long>(row >> p.shift) * N + col]) : 0.f;
+      return col < N ? __ldg(scales + static_cast<long long>(row >> p.shift) * N + col) : uint16_t(0);
     };
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) sv[u] = load_s(u);
@@ -264,12 +276,12 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
       for (int u = 0; u < kAhead; ++u) {
         const int part = base + u;
         if (part >= parts) break;
-        if (!warp_wait(tfull + (part & 1), static_cast<uint32_t>(part >> 1) & 1u, wc, kSiteW4TcScale)) {
+        if (!warp_wait_spin(tfull + (part & 1), static_cast<uint32_t>(part >> 1) & 1u, wc, kSiteW4TcScale)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const float s = sv[u];
+        const float s = __uint_as_float(static_cast<uint32_t>(sv[u]) << 16);
         sv[u] = load_s(part + kAhead);
         uint32_t r[2][16];
         tmem_load_16cols_async(d_lane + (part & 1) * 2 * BT, r[0]);
