@@ -37,7 +37,8 @@ struct W4TcShape {
   static constexpr int kD = kABufs * 128;              // partial sums behind them: [buffer][block][BT]
   static constexpr int kTmemCols = 512;
   static constexpr int kWarps = 2 + 8 + 8, kThreads = 32 * kWarps;
-  static constexpr int kSmem = 1024 + kStages * kStage + 256;
+  static constexpr int kSlots = 8 * 4 * 4 * (64 + 32);  // scales and zero points in flight: [warp][slot][group]
+  static constexpr int kSmem = 1024 + kStages * kStage + kSlots + 256;
   static_assert(kD + 4 * BT <= kTmemCols, "tensor memory");
   static_assert(kStages * kStage >= 2 * BT * 128 * 4, "the sums are joined in the ring's memory");
   static_assert(kSmem <= 232448, "shared memory per block");
@@ -62,7 +63,9 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
   constexpr int STAGES = S::kStages, ABUFS = S::kABufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * S::kStage);
+  uint8_t* smem_s = smem + STAGES * S::kStage;
+  uint8_t* smem_z = smem_s + 8 * 4 * 4 * 64;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem_s + S::kSlots);
   uint64_t* empty = full + STAGES;
   uint64_t* a_full = empty + STAGES;
   uint64_t* a_empty = a_full + ABUFS;
@@ -156,20 +159,24 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
         break;
       const uint32_t x_base = smem_u32(smem + stage * S::kStage + S::kCodes);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j >= steps) break;
-        const int i = 8 * st + j, part = i / STEPS;
-        if (j % STEPS == 0 && !warp_wait_spin(tempty + (part & 1), (static_cast<uint32_t>(part >> 1) & 1u) ^ 1u, wc, kSiteW4TcMmaD)) {
+      for (int h = 0; h < 8 / STEPS; ++h) {  // groups
+        if (h * STEPS >= steps) break;
+        const int part = 8 / STEPS * st + h;
+        if (!warp_wait_spin(tempty + (part & 1), (static_cast<uint32_t>(part >> 1) & 1u) ^ 1u, wc, kSiteW4TcMmaD)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
         if (elected) {
+          const uint32_t d = tmem_base + S::kD + (part & 1) * 2 * BT, a = tmem_base + abuf * 128;
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
-            umma_bf16_tmem_a(tmem_base + S::kD + ((part & 1) * 2 + b) * BT, tmem_base + (abuf * 2 + b) * 64 + 8 * j,
-                             sdesc_sw128(x_base + (j >> 2) * (BT * 128) + (j & 3) * 32, 16, 1024), idesc, j % STEPS != 0 ? 1u : 0u);
-          if (j % STEPS == STEPS - 1 || j == steps - 1) umma_commit(tfull + (part & 1));
+          for (int j = h * STEPS; j < (h + 1) * STEPS; ++j) {
+            if (j >= steps) break;  // a last, single row tile
+            const uint64_t x = sdesc_sw128(x_base + (j >> 2) * (BT * 128) + (j & 3) * 32, 16, 1024);
+            umma_bf16_tmem_a(d, a + 8 * j, x, idesc, j % STEPS != 0 ? 1u : 0u);
+            umma_bf16_tmem_a(d + BT, a + 64 + 8 * j, x, idesc, j % STEPS != 0 ? 1u : 0u);
+          }
+          umma_commit(tfull + (part & 1));
         }
         __syncwarp();
       }
@@ -188,32 +195,36 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
   } else if (warp < 10) {
     // -------------------------------------------------------------------- unpacking
     const int quad = warp & 3, block = (warp - 2) >> 2, g = static_cast<int>(lane) >> 2;
-    const int col = n0 + (gated ? 0 : 128 * block) + 32 * quad + static_cast<int>(lane);
+    const int col = n0 + (gated ? 0 : 128 * block) + 32 * quad;  // the quadrant's first
     const uint8_t* zeros = p.g.w[gated ? block : 0].zeros;
     constexpr int kGroups = 8 / STEPS;  // of a stage
-    constexpr int kAhead = 2;           // stages whose zero points are on their way, a column a lane
-    uint32_t zv[kAhead][kGroups];
-    auto load_z = [&](int st, uint32_t (&z)[kGroups]) {
-#pragma unroll
-      for (int h = 0; h < kGroups; ++h) {
-        const int row = min((kt0 + 2 * st) * kW4Rows + 16 * STEPS * h, K - 1);
-        z[h] = ZEROS && col < N ? __ldg(zeros + static_cast<long long>(row >> p.shift) * N + col) : 8u;
+    // Zero points of the quadrant's columns three stages ahead, by copies that no register waits for: a load among the
+    // others makes them wait for it.
+    uint8_t* slots = smem_z + (warp - 2) * (4 * kGroups * 32);
+    auto fetch = [&](int st) {
+      if (ZEROS && st < st1 - st0 && lane < 4 * kGroups) {
+        const int row = min((kt0 + 2 * st) * kW4Rows + 16 * STEPS * (static_cast<int>(lane) >> 2), K - 1), at = col + 8 * (static_cast<int>(lane) & 3);
+        cp_async<8>(slots + (st & 3) * (kGroups * 32) + lane * 8, zeros + static_cast<long long>(row >> p.shift) * N + (at < N ? at : 0), at < N ? 8 : 0);
       }
+      if (ZEROS) cp_async_commit();
     };
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) load_z(u, zv[u]);
+    for (int u = 0; u < 3; ++u) fetch(u);
     const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(block * 64);
     bool ok = true;
-    for (int base = 0; ok && base < st1 - st0; base += kAhead) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int st = base + u;
-        if (st >= st1 - st0) break;
+    for (int st = 0; ok && st < st1 - st0; ++st) {
+      {
         const int stage = st % STAGES, abuf = st % ABUFS;
         if (!warp_wait_spin(full + stage, static_cast<uint32_t>(st / STAGES) & 1u, wc, kSiteW4TcUnpack)) {
           ok = false;
           break;
         }
+        if (ZEROS) {
+          cp_async_wait<2>();
+          __syncwarp();  // this stage's are there for all lanes, and the slot before has been read
+          fetch(st + 3);
+        }
+        const uint8_t* zs = slots + (st & 3) * (kGroups * 32) + g;
         // two column tiles of two row tiles (what the second holds of a last, single one is not multiplied)
         const uint4* src = reinterpret_cast<const uint4*>(smem + stage * S::kStage + (block * 8 + 2 * quad) * 1024) + lane;
         uint4 q4[2][2];
@@ -231,8 +242,8 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
           for (int h = 0; h < kGroups; ++h) {
             uint32_t b0 = kW4Base8, b1 = kW4Base8;
             if (ZEROS) {
-              b0 = w4_base(__shfl_sync(0xffffffffu, zv[u][h], 16 * c + g) & 15u);
-              b1 = w4_base(__shfl_sync(0xffffffffu, zv[u][h], 16 * c + g + 8) & 15u);
+              b0 = w4_base(zs[h * 32 + 16 * c] & 15u);
+              b1 = w4_base(zs[h * 32 + 16 * c + 8] & 15u);
             }
 #pragma unroll
             for (int j = h * STEPS; j < (h + 1) * STEPS; ++j) w4_unpack_bf16(q[j], b0, b1, a + 4 * j);
@@ -247,7 +258,6 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
           tmem_st_16x64(a_lane + (static_cast<uint32_t>(16 * c) << 16) + static_cast<uint32_t>(abuf * 128), a);
         }
         if (!ok) break;
-        load_z(st + kAhead, zv[u]);
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
@@ -257,32 +267,39 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
   } else {
     // -------------------------------------------------------------------- scaling
     const int quad = warp & 3, block = (warp - 10) >> 2;
-    const int col = n0 + (gated ? 0 : 128 * block) + 32 * quad + static_cast<int>(lane);
+    const int col = n0 + (gated ? 0 : 128 * block) + 32 * quad;  // the quadrant's first
     const uint16_t* scales = static_cast<const uint16_t*>(p.g.w[gated ? block : 0].scales);
-    constexpr int kAhead = 4;
-    uint16_t sv[kAhead];  // as they are: a conversion here would wait for the load
-    auto load_s = [&](int part) {
-      const int row = min(kt0 * kW4Rows + part * (16 * STEPS), K - 1);
-      return col < N ? __ldg(scales + static_cast<long long>(row >> p.shift) * N + col) : uint16_t(0);
+    constexpr int kGroups = 8 / STEPS;  // of a stage
+    // the quadrant's scales, three stages ahead as the zero points are
+    uint8_t* slots = smem_s + (warp - 10) * (4 * kGroups * 64);
+    auto fetch = [&](int st) {
+      if (st < st1 - st0 && lane < 4 * kGroups) {
+        const int row = min((kt0 + 2 * st) * kW4Rows + 16 * STEPS * (static_cast<int>(lane) >> 2), K - 1), at = col + 8 * (static_cast<int>(lane) & 3);
+        cp_async<16>(slots + (st & 3) * (kGroups * 64) + lane * 16, scales + static_cast<long long>(row >> p.shift) * N + (at < N ? at : 0), at < N ? 16 : 0);
+      }
+      cp_async_commit();
     };
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) sv[u] = load_s(u);
+    for (int u = 0; u < 3; ++u) fetch(u);
 #pragma unroll
     for (int j = 0; j < BT; ++j) acc[j] = 0.f;
     const uint32_t d_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(S::kD + block * BT);
     bool ok = true;
-    for (int base = 0; ok && base < parts; base += kAhead) {
+    for (int st = 0; ok && st < st1 - st0; ++st) {
+      cp_async_wait<2>();
+      __syncwarp();
+      fetch(st + 3);
+      const uint16_t* ss = reinterpret_cast<const uint16_t*>(slots + (st & 3) * (kGroups * 64)) + lane;
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int part = base + u;
+      for (int h = 0; h < kGroups; ++h) {
+        const int part = kGroups * st + h;
         if (part >= parts) break;
         if (!warp_wait_spin(tfull + (part & 1), static_cast<uint32_t>(part >> 1) & 1u, wc, kSiteW4TcScale)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const float s = __uint_as_float(static_cast<uint32_t>(sv[u]) << 16);
-        sv[u] = load_s(part + kAhead);
+        const float s = __uint_as_float(static_cast<uint32_t>(ss[h * 32]) << 16);
         uint32_t r[2][16];
         tmem_load_16cols_async(d_lane + (part & 1) * 2 * BT, r[0]);
 #pragma unroll
