@@ -1716,7 +1716,7 @@ tpmlp_status tpmlp_quantize_w4(const void* W, int64_t K, int64_t N, int group, v
   if (st != TPMLP_OK) return st;
   if (N == 0 || K == 0) return TPMLP_OK;
   if (!ptrs_ok({W, Q, scales}) || !opt_ok(zeros)) return TPMLP_ERR_INVALID_ARG;
-  if ((K + kW4Rows - 1) / kW4Rows > 65535 / 2) return TPMLP_ERR_UNSUPPORTED;
+  if ((K + 127) / 128 > 65535) return TPMLP_ERR_UNSUPPORTED;
   const W4Pack p{const_cast<void*>(W), static_cast<uint4*>(Q), scales, zeros, static_cast<int>(K), static_cast<int>(N), group};
   return cuda_status(launch_quantize_w4(p, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -1727,7 +1727,7 @@ tpmlp_status tpmlp_dequantize_w4(const void* Q, const void* scales, const uint8_
   if (st != TPMLP_OK) return st;
   if (N == 0 || K == 0) return TPMLP_OK;
   if (!ptrs_ok({W, Q, scales}) || !opt_ok(zeros)) return TPMLP_ERR_INVALID_ARG;
-  if ((K + kW4Rows - 1) / kW4Rows > 65535 / 2) return TPMLP_ERR_UNSUPPORTED;
+  if ((K + 127) / 128 > 65535) return TPMLP_ERR_UNSUPPORTED;
   const W4Pack p{W, static_cast<uint4*>(const_cast<void*>(Q)), const_cast<void*>(scales), const_cast<uint8_t*>(zeros),
                  static_cast<int>(K), static_cast<int>(N), group};
   return cuda_status(launch_dequantize_w4(p, reinterpret_cast<cudaStream_t>(stream)));

@@ -32,6 +32,9 @@ enum BoundsSite : uint32_t {
   kBoundsBlockBias = 134,    // its bias
   kBoundsGemmFew = 135,      // the few-row bf16 GEMM's outputs
   kBoundsW4Out = 140,        // products with 4-bit weights: the output
+  kBoundsW4Scales = 141,     // the 4-bit quantiser's scales and zero points
+  kBoundsW4Codes = 142,      // its codes
+  kBoundsW4Weights = 143,    // its inverse's output
 };
 
 #ifdef TPMLP_DEBUG_BOUNDS

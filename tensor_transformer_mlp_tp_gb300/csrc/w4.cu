@@ -451,56 +451,169 @@ cudaError_t launch_w4_few(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t 
   return z ? run_w4_few<MATS, TT, false, true>(g, ctx, s) : run_w4_few<MATS, TT, false, false>(g, ctx, s);
 }
 
-// One warp a group of a column tile: lane l < 16 takes column l.
-__global__ void __launch_bounds__(128) k_quantize_w4_scales(const __grid_constant__ W4Pack p) {
-  const int col = blockIdx.x * blockDim.x + threadIdx.x, grp = blockIdx.y;
-  if (col >= p.N) return;
-  float lo = 0.f, hi = 0.f;
-  for (int k = grp * p.group; k < min(p.K, (grp + 1) * p.group); ++k) {
-    const float v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.w)[static_cast<long long>(k) * p.N + col]);
-    lo = fminf(lo, v);
-    hi = fmaxf(hi, v);
-  }
-  const float span = fminf(fmaxf(p.zeros != nullptr ? hi - lo : fmaxf(hi, -lo), kW4Tiny), kW4Big);
-  const __nv_bfloat16 s = __float2bfloat16_rn(span / (p.zeros != nullptr ? 15.f : 7.f));
-  const long long at = static_cast<long long>(grp) * p.N + col;
-  static_cast<__nv_bfloat16*>(p.scales)[at] = s;
-  if (p.zeros != nullptr) p.zeros[at] = static_cast<uint8_t>(fminf(fmaxf(rintf(-lo / __bfloat162float(s)), 0.f), 15.f));
+// 16 bytes that are read once.
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
 }
 
-// One thread a word of a tile.
-__global__ void __launch_bounds__(128) k_quantize_w4_codes(const __grid_constant__ W4Pack p) {
-  const int word = threadIdx.x, l = word >> 2, j = word & 3, g = l >> 2, t = l & 3;
-  uint32_t w = 0;
-  for (int b = 0; b < 8; ++b) {
-    const int i = b & 3, h = b >> 2;
-    const int n = blockIdx.x * kW4Cols + 8 * (i & 1) + g, k = blockIdx.y * kW4Rows + 16 * j + 8 * (i >> 1) + 2 * t + h;
-    uint32_t q = 8;
-    if (n < p.N && k < p.K) {
-      const long long at = static_cast<long long>(k / p.group) * p.N + n;
-      float v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.w)[static_cast<long long>(k) * p.N + n]);
-      if (isnan(v)) v = 0.f;
-      const float s = __bfloat162float(static_cast<const __nv_bfloat16*>(p.scales)[at]);
-      const float z = p.zeros != nullptr ? static_cast<float>(p.zeros[at]) : 8.f;
-      q = static_cast<uint32_t>(fminf(fmaxf(rintf(fminf(fmaxf(v / s, -16.f), 16.f)) + z, 0.f), 15.f));
+// The quantiser and its inverse: a block takes 128 rows x 64 columns, a whole number of groups and 4 x 2 tiles, through
+// shared memory, rows there 34 words apart: the threads of a tile, which read columns g and rows 2 t, then hit 16 banks.
+constexpr int kPackRows = 128, kPackCols = 64, kPackPitch = 68;  // elements
+
+// Largest and smallest of every column of 16 rows (two columns a thread), joined to groups; scale and zero point of a
+// group; then a tile's words, a lane's 16 bytes a thread.  The quotient of a code is w (1 / s), off by less than 2^-19; a
+// quotient of two bf16 numbers is a half of an odd number or at least 1/1020 away from one, so that rounding it to
+// multiples of 2^-10 first gives the division's code.
+// What bounds it: HBM.  4096 x 16384, 167 MB: see launch_quantize_w4.
+template <bool ZEROS>
+__global__ void __launch_bounds__(256) k_quantize_w4(const __grid_constant__ W4Pack p) {
+  __shared__ __align__(16) __nv_bfloat16 tile[kPackRows * kPackPitch];
+  __shared__ __nv_bfloat162 low[8][32], high[8][32];  // [16 rows][two columns]
+  __shared__ float s_inv[4][kPackCols];               // [group of the block][column]
+  __shared__ int s_zero[4][kPackCols];
+  const int n0 = blockIdx.x * kPackCols, k0 = blockIdx.y * kPackRows;
+  const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 32 + (threadIdx.x >> 3), c = (threadIdx.x & 7) * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (k0 + r < p.K && n0 + c < p.N) v = __ldg(reinterpret_cast<const uint4*>(w + static_cast<long long>(k0 + r) * p.N + n0 + c));
+    uint32_t* u = &v.x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {  // NaN to zero
+      const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(u + e);
+      u[e] &= __heq2_mask(x, x);
     }
-    w |= q << (4 * i + 16 * h);
+    uint2* dst = reinterpret_cast<uint2*>(tile + r * kPackPitch + c);
+    dst[0] = make_uint2(v.x, v.y);
+    dst[1] = make_uint2(v.z, v.w);
   }
-  reinterpret_cast<uint32_t*>(p.q)[(static_cast<long long>(blockIdx.x) * gridDim.y + blockIdx.y) * 128 + word] = w;
+  __syncthreads();
+  {
+    const int c2 = threadIdx.x & 31, seg = threadIdx.x >> 5;
+    __nv_bfloat162 lo = __floats2bfloat162_rn(0.f, 0.f), hi = lo;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(tile + (seg * 16 + r) * kPackPitch + c2 * 2);
+      lo = __hmin2(lo, v);
+      hi = __hmax2(hi, v);
+    }
+    low[seg][c2] = lo;
+    high[seg][c2] = hi;
+  }
+  __syncthreads();
+  const int groups = kPackRows / p.group, segs = p.group / 16;  // of the block; of a group
+  for (int i = threadIdx.x; i < groups * kPackCols; i += blockDim.x) {
+    const int c = i % kPackCols, grp = i / kPackCols;
+    float lo = 0.f, hi = 0.f;
+    for (int q = grp * segs; q < (grp + 1) * segs; ++q) {
+      lo = fminf(lo, __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(low[q])[c]));
+      hi = fmaxf(hi, __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(high[q])[c]));
+    }
+    const float span = fminf(fmaxf(ZEROS ? hi - lo : fmaxf(hi, -lo), kW4Tiny), kW4Big);
+    const __nv_bfloat16 s = __float2bfloat16_rn(span / (ZEROS ? 15.f : 7.f));
+    const int z = ZEROS ? static_cast<int>(fminf(fmaxf(rintf(-lo / __bfloat162float(s)), 0.f), 15.f)) : 8;
+    s_inv[grp][c] = 1.f / __bfloat162float(s);
+    s_zero[grp][c] = z;
+    const int col = n0 + c, row = k0 + grp * p.group;
+    if (col < p.N && row < p.K) {
+      const long long at = static_cast<long long>(row / p.group) * p.N + col;
+      if (TPMLP_IN_BOUNDS(at, static_cast<long long>((p.K + p.group - 1) / p.group) * p.N, kBoundsW4Scales)) {
+        static_cast<__nv_bfloat16*>(p.scales)[at] = s;
+        if (ZEROS) p.zeros[at] = static_cast<uint8_t>(z);
+      }
+    }
+  }
+  __syncthreads();
+  const int kt = threadIdx.x >> 7, ct = threadIdx.x >> 5 & 3, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int n_tile = blockIdx.x * 4 + ct, k_tile = blockIdx.y * 2 + kt;
+  const int n_tiles = (p.N + kW4Cols - 1) / kW4Cols, k_tiles = (p.K + kW4Rows - 1) / kW4Rows;
+  if (n_tile >= n_tiles || k_tile >= k_tiles) return;
+  uint32_t words[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int grp = (kt * kW4Rows + 16 * j) / p.group;
+    uint32_t word = 0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int n = ct * kW4Cols + 8 * c + g;
+      const float inv = s_inv[grp][n];
+      const int z = s_zero[grp][n];
+      const float lo = static_cast<float>(-z), hi = static_cast<float>(15 - z);
+      const __nv_bfloat16* src = tile + (kt * kW4Rows + 16 * j + 2 * t) * kPackPitch + n;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {  // rows 2 t + h and 8 + 2 t + h
+        const int h = b & 1, half = b >> 1;
+        float y = __bfloat162float(src[(8 * half + h) * kPackPitch]) * inv;
+        y = fminf(fmaxf(y, lo), hi);
+        y = (y + 12288.f) - 12288.f;
+        // the low bits of 2^23 + 2^22 + rint(y)
+        word += (__float_as_uint(y + 12582912.f) - 0x4B400000u + static_cast<uint32_t>(z)) << (4 * (c + 2 * half) + 16 * h);
+      }
+    }
+    if (ZEROS && ((k_tile + 1) * kW4Rows > p.K || (n_tile + 1) * kW4Cols > p.N)) {  // places past the matrix hold 8, not z
+      for (int b = 0; b < 8; ++b) {
+        const int i = b & 3, h = b >> 2;
+        if (n_tile * kW4Cols + 8 * (i & 1) + g >= p.N || k_tile * kW4Rows + 16 * j + 8 * (i >> 1) + 2 * t + h >= p.K)
+          word = (word & ~(15u << (4 * i + 16 * h))) | 8u << (4 * i + 16 * h);
+      }
+    }
+    words[j] = word;
+  }
+  const long long at = (static_cast<long long>(n_tile) * k_tiles + k_tile) * 32 + lane;
+  if (TPMLP_IN_BOUNDS(at, static_cast<long long>(n_tiles) * k_tiles * 32, kBoundsW4Codes))
+    p.q[at] = make_uint4(words[0], words[1], words[2], words[3]);
 }
 
-__global__ void __launch_bounds__(128) k_dequantize_w4(const __grid_constant__ W4Pack p) {
-  const int word = threadIdx.x, l = word >> 2, j = word & 3, g = l >> 2, t = l & 3;
-  const uint32_t w = reinterpret_cast<const uint32_t*>(p.q)[(static_cast<long long>(blockIdx.x) * gridDim.y + blockIdx.y) * 128 + word];
-  for (int b = 0; b < 8; ++b) {
-    const int i = b & 3, h = b >> 2;
-    const int n = blockIdx.x * kW4Cols + 8 * (i & 1) + g, k = blockIdx.y * kW4Rows + 16 * j + 8 * (i >> 1) + 2 * t + h;
-    if (n < p.N && k < p.K) {
-      const long long at = static_cast<long long>(k / p.group) * p.N + n;
-      const float s = __bfloat162float(static_cast<const __nv_bfloat16*>(p.scales)[at]);
-      const int z = p.zeros != nullptr ? p.zeros[at] : 8;
-      static_cast<__nv_bfloat16*>(p.w)[static_cast<long long>(k) * p.N + n] =
-          __float2bfloat16_rn(s * static_cast<float>(static_cast<int>(w >> (4 * i + 16 * h) & 15u) - z));
+// A thread's 32 codes to bf16 in pairs of rows: (q - z) s is exact before its one rounding.
+template <bool ZEROS>
+__global__ void __launch_bounds__(256) k_dequantize_w4(const __grid_constant__ W4Pack p) {
+  __shared__ __align__(16) __nv_bfloat16 tile[kPackRows * kPackPitch];
+  const int n0 = blockIdx.x * kPackCols, k0 = blockIdx.y * kPackRows;
+  const int kt = threadIdx.x >> 7, ct = threadIdx.x >> 5 & 3, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int n_tile = blockIdx.x * 4 + ct, k_tile = blockIdx.y * 2 + kt;
+  const int n_tiles = (p.N + kW4Cols - 1) / kW4Cols, k_tiles = (p.K + kW4Rows - 1) / kW4Rows;
+  if (n_tile < n_tiles && k_tile < k_tiles) {
+    const uint4 q4 = ld_stream(p.q + (static_cast<long long>(n_tile) * k_tiles + k_tile) * 32 + lane);
+    const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
+    const int last = (p.K + p.group - 1) / p.group - 1;
+    __nv_bfloat162 s[2][2];  // [half of the row tile][columns g, g + 8]
+    uint32_t base[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = n_tile * kW4Cols + 8 * c + g, grp = min((k_tile * kW4Rows + 32 * h) / p.group, last);
+        const long long at = static_cast<long long>(grp) * p.N + min(col, p.N - 1);
+        const __nv_bfloat16 v = static_cast<const __nv_bfloat16*>(p.scales)[at];
+        s[h][c] = __nv_bfloat162(v, v);
+        base[h][c] = ZEROS ? w4_base(p.zeros[at] & 15u) : kW4Base8;
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t a[4];
+      w4_unpack_bf16(q[j], base[j >> 1][0], base[j >> 1][1], a);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(a + i), s[j >> 1][i & 1]);
+        __nv_bfloat16* dst = tile + (kt * kW4Rows + 16 * j + 8 * (i >> 1) + 2 * t) * kPackPitch + ct * kW4Cols + 8 * (i & 1) + g;
+        dst[0] = v.x;
+        dst[kPackPitch] = v.y;
+      }
+    }
+  }
+  __syncthreads();
+  __nv_bfloat16* w = static_cast<__nv_bfloat16*>(p.w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 32 + (threadIdx.x >> 3), c = (threadIdx.x & 7) * 8;
+    const long long at = static_cast<long long>(k0 + r) * p.N + n0 + c;
+    if (k0 + r < p.K && n0 + c < p.N && TPMLP_IN_BOUNDS(at + 7, static_cast<long long>(p.K) * p.N, kBoundsW4Weights)) {
+      const uint2* src = reinterpret_cast<const uint2*>(tile + r * kPackPitch + c);
+      const uint2 a = src[0], b = src[1];
+      *reinterpret_cast<uint4*>(w + at) = make_uint4(a.x, a.y, b.x, b.y);
     }
   }
 }
@@ -578,17 +691,16 @@ cudaError_t launch_gemm_w4(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t
 }
 
 cudaError_t launch_quantize_w4(const W4Pack& p, cudaStream_t s) {
-  const dim3 tiles((p.N + kW4Cols - 1) / kW4Cols, (p.K + kW4Rows - 1) / kW4Rows);
-  k_quantize_w4_scales<<<dim3((p.N + 127) / 128, (p.K + p.group - 1) / p.group), 128, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  k_quantize_w4_codes<<<tiles, 128, 0, s>>>(p);
+  const dim3 grid((p.N + kPackCols - 1) / kPackCols, (p.K + kPackRows - 1) / kPackRows);
+  if (p.zeros != nullptr) k_quantize_w4<true><<<grid, 256, 0, s>>>(p);
+  else k_quantize_w4<false><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_dequantize_w4(const W4Pack& p, cudaStream_t s) {
-  const dim3 tiles((p.N + kW4Cols - 1) / kW4Cols, (p.K + kW4Rows - 1) / kW4Rows);
-  k_dequantize_w4<<<tiles, 128, 0, s>>>(p);
+  const dim3 grid((p.N + kPackCols - 1) / kPackCols, (p.K + kPackRows - 1) / kPackRows);
+  if (p.zeros != nullptr) k_dequantize_w4<true><<<grid, 256, 0, s>>>(p);
+  else k_dequantize_w4<false><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
