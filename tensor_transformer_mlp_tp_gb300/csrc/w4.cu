@@ -462,61 +462,72 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
 // shared memory, rows there 34 words apart: the threads of a tile, which read columns g and rows 2 t, then hit 16 banks.
 constexpr int kPackRows = 128, kPackCols = 64, kPackPitch = 68;  // elements
 
-// Largest and smallest of every column of 16 rows (two columns a thread), joined to groups; scale and zero point of a
-// group; then a tile's words, a lane's 16 bytes a thread.  The quotient of a code is w (1 / s), off by less than 2^-19; a
-// quotient of two bf16 numbers is a half of an odd number or at least 1/1020 away from one, so that rounding it to
-// multiples of 2^-10 first gives the division's code.
-// What bounds it: HBM.  4096 x 16384, 167 MB: see launch_quantize_w4.
+// Largest and smallest of every column: four rows a thread as they are loaded, 16 by shuffles, a group's by the thread that
+// makes its scale; then a tile's words, a lane's 16 bytes a thread.  A code's quotient is w (1 / s), off by less than 2^-19;
+// a quotient of two bf16 numbers is half of an odd number or at least 1/1020 away from one, so that rounding it to multiples
+// of 2^-10 first gives the division's code.  Without infinities it is within +-16, so that codes are made in pairs of rows:
+// packed fp32, then 16-bit halves.  (A block with an infinity goes value by value.)
 template <bool ZEROS>
 __global__ void __launch_bounds__(256) k_quantize_w4(const __grid_constant__ W4Pack p) {
   __shared__ __align__(16) __nv_bfloat16 tile[kPackRows * kPackPitch];
-  __shared__ __nv_bfloat162 low[8][32], high[8][32];  // [16 rows][two columns]
+  __shared__ __nv_bfloat162 low[8][32], high[8][32];  // [16 rows][two columns]; the magnitudes' largest without zero points
   __shared__ float s_inv[4][kPackCols];               // [group of the block][column]
-  __shared__ int s_zero[4][kPackCols];
+  __shared__ uint32_t s_zero[4][kPackCols];           // twice, in both halves
   const int n0 = blockIdx.x * kPackCols, k0 = blockIdx.y * kPackRows;
   const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.w);
+  const int c0 = (threadIdx.x & 7) * 8, r0 = (threadIdx.x >> 3) * 4;
+  __nv_bfloat162 lo[4], hi[4];
+  uint4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = k0 + r0 + i < p.K && n0 + c0 < p.N ? ld_stream(reinterpret_cast<const uint4*>(w + static_cast<long long>(k0 + r0 + i) * p.N + n0 + c0))
+                                               : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) lo[e] = hi[e] = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = i * 32 + (threadIdx.x >> 3), c = (threadIdx.x & 7) * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (k0 + r < p.K && n0 + c < p.N) v = __ldg(reinterpret_cast<const uint4*>(w + static_cast<long long>(k0 + r) * p.N + n0 + c));
-    uint32_t* u = &v.x;
+    uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {  // NaN to zero
-      const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(u + e);
-      u[e] &= __heq2_mask(x, x);
+    for (int e = 0; e < 4; ++e) {
+      __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(u + e);
+      u[e] &= __heq2_mask(x, x);  // NaN to zero
+      x = *reinterpret_cast<const __nv_bfloat162*>(u + e);
+      if (ZEROS) lo[e] = __hmin2(lo[e], x);
+      hi[e] = __hmax2(hi[e], ZEROS ? x : __habs2(x));
     }
-    uint2* dst = reinterpret_cast<uint2*>(tile + r * kPackPitch + c);
-    dst[0] = make_uint2(v.x, v.y);
-    dst[1] = make_uint2(v.z, v.w);
+    uint2* dst = reinterpret_cast<uint2*>(tile + (r0 + i) * kPackPitch + c0);
+    dst[0] = make_uint2(u[0], u[1]);
+    dst[1] = make_uint2(u[2], u[3]);
   }
-  __syncthreads();
-  {
-    const int c2 = threadIdx.x & 31, seg = threadIdx.x >> 5;
-    __nv_bfloat162 lo = __floats2bfloat162_rn(0.f, 0.f), hi = lo;
+  bool infinite = false;
+  const __nv_bfloat162 top = __floats2bfloat162_rn(kW4Big, kW4Big);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(tile + (seg * 16 + r) * kPackPitch + c2 * 2);
-      lo = __hmin2(lo, v);
-      hi = __hmax2(hi, v);
+  for (int e = 0; e < 4; ++e) {
+    infinite |= !__hble2(hi[e], top) || (ZEROS && !__hbge2(lo[e], __hneg2(top)));
+#pragma unroll
+    for (int o = 8; o < 32; o *= 2) {
+      hi[e] = __hmax2(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
+      if (ZEROS) lo[e] = __hmin2(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
     }
-    low[seg][c2] = lo;
-    high[seg][c2] = hi;
+    if ((threadIdx.x & 31) < 8) {
+      high[threadIdx.x >> 5][c0 / 2 + e] = hi[e];
+      if (ZEROS) low[threadIdx.x >> 5][c0 / 2 + e] = lo[e];
+    }
   }
-  __syncthreads();
+  infinite = __syncthreads_or(infinite);
   const int groups = kPackRows / p.group, segs = p.group / 16;  // of the block; of a group
   for (int i = threadIdx.x; i < groups * kPackCols; i += blockDim.x) {
     const int c = i % kPackCols, grp = i / kPackCols;
-    float lo = 0.f, hi = 0.f;
+    float least = 0.f, most = 0.f;
     for (int q = grp * segs; q < (grp + 1) * segs; ++q) {
-      lo = fminf(lo, __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(low[q])[c]));
-      hi = fmaxf(hi, __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(high[q])[c]));
+      if (ZEROS) least = fminf(least, __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(low[q])[c]));
+      most = fmaxf(most, __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(high[q])[c]));
     }
-    const float span = fminf(fmaxf(ZEROS ? hi - lo : fmaxf(hi, -lo), kW4Tiny), kW4Big);
+    const float span = fminf(fmaxf(most - least, kW4Tiny), kW4Big);
     const __nv_bfloat16 s = __float2bfloat16_rn(span / (ZEROS ? 15.f : 7.f));
-    const int z = ZEROS ? static_cast<int>(fminf(fmaxf(rintf(-lo / __bfloat162float(s)), 0.f), 15.f)) : 8;
+    const uint32_t z = ZEROS ? static_cast<uint32_t>(fminf(fmaxf(rintf(-least / __bfloat162float(s)), 0.f), 15.f)) : 8u;
     s_inv[grp][c] = 1.f / __bfloat162float(s);
-    s_zero[grp][c] = z;
+    s_zero[grp][c] = z * 0x00010001u;
     const int col = n0 + c, row = k0 + grp * p.group;
     if (col < p.N && row < p.K) {
       const long long at = static_cast<long long>(row / p.group) * p.N + col;
@@ -540,17 +551,17 @@ __global__ void __launch_bounds__(256) k_quantize_w4(const __grid_constant__ W4P
     for (int c = 0; c < 2; ++c) {
       const int n = ct * kW4Cols + 8 * c + g;
       const float inv = s_inv[grp][n];
-      const int z = s_zero[grp][n];
-      const float lo = static_cast<float>(-z), hi = static_cast<float>(15 - z);
+      const uint32_t z2 = s_zero[grp][n];
       const __nv_bfloat16* src = tile + (kt * kW4Rows + 16 * j + 2 * t) * kPackPitch + n;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {  // rows 2 t + h and 8 + 2 t + h
-        const int h = b & 1, half = b >> 1;
-        float y = __bfloat162float(src[(8 * half + h) * kPackPitch]) * inv;
-        y = fminf(fmaxf(y, lo), hi);
-        y = (y + 12288.f) - 12288.f;
-        // the low bits of 2^23 + 2^22 + rint(y)
-        word += (__float_as_uint(y + 12582912.f) - 0x4B400000u + static_cast<uint32_t>(z)) << (4 * (c + 2 * half) + 16 * h);
+      for (int half = 0; half < 2; ++half) {  // rows 8 half + 2 t and the next
+        float2 y = make_float2(__bfloat162float(src[8 * half * kPackPitch]), __bfloat162float(src[(8 * half + 1) * kPackPitch]));
+        y = __fmul2_rn(y, make_float2(inv, inv));
+        if (infinite) y = make_float2(fminf(fmaxf(y.x, -16.f), 16.f), fminf(fmaxf(y.y, -16.f), 16.f));
+        y = __fadd2_rn(__fadd2_rn(y, make_float2(12288.f, 12288.f)), make_float2(-12288.f, -12288.f));
+        y = __fadd2_rn(y, make_float2(12582912.f, 12582912.f));  // the low halves are rint(y)
+        const uint32_t q2 = __vadd2(__byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x5410), z2);
+        word |= __vimin_s16x2_relu(q2, 0x000F000Fu) << (4 * (c + 2 * half));
       }
     }
     if (ZEROS && ((k_tile + 1) * kW4Rows > p.K || (n_tile + 1) * kW4Cols > p.N)) {  // places past the matrix hold 8, not z
