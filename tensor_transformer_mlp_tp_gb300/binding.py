@@ -870,7 +870,7 @@ def tpmlp_gemm1_fp8_block(Xq, x_scales, AqT, a_scales, bias, N, Hq, h_scales, Hp
 #
 # Checked like the block-scaled calls: contiguous bf16 tensors of the current device whose sizes fit one another.
 
-_KEPT_BYTES = 16 << 20  # a larger workspace is not kept for a stream: its call is long beside an allocation
+_KEPT_BYTES = 64 << 20  # a larger workspace is not kept for a stream: its call is long beside an allocation
 
 
 @functools.lru_cache(maxsize=256)

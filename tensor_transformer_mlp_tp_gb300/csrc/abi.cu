@@ -175,6 +175,17 @@ Sizes sizes_of(const tpmlp_shape* s) {
   return z;
 }
 
+// Parts of K of the gated block's row-parallel product (more than kFewRows tokens), or of its dX; bytes of their sums.
+int gated_parts(const tpmlp_shape* s, bool dx) {
+  if (!dx && s->tokens <= kFewRows) return 1;
+  return gated_splits(s->tokens, s->d, (dx ? 2 : 1) * ((s->ffn + kBK - 1) / kBK));
+}
+
+size_t gated_partial_bytes(const tpmlp_shape* s, bool dx) {
+  const int n = gated_parts(s, dx);
+  return n > 1 ? align_up(static_cast<size_t>(n) * static_cast<size_t>(s->tokens) * static_cast<size_t>(s->d) * 4) : 0;
+}
+
 size_t ws_bytes(const tpmlp_shape* s, int op) {
   const Sizes z = sizes_of(s);
   switch (op) {
@@ -188,8 +199,8 @@ size_t ws_bytes(const tpmlp_shape* s, int op) {
     case TPMLP_OP_SP_BLOCK_BWD: return 3 * z.tf + z.colsum + 3 * z.td + z.lnbwd + z.dropcol;
     case TPMLP_OP_DROPOUT_BWD: return z.dropcol;
     case TPMLP_OP_SP_FWD_FP8: return 2 * z.df8 + z.td8 + z.tf8;
-    case TPMLP_OP_GATED_FWD: return z.tf;
-    case TPMLP_OP_GATED_BWD: return 5 * z.tf + 2 * z.colsum;
+    case TPMLP_OP_GATED_FWD: return z.tf + gated_partial_bytes(s, false);
+    case TPMLP_OP_GATED_BWD: return 5 * z.tf + 2 * z.colsum + gated_partial_bytes(s, true);
     case TPMLP_OP_DH_GATED: return 2 * z.colsum;
     case TPMLP_OP_SP_BWD_FP8: return 2 * z.td + 3 * z.td8 + 2 * z.df8 + 3 * z.tf8 + z.colsum + z.lnbwd;
     default: return 0;
@@ -617,8 +628,8 @@ cudaError_t do_gemm1_gated(const DeviceCtx& c, const void* X, const void* Ag, co
 }
 
 cudaError_t do_dh_gated(const DeviceCtx& c, const void* dY, const void* B, const void* Gpre, const void* Upre, int act,
-                        const tpmlp_shape* s, void* dG, void* dU, void* H, void* dbg, void* dbu, float* colsum_g,
-                        float* colsum_u, cudaStream_t st) {
+                        const tpmlp_shape* s, void* dG, void* dU, void* H, void* dbg, void* dbu, float* colsum,
+                        cudaStream_t st) {
   GemmLaunch g;
   g.M = static_cast<int>(s->tokens);
   g.N = static_cast<int>(s->ffn);
@@ -635,18 +646,25 @@ cudaError_t do_dh_gated(const DeviceCtx& c, const void* dY, const void* B, const
   g.aux = Gpre;
   g.aux_u = Upre;
   g.ld_aux = s->ffn;
-  g.colsum = dbg != nullptr ? colsum_g : nullptr;
-  g.colsum_u = dbu != nullptr ? colsum_u : nullptr;
-  cudaError_t e = launch_gemm(g, c, st);
+  // partial rows of both sums side by side, or of the one that is wanted
+  const bool both = dbg != nullptr && dbu != nullptr;
+  g.ld_colsum = (both ? 2 : 1) * s->ffn;
+  g.colsum = dbg != nullptr ? colsum : nullptr;
+  g.colsum_u = dbu != nullptr ? colsum + (both ? s->ffn : 0) : nullptr;
+  const cudaError_t e = launch_gemm(g, c, st);
+  if (e != cudaSuccess || (dbg == nullptr && dbu == nullptr)) return e;
   const int rows = 4 * static_cast<int>((s->tokens + kBM - 1) / kBM), cols = static_cast<int>(s->ffn);
-  if (e == cudaSuccess && dbg != nullptr) e = launch_column_sum(colsum_g, rows, cols, dbg, true, st);
-  if (e == cudaSuccess && dbu != nullptr) e = launch_column_sum(colsum_u, rows, cols, dbu, true, st);
-  return e;
+  return both ? launch_column_sum_pair(colsum, rows, cols, dbg, dbu, st)
+              : launch_column_sum(colsum, rows, cols, dbg != nullptr ? dbg : dbu, true, st);
 }
 
 cudaError_t do_dx_gated(const DeviceCtx& c, const void* dG, const void* dU, const void* Ag, const void* Au,
-                        const tpmlp_shape* s, void* dX, cudaStream_t st) {
+                        const tpmlp_shape* s, void* dX, cudaStream_t st, float* partial = nullptr) {
   GemmLaunch g;
+  if (partial != nullptr) {
+    g.splits = gated_parts(s, true);
+    g.partial = partial;
+  }
   g.M = static_cast<int>(s->tokens);
   g.N = static_cast<int>(s->d);
   g.K = static_cast<int>(s->ffn);
@@ -663,8 +681,21 @@ cudaError_t do_dx_gated(const DeviceCtx& c, const void* dG, const void* dU, cons
 
 // The gated block's row-parallel product, right behind do_gemm1_gated.
 cudaError_t do_gemm2_gated(const DeviceCtx& c, const void* H, const void* B, const tpmlp_shape* s, void* Y,
-                           cudaStream_t st) {
-  if (s->tokens > kFewRows) return do_gemm2(c, H, B, s, Y, nullptr, st);
+                           float* partial, cudaStream_t st) {
+  if (s->tokens > kFewRows) {
+    GemmLaunch g;
+    g.splits = gated_parts(s, false);
+    g.partial = partial;
+    g.M = static_cast<int>(s->tokens);
+    g.N = static_cast<int>(s->d);
+    g.K = static_cast<int>(s->ffn);
+    g.a = {H, s->ffn, false};
+    g.b = {B, s->d, true};
+    g.epi = kEpiStore;
+    g.out0 = Y;
+    g.ld0 = s->d;
+    return launch_gemm(g, c, st);
+  }
   GemmFewLaunch f;
   f.M = static_cast<int>(s->tokens);
   f.N = static_cast<int>(s->d);
@@ -1616,10 +1647,7 @@ tpmlp_status tpmlp_gemm_dh_gated(const void* dY, const void* B, const void* Gpre
     return TPMLP_ERR_WORKSPACE;
   DeviceCtx c;
   if ((st = device_ctx(&c)) != TPMLP_OK) return st;
-  const size_t colsum = sizes_of(shape).colsum;
-  uint8_t* w = static_cast<uint8_t*>(workspace);
-  return cuda_status(do_dh_gated(c, dY, B, Gpre, Upre, act, shape, dG, dU, H, dbg, dbu, reinterpret_cast<float*>(w),
-                                 w == nullptr ? nullptr : reinterpret_cast<float*>(w + colsum),
+  return cuda_status(do_dh_gated(c, dY, B, Gpre, Upre, act, shape, dG, dU, H, dbg, dbu, static_cast<float*>(workspace),
                                  reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1650,9 +1678,12 @@ tpmlp_status tpmlp_gated_forward(const void* X, const void* Ag, const void* Au, 
   DeviceCtx c;
   if ((st = device_ctx(&c)) != TPMLP_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  void* H = H_out != nullptr ? H_out : workspace;
+  Carve ws(workspace);
+  void* h_ws = ws.take(sizes_of(shape).tf);
+  float* partial = static_cast<float*>(ws.take(gated_partial_bytes(shape, false)));
+  void* H = H_out != nullptr ? H_out : h_ws;
   cudaError_t e = do_gemm1_gated(c, X, Ag, Au, bg, bu, act, shape, H, Gpre_out, Upre_out, s);
-  if (e == cudaSuccess) e = do_gemm2_gated(c, H, B, shape, Y, s);
+  if (e == cudaSuccess) e = do_gemm2_gated(c, H, B, shape, Y, partial, s);
   return cuda_status(e);
 }
 
@@ -1680,8 +1711,8 @@ tpmlp_status tpmlp_gated_backward(const void* X, const void* Ag, const void* Au,
   void* h_ws = ws.take(z.tf);
   void* g_ws = ws.take(z.tf);
   void* u_ws = ws.take(z.tf);
-  float* colsum_g = static_cast<float*>(ws.take(z.colsum));
-  float* colsum_u = static_cast<float*>(ws.take(z.colsum));
+  float* colsum = static_cast<float*>(ws.take(2 * z.colsum));
+  float* partial = static_cast<float*>(ws.take(gated_partial_bytes(shape, true)));
   cudaError_t e = cudaSuccess;
   void* h_out = nullptr;  // H emitted by the derivatives' epilogue only when nobody supplied it
   if (Gpre == nullptr) {
@@ -1694,11 +1725,11 @@ tpmlp_status tpmlp_gated_backward(const void* X, const void* Ag, const void* Au,
     H = h_ws;
   }
   if (e == cudaSuccess)
-    e = do_dh_gated(c, dY, B, Gpre, Upre, act, shape, dG, dU, h_out, dbg, dbu, colsum_g, colsum_u, s);
+    e = do_dh_gated(c, dY, B, Gpre, Upre, act, shape, dG, dU, h_out, dbg, dbu, colsum, s);
   if (e == cudaSuccess) e = do_wgrad_b(c, H, dY, shape, dB, s);
   if (e == cudaSuccess) e = do_wgrad_a(c, X, dG, shape, dAg, s);
   if (e == cudaSuccess) e = do_wgrad_a(c, X, dU, shape, dAu, s);
-  if (e == cudaSuccess) e = do_dx_gated(c, dG, dU, Ag, Au, shape, dX, s);
+  if (e == cudaSuccess) e = do_dx_gated(c, dG, dU, Ag, Au, shape, dX, s, partial);
   return cuda_status(e);
 }
 

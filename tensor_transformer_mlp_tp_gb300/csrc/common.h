@@ -60,6 +60,7 @@ enum Epilogue : int {
                       // (optional) = bf16(G + bias), bf16(U + bias_u)
   kEpiDGated = 7,     // d = acc, G = aux, U = aux_u: out0 = bf16(d * U * act'(G)), out1 = bf16(d * act(G)),
                       // out2 (optional) = bf16(act(G) * U); optional column sums of the first two
+  kEpiPartial = 8,    // acc in fp32 to part `shard` of tmC0's three dimensions, for a later join
 };
 
 // Activations of the gated epilogues.
@@ -127,6 +128,7 @@ struct GemmParams {
   const void* bias_u;         // [N] bf16 or nullptr
   const void* aux_u;          // U; the row stride is ld_aux
   float* colsum_u;            // column partial sums of out1, as colsum
+  long long ld_colsum;        // between partial rows of the gated epilogue's column sums
   int k_first;                // a sum of two products: k-blocks of the first
   unsigned int* err;
   unsigned long long timeout_ns;

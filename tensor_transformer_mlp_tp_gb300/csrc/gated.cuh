@@ -74,7 +74,7 @@ __device__ __forceinline__ void colsum_32(const GemmParams& p, float* colsum, fl
   const float s = warp_column_sums(v, lane);
   const int col = col0 + static_cast<int>(lane);
   if (col < p.N && mb * kBM < p.M && TPMLP_IN_BOUNDS(mb * 4 + quad, 4 * ((p.M + kBM - 1) / kBM), kBoundsGemmColsum))
-    colsum[static_cast<long long>(mb * 4 + quad) * p.N + col] = s;
+    colsum[(mb * 4 + quad) * p.ld_colsum + col] = s;
 }
 
 // d: 32 columns of dH = dY B^T; raw: G and U there (zeros outside the matrix).

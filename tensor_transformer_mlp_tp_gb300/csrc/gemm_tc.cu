@@ -64,6 +64,18 @@ bool make_map(CUtensorMap* m, const void* base, long long inner, long long outer
                          base, inner, outer, ld, box_inner, box_outer, swizzle);
 }
 
+// Parts [splits][rows][cols] of fp32, boxes of 16 x 32 (64-byte rows).
+bool make_parts_map(CUtensorMap* m, float* base, long long cols, long long rows, int splits) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(splits)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 4, static_cast<cuuint64_t>(cols) * static_cast<cuuint64_t>(rows) * 4};
+  cuuint32_t box[3] = {16, 32, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool AMN, bool BMN, int EPI>
 cudaError_t run(const GemmParams& p, int grid, cudaStream_t s) {
   using S = GemmShape<kBN, kStages, kEpiWarps>;
@@ -122,7 +134,7 @@ cudaError_t run_pair(GemmParams p, cudaStream_t s) {
   // A last wave of whole tiles that would leave more than half of the pairs idle runs as one round of
   // half-width tiles instead (each pair then finishes its share in half a tile's time).
   const long long rem = tiles % pairs;
-  if (BN == kBN && EPI != kEpiGated && !DUAL && p.shards == 1 && rem != 0 && 2 * rem <= pairs && (BMN || half_map_ok(p))) {
+  if (BN == kBN && !DUAL && p.shards == 1 && rem != 0 && 2 * rem <= pairs && (BMN || half_map_ok(p))) {
     p.full_units = static_cast<int>(tiles - rem);
     units = tiles + rem;
   }
@@ -212,17 +224,32 @@ static cudaError_t launch_gemm_fp8(const GemmLaunch& g, const DeviceCtx& ctx, cu
   }
 }
 
+// Sum of `splits` fp32 parts [rows x cols], in their order, as bf16: eight columns a thread.
+static __global__ void __launch_bounds__(256) k_join_parts(const float* __restrict__ parts, int splits, long long n, __nv_bfloat16* out) {
+  const long long at = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) * 8;
+  if (at >= n) return;
+  float v[8] = {};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(parts + s * n + at)), b = __ldcs(reinterpret_cast<const float4*>(parts + s * n + at + 4));
+    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  }
+  if (TPMLP_IN_BOUNDS(at + 7, n, kBoundsGemmChunk))
+    *reinterpret_cast<uint4*>(out + at) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
 // The gated block's products, on CTA pairs whatever M is: G and U of one tile with their epilogue (kEpiGated), dH with
-// both derivatives (kEpiDGated), and the sum of two products (dual).
+// both derivatives (kEpiDGated), the sum of two products (dual), and products in parts of K (splits > 1: contiguous out0).
 static cudaError_t launch_gemm_gated(const GemmLaunch& g, const DeviceCtx& ctx, cudaStream_t s) {
   GemmParams p;
   memset(&p, 0, sizeof(p));
-  const bool gated = g.epi == kEpiGated;
+  const bool gated = g.epi == kEpiGated, parts = g.splits > 1;
   const int tile_cols = gated ? kBN / 2 : kBN;
   // the operands: X [M x K] and [K x N] weights (gated); rows of K both (the derivatives and the dual product)
   bool ok = make_map(&p.tmA, g.a.ptr, g.K, g.M, g.a.ld, kBK, kBM);
-  if (gated) {
-    ok = ok && make_map(&p.tmB, g.b.ptr, g.N, g.K, g.b.ld, 64, kBK) && make_map(&p.tmB_2, g.b2.ptr, g.N, g.K, g.b2.ld, 64, kBK);
+  if (g.b.mn_major) {
+    ok = ok && make_map(&p.tmB, g.b.ptr, g.N, g.K, g.b.ld, 64, kBK) && (!gated || make_map(&p.tmB_2, g.b2.ptr, g.N, g.K, g.b2.ld, 64, kBK));
   } else {
     ok = ok && make_map(&p.tmB, g.b.ptr, g.K, g.N, g.b.ld, kBK, kBN / 2);
     if (g.dual)
@@ -237,9 +264,10 @@ static cudaError_t launch_gemm_gated(const GemmLaunch& g, const DeviceCtx& ctx, 
   p.K = g.K;
   p.m_blocks = (g.M + 2 * kBM - 1) / (2 * kBM);
   p.n_blocks = (g.N + tile_cols - 1) / tile_cols;
-  p.shards = 1;
+  p.shards = g.splits;
   p.k_first = (g.K + kBK - 1) / kBK;
-  p.k_blocks_per_shard = (g.dual ? 2 : 1) * p.k_first;
+  // (k-blocks past the end, of the last part, are zeros)
+  p.k_blocks_per_shard = ((g.dual ? 2 : 1) * p.k_first + g.splits - 1) / g.splits;
   p.group_m = kGroupM / 2;
   p.out0 = g.out0;
   p.ld0 = g.ld0;
@@ -253,9 +281,19 @@ static cudaError_t launch_gemm_gated(const GemmLaunch& g, const DeviceCtx& ctx, 
   p.ld_aux = g.ld_aux;
   p.colsum = g.colsum;
   p.colsum_u = g.colsum_u;
+  p.ld_colsum = g.ld_colsum;
   p.act = g.act;
   p.err = ctx.err;
   p.timeout_ns = ctx.timeout_ns;
+  if (parts) {
+    const long long n = static_cast<long long>(g.M) * g.N;
+    if (!make_parts_map(&p.tmC0, g.partial, g.N, g.M, g.splits)) return cudaErrorInvalidValue;
+    const cudaError_t e = g.dual ? run_pair<kBN, false, false, kEpiPartial, false, kBalWarps, true>(p, s)
+                                 : run_pair<kBN, false, true, kEpiPartial, false, kBalWarps>(p, s);
+    if (e != cudaSuccess) return e;
+    k_join_parts<<<static_cast<unsigned>((n / 8 + 255) / 256), 256, 0, s>>>(g.partial, g.splits, n, static_cast<__nv_bfloat16*>(g.out0));
+    return cudaGetLastError();
+  }
   constexpr CUtensorMapSwizzle kSw = CU_TENSOR_MAP_SWIZZLE_64B;
   if (make_map(&p.tmC0, g.out0, g.N, g.M, g.ld0, 32, 32, false, kSw)) p.tma_out |= 1;
   if (g.out1 != nullptr && make_map(&p.tmC1, g.out1, g.N, g.M, g.ld1, 32, 32, false, kSw)) p.tma_out |= 2;
@@ -277,7 +315,7 @@ cudaError_t gemm_bounds_status(unsigned int* count, unsigned int* site) {
 cudaError_t launch_gemm(const GemmLaunch& g, const DeviceCtx& ctx, cudaStream_t s) {
   if (g.M <= 0 || g.N <= 0 || g.K <= 0) return cudaSuccess;
   if (g.fp8) return launch_gemm_fp8(g, ctx, s);
-  if (g.epi == kEpiGated || g.epi == kEpiDGated || g.dual) return launch_gemm_gated(g, ctx, s);
+  if (g.epi == kEpiGated || g.epi == kEpiDGated || g.dual || g.splits > 1) return launch_gemm_gated(g, ctx, s);
   GemmParams p;
   memset(&p, 0, sizeof(p));
   // A operand (the M side): box of 128 rows x 64 k (K-major) or 64 m x 64 k rows (MN-major).

@@ -199,6 +199,27 @@ __device__ __forceinline__ void box_store_bf16_32(const CUtensorMap* map, uint8_
   }
 }
 
+// The same for fp32 into part `part` of a [parts x M x N] tensor: two boxes of 16 columns, one after the other from `buf`.
+__device__ __forceinline__ void box_store_fp32_32(const CUtensorMap* map, uint8_t* buf, const float (&x)[32], uint32_t lane,
+                                                  int col0, int row0, int part, int M, int N) {
+  uint8_t* r = buf + lane * 64;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    if (lane == 0) bulk_wait_read_all();
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<float4*>(r + ((j ^ ((lane >> 1) & 3)) << 4)) =
+          make_float4(x[16 * b + 4 * j], x[16 * b + 4 * j + 1], x[16 * b + 4 * j + 2], x[16 * b + 4 * j + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && row0 < M && col0 + 16 * b < N) {
+      tma_store_3d(map, buf, col0 + 16 * b, row0, part);
+      bulk_commit_group();
+    }
+  }
+}
+
 // `sbuf` != nullptr: the bf16 outputs that p.tma_out marks leave through box_store_bf16_32.
 template <int EPI>
 __device__ __forceinline__ void epilogue_32(const GemmParams& p, float (&v)[32], const uint4 (&aux_raw)[4], int row,

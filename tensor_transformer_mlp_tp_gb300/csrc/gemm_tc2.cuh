@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
         const int kb0 = shard * p.k_blocks_per_shard;
         const int m0 = mb * 256 + static_cast<int>(rank) * 128;
         // this CTA's half of the columns
-        const int n0 = kGated ? nb * (BN / 2) : nb * BN + col_off + static_cast<int>(rank) * (width / 2);
+        const int n0 = kGated ? nb * (BN / 2) + col_off / 2 : nb * BN + col_off + static_cast<int>(rank) * (width / 2);
         const uint32_t stage_bytes = static_cast<uint32_t>(S::kATile + (width / 2) * kBK * 2);
         for (int kb = 0; kb < p.k_blocks_per_shard; ++kb) {
           if (!wait_bounded(empty + stage, phase ^ 1u, wc, kSiteProducerEmpty)) {
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
           }
           if (leader) mbar_arrive_expect_tx(full + stage, 2 * stage_bytes);
           const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
-          const bool second = DUAL && kb >= p.k_first;  // DUAL: one shard, kb0 = 0
+          const bool second = DUAL && kb0 + kb >= p.k_first;
           const int k0 = (kb0 + kb - (second ? p.k_first : 0)) * kKElems;
           uint8_t* a_dst = sA + stage * S::kATile;
           uint8_t* b_dst = sB + stage * S::kBTile;
@@ -305,8 +305,8 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
       unit_of<BN>(p, u, tile, col_off, width);
       int shard, mb, nb;
       tile_coords(p, tile, shard, mb, nb);
-      const int n_base = nb * kOutCols + col_off;     // the unit's first output column
-      const int c_stop = min(c_end, width);     // this warp's chunks within the unit
+      const int n_base = nb * kOutCols + col_off * kOutCols / BN;     // the unit's first output column
+      const int c_stop = min(c_end, width * kOutCols / BN);     // this warp's chunks within the unit
       const int acc = local & 1;
       const uint32_t acc_phase = (local >> 1) & 1;
       const int mb128 = mb * 2 + static_cast<int>(rank);
@@ -346,13 +346,15 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
         tmem_load_32cols(trow + static_cast<uint32_t>(c), v);
         if constexpr (kGated) {
           float u[32];
-          tmem_load_32cols(trow + static_cast<uint32_t>(BN / 2 + c), u);
+          tmem_load_32cols(trow + static_cast<uint32_t>(width / 2 + c), u);
           gated_epilogue_32(p, v, u, row, n_base + c, lane, sbuf);
         } else if constexpr (EPI == kEpiDGated) {
           uint4 u_raw[4];
           load_raw32(static_cast<const __nv_bfloat16*>(p.aux_u) + (aux_row - static_cast<const __nv_bfloat16*>(p.aux)),
                      n_base + c, p.N, row < p.M, u_raw);
           dgated_epilogue_32(p, v, aux_cur, u_raw, row, n_base + c, mb128, quad, lane, sbuf);
+        } else if constexpr (EPI == kEpiPartial) {
+          box_store_fp32_32(&p.tmC0, sbuf, v, lane, n_base + c, row - static_cast<int>(lane), shard, p.M, p.N);
         } else {
           epilogue_32<EPI>(p, v, aux_cur, row, n_base + c, shard, mb128, quad, lane, est, sbuf);
         }

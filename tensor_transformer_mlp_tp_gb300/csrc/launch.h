@@ -63,7 +63,23 @@ struct GemmLaunch {
   const void* bias_u = nullptr;
   const void* aux_u = nullptr;
   float* colsum_u = nullptr;
+  long long ld_colsum = 0;
+  // Parts of K (kEpiStore of launch_gemm_gated's products) that are summed apart, in `partial` (splits x M x N floats), and joined
+  int splits = 1;
+  float* partial = nullptr;
 };
+
+// Parts of K for a product of the gated block: where whole tiles leave half of the pairs without work and K is long, as
+// many as give each pair one.  A k-block takes a pair about 0.2 us on a half tile and 0.33 on a whole one, the join about 4
+// (320 x 1024 with K = 2 x 4096, dX: 41 us in one part, 10 in nine).
+inline int gated_splits(long long M, long long N, long long k_blocks) {
+  constexpr int kPairs = 76;  // of a GB300: a workspace's size must not depend on the device
+  const long long tiles = (M + 255) / 256 * ((N + 255) / 256);
+  long long s = kPairs / tiles;
+  if (s > 16) s = 16;
+  if (s > k_blocks / 4) s = k_blocks / 4;
+  return s >= 2 && k_blocks * (0.2 - 0.33 / static_cast<double>(s)) >= 4.0 ? static_cast<int>(s) : 1;
+}
 
 // Tensor map of a row-major matrix of `outer` rows of `inner` elements, `ld` elements apart; copies fill zeros out of
 // bounds.  False where the driver refuses it.
@@ -143,6 +159,8 @@ cudaError_t launch_gather_rows(const RowParams& r, const DeviceCtx& ctx, cudaStr
 cudaError_t launch_dropout_bwd(const RowParams& r, float* partial, void* dbias2, cudaStream_t s);
 size_t dropout_bwd_scratch_floats(int rows, int d);
 // out[c] = sum_r partial[r * cols + c] over r < rows, fixed order; bf16 or fp32 output.
+// The same for two outputs side by side: columns 0 .. cols - 1 of a partial row (2 cols floats) to out0, the rest to out1.
+cudaError_t launch_column_sum_pair(const float* partial, int rows, int cols, void* out0, void* out1, cudaStream_t s);
 cudaError_t launch_column_sum(const float* partial, int rows, int cols, void* out, bool out_bf16, cudaStream_t s);
 // out[c] (bf16) = sum_r src[r ld + c] for a bf16 matrix [rows x cols] (cols and ld multiples of 8), through
 // `partial` (column_sum_bf16_scratch_floats(rows, cols) floats) in a fixed order.
