@@ -97,9 +97,9 @@ enum {
   TPMLP_OP_DROPOUT_BWD = 8,    /* tpmlp_dropout_backward with a dbias2 output */
   TPMLP_OP_SP_FWD_FP8 = 9,     /* tpmlp_sp_forward_fp8 */
   TPMLP_OP_SP_BWD_FP8 = 10,    /* tpmlp_sp_backward_fp8 */
-  TPMLP_OP_GATED_FWD = 11,     /* tpmlp_gated_forward */
-  TPMLP_OP_GATED_BWD = 12,     /* tpmlp_gated_backward */
-  TPMLP_OP_DH_GATED = 13       /* tpmlp_gemm_dh_gated with a dbg or dbu output */
+  TPMLP_OP_GATED_FWD = 16,     /* tpmlp_gated_forward */
+  TPMLP_OP_GATED_BWD = 17,     /* tpmlp_gated_backward */
+  TPMLP_OP_DH_GATED = 18       /* tpmlp_gemm_dh_gated with a dbg or dbu output */
 };
 
 /* Dropout of the sequence-parallel region.  The pages name Dropout in the
@@ -560,8 +560,12 @@ TPMLP_API tpmlp_status tpmlp_dequantize_w4(const void* Q, const void* scales, co
 
 /* Y [M x N] bf16 = X [M x K] W + bias (bias [N] bf16 or NULL): per group the sum
  * of x (q - z), exact products in fp32, is scaled as a whole and added to an
- * fp32 sum, so the weights are never rounded.  Any M; made for up to a few
- * hundred tokens.  M or N == 0 is an empty call; K == 0 is an error. */
+ * fp32 sum, so the weights are never rounded.  For M <= 16 a token's values are
+ * taken to 2^-39 of its largest (exact within 2^-32 of it).  Any M; made for up
+ * to a few hundred tokens: a long prompt's product is faster in bf16 on the
+ * weights of tpmlp_dequantize_w4.  zeros hold 0..15.  Reads of X, Q, scales and
+ * zeros only; Y must not overlap them.  M or N == 0 is an empty call; K == 0 is
+ * an error. */
 TPMLP_API tpmlp_status tpmlp_gemm_w4(const void* X, const void* Q, const void* scales, const uint8_t* zeros,
                                      const void* bias, int64_t M, int64_t N, int64_t K, int group, void* Y,
                                      tpmlp_stream_t stream);

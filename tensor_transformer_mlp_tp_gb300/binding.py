@@ -25,7 +25,8 @@ _lib = None
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE = range(6)
 BF16, FP32 = 0, 1
 (OP_FWD, OP_SP_FWD, OP_SP_FWD_PARTIALS, OP_BWD, OP_SP_BWD, OP_DH_GELUPRIME, OP_LN_BWD, OP_SP_BLOCK_BWD,
- OP_DROPOUT_BWD, OP_SP_FWD_FP8, OP_SP_BWD_FP8, OP_GATED_FWD, OP_GATED_BWD, OP_DH_GATED) = range(14)
+ OP_DROPOUT_BWD, OP_SP_FWD_FP8, OP_SP_BWD_FP8) = range(11)
+OP_GATED_FWD, OP_GATED_BWD, OP_DH_GATED = range(16, 19)
 ACT_SILU, ACT_GELU = 0, 1
 E4M3, E5M2 = 0, 1
 RS_FUSED, RS_PARTIALS = 0, 1
@@ -741,12 +742,15 @@ _WORKSPACES = {}  # (device index, stream id) -> the stream's workspace
 _WORKSPACE_LOCK = threading.RLock()
 
 
+_KEPT_BYTES = 64 << 20  # a larger workspace is not kept: its call is long beside an allocation
+
+
 def _stream_workspace(nbytes, dev, stream):
     """A workspace that the current stream keeps for its calls, which it runs one after the other: an allocation between
     two launches costs as much host time as a launch.  Fresh where that order does not hold: for an explicit stream, in a
     capture (the graph may be replayed on any stream), and on streams that are not torch's own (a handle may be used
     again for another stream)."""
-    if stream is None:
+    if stream is None and nbytes <= _KEPT_BYTES:
         sid = _current_stream(dev)[0]
         if (sid == 0 or sid & 1) and not _capturing():
             ws = _WORKSPACES.get((dev, sid))
@@ -870,29 +874,16 @@ def tpmlp_gemm1_fp8_block(Xq, x_scales, AqT, a_scales, bias, N, Hq, h_scales, Hp
 #
 # Checked like the block-scaled calls: contiguous bf16 tensors of the current device whose sizes fit one another.
 
-_KEPT_BYTES = 64 << 20  # a larger workspace is not kept for a stream: its call is long beside an allocation
-
-
 @functools.lru_cache(maxsize=256)
 def _op_workspace_size(tokens, d, ffn, n_shards, op) -> int:
     return tpmlp_workspace_size(_shape(tokens, d, ffn, n_shards), op)
 
 
-def _call_with_workspace(fn, call, args, nbytes, dev, ws, stream):
-    """Runs call(*args, workspace, its size, stream) on the workspace that is given, or else on one of nbytes."""
-    to = _raw_stream(dev) if stream is None else _stream(stream)
-    if ws is None and nbytes <= _KEPT_BYTES:
-        with _WORKSPACE_LOCK:
-            ws = _stream_workspace(nbytes, dev, stream)
-            st = call(*args, ws.data_ptr(), ws.nbytes, to)
-    else:
-        if ws is None:
-            ws = _scratch(nbytes, torch.device("cuda", dev), stream)
-        elif ws.get_device() != dev or not ws.is_contiguous():
-            _refuse(fn)
-        st = call(*args, ws.data_ptr(), ws.nbytes, to)
-    if st:
-        raise TpMlpError(fn, st)
+def _given(ws, dev, fn):
+    """Address and size of a workspace of the caller's own."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(fn)
+    return ws.data_ptr(), ws.nbytes
 
 
 def _matrix(t, rows, cols, dev, fn):
@@ -927,13 +918,17 @@ def tpmlp_gemm_dh_gated(dY, B, Gpre, Upre, N, dG, dU, act=ACT_SILU, H=None, dbg=
             _matrix(Upre, T, F, dev, fn), act, _shape(T, d, F, N), _matrix(dG, T, F, dev, fn),
             _matrix(dU, T, F, dev, fn), _matrix(H, T, F, dev, fn), _typed(dbg, _BF16, F, dev, fn),
             _typed(dbu, _BF16, F, dev, fn))
-    call = (_lib or lib()).tpmlp_gemm_dh_gated
-    if dbg is None and dbu is None:
-        st = call(*args, None, 0, _raw_stream(dev) if stream is None else _stream(stream))
-        if st:
-            raise TpMlpError(fn, st)
+    call, to = (_lib or lib()).tpmlp_gemm_dh_gated, _raw_stream(dev) if stream is None else _stream(stream)
+    if ws is not None:
+        st = call(*args, *_given(ws, dev, fn), to)
+    elif dbg is None and dbu is None:
+        st = call(*args, None, 0, to)
     else:
-        _call_with_workspace(fn, call, args, _op_workspace_size(T, d, F, N, OP_DH_GATED), dev, ws, stream)
+        with _WORKSPACE_LOCK:
+            ws = _stream_workspace(_op_workspace_size(T, d, F, N, OP_DH_GATED), dev, stream)
+            st = call(*args, ws.data_ptr(), ws.nbytes, to)
+    if st:
+        raise TpMlpError(fn, st)
 
 
 def tpmlp_gemm_dx_gated(dG, dU, Ag, Au, N, dX, stream=None):
@@ -959,8 +954,15 @@ def tpmlp_gated_forward(X, Ag, Au, B, N, Y, act=ACT_SILU, bg=None, bu=None, Gpre
             _matrix(B, F, d, dev, fn), _typed(bg, _BF16, F, dev, fn), _typed(bu, _BF16, F, dev, fn), act,
             _shape(T, d, F, N), _matrix(Y, T, d, dev, fn), _matrix(Gpre_out, T, F, dev, fn),
             _matrix(Upre_out, T, F, dev, fn), _matrix(H_out, T, F, dev, fn))
-    _call_with_workspace(fn, (_lib or lib()).tpmlp_gated_forward, args, _op_workspace_size(T, d, F, N, OP_GATED_FWD),
-                         dev, ws, stream)
+    call, to = (_lib or lib()).tpmlp_gated_forward, _raw_stream(dev) if stream is None else _stream(stream)
+    if ws is None:
+        with _WORKSPACE_LOCK:
+            ws = _stream_workspace(_op_workspace_size(T, d, F, N, OP_GATED_FWD), dev, stream)
+            st = call(*args, ws.data_ptr(), ws.nbytes, to)
+    else:
+        st = call(*args, *_given(ws, dev, fn), to)
+    if st:
+        raise TpMlpError(fn, st)
     return Y
 
 
@@ -977,8 +979,15 @@ def tpmlp_gated_backward(X, Ag, Au, B, Gpre, Upre, dY, N, dX, dAg, dAu, dB, act=
             _matrix(dY, T, d, dev, fn), _shape(T, d, F, N), _matrix(dX, T, d, dev, fn), _matrix(dAg, d, F, dev, fn),
             _matrix(dAu, d, F, dev, fn), _matrix(dB, F, d, dev, fn), _typed(dbg, _BF16, F, dev, fn),
             _typed(dbu, _BF16, F, dev, fn))
-    _call_with_workspace(fn, (_lib or lib()).tpmlp_gated_backward, args, _op_workspace_size(T, d, F, N, OP_GATED_BWD),
-                         dev, ws, stream)
+    call, to = (_lib or lib()).tpmlp_gated_backward, _raw_stream(dev) if stream is None else _stream(stream)
+    if ws is None:
+        with _WORKSPACE_LOCK:
+            ws = _stream_workspace(_op_workspace_size(T, d, F, N, OP_GATED_BWD), dev, stream)
+            st = call(*args, ws.data_ptr(), ws.nbytes, to)
+    else:
+        st = call(*args, *_given(ws, dev, fn), to)
+    if st:
+        raise TpMlpError(fn, st)
 
 
 # ----------------------------------------------------------------------------- 4-bit weights
@@ -994,12 +1003,18 @@ def w4_groups(K, group):
 
 
 def _w4(Q, scales, zeros, K, N, group, dev, fn):
-    """Addresses of a 4-bit matrix's codes, scales and zero points."""
+    """Addresses of a 4-bit matrix's codes, scales and zero points, whose sizes have to be this matrix's: a larger buffer is
+    another matrix's, laid out otherwise."""
     if group not in (32, 64, 128):
         _refuse(fn)
-    n = (K + group - 1) // group * N
-    return (_typed(Q, _U8, ((N + 15) >> 4) * ((K + 63) >> 6) * 512, dev, fn), _typed(scales, _BF16, n, dev, fn),
-            _typed(zeros, _U8, n, dev, fn))
+    n = ((N + 15) >> 4) * ((K + 63) >> 6) * 512
+    groups = ((K + group - 1) // group, N)
+    for t, size in ((scales, groups), (zeros, groups)):
+        if t is not None and t.shape != size:
+            _refuse(fn)
+    if Q is not None and Q.numel() != n:
+        _refuse(fn)
+    return (_typed(Q, _U8, n, dev, fn), _typed(scales, _BF16, 0, dev, fn), _typed(zeros, _U8, 0, dev, fn))
 
 
 def tpmlp_quantize_w4(W, group, Q, scales, zeros=None, stream=None):

@@ -737,7 +737,8 @@ tpmlp_status tpmlp_workspace_size(const tpmlp_shape* shape, int op, size_t* byte
   tpmlp_status st = check_shape(shape, sp, bf16_only);
   if (st != TPMLP_OK) return st;
   if (shape->tokens == 0) return TPMLP_OK;  // empty batch: nothing to launch, pointers may be NULL
-  if (op < TPMLP_OP_FWD || op > TPMLP_OP_DH_GATED) return TPMLP_ERR_INVALID_ARG;
+  if ((op < TPMLP_OP_FWD || op > TPMLP_OP_SP_BWD_FP8) && (op < TPMLP_OP_GATED_FWD || op > TPMLP_OP_DH_GATED))
+    return TPMLP_ERR_INVALID_ARG;
   if ((op == TPMLP_OP_SP_FWD_FP8 || op == TPMLP_OP_SP_BWD_FP8) && (shape->d % 16 != 0 || shape->ffn % 16 != 0))
     return TPMLP_ERR_INVALID_ARG;
   if (op == TPMLP_OP_SP_BWD_FP8 && shape->tokens % 16 != 0) return TPMLP_ERR_INVALID_ARG;
