@@ -1005,16 +1005,20 @@ def w4_groups(K, group):
 def _w4(Q, scales, zeros, K, N, group, dev, fn):
     """Addresses of a 4-bit matrix's codes, scales and zero points, whose sizes have to be this matrix's: a larger buffer is
     another matrix's, laid out otherwise."""
-    if group not in (32, 64, 128):
+    if group != 128 and group != 64 and group != 32:
         _refuse(fn)
-    n = ((N + 15) >> 4) * ((K + 63) >> 6) * 512
     groups = ((K + group - 1) // group, N)
-    for t, size in ((scales, groups), (zeros, groups)):
-        if t is not None and t.shape != size:
-            _refuse(fn)
-    if Q is not None and Q.numel() != n:
+    if Q is None or scales is None:  # the library's to refuse, unless the call is empty
+        return None, None, None
+    if (Q.dtype is not _U8 or Q.numel() != ((N + 15) >> 4) * ((K + 63) >> 6) * 512 or not Q.is_contiguous() or
+            Q.get_device() != dev or scales.dtype is not _BF16 or scales.shape != groups or not scales.is_contiguous() or
+            scales.get_device() != dev):
         _refuse(fn)
-    return (_typed(Q, _U8, n, dev, fn), _typed(scales, _BF16, 0, dev, fn), _typed(zeros, _U8, 0, dev, fn))
+    if zeros is None:
+        return Q.data_ptr(), scales.data_ptr(), None
+    if zeros.dtype is not _U8 or zeros.shape != groups or not zeros.is_contiguous() or zeros.get_device() != dev:
+        _refuse(fn)
+    return Q.data_ptr(), scales.data_ptr(), zeros.data_ptr()
 
 
 def tpmlp_quantize_w4(W, group, Q, scales, zeros=None, stream=None):
