@@ -38,15 +38,14 @@ int max_clusters(K kern, int cluster, int smem, int threads, std::atomic<int>* c
 // query answers one block an SM, while two are resident (their TMEM is half of it each).
 __global__ void __launch_bounds__(640) k_slot() {}
 
-// Clusters of `ranks` (1, 2, 4 or 8) CTAs of a kernel of shape S that the device holds at once.  (Clusters of eight with
+// Clusters of `ranks` (1 to 8) CTAs of a kernel of shape S that the device holds at once.  (Clusters of eight with
 // a CTA an SM leave a fifth of the SMs unused: 15 fit, 120 CTAs of 152.)
 template <typename S>
 int few_clusters(int ranks, const DeviceCtx& ctx) {
-  static std::atomic<int> cache[4][64] = {};
+  static std::atomic<int> cache[8][64] = {};
   static std::atomic<unsigned long long> set[64] = {};
   if (raise_smem_once(k_slot, 227 * 1024, ctx, set) != cudaSuccess) return 1;
-  const int slot = ranks == 1 ? 0 : ranks == 2 ? 1 : ranks == 4 ? 2 : 3;
-  return max_clusters(k_slot, ranks, S::kSmem, S::kThreads, cache[slot]);
+  return max_clusters(k_slot, ranks, S::kSmem, S::kThreads, cache[ranks - 1]);
 }
 
 // CTAs that share a tile's k-blocks: as many (a power of two up to max_ranks) as the device holds for all tiles at once,
@@ -55,6 +54,15 @@ template <typename S>
 int few_ranks(long long tiles, int k_blocks, int max_ranks, const DeviceCtx& ctx) {
   int ranks = 1;
   while (ranks < max_ranks && 4 * ranks <= k_blocks && tiles <= few_clusters<S>(2 * ranks, ctx)) ranks *= 2;
+  return ranks;
+}
+
+// The same, of any number up to max_ranks, for a kernel whose tiles are long: 16 tiles that find no room in clusters of eight
+// then take clusters of six, not four.
+template <typename S>
+int few_ranks_any(long long tiles, int k_blocks, int max_ranks, const DeviceCtx& ctx) {
+  int ranks = max_ranks;
+  while (ranks > 1 && (2 * ranks > k_blocks || tiles > few_clusters<S>(ranks, ctx))) --ranks;
   return ranks;
 }
 

@@ -23,9 +23,9 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// Up to 16 tokens (TT tiles of eight, the m16n8k16 product's columns).  One block an SM, blocks in clusters of `ranks`; a
-// cluster takes every so many-th column tile (both matrices of the gated form), its blocks share K, and eight warps share
-// a block's part of it; up to eight tokens two such teams take turns with the tiles.  One lane of a warp of its own streams the
+// Up to eight tokens, the m16n8k16 product's columns.  One block an SM, blocks in clusters of `ranks`; a cluster takes
+// every so many-th column tile (both matrices of the gated form), its blocks share K, and eight warps share a block's part
+// of it; two such teams take turns with the tiles.  One lane of a warp of its own streams the
 // codes of one tile after the other into a ring by bulk copies of up to 32 KB, so that the bytes in flight cost neither
 // registers nor instructions.  What a weight costs is its unpacking, nine instructions for eight codes.
 //
@@ -37,7 +37,8 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 // bytes and 16 apart (conflict-free); lanes past the last token read a row of zeros.  The sums of a round of tiles are joined
 // in a fixed order, the warps' and then the blocks'.
 constexpr int kWarps = 8;        // of a team
-constexpr int kW4FewTokens = 16;
+// Two tiles of tokens took 17.3 us for 9 tokens and 21.8 for 16 (K = 4096, N = 16384, groups of 128), the UMMA 15.1 and 15.3.
+constexpr int kW4FewTokens = 8;
 constexpr int kW4Ranks = 4;
 constexpr int kW4Stages = 4;      // copies in flight a team at most
 
@@ -51,15 +52,15 @@ struct W4FewParams {
   unsigned long long timeout_ns;
 };
 
-template <int TT, bool G32, bool ZEROS>
+template <bool G32, bool ZEROS>
 struct W4FewShape {
-  static constexpr int kTeams = TT == 1 ? 2 : 1;
+  static constexpr int kTeams = 2;
   static constexpr int kConsumers = 32 * kTeams * kWarps, kThreads = kConsumers + 32;
-  static constexpr int kSums = 8 * TT * 16;  // of a tile
+  static constexpr int kSums = kW4FewTokens * 16;  // of a tile
   // Scales and zero points of a warp's part of a chunk: 16 columns of each, for every row tile or half of one.
   static constexpr int kParts = G32 ? 16 : 8, kPartBytes = ZEROS ? 48 : 32, kSlot = kParts * kPartBytes;
   // rows of zeros, scales in flight, the tokens' powers of two, barriers
-  static constexpr int kFixed = 512 + kTeams * kWarps * 4 * kSlot + kWarps * 16 * 4 + 256;
+  static constexpr int kFixed = 512 + kTeams * kWarps * 4 * kSlot + kWarps * kW4FewTokens * 4 + 256;
   static constexpr int kSmem = 232448;
 };
 
@@ -88,9 +89,9 @@ __device__ __forceinline__ uint32_t x_half2(uint32_t pair, float f) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int MATS, int TT, bool G32, bool ZEROS>
-__global__ void __launch_bounds__(W4FewShape<TT, G32, ZEROS>::kThreads, 1) k_gemm_w4_few(const __grid_constant__ W4FewParams p) {
-  using S = W4FewShape<TT, G32, ZEROS>;
+template <int MATS, bool G32, bool ZEROS>
+__global__ void __launch_bounds__(W4FewShape<G32, ZEROS>::kThreads, 1) k_gemm_w4_few(const __grid_constant__ W4FewParams p) {
+  using S = W4FewShape<G32, ZEROS>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int M = p.g.M, N = p.g.N, K = p.g.K, ranks = p.ranks;
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(W4FewShape<TT, G32, ZEROS>::kThreads, 1) k_gem
   uint8_t* slot_mem = zero_row + 512;  // [warp][slot]
   uint8_t* sx = slot_mem + S::kTeams * kWarps * 4 * S::kSlot;
   float* tok = reinterpret_cast<float*>(sx + M * p.x_pitch);  // [warp][token]: the power of two to take back
-  uint64_t* full = reinterpret_cast<uint64_t*>(tok + kWarps * 16);
+  uint64_t* full = reinterpret_cast<uint64_t*>(tok + kWarps * kW4FewTokens);
   uint64_t* empty = full + S::kTeams * p.stages;
   int* abort_flag = reinterpret_cast<int*>(empty + S::kTeams * p.stages);
   if (threadIdx.x == 0) {
@@ -193,8 +194,7 @@ __global__ void __launch_bounds__(W4FewShape<TT, G32, ZEROS>::kThreads, 1) k_gem
     if (++f_chunk == chunks) {
       f_chunk = 0;
       f_tile += S::kTeams;
-      if (MATS == 1) f_col += S::kTeams * p.clusters * kW4Cols;
-      else if (S::kTeams == 2 || (f_tile & 1) == 0) f_col += p.clusters * kW4Cols;
+      f_col += S::kTeams / MATS * p.clusters * kW4Cols;
     }
   };
 
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(W4FewShape<TT, G32, ZEROS>::kThreads, 1) k_gem
     // its exponent e (infinities and NaN count as the largest finite values); 2^(14 - e), and 2^(e + 1) back
     const int e = min(max(static_cast<int>(largest >> 7) - 127, -112), 126);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-    if (lane == 0) tok[w * 16 + m] = __uint_as_float(static_cast<uint32_t>(127 + e + 1) << 23);
+    if (lane == 0) tok[w * kW4FewTokens + m] = __uint_as_float(static_cast<uint32_t>(127 + e + 1) << 23);
     for (int c = 0; c < chunks; ++c) {
       int first, pieces;
       part_of(c, first, pieces);
@@ -261,15 +261,9 @@ __global__ void __launch_bounds__(W4FewShape<TT, G32, ZEROS>::kThreads, 1) k_gem
         }
     }
   }
-  // this lane's tokens: their rows, or the zeros, which do not advance
-  const uint8_t* x_row[TT];
-  int x_step[TT];
-#pragma unroll
-  for (int tt = 0; tt < TT; ++tt) {
-    const bool in = 8 * tt + g < M;
-    x_row[tt] = in ? sx + (8 * tt + g) * p.x_pitch + t * 32 : zero_row + t * 32;
-    x_step[tt] = in ? 128 : 0;
-  }
+  // this lane's token: its row, or the zeros, which do not advance
+  const uint8_t* x_row = g < M ? sx + g * p.x_pitch + t * 32 : zero_row + t * 32;
+  const int x_step = g < M ? 128 : 0;
   consumers_sync<S::kConsumers>();  // both teams' tokens
   int stage = team * p.stages, slot = 0;
   uint32_t phase = 0;
@@ -277,7 +271,7 @@ __global__ void __launch_bounds__(W4FewShape<TT, G32, ZEROS>::kThreads, 1) k_gem
     const int nt = min(p.round, tiles - round0);
     float* dst = red + (team * kWarps + w) * S::kSums + 2 * t * 16 + g;
     for (int tile = team; tile < nt; tile += S::kTeams, dst += S::kTeams * kWarps * S::kSums) {
-      float sum[TT][4] = {};
+      float sum[4] = {};
       for (int c = 0; c < chunks; ++c) {
         int first, pieces;
         part_of(c, first, pieces);
@@ -288,20 +282,12 @@ __global__ void __launch_bounds__(W4FewShape<TT, G32, ZEROS>::kThreads, 1) k_gem
         fetch();
         (void)warp_wait(full + stage, phase, wc, kSiteW4Consumer);
         const uint4* src = reinterpret_cast<const uint4*>(ring + (stage * p.chunk + first - c * p.chunk) * 512) + lane;
-        const uint8_t* xs[TT];
-#pragma unroll
-        for (int tt = 0; tt < TT; ++tt) xs[tt] = x_row[tt] + first * x_step[tt];
+        const uint8_t* xs = x_row + first * x_step;
 #pragma unroll 4
-        for (int i = 0; i < pieces; i += 8, src += 32) {
+        for (int i = 0; i < pieces; i += 8, src += 32, xs += x_step) {
           const uint4 q4 = *src;
           const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
-          uint4 b4[TT][2];
-#pragma unroll
-          for (int tt = 0; tt < TT; ++tt) {
-            b4[tt][0] = reinterpret_cast<const uint4*>(xs[tt])[0];
-            b4[tt][1] = reinterpret_cast<const uint4*>(xs[tt])[1];
-            xs[tt] += x_step[tt];
-          }
+          const uint4 b4[2] = {reinterpret_cast<const uint4*>(xs)[0], reinterpret_cast<const uint4*>(xs)[1]};
           constexpr int kSteps = G32 ? 2 : 4;  // of 16 rows, with one scale
 #pragma unroll
           for (int j0 = 0; j0 < 4; j0 += kSteps, sl += S::kPartBytes) {
@@ -309,25 +295,19 @@ __global__ void __launch_bounds__(W4FewShape<TT, G32, ZEROS>::kThreads, 1) k_gem
             const float s0 = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sl)[g]) * 0x1p-15f;
             const float s1 = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sl)[g + 8]) * 0x1p-19f;
             const uint32_t z0 = w4_base0(ZEROS ? sl[32 + g] : 8u), z1 = w4_base1(ZEROS ? sl[40 + g] : 8u);
-            float c4[TT][4] = {};
+            float c4[4] = {};
 #pragma unroll
             for (int j = j0; j < j0 + kSteps; ++j) {
               uint32_t a[4];
               w4_unpack(q[j], z0, z1, a);
-#pragma unroll
-              for (int tt = 0; tt < TT; ++tt) {
-                const uint4 v = b4[tt][j >> 1];
-                const uint32_t b[2] = {j & 1 ? v.z : v.x, j & 1 ? v.w : v.y};
-                mma_16816(c4[tt], a, b);
-              }
+              const uint4 v = b4[j >> 1];
+              const uint32_t b[2] = {j & 1 ? v.z : v.x, j & 1 ? v.w : v.y};
+              mma_16816(c4, a, b);
             }
-#pragma unroll
-            for (int tt = 0; tt < TT; ++tt) {
-              sum[tt][0] = fmaf(c4[tt][0], s0, sum[tt][0]);
-              sum[tt][1] = fmaf(c4[tt][1], s0, sum[tt][1]);
-              sum[tt][2] = fmaf(c4[tt][2], s1, sum[tt][2]);
-              sum[tt][3] = fmaf(c4[tt][3], s1, sum[tt][3]);
-            }
+            sum[0] = fmaf(c4[0], s0, sum[0]);
+            sum[1] = fmaf(c4[1], s0, sum[1]);
+            sum[2] = fmaf(c4[2], s1, sum[2]);
+            sum[3] = fmaf(c4[3], s1, sum[3]);
           }
         }
         __syncwarp();
@@ -338,9 +318,7 @@ __global__ void __launch_bounds__(W4FewShape<TT, G32, ZEROS>::kThreads, 1) k_gem
         }
       }
 #pragma unroll
-      for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) dst[(8 * tt + (r & 1)) * 16 + 8 * (r >> 1)] = sum[tt][r];
+      for (int r = 0; r < 4; ++r) dst[(r & 1) * 16 + 8 * (r >> 1)] = sum[r];
     }
     consumers_sync<S::kConsumers>();
     // the block's sums of tile i (column tile c, matrix k), token m, column n; ranks > 1: into the first warp's place
@@ -354,7 +332,7 @@ __global__ void __launch_bounds__(W4FewShape<TT, G32, ZEROS>::kThreads, 1) k_gem
         const float* at = red + (tile + k) * kWarps * S::kSums + r;
         v[k] = 0.f;
 #pragma unroll
-        for (int o = 0; o < kWarps; ++o) v[k] = fmaf(at[o * S::kSums], tok[o * 16 + m], v[k]);
+        for (int o = 0; o < kWarps; ++o) v[k] = fmaf(at[o * S::kSums], tok[o * kW4FewTokens + m], v[k]);
       }
       if (ranks > 1) {
         red[tile * kWarps * S::kSums + r] = v[0];
@@ -387,10 +365,10 @@ __global__ void __launch_bounds__(W4FewShape<TT, G32, ZEROS>::kThreads, 1) k_gem
   }
 }
 
-template <int MATS, int TT, bool G32, bool ZEROS>
+template <int MATS, bool G32, bool ZEROS>
 cudaError_t run_w4_few(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t s) {
-  using S = W4FewShape<TT, G32, ZEROS>;
-  auto kern = k_gemm_w4_few<MATS, TT, G32, ZEROS>;
+  using S = W4FewShape<G32, ZEROS>;
+  auto kern = k_gemm_w4_few<MATS, G32, ZEROS>;
   static std::atomic<unsigned long long> set[64] = {};
   const cudaError_t e = raise_smem_once(kern, S::kSmem, ctx, set);
   if (e != cudaSuccess) return e;
@@ -444,11 +422,11 @@ cudaError_t run_w4_few(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t s) 
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int MATS, int TT>
+template <int MATS>
 cudaError_t launch_w4_few(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t s) {
   const bool z = g.w[0].zeros != nullptr;
-  if (g.group == 32) return z ? run_w4_few<MATS, TT, true, true>(g, ctx, s) : run_w4_few<MATS, TT, true, false>(g, ctx, s);
-  return z ? run_w4_few<MATS, TT, false, true>(g, ctx, s) : run_w4_few<MATS, TT, false, false>(g, ctx, s);
+  if (g.group == 32) return z ? run_w4_few<MATS, true, true>(g, ctx, s) : run_w4_few<MATS, true, false>(g, ctx, s);
+  return z ? run_w4_few<MATS, false, true>(g, ctx, s) : run_w4_few<MATS, false, false>(g, ctx, s);
 }
 
 // 16 bytes that are read once.
@@ -659,7 +637,7 @@ cudaError_t run_w4_tc(W4TcParams& p, const DeviceCtx& ctx, cudaStream_t s) {
       return cudaErrorInvalidValue;
   const int cols = g.gated ? 128 : 256, blocks = (g.N + cols - 1) / cols, tiles = (g.M + BT - 1) / BT;
   if (tiles > 65535) return cudaErrorNotSupported;
-  p.ranks = few_ranks<S>(static_cast<long long>(blocks) * tiles, (g.K + kW4TcRows - 1) / kW4TcRows, kW4TcRanks, ctx);
+  p.ranks = few_ranks_any<S>(static_cast<long long>(blocks) * tiles, (g.K + kW4TcRows - 1) / kW4TcRows, kW4TcRanks, ctx);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.ranks * blocks, tiles);
   cfg.blockDim = dim3(S::kThreads);
@@ -695,8 +673,7 @@ cudaError_t launch_w4_tc(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t s
 
 cudaError_t launch_gemm_w4(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t s) {
   cudaError_t e = cudaErrorNotSupported;
-  if (g.M <= 8) e = g.gated ? launch_w4_few<2, 1>(g, ctx, s) : launch_w4_few<1, 1>(g, ctx, s);
-  else if (g.M <= kW4FewTokens) e = g.gated ? launch_w4_few<2, 2>(g, ctx, s) : launch_w4_few<1, 2>(g, ctx, s);
+  if (g.M <= kW4FewTokens) e = g.gated ? launch_w4_few<2>(g, ctx, s) : launch_w4_few<1>(g, ctx, s);
   if (e != cudaErrorNotSupported) return e;  // no room for X there
   return g.M <= 32 ? launch_w4_tc<32>(g, ctx, s) : launch_w4_tc<64>(g, ctx, s);
 }

@@ -229,7 +229,7 @@ def test_a_token_times_a_power_of_two(M, power):
     scaled = (X.to(F64) * 2.0 ** max(power, -122)).to(BF16)
     binding.tpmlp_gemm_w4(scaled, m[0], m[1], group, Z)
     assert bool((Y[0] == 0).all()) and bool((Z[0] == 0).all())
-    if M > 16 and power == -126:
+    if M > 8 and power == -126:
         # On the UMMA X is multiplied as it is.  Its values are multiples of 2^-133 here, so sums of products can be subnormal
         # in fp32, where the tensor core may flush: up to 2^-126 for each of the K additions, times the scale.  (At 2^-110
         # every sum is a multiple of 2^-121, and the scaled one has the same bits.)
@@ -243,7 +243,7 @@ def test_a_token_times_a_power_of_two(M, power):
 @pytest.mark.parametrize("M", [2, 10])
 def test_tokens_with_outlying_channels(M):
     """A value of 2^28 where the weights are zero, beside normal ones: those count as far as they lie within 2^-32 of it.  (Up
-    to 16 tokens the values are brought below 2^15 and into fp16, whose least step is 2^-24: a half of it is 2^-39 of a
+    to 8 tokens the values are brought below 2^15 and into fp16, whose least step is 2^-24: a half of it is 2^-39 of a
     largest value that becomes 2^14.)"""
     K, N, group = 256, 64, 32
     g = torch.Generator(device="cuda").manual_seed(4)

@@ -86,7 +86,9 @@ def test_quantize_halves_and_extremes(zeros):
 PRODUCTS = [(1, 8, 8), (1, 64, 16), (1, 4096, 1024), (2, 72, 40), (3, 200, 264), (5, 1024, 4096), (8, 136, 128),
             (9, 520, 72), (16, 2048, 512), (17, 328, 520), (31, 128, 2048), (32, 1032, 264), (33, 64, 8), (48, 4096, 136),
             (64, 512, 1000), (65, 256, 392), (100, 1000, 200), (128, 384, 640), (129, 640, 384), (200, 72, 2056),
-            (256, 1024, 1024)]
+            (256, 1024, 1024),
+            # as many column blocks as leave room for clusters of 7 to 3 blocks
+            (24, 2048, 4096), (40, 1928, 5000), (12, 1544, 6152), (9, 1024, 9000)]
 
 
 @pytest.mark.parametrize("M,K,N", PRODUCTS)
