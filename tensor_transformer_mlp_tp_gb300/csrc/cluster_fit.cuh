@@ -36,7 +36,7 @@ int max_clusters(K kern, int cluster, int smem, int threads, std::atomic<int>* c
 
 // Stands for a few-row kernel in occupancy queries and is never launched: for a kernel that uses tensor memory the
 // query answers one block an SM, while two are resident (their TMEM is half of it each).
-__global__ void __launch_bounds__(640) k_slot() {}
+__global__ void __launch_bounds__(1024) k_slot() {}
 
 // Clusters of `ranks` (1 to 8) CTAs of a kernel of shape S that the device holds at once.  (Clusters of eight with
 // a CTA an SM leave a fifth of the SMs unused: 15 fit, 120 CTAs of 152.)

@@ -36,8 +36,12 @@ struct W4TcShape {
   static constexpr int kABufs = 2;                     // unpacked stages in TMEM, 64 columns a block
   static constexpr int kD = kABufs * 128;              // partial sums behind them: [buffer][block][BT]
   static constexpr int kTmemCols = 512;
-  static constexpr int kWarps = 2 + 8 + 8, kThreads = 32 * kWarps;
-  static constexpr int kSlots = 8 * 4 * 4 * (64 + 32);  // scales and zero points in flight: [warp][slot][group]
+  // A warpgroup copies and issues, four unpack, two scale; their registers, together what the block is launched with (72 a
+  // thread): a scaling thread holds BT sums, an unpacking one 32 words on their way to tensor memory.
+  static constexpr int kUnpackWarps = 16, kScaleWarp = 4 + kUnpackWarps, kWarps = kScaleWarp + 8, kThreads = 32 * kWarps;
+  static constexpr int kIssueRegs = 40, kUnpackRegs = 64, kScaleRegs = 104;
+  static_assert(128 * kIssueRegs + 32 * kUnpackWarps * kUnpackRegs + 256 * kScaleRegs <= 72 * kThreads, "setmaxnreg split");
+  static constexpr int kSlots = 4 * 4 * (8 * 64 + kUnpackWarps * 16);  // scales and zero points in flight: [warp][slot][group]
   static constexpr int kSmem = 1024 + kStages * kStage + kSlots + 256;
   static_assert(kD + 4 * BT <= kTmemCols, "tensor memory");
   static_assert(kStages * kStage >= 2 * BT * 128 * 4, "the sums are joined in the ring's memory");
@@ -90,10 +94,10 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full + s, 1);
-      mbar_init(empty + s, 9);
+      mbar_init(empty + s, S::kUnpackWarps + 1);
     }
     for (int i = 0; i < ABUFS; ++i) {
-      mbar_init(a_full + i, 8);
+      mbar_init(a_full + i, S::kUnpackWarps);
       mbar_init(a_empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -122,7 +126,9 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
   griddep_launch_dependents();
   const WaitCtx wc{abort_flag, p.err, p.timeout_ns};
 
-  float acc[BT];
+  float* red = reinterpret_cast<float*>(smem);
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kIssueRegs));
   if (warp == 0) {
     // four boxes a stage (past the matrix's ends they fill zeros): single column tiles by bulk copies of 1 KB, 16 of them, took
     // longer to issue than to multiply
@@ -192,86 +198,81 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
       wait_drain(drain, 0, p.timeout_ns);
     }
     __syncwarp();
-  } else if (warp < 10) {
+  }
+    __syncthreads();
+    if (warp == 1) {
+      tc_fence_after_sync();
+      tmem_dealloc(tmem_base, S::kTmemCols);
+    }
+    cluster_sync_all();
+    cluster_sync_all();
+    return;
+  }
+  if (warp < S::kScaleWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kUnpackRegs));
     // -------------------------------------------------------------------- unpacking
-    const int quad = warp & 3, block = (warp - 2) >> 2, g = static_cast<int>(lane) >> 2;
-    const int col = n0 + (gated ? 0 : 128 * block) + 32 * quad;  // the quadrant's first
+    // a column tile each
+    const int quad = warp & 3, half = (warp >> 2) & 1, block = (warp - 4) >> 3, g = static_cast<int>(lane) >> 2;
+    const int col = n0 + (gated ? 0 : 128 * block) + 32 * quad + 16 * half;  // the first
     const uint8_t* zeros = p.g.w[gated ? block : 0].zeros;
     constexpr int kGroups = 8 / STEPS;  // of a stage
-    // Zero points of the quadrant's columns three stages ahead, by copies that no register waits for: a load among the
+    // Zero points of the tile's columns three stages ahead, by copies that no register waits for: a load among the
     // others makes them wait for it.
-    uint8_t* slots = smem_z + (warp - 2) * (4 * kGroups * 32);
+    uint8_t* slots = smem_z + (warp - 4) * (4 * kGroups * 16);
     auto fetch = [&](int st) {
-      if (ZEROS && st < st1 - st0 && lane < 4 * kGroups) {
-        const int row = min((kt0 + 2 * st) * kW4Rows + 16 * STEPS * (static_cast<int>(lane) >> 2), K - 1), at = col + 8 * (static_cast<int>(lane) & 3);
-        cp_async<8>(slots + (st & 3) * (kGroups * 32) + lane * 8, zeros + static_cast<long long>(row >> p.shift) * N + (at < N ? at : 0), at < N ? 8 : 0);
+      if (ZEROS && st < st1 - st0 && lane < 2 * kGroups) {
+        const int row = min((kt0 + 2 * st) * kW4Rows + 16 * STEPS * (static_cast<int>(lane) >> 1), K - 1), at = col + 8 * (static_cast<int>(lane) & 1);
+        cp_async<8>(slots + (st & 3) * (kGroups * 16) + lane * 8, zeros + static_cast<long long>(row >> p.shift) * N + (at < N ? at : 0), at < N ? 8 : 0);
       }
       if (ZEROS) cp_async_commit();
     };
 #pragma unroll
     for (int u = 0; u < 3; ++u) fetch(u);
-    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(block * 64);
-    bool ok = true;
-    for (int st = 0; ok && st < st1 - st0; ++st) {
-      {
-        const int stage = st % STAGES, abuf = st % ABUFS;
-        if (!warp_wait_spin(full + stage, static_cast<uint32_t>(st / STAGES) & 1u, wc, kSiteW4TcUnpack)) {
-          ok = false;
-          break;
-        }
-        if (ZEROS) {
-          cp_async_wait<2>();
-          __syncwarp();  // this stage's are there for all lanes, and the slot before has been read
-          fetch(st + 3);
-        }
-        const uint8_t* zs = slots + (st & 3) * (kGroups * 32) + g;
-        // two column tiles of two row tiles (what the second holds of a last, single one is not multiplied)
-        const uint4* src = reinterpret_cast<const uint4*>(smem + stage * S::kStage + (block * 8 + 2 * quad) * 1024) + lane;
-        uint4 q4[2][2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) q4[c][r] = src[c * 64 + r * 32];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + stage);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t q[8] = {q4[c][0].x, q4[c][0].y, q4[c][0].z, q4[c][0].w, q4[c][1].x, q4[c][1].y, q4[c][1].z, q4[c][1].w};
-          uint32_t a[32];
-#pragma unroll
-          for (int h = 0; h < kGroups; ++h) {
-            uint32_t b0 = kW4Base8, b1 = kW4Base8;
-            if (ZEROS) {
-              b0 = w4_base(zs[h * 32 + 16 * c] & 15u);
-              b1 = w4_base(zs[h * 32 + 16 * c + 8] & 15u);
-            }
-#pragma unroll
-            for (int j = h * STEPS; j < (h + 1) * STEPS; ++j) w4_unpack_bf16(q[j], b0, b1, a + 4 * j);
-          }
-          if (c == 0) {
-            if (!warp_wait_spin(a_empty + abuf, (static_cast<uint32_t>(st / ABUFS) & 1u) ^ 1u, wc, kSiteW4TcUnpackA)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-          }
-          tmem_st_16x64(a_lane + (static_cast<uint32_t>(16 * c) << 16) + static_cast<uint32_t>(abuf * 128), a);
-        }
-        if (!ok) break;
-        tmem_wait_st();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(a_full + abuf);
+    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(quad * 32 + 16 * half) << 16) + static_cast<uint32_t>(block * 64);
+    for (int st = 0; st < st1 - st0; ++st) {
+      const int stage = st % STAGES, abuf = st % ABUFS;
+      if (!warp_wait_spin(full + stage, static_cast<uint32_t>(st / STAGES) & 1u, wc, kSiteW4TcUnpack)) break;
+      if (ZEROS) {
+        cp_async_wait<2>();
+        __syncwarp();  // this stage's are there for all lanes, and the slot before has been read
+        fetch(st + 3);
       }
+      const uint8_t* zs = slots + (st & 3) * (kGroups * 16) + g;
+      // two row tiles (what the second holds of a last, single one is not multiplied)
+      const uint4* src = reinterpret_cast<const uint4*>(smem + stage * S::kStage + (block * 8 + 2 * quad + half) * 1024) + lane;
+      const uint4 q0 = src[0], q1 = src[32];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + stage);
+      const uint32_t q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+      uint32_t a[32];
+#pragma unroll
+      for (int h = 0; h < kGroups; ++h) {
+        uint32_t b0 = kW4Base8, b1 = kW4Base8;
+        if (ZEROS) {
+          b0 = w4_base(zs[h * 16] & 15u);
+          b1 = w4_base(zs[h * 16 + 8] & 15u);
+        }
+#pragma unroll
+        for (int j = h * STEPS; j < (h + 1) * STEPS; ++j) w4_unpack_bf16(q[j], b0, b1, a + 4 * j);
+      }
+      if (!warp_wait_spin(a_empty + abuf, (static_cast<uint32_t>(st / ABUFS) & 1u) ^ 1u, wc, kSiteW4TcUnpackA)) break;
+      tc_fence_after_sync();
+      tmem_st_16x64(a_lane + static_cast<uint32_t>(abuf * 128), a);
+      tmem_wait_st();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(a_full + abuf);
     }
+    __syncthreads();  // the ring is drained: its memory holds the CTA's sums [block][token][128] from here on
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kScaleRegs));
     // -------------------------------------------------------------------- scaling
-    const int quad = warp & 3, block = (warp - 10) >> 2;
+    const int quad = warp & 3, block = (warp - S::kScaleWarp) >> 2;
     const int col = n0 + (gated ? 0 : 128 * block) + 32 * quad;  // the quadrant's first
     const uint16_t* scales = static_cast<const uint16_t*>(p.g.w[gated ? block : 0].scales);
     constexpr int kGroups = 8 / STEPS;  // of a stage
     // the quadrant's scales, three stages ahead as the zero points are
-    uint8_t* slots = smem_s + (warp - 10) * (4 * kGroups * 64);
+    uint8_t* slots = smem_s + (warp - S::kScaleWarp) * (4 * kGroups * 64);
     auto fetch = [&](int st) {
       if (st < st1 - st0 && lane < 4 * kGroups) {
         const int row = min((kt0 + 2 * st) * kW4Rows + 16 * STEPS * (static_cast<int>(lane) >> 2), K - 1), at = col + 8 * (static_cast<int>(lane) & 3);
@@ -281,8 +282,7 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
     };
 #pragma unroll
     for (int u = 0; u < 3; ++u) fetch(u);
-#pragma unroll
-    for (int j = 0; j < BT; ++j) acc[j] = 0.f;
+    float acc[BT] = {};
     const uint32_t d_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(S::kD + block * BT);
     bool ok = true;
     for (int st = 0; ok && st < st1 - st0; ++st) {
@@ -300,39 +300,30 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
         }
         tc_fence_after_sync();
         const float s = __uint_as_float(static_cast<uint32_t>(ss[h * 32]) << 16);
-        uint32_t r[2][16];
-        tmem_load_16cols_async(d_lane + (part & 1) * 2 * BT, r[0]);
 #pragma unroll
         for (int c = 0; c < BT / 16; ++c) {
-          if (c + 1 < BT / 16) tmem_load_16cols_async(d_lane + (part & 1) * 2 * BT + (c + 1) * 16, r[(c + 1) & 1]);
-          tmem_wait_ld(r[c & 1]);
+          uint32_t r[16];
+          tmem_load_16cols_async(d_lane + (part & 1) * 2 * BT + c * 16, r);
+          tmem_wait_ld(r);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[c * 16 + j] = fmaf(__uint_as_float(r[c & 1][j]), s, acc[c * 16 + j]);
+          for (int j = 0; j < 16; ++j) acc[c * 16 + j] = fmaf(__uint_as_float(r[j]), s, acc[c * 16 + j]);
         }
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(tempty + (part & 1));
       }
     }
-  }
-  // The ring is drained: its memory holds the CTA's sums [block][token][128] from here on.
-  __syncthreads();
-  float* red = reinterpret_cast<float*>(smem);
-  if (warp >= 10) {
-    float* at = red + ((warp - 10) >> 2) * (BT * 128) + (warp & 3) * 32 + lane;
+    __syncthreads();
+    float* at = red + block * (BT * 128) + quad * 32 + lane;
 #pragma unroll
     for (int j = 0; j < BT; ++j) at[j * 128] = acc[j];
-  }
-  if (warp == 1) {
-    __syncwarp();
-    tc_fence_after_sync();
-    tmem_dealloc(tmem_base, S::kTmemCols);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kUnpackRegs));
   }
   cluster_sync_all();  // every CTA's sums are written (a cluster of one: a block barrier)
   const int rows = min(BT, p.g.M - m0);
   const uint32_t red_addr = smem_u32(red);
   // a token of a block of columns a warp; the gated form takes both blocks together
-  for (int i = rank + ranks * warp; i < (gated ? rows : 2 * rows); i += ranks * S::kWarps) {
+  for (int i = rank + ranks * (warp - 4); i < (gated ? rows : 2 * rows); i += ranks * (S::kWarps - 4)) {
     const int j = gated ? i : i >> 1, first = gated ? 0 : i & 1;
     const int col = n0 + 128 * first + static_cast<int>(lane) * 4;
     float v[2][4];
