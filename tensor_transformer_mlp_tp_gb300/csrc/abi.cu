@@ -1727,9 +1727,21 @@ tpmlp_status tpmlp_gated_backward(const void* X, const void* Ag, const void* Au,
   }
   if (e == cudaSuccess)
     e = do_dh_gated(c, dY, B, Gpre, Upre, act, shape, dG, dU, h_out, dbg, dbu, colsum, s);
-  if (e == cudaSuccess) e = do_wgrad_b(c, H, dY, shape, dB, s);
-  if (e == cudaSuccess) e = do_wgrad_a(c, X, dG, shape, dAg, s);
-  if (e == cudaSuccess) e = do_wgrad_a(c, X, dU, shape, dAu, s);
+  if (e == cudaSuccess) {
+    GatedWgradsLaunch g;
+    g.tokens = static_cast<int>(shape->tokens);
+    g.d = static_cast<int>(shape->d);
+    g.ffn = static_cast<int>(shape->ffn);
+    g.x = X;
+    g.dg = dG;
+    g.du = dU;
+    g.h = H;
+    g.dy = dY;
+    g.dag = dAg;
+    g.dau = dAu;
+    g.db = dB;
+    e = launch_gated_wgrads(g, c, s);
+  }
   if (e == cudaSuccess) e = do_dx_gated(c, dG, dU, Ag, Au, shape, dX, s, partial);
   return cuda_status(e);
 }

@@ -61,6 +61,7 @@ enum Epilogue : int {
   kEpiDGated = 7,     // d = acc, G = aux, U = aux_u: out0 = bf16(d * U * act'(G)), out1 = bf16(d * act(G)),
                       // out2 (optional) = bf16(act(G) * U); optional column sums of the first two
   kEpiPartial = 8,    // acc in fp32 to part `shard` of tmC0's three dimensions, for a later join
+  kEpiWgrads = 9,     // three products of one depth, as many tiles each: out0, out1, out2 = bf16(acc); see k_gemm_tc2
 };
 
 // Activations of the gated epilogues.
@@ -130,6 +131,7 @@ struct GemmParams {
   float* colsum_u;            // column partial sums of out1, as colsum
   long long ld_colsum;        // between partial rows of the gated epilogue's column sums
   int k_first;                // a sum of two products: k-blocks of the first
+  int k_steps;                // kEpiWgrads: UMMAs of a k-block (fewer than four when there are fewer than 49 tokens)
   unsigned int* err;
   unsigned long long timeout_ns;
 };

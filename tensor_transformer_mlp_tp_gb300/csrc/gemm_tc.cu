@@ -134,7 +134,7 @@ cudaError_t run_pair(GemmParams p, cudaStream_t s) {
   // A last wave of whole tiles that would leave more than half of the pairs idle runs as one round of
   // half-width tiles instead (each pair then finishes its share in half a tile's time).
   const long long rem = tiles % pairs;
-  if (BN == kBN && !DUAL && p.shards == 1 && rem != 0 && 2 * rem <= pairs && (BMN || half_map_ok(p))) {
+  if (BN == kBN && !DUAL && (p.shards == 1 || EPI == kEpiWgrads) && rem != 0 && 2 * rem <= pairs && (BMN || half_map_ok(p))) {
     p.full_units = static_cast<int>(tiles - rem);
     units = tiles + rem;
   }
@@ -301,6 +301,34 @@ static cudaError_t launch_gemm_gated(const GemmLaunch& g, const DeviceCtx& ctx, 
   if (gated) return run_pair<kBN, false, true, kEpiGated, false, kBalGated>(p, s);
   if (g.dual) return run_pair<kBN, false, false, kEpiStore, false, kBalWarps, true>(p, s);
   return run_pair<kBN, false, false, kEpiDGated, false, kBalGated>(p, s);
+}
+
+cudaError_t launch_gated_wgrads(const GatedWgradsLaunch& g, const DeviceCtx& ctx, cudaStream_t s) {
+  GemmParams p;
+  memset(&p, 0, sizeof(p));
+  // A k-block of fewer rows for a few tokens: copies fill the rows past the last one at the same cost as others (one token of
+  // d = 1024, F = 4096: 9 us a gradient with 64 rows).
+  const int rows = g.tokens < kBK ? (g.tokens + kUmmaK - 1) / kUmmaK * kUmmaK : kBK;
+  const int T = g.tokens, d = g.d, F = g.ffn;
+  constexpr CUtensorMapSwizzle kSw = CU_TENSOR_MAP_SWIZZLE_64B;
+  if (!make_map(&p.tmA, g.x, d, T, d, 64, rows) || !make_map(&p.tmB, g.dg, F, T, F, 64, rows) ||
+      !make_map(&p.tmB_2, g.du, F, T, F, 64, rows) || !make_map(&p.tmA_2, g.h, F, T, F, 64, rows) ||
+      !make_map(&p.tmB_half, g.dy, d, T, d, 64, rows) || !make_map(&p.tmC0, g.dag, F, d, F, 32, 32, false, kSw) ||
+      !make_map(&p.tmC1, g.dau, F, d, F, 32, 32, false, kSw) || !make_map(&p.tmC2, g.db, d, F, d, 32, 32, false, kSw))
+    return cudaErrorInvalidValue;
+  p.tma_out = 7;
+  p.M = d;
+  p.N = F;
+  p.K = T;
+  p.m_blocks = (d + 2 * kBM - 1) / (2 * kBM);
+  p.n_blocks = (F + kBN - 1) / kBN;
+  p.shards = 3;
+  p.k_blocks_per_shard = (T + kBK - 1) / kBK;
+  p.k_steps = rows / kUmmaK;
+  p.group_m = kGroupM / 2;
+  p.err = ctx.err;
+  p.timeout_ns = ctx.timeout_ns;
+  return run_pair<kBN, true, true, kEpiWgrads, false, kBalWarps>(p, s);
 }
 
 cudaError_t gemm_bounds_status(unsigned int* count, unsigned int* site) {

@@ -75,6 +75,12 @@ __device__ __forceinline__ void unit_of(const GemmParams& p, int u, int& tile, i
   }
 }
 
+__device__ __forceinline__ void swap_coords(int& a, int& b) {
+  const int t = a;
+  a = b;
+  b = t;
+}
+
 // FP8: E4M3 A and B (both K-major), .kind::f8f6f4; a 128-byte k-block row then holds 128 elements and
 // one UMMA covers 32 of them, so shared-memory layouts, descriptors and byte counts are those of bf16.
 // BAL > 0: BAL epilogue warps (warps 2 .. BAL + 1), each reading TMEM itself, with the epilogue math
@@ -84,6 +90,8 @@ __device__ __forceinline__ void unit_of(const GemmParams& p, int u, int& tile, i
 // kEpiGated: a tile is BN / 2 output columns.  The UMMA's first BN / 2 columns are the gate projection's, loaded by the
 // even CTA, the others the up projection's, loaded by the odd one, so that each CTA's TMEM holds both factors of its 128
 // rows and the epilogue multiplies them.
+// kEpiWgrads: the "shards" are the gated block's three weight gradients over K tokens, [M x N] = X^T dG (tmA, tmB, tmC0) and
+// X^T dU (tmA, tmB_2, tmC1) and [N x M] = H^T dY (tmA_2, tmB_half, tmC2), whose tiles are the others' transposed.
 // DUAL: the k-blocks of a second product (tmA_2, tmB_2) follow the first one's into the same sums.
 template <int BN, bool A_MN, bool B_MN, int EPI, int STAGES, int EPI_WARPS, bool FP8 = false, int BAL = 0,
           bool DUAL = false>
@@ -92,6 +100,8 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
   static_assert(!FP8 || (!A_MN && !B_MN), "FP8 operands are K-major");
   static_assert(FP8 || (EPI != kEpiBiasGeluQ && EPI != kEpiDGeluQ), "the quantising epilogues follow FP8 operands");
   constexpr bool kGated = EPI == kEpiGated;
+  constexpr bool kWgrads = EPI == kEpiWgrads;
+  static_assert(!kWgrads || (A_MN && B_MN && BAL > 0 && !FP8), "weight gradients: operands of K rows, balanced epilogue");
   static_assert((!kGated && EPI != kEpiDGated) || (BAL > 0 && !FP8), "the gated epilogues are balanced ones, bf16");
   constexpr bool kAux = EPI == kEpiDGelu || EPI == kEpiDGeluQ || EPI == kEpiDGated;  // reads the pre-activation tile
   // FP8 GEMMs with a GeLU / GeLU' epilogue are epilogue-bound at the doubled MMA rate: there every epilogue
@@ -143,8 +153,9 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&p.tmA);
     tma_prefetch_desc(&p.tmB);
-    if (kGated || DUAL) tma_prefetch_desc(&p.tmB_2);
-    if (DUAL) tma_prefetch_desc(&p.tmA_2);
+    if (kGated || DUAL || kWgrads) tma_prefetch_desc(&p.tmB_2);
+    if (DUAL || kWgrads) tma_prefetch_desc(&p.tmA_2);
+    if (kWgrads) tma_prefetch_desc(&p.tmB_half);
     if (!B_MN && !kGated && p.full_units < p.m_blocks * p.n_blocks * p.shards) tma_prefetch_desc(&p.tmB_half);
     if (p.tma_out & 1) tma_prefetch_desc(&p.tmC0);
     if (p.tma_out & 2) tma_prefetch_desc(&p.tmC1);
@@ -185,11 +196,13 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
         unit_of<BN>(p, u, tile, col_off, width);
         int shard, mb, nb;
         tile_coords(p, tile, shard, mb, nb);
-        const int kb0 = shard * p.k_blocks_per_shard;
+        if (kWgrads && shard == 2) swap_coords(mb, nb);
+        const int kb0 = kWgrads ? 0 : shard * p.k_blocks_per_shard;
         const int m0 = mb * 256 + static_cast<int>(rank) * 128;
         // this CTA's half of the columns
         const int n0 = kGated ? nb * (BN / 2) + col_off / 2 : nb * BN + col_off + static_cast<int>(rank) * (width / 2);
-        const uint32_t stage_bytes = static_cast<uint32_t>(S::kATile + (width / 2) * kBK * 2);
+        const uint32_t stage_bytes = kWgrads ? static_cast<uint32_t>((256 + width) * kUmmaK * p.k_steps)
+                                             : static_cast<uint32_t>(S::kATile + (width / 2) * kBK * 2);
         for (int kb = 0; kb < p.k_blocks_per_shard; ++kb) {
           if (!wait_bounded(empty + stage, phase ^ 1u, wc, kSiteProducerEmpty)) {
             ok = false;
@@ -201,8 +214,9 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
           const int k0 = (kb0 + kb - (second ? p.k_first : 0)) * kKElems;
           uint8_t* a_dst = sA + stage * S::kATile;
           uint8_t* b_dst = sB + stage * S::kBTile;
-          const CUtensorMap* map_a = second ? &p.tmA_2 : &p.tmA;
-          const CUtensorMap* map_b = second || (kGated && rank == 1) ? &p.tmB_2 : &p.tmB;
+          const CUtensorMap* map_a = second || (kWgrads && shard == 2) ? &p.tmA_2 : &p.tmA;
+          const CUtensorMap* map_b = second || (kGated && rank == 1) || (kWgrads && shard == 1) ? &p.tmB_2 : &p.tmB;
+          if (kWgrads && shard == 2) map_b = &p.tmB_half;
           if constexpr (!A_MN) {
             tma_load_2d_pair(a_dst, map_a, bar, k0, m0, pol_a);
           } else {
@@ -260,6 +274,7 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
           const uint32_t b_base = smem_u32(sB + stage * S::kBTile);
 #pragma unroll
           for (int k = 0; k < kBK / kUmmaK; ++k) {
+            if (kWgrads && k >= p.k_steps) break;
             const uint64_t ad = A_MN ? sdesc_sw128(a_base + k * 2048, 64 * kBK * 2, 1024)
                                      : sdesc_sw128(a_base + k * 32, 16, 1024);
             const uint64_t bd = B_MN ? sdesc_sw128(b_base + k * 2048, 64 * kBK * 2, 1024)
@@ -305,6 +320,7 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
       unit_of<BN>(p, u, tile, col_off, width);
       int shard, mb, nb;
       tile_coords(p, tile, shard, mb, nb);
+      if (kWgrads && shard == 2) swap_coords(mb, nb);
       const int n_base = nb * kOutCols + col_off * kOutCols / BN;     // the unit's first output column
       const int c_stop = min(c_end, width * kOutCols / BN);     // this warp's chunks within the unit
       const int acc = local & 1;
@@ -353,6 +369,10 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
           load_raw32(static_cast<const __nv_bfloat16*>(p.aux_u) + (aux_row - static_cast<const __nv_bfloat16*>(p.aux)),
                      n_base + c, p.N, row < p.M, u_raw);
           dgated_epilogue_32(p, v, aux_cur, u_raw, row, n_base + c, mb128, quad, lane, sbuf);
+        } else if constexpr (kWgrads) {
+          const bool last = shard == 2;
+          box_store_bf16_32(last ? &p.tmC2 : shard == 1 ? &p.tmC1 : &p.tmC0, sbuf, v, lane, n_base + c, row - static_cast<int>(lane),
+                            last ? p.N : p.M, last ? p.M : p.N);
         } else if constexpr (EPI == kEpiPartial) {
           box_store_fp32_32(&p.tmC0, sbuf, v, lane, n_base + c, row - static_cast<int>(lane), shard, p.M, p.N);
         } else {

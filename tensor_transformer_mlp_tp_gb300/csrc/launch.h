@@ -117,6 +117,14 @@ cudaError_t gemm_few_bounds_status(unsigned int* count, unsigned int* site);
 // Returns cudaErrorNotSupported for operand/epilogue combinations without a kernel.
 cudaError_t launch_gemm(const GemmLaunch& g, const DeviceCtx& ctx, cudaStream_t s);
 
+// The gated block's weight gradients over its tokens, in one launch: dag, dau [d x ffn] = x^T dg, x^T du; db [ffn x d] = h^T dy.
+struct GatedWgradsLaunch {
+  int tokens = 0, d = 0, ffn = 0;
+  const void *x = nullptr, *dg = nullptr, *du = nullptr, *h = nullptr, *dy = nullptr;
+  void *dag = nullptr, *dau = nullptr, *db = nullptr;
+};
+cudaError_t launch_gated_wgrads(const GatedWgradsLaunch& g, const DeviceCtx& ctx, cudaStream_t s);
+
 // out [M x N] bf16 = x [M x K] w[0] + bias[0], or with w[1] act(x w[0] + bias[0]) * (x w[1] + bias[1]), for up to kFewRows
 // rows; w [K x N] row-major.
 constexpr int kFewRows = 128;
