@@ -131,6 +131,7 @@ struct GemmParams {
   float* colsum_u;            // column partial sums of out1, as colsum
   long long ld_colsum;        // between partial rows of the gated epilogue's column sums
   int k_first;                // a sum of two products: k-blocks of the first
+  int a_bytes;                // the gated block's products: of a CTA's copy of A for a k-block (fewer rows than 128: not all)
   int k_steps;                // kEpiWgrads: UMMAs of a k-block (fewer than four when there are fewer than 49 tokens)
   unsigned int* err;
   unsigned long long timeout_ns;

@@ -247,13 +247,17 @@ static cudaError_t launch_gemm_gated(const GemmLaunch& g, const DeviceCtx& ctx, 
   const bool gated = g.epi == kEpiGated, parts = g.splits > 1;
   const int tile_cols = gated ? kBN / 2 : kBN;
   // the operands: X [M x K] and [K x N] weights (gated); rows of K both (the derivatives and the dual product)
-  bool ok = make_map(&p.tmA, g.a.ptr, g.K, g.M, g.a.ld, kBK, kBM);
+  // (of a few rows no more is copied than their multiple of eight, which the swizzle repeats with: what else the tile holds
+  // reaches no row that is stored.  One token of d = 1024, F = 4096: XXX)
+  const int a_rows = g.M < kBM ? (g.M + 7) / 8 * 8 : kBM;
+  p.a_bytes = a_rows * kBK * 2;
+  bool ok = make_map(&p.tmA, g.a.ptr, g.K, g.M, g.a.ld, kBK, a_rows);
   if (g.b.mn_major) {
     ok = ok && make_map(&p.tmB, g.b.ptr, g.N, g.K, g.b.ld, 64, kBK) && (!gated || make_map(&p.tmB_2, g.b2.ptr, g.N, g.K, g.b2.ld, 64, kBK));
   } else {
     ok = ok && make_map(&p.tmB, g.b.ptr, g.K, g.N, g.b.ld, kBK, kBN / 2);
     if (g.dual)
-      ok = ok && make_map(&p.tmA_2, g.a2.ptr, g.K, g.M, g.a2.ld, kBK, kBM) &&
+      ok = ok && make_map(&p.tmA_2, g.a2.ptr, g.K, g.M, g.a2.ld, kBK, a_rows) &&
            make_map(&p.tmB_2, g.b2.ptr, g.K, g.N, g.b2.ld, kBK, kBN / 2);
     else
       ok = ok && make_map(&p.tmB_half, g.b.ptr, g.K, g.N, g.b.ld, kBK, kBN / 4);

@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
   static_assert(FP8 || (EPI != kEpiBiasGeluQ && EPI != kEpiDGeluQ), "the quantising epilogues follow FP8 operands");
   constexpr bool kGated = EPI == kEpiGated;
   constexpr bool kWgrads = EPI == kEpiWgrads;
+  constexpr bool kShortA = !A_MN && (kGated || EPI == kEpiDGated || DUAL || EPI == kEpiPartial);
   static_assert(!kWgrads || (A_MN && B_MN && BAL > 0 && !FP8), "weight gradients: operands of K rows, balanced epilogue");
   static_assert((!kGated && EPI != kEpiDGated) || (BAL > 0 && !FP8), "the gated epilogues are balanced ones, bf16");
   constexpr bool kAux = EPI == kEpiDGelu || EPI == kEpiDGeluQ || EPI == kEpiDGated;  // reads the pre-activation tile
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
         // this CTA's half of the columns
         const int n0 = kGated ? nb * (BN / 2) + col_off / 2 : nb * BN + col_off + static_cast<int>(rank) * (width / 2);
         const uint32_t stage_bytes = kWgrads ? static_cast<uint32_t>((256 + width) * kUmmaK * p.k_steps)
-                                             : static_cast<uint32_t>(S::kATile + (width / 2) * kBK * 2);
+                                             : static_cast<uint32_t>((kShortA ? p.a_bytes : S::kATile) + (width / 2) * kBK * 2);
         for (int kb = 0; kb < p.k_blocks_per_shard; ++kb) {
           if (!wait_bounded(empty + stage, phase ^ 1u, wc, kSiteProducerEmpty)) {
             ok = false;
