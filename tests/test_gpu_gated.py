@@ -33,7 +33,8 @@ def make(T, d, F, seed=0, bias=True):
 # one token to several row blocks; widths that end inside tiles of 64, 128 and 256; shards of eight columns
 SHAPES = [(1, 8, 8, 1), (1, 64, 64, 8), (1, 1024, 4096, 4), (2, 136, 72, 1), (5, 200, 1024, 64), (16, 512, 264, 1),
           (17, 64, 128, 2), (37, 1024, 512, 4), (63, 72, 392, 1), (64, 256, 256, 2), (100, 328, 640, 8), (128, 128, 384, 1),
-          (129, 136, 264, 1), (256, 64, 512, 8), (257, 200, 392, 1), (320, 1024, 1024, 4), (1000, 248, 1032, 1)]
+          (129, 136, 264, 1), (256, 64, 512, 8), (257, 200, 392, 1), (320, 1024, 1024, 4), (1000, 248, 1032, 1),
+          (48, 512, 1280, 2), (9, 72, 1032, 1)]
 
 
 @pytest.mark.parametrize("T,d,F,N", SHAPES)
