@@ -1,7 +1,9 @@
 // Epilogues of the gated feed-forward block: H = act(G) * U of two products that lie side by side in TMEM, and its
 // derivatives  dU = dH act(G),  dG = dH U act'(G).
 // SiLU(x) = x s(x) with s(x) = 1 / (1 + exp(-x)), SiLU'(x) = s(x) (1 + x (1 - s(x))); the exact GeLU x Phi(x) as in
-// ptx.cuh.  All of it in fp32 on the hardware's 2^x and 1/x; an output is rounded once.
+// ptx.cuh.  All of it in fp32 on the hardware's 2^x and 1/x; an output is rounded once.  H, dG and dU are rounded to bf16
+// between the products, whose operands are bf16: Y and the gradients are then off by about 1.4 roundings of their type instead
+// of one (2.3e-3 instead of 1.7e-3 of the norm).
 #pragma once
 
 #include "gemm_tc.cuh"

@@ -89,9 +89,12 @@ __device__ __forceinline__ void swap_coords(int& a, int& b) {
 // two helper warps.
 // kEpiGated: a tile is BN / 2 output columns.  The UMMA's first BN / 2 columns are the gate projection's, loaded by the
 // even CTA, the others the up projection's, loaded by the odd one, so that each CTA's TMEM holds both factors of its 128
-// rows and the epilogue multiplies them.
+// rows and the epilogue multiplies them: H takes no second pass over G and U (8192 tokens of d = 4096, F = 16384, forward
+// with both factors saved: 1740 us, 1.90 PFLOP/s).
 // kEpiWgrads: the "shards" are the gated block's three weight gradients over K tokens, [M x N] = X^T dG (tmA, tmB, tmC0) and
-// X^T dU (tmA, tmB_2, tmC1) and [N x M] = H^T dY (tmA_2, tmB_half, tmC2), whose tiles are the others' transposed.
+// X^T dU (tmA, tmB_2, tmC1) and [N x M] = H^T dY (tmA_2, tmB_half, tmC2), whose tiles are the others' transposed.  Over few
+// tokens a tile is mostly its store: in one launch the next tile's products run under it, and two last waves are saved
+// (320 tokens of d = 1024, F = 4096: 14.9 us; in three launches 12 each).
 // DUAL: the k-blocks of a second product (tmA_2, tmB_2) follow the first one's into the same sums.
 template <int BN, bool A_MN, bool B_MN, int EPI, int STAGES, int EPI_WARPS, bool FP8 = false, int BAL = 0,
           bool DUAL = false>

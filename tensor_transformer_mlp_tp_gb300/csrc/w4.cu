@@ -36,6 +36,11 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 // X is staged once, so that a lane's B registers of a 64-row tile are 32 consecutive bytes, the rows a multiple of 128
 // bytes and 16 apart (conflict-free); lanes past the last token read a row of zeros.  The sums of a round of tiles are joined
 // in a fixed order, the warps' and then the blocks'.
+//
+// Measured (groups of 128): one token of 4096 x 16384 9.7 us (3.6 TB/s; 7.0 without the products), 4 tokens 10.8, 8 14.4;
+// both matrices of the gated form 15.7 (4.4 TB/s; 11.8 without).  Bound by the unpacking: 97 warp instructions for 64 rows of
+// 16 columns, issue 64% of the cycles, the ALU 46%, shared memory 51%.  Not kept: pairs of column tiles that read X once and
+// share a group's scales (10.0 us for one token, 15.6 for 8: fewer warps wait for each copy).
 constexpr int kWarps = 8;        // of a team
 // Two tiles of tokens took 17.3 us for 9 tokens and 21.8 for 16 (K = 4096, N = 16384, groups of 128), the UMMA 15.1 and 15.3.
 constexpr int kW4FewTokens = 8;
@@ -438,15 +443,51 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
 
 // The quantiser and its inverse: a block takes 128 rows x 64 columns, a whole number of groups and 4 x 2 tiles, through
 // shared memory, rows there 34 words apart: the threads of a tile, which read columns g and rows 2 t, then hit 16 banks.
+// Measured, 4096 x 16384 with groups of 128, both ways: 62.9 us for 337 MB (5.4 TB/s); straight from global memory, where a
+// tile's reads are 16 bytes of each of 64 rows, 398.  The quantiser is bound by its phases (load, extremes, scales, codes): issue
+// 73%, the ALU 59%; eight blocks an SM (32 registers) keep more of them apart: six took 64.2, 71.5 for 63.6 with zero points.
 constexpr int kPackRows = 128, kPackCols = 64, kPackPitch = 68;  // elements
 
 // Largest and smallest of every column: four rows a thread as they are loaded, 16 by shuffles, a group's by the thread that
 // makes its scale; then a tile's words, a lane's 16 bytes a thread.  A code's quotient is w (1 / s), off by less than 2^-19;
 // a quotient of two bf16 numbers is half of an odd number or at least 1/1020 away from one, so that rounding it to multiples
 // of 2^-10 first gives the division's code.  Without infinities it is within +-16, so that codes are made in pairs of rows:
-// packed fp32, then 16-bit halves.  (A block with an infinity goes value by value.)
+// packed fp32, then 16-bit halves.  (A block with an infinity brings quotients to +-16 first.)
+template <bool INFINITE, bool ZEROS>
+__device__ __forceinline__ void quantize_words(const __nv_bfloat16* tile, const float (&s_inv)[4][kPackCols],
+                                               const uint32_t (&s_zero)[4][kPackCols], int kt, int ct, int g, int t, int shift,
+                                               uint32_t (&words)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int grp = (kt * kW4Rows + 16 * j) >> shift;
+    uint32_t word = 0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int n = ct * kW4Cols + 8 * c + g;
+      const float2 inv = make_float2(s_inv[grp][n], s_inv[grp][n]);
+      const uint32_t z2 = ZEROS ? s_zero[grp][n] : 0x00080008u;
+      const __nv_bfloat16* src = tile + (kt * kW4Rows + 16 * j + 2 * t) * kPackPitch + n;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {  // rows 8 half + 2 t and the next
+        float2 y = make_float2(__bfloat162float(src[8 * half * kPackPitch]), __bfloat162float(src[(8 * half + 1) * kPackPitch]));
+        if (INFINITE) {
+          y = __fmul2_rn(y, inv);
+          y = make_float2(fminf(fmaxf(y.x, -16.f), 16.f), fminf(fmaxf(y.y, -16.f), 16.f));
+          y = __fadd2_rn(y, make_float2(12288.f, 12288.f));
+        } else {
+          y = __ffma2_rn(y, inv, make_float2(12288.f, 12288.f));  // multiples of 2^-10 there
+        }
+        y = __fadd2_rn(y, make_float2(12570624.f, 12570624.f));  // 1.5 2^23 in all: the low halves are the quotient's rint
+        const uint32_t q2 = __vadd2(__byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x5410), z2);
+        word |= __vimin_s16x2_relu(q2, 0x000F000Fu) << (4 * (c + 2 * half));
+      }
+    }
+    words[j] = word;
+  }
+}
+
 template <bool ZEROS>
-__global__ void __launch_bounds__(256) k_quantize_w4(const __grid_constant__ W4Pack p) {
+__global__ void __launch_bounds__(256, 8) k_quantize_w4(const __grid_constant__ W4Pack p) {
   __shared__ __align__(16) __nv_bfloat16 tile[kPackRows * kPackPitch];
   __shared__ __nv_bfloat162 low[8][32], high[8][32];  // [16 rows][two columns]; the magnitudes' largest without zero points
   __shared__ float s_inv[4][kPackCols];               // [group of the block][column]
@@ -493,7 +534,7 @@ __global__ void __launch_bounds__(256) k_quantize_w4(const __grid_constant__ W4P
     }
   }
   infinite = __syncthreads_or(infinite);
-  const int groups = kPackRows / p.group, segs = p.group / 16;  // of the block; of a group
+  const int shift = 31 - __clz(p.group), groups = kPackRows >> shift, segs = p.group / 16;  // of the block; of a group
   for (int i = threadIdx.x; i < groups * kPackCols; i += blockDim.x) {
     const int c = i % kPackCols, grp = i / kPackCols;
     float least = 0.f, most = 0.f;
@@ -508,7 +549,7 @@ __global__ void __launch_bounds__(256) k_quantize_w4(const __grid_constant__ W4P
     s_zero[grp][c] = z * 0x00010001u;
     const int col = n0 + c, row = k0 + grp * p.group;
     if (col < p.N && row < p.K) {
-      const long long at = static_cast<long long>(row / p.group) * p.N + col;
+      const long long at = static_cast<long long>(row >> shift) * p.N + col;
       if (TPMLP_IN_BOUNDS(at, static_cast<long long>((p.K + p.group - 1) / p.group) * p.N, kBoundsW4Scales)) {
         static_cast<__nv_bfloat16*>(p.scales)[at] = s;
         if (ZEROS) p.zeros[at] = static_cast<uint8_t>(z);
@@ -521,35 +562,16 @@ __global__ void __launch_bounds__(256) k_quantize_w4(const __grid_constant__ W4P
   const int n_tiles = (p.N + kW4Cols - 1) / kW4Cols, k_tiles = (p.K + kW4Rows - 1) / kW4Rows;
   if (n_tile >= n_tiles || k_tile >= k_tiles) return;
   uint32_t words[4];
+  if (infinite) quantize_words<true, ZEROS>(tile, s_inv, s_zero, kt, ct, g, t, shift, words);
+  else quantize_words<false, ZEROS>(tile, s_inv, s_zero, kt, ct, g, t, shift, words);
+  if (ZEROS && ((k_tile + 1) * kW4Rows > p.K || (n_tile + 1) * kW4Cols > p.N)) {  // places past the matrix hold 8, not z
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int grp = (kt * kW4Rows + 16 * j) / p.group;
-    uint32_t word = 0;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int n = ct * kW4Cols + 8 * c + g;
-      const float inv = s_inv[grp][n];
-      const uint32_t z2 = s_zero[grp][n];
-      const __nv_bfloat16* src = tile + (kt * kW4Rows + 16 * j + 2 * t) * kPackPitch + n;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {  // rows 8 half + 2 t and the next
-        float2 y = make_float2(__bfloat162float(src[8 * half * kPackPitch]), __bfloat162float(src[(8 * half + 1) * kPackPitch]));
-        y = __fmul2_rn(y, make_float2(inv, inv));
-        if (infinite) y = make_float2(fminf(fmaxf(y.x, -16.f), 16.f), fminf(fmaxf(y.y, -16.f), 16.f));
-        y = __fadd2_rn(__fadd2_rn(y, make_float2(12288.f, 12288.f)), make_float2(-12288.f, -12288.f));
-        y = __fadd2_rn(y, make_float2(12582912.f, 12582912.f));  // the low halves are rint(y)
-        const uint32_t q2 = __vadd2(__byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x5410), z2);
-        word |= __vimin_s16x2_relu(q2, 0x000F000Fu) << (4 * (c + 2 * half));
-      }
-    }
-    if (ZEROS && ((k_tile + 1) * kW4Rows > p.K || (n_tile + 1) * kW4Cols > p.N)) {  // places past the matrix hold 8, not z
+    for (int j = 0; j < 4; ++j)
       for (int b = 0; b < 8; ++b) {
         const int i = b & 3, h = b >> 2;
         if (n_tile * kW4Cols + 8 * (i & 1) + g >= p.N || k_tile * kW4Rows + 16 * j + 8 * (i >> 1) + 2 * t + h >= p.K)
-          word = (word & ~(15u << (4 * i + 16 * h))) | 8u << (4 * i + 16 * h);
+          words[j] = (words[j] & ~(15u << (4 * i + 16 * h))) | 8u << (4 * i + 16 * h);
       }
-    }
-    words[j] = word;
   }
   const long long at = (static_cast<long long>(n_tile) * k_tiles + k_tile) * 32 + lane;
   if (TPMLP_IN_BOUNDS(at, static_cast<long long>(n_tiles) * k_tiles * 32, kBoundsW4Codes))
@@ -567,14 +589,14 @@ __global__ void __launch_bounds__(256) k_dequantize_w4(const __grid_constant__ W
   if (n_tile < n_tiles && k_tile < k_tiles) {
     const uint4 q4 = ld_stream(p.q + (static_cast<long long>(n_tile) * k_tiles + k_tile) * 32 + lane);
     const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
-    const int last = (p.K + p.group - 1) / p.group - 1;
+    const int shift = 31 - __clz(p.group), last = ((p.K + p.group - 1) >> shift) - 1;
     __nv_bfloat162 s[2][2];  // [half of the row tile][columns g, g + 8]
     uint32_t base[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int col = n_tile * kW4Cols + 8 * c + g, grp = min((k_tile * kW4Rows + 32 * h) / p.group, last);
+        const int col = n_tile * kW4Cols + 8 * c + g, grp = min((k_tile * kW4Rows + 32 * h) >> shift, last);
         const long long at = static_cast<long long>(grp) * p.N + min(col, p.N - 1);
         const __nv_bfloat16 v = static_cast<const __nv_bfloat16*>(p.scales)[at];
         s[h][c] = __nv_bfloat162(v, v);
