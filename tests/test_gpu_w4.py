@@ -88,7 +88,9 @@ PRODUCTS = [(1, 8, 8), (1, 64, 16), (1, 4096, 1024), (2, 72, 40), (3, 200, 264),
             (64, 512, 1000), (65, 256, 392), (100, 1000, 200), (128, 384, 640), (129, 640, 384), (200, 72, 2056),
             (256, 1024, 1024),
             # as many column blocks as leave room for clusters of 7 to 3 blocks
-            (24, 2048, 4096), (40, 1928, 5000), (12, 1544, 6152), (9, 1024, 9000)]
+            (24, 2048, 4096), (40, 1928, 5000), (12, 1544, 6152), (9, 1024, 9000),
+            # more of X than a block's shared memory holds beside the codes in flight
+            (8, 65544, 24), (1, 524296, 8)]
 
 
 @pytest.mark.parametrize("M,K,N", PRODUCTS)
