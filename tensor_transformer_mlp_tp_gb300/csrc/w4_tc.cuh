@@ -2,17 +2,18 @@
 // shared memory.
 //
 // A CTA takes two blocks of 128 columns of W (256 columns, or the same 128 of both matrices of the gated form) as the
-// UMMA's rows and up to BT tokens as its columns; a cluster of CTAs shares K.  Warp 0 copies codes and X (TMA boxes), warp 1
-// issues, sixteen warps unpack, a column tile each: a lane's 16 bytes of a 16 x 64 tile are registers in the order of the
-// m16n8k16 product's A operand, which is that of tcgen05.st's 16x128b shape, so two row tiles go to tensor memory by one
-// instruction as the UMMA's A operand.  Codes become bf16 q - z, exact.  Eight warps scale: the UMMAs of a group make a
-// partial sum in TMEM, a thread has those of one column of W, one scale for all of them.  The cluster's sums are joined
-// through distributed shared memory in rank order.
+// UMMA's rows and up to BT tokens as its columns (128 tokens: one block, plain products only); a cluster of CTAs shares K.
+// Warp 0 copies codes and X (TMA boxes), warp 1 issues, sixteen warps unpack: a lane's 16 bytes of a 16 x 64 tile are
+// registers in the order of the m16n8k16 product's A operand, which is that of tcgen05.st's 16x128b shape, so tiles go to
+// tensor memory by one instruction as the UMMA's A operand.  Codes become bf16 q - z, exact.  Eight warps scale: the UMMAs
+// of a group make a partial sum in TMEM, a thread has those of one column of W, one scale for all of them.  The cluster's
+// sums are joined through distributed shared memory in rank order.
 //
-// Measured, K = 4096, N = 16384, groups of 128: 14.2 us for 17 tokens, 17.3 for 64, 28.6 for 128 (groups of 32 with zero
-// points: 29.7 for 64).  A stage (128 rows of 256 columns) takes about 1100 cycles, of which its 16 UMMAs are 540: the chain of
-// copy, unpacking, UMMAs and scaling binds, no part of it alone (each left out by itself: 1 to 2 us less).  Eight unpacking
-// warps: 15.2 and 18.6; scaling and unpacking by the same warps 22.7; a third buffer of unpacked stages, at 32 tokens: no change.
+// Measured, K = 4096, N = 16384, groups of 128: 14.2 us for 17 tokens, 17.3 for 64, 25.6 for 128, 49.7 for 256 (groups of 32
+// with zero points: 29.7 for 64).  A stage (128 rows of 256 columns) takes about 1100 cycles, of which its 16 UMMAs are 540:
+// the chain of copy, unpacking, UMMAs and scaling binds, no part of it alone (each left out by itself: 1 to 2 us less).
+// Eight unpacking warps: 15.2 and 18.6; scaling and unpacking by the same warps 22.7; a third buffer of unpacked stages, at
+// 32 tokens: no change.
 #pragma once
 
 #include "gated.cuh"
@@ -34,23 +35,25 @@ struct W4TcParams {
 
 template <int BT>
 struct W4TcShape {
-  static_assert(BT == 32 || BT == 64, "BT");
-  static constexpr int kCodes = 2 * 8 * 2 * 512;       // two blocks of eight column tiles, two row tiles
+  static_assert(BT == 32 || BT == 64 || BT == 128, "BT");
+  static constexpr int kBlocks = BT == 128 ? 1 : 2;    // of 128 columns of W
+  static constexpr int kCodes = kBlocks * 8 * 2 * 512;  // blocks of eight column tiles, two row tiles
   static constexpr int kX = 2 * BT * 128;
   static constexpr int kStage = kCodes + kX;
-  static constexpr int kStages = BT == 64 ? 6 : 8;
+  static constexpr int kStages = BT == 128 ? 5 : BT == 64 ? 6 : 8;
   static constexpr int kABufs = 2;                     // unpacked stages in TMEM, 64 columns a block
-  static constexpr int kD = kABufs * 128;              // partial sums behind them: [buffer][block][BT]
+  static constexpr int kD = kABufs * kBlocks * 64;     // partial sums behind them: [buffer][block][BT]
+  static constexpr int kAcc = kBlocks * BT / 2;        // sums of a scaling thread: a block's, or half the tokens' of the one
   static constexpr int kTmemCols = 512;
   // A warpgroup copies and issues, four unpack, two scale; their registers, together what the block is launched with (72 a
-  // thread): a scaling thread holds BT sums, an unpacking one 32 words on their way to tensor memory.
+  // thread): a scaling thread holds up to 64 sums, an unpacking one up to 32 words on their way to tensor memory.
   static constexpr int kUnpackWarps = 16, kScaleWarp = 4 + kUnpackWarps, kWarps = kScaleWarp + 8, kThreads = 32 * kWarps;
   static constexpr int kIssueRegs = 40, kUnpackRegs = 64, kScaleRegs = 104;
   static_assert(128 * kIssueRegs + 32 * kUnpackWarps * kUnpackRegs + 256 * kScaleRegs <= 72 * kThreads, "setmaxnreg split");
   static constexpr int kSlots = 4 * 4 * (8 * 64 + kUnpackWarps * 16);  // scales and zero points in flight: [warp][slot][group]
   static constexpr int kSmem = 1024 + kStages * kStage + kSlots + 256;
-  static_assert(kD + 4 * BT <= kTmemCols, "tensor memory");
-  static_assert(kStages * kStage >= 2 * BT * 128 * 4, "the sums are joined in the ring's memory");
+  static_assert(kD + 2 * kBlocks * BT <= kTmemCols, "tensor memory");
+  static_assert(kStages * kStage >= kBlocks * BT * 128 * 4, "the sums are joined in the ring's memory");
   static_assert(kSmem <= 232448, "shared memory per block");
 };
 
@@ -66,11 +69,21 @@ __device__ __forceinline__ void tmem_st_16x64(uint32_t taddr, const uint32_t (&r
       : "memory");
 }
 
+// The same of 32 columns.
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 // STEPS: UMMAs (16 rows of W each) of a group.  grid: (cluster size x column blocks, token tiles)
 template <int BT, int STEPS, bool ZEROS>
 __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const __grid_constant__ W4TcParams p) {
   using S = W4TcShape<BT>;
-  constexpr int STAGES = S::kStages, ABUFS = S::kABufs;
+  constexpr int STAGES = S::kStages, ABUFS = S::kABufs, BLOCKS = S::kBlocks;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* smem_s = smem + STAGES * S::kStage;
@@ -87,10 +100,10 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
 
   const int warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31u;
-  const bool gated = p.g.gated;
+  const bool gated = BLOCKS == 2 && p.g.gated;
   const int rank = static_cast<int>(cluster_ctarank()), ranks = p.ranks;
   const int N = p.g.N, K = p.g.K;
-  const int n0 = static_cast<int>(blockIdx.x) / ranks * (gated ? 128 : 256), m0 = static_cast<int>(blockIdx.y) * BT;
+  const int n0 = static_cast<int>(blockIdx.x) / ranks * (gated ? 128 : 128 * BLOCKS), m0 = static_cast<int>(blockIdx.y) * BT;
   const int k_tiles = (K + kW4Rows - 1) / kW4Rows, all_stages = (k_tiles + 1) / 2;
   const int st0 = static_cast<int>(static_cast<long long>(all_stages) * rank / ranks);
   const int st1 = static_cast<int>(static_cast<long long>(all_stages) * (rank + 1) / ranks);
@@ -136,8 +149,8 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kIssueRegs));
   if (warp == 0) {
-    // four boxes a stage (past the matrix's ends they fill zeros): single column tiles by bulk copies of 1 KB, 16 of them, took
-    // longer to issue than to multiply
+    // up to four boxes a stage (past the matrix's ends they fill zeros): single column tiles by bulk copies of 1 KB, 16 of
+    // them, took longer to issue than to multiply
     const uint64_t pol = policy_evict_normal();
     const int tile = n0 / kW4Cols;
     uint32_t issued = 0, issued_parity = 0;
@@ -148,7 +161,7 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
       uint8_t* dst = smem + stage * S::kStage;
       if (lane == 0) {
         mbar_arrive_expect_tx(full + stage, static_cast<uint32_t>(S::kCodes + 2 * p.box_rows * 128));
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < BLOCKS; ++b)
           tma_load_2d(dst + b * 8192, &p.tmQ[gated ? b : 0], full + stage, at * 128, tile + (gated ? 0 : 8 * b), pol);
         for (int r = 0; r < 2; ++r)
           tma_load_2d(dst + S::kCodes + r * (BT * 128), &p.tmX, full + stage, (at + r) * kW4Rows, m0, pol);
@@ -180,13 +193,13 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
         }
         tc_fence_after_sync();
         if (elected) {
-          const uint32_t d = tmem_base + S::kD + (part & 1) * 2 * BT, a = tmem_base + abuf * 128;
+          const uint32_t d = tmem_base + S::kD + (part & 1) * BLOCKS * BT, a = tmem_base + abuf * BLOCKS * 64;
 #pragma unroll
           for (int j = h * STEPS; j < (h + 1) * STEPS; ++j) {
             if (j >= steps) break;  // a last, single row tile
             const uint64_t x = sdesc_sw128(x_base + (j >> 2) * (BT * 128) + (j & 3) * 32, 16, 1024);
             umma_bf16_tmem_a(d, a + 8 * j, x, idesc, j % STEPS != 0 ? 1u : 0u);
-            umma_bf16_tmem_a(d + BT, a + 64 + 8 * j, x, idesc, j % STEPS != 0 ? 1u : 0u);
+            if (BLOCKS == 2) umma_bf16_tmem_a(d + BT, a + 64 + 8 * j, x, idesc, j % STEPS != 0 ? 1u : 0u);
           }
           umma_commit(tfull + (part & 1));
         }
@@ -217,8 +230,9 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
   if (warp < S::kScaleWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kUnpackRegs));
     // -------------------------------------------------------------------- unpacking
-    // a column tile each
-    const int quad = warp & 3, half = (warp >> 2) & 1, block = (warp - 4) >> 3, g = static_cast<int>(lane) >> 2;
+    // a column tile each, or of one block a column tile's row tile
+    const int quad = warp & 3, half = (warp >> 2) & 1, upper = (warp - 4) >> 3, g = static_cast<int>(lane) >> 2;
+    const int block = BLOCKS == 2 ? upper : 0, row_tile = BLOCKS == 2 ? 0 : upper;
     const int col = n0 + (gated ? 0 : 128 * block) + 32 * quad + 16 * half;  // the first
     const uint8_t* zeros = p.g.w[gated ? block : 0].zeros;
     constexpr int kGroups = 8 / STEPS;  // of a stage
@@ -234,7 +248,8 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
     };
 #pragma unroll
     for (int u = 0; u < 3; ++u) fetch(u);
-    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(quad * 32 + 16 * half) << 16) + static_cast<uint32_t>(block * 64);
+    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(quad * 32 + 16 * half) << 16) + static_cast<uint32_t>(block * 64 + row_tile * 32);
+    constexpr int kWords = 4 * BLOCKS;  // of codes a lane, a stage
     for (int st = 0; st < st1 - st0; ++st) {
       const int stage = st % STAGES, abuf = st % ABUFS;
       if (!warp_wait_spin(full + stage, static_cast<uint32_t>(st / STAGES) & 1u, wc, kSiteW4TcUnpack)) break;
@@ -243,27 +258,34 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
         __syncwarp();  // this stage's are there for all lanes, and the slot before has been read
         fetch(st + 3);
       }
-      const uint8_t* zs = slots + (st & 3) * (kGroups * 16) + g;
-      // two row tiles (what the second holds of a last, single one is not multiplied)
-      const uint4* src = reinterpret_cast<const uint4*>(smem + stage * S::kStage + (block * 8 + 2 * quad + half) * 1024) + lane;
-      const uint4 q0 = src[0], q1 = src[32];
+      const uint8_t* zs = slots + (st & 3) * (kGroups * 16) + 4 * row_tile / STEPS * 16 + g;
+      // (what a second row tile holds behind a last, single one is not multiplied)
+      const uint4* src = reinterpret_cast<const uint4*>(smem + stage * S::kStage + (block * 8 + 2 * quad + half) * 1024 + row_tile * 512) + lane;
+      uint32_t q[kWords];
+#pragma unroll
+      for (int r = 0; r < BLOCKS; ++r) {
+        const uint4 v = src[r * 32];
+        q[4 * r] = v.x;
+        q[4 * r + 1] = v.y;
+        q[4 * r + 2] = v.z;
+        q[4 * r + 3] = v.w;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + stage);
-      const uint32_t q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-      uint32_t a[32];
+      uint32_t a[4 * kWords];
+      uint32_t b0 = kW4Base8, b1 = kW4Base8;
 #pragma unroll
-      for (int h = 0; h < kGroups; ++h) {
-        uint32_t b0 = kW4Base8, b1 = kW4Base8;
-        if (ZEROS) {
-          b0 = w4_base(zs[h * 16] & 15u);
-          b1 = w4_base(zs[h * 16 + 8] & 15u);
+      for (int j = 0; j < kWords; ++j) {
+        if (ZEROS && j % STEPS == 0) {
+          b0 = w4_base(zs[j / STEPS * 16] & 15u);
+          b1 = w4_base(zs[j / STEPS * 16 + 8] & 15u);
         }
-#pragma unroll
-        for (int j = h * STEPS; j < (h + 1) * STEPS; ++j) w4_unpack_bf16(q[j], b0, b1, a + 4 * j);
+        w4_unpack_bf16(q[j], b0, b1, a + 4 * j);
       }
       if (!warp_wait_spin(a_empty + abuf, (static_cast<uint32_t>(st / ABUFS) & 1u) ^ 1u, wc, kSiteW4TcUnpackA)) break;
       tc_fence_after_sync();
-      tmem_st_16x64(a_lane + static_cast<uint32_t>(abuf * 128), a);
+      if constexpr (BLOCKS == 2) tmem_st_16x64(a_lane + static_cast<uint32_t>(abuf * 128), a);
+      else tmem_st_16x32(a_lane + static_cast<uint32_t>(abuf * 64), a);
       tmem_wait_st();
       tc_fence_before_sync();
       __syncwarp();
@@ -273,7 +295,8 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kScaleRegs));
     // -------------------------------------------------------------------- scaling
-    const int quad = warp & 3, block = (warp - S::kScaleWarp) >> 2;
+    const int quad = warp & 3, upper = (warp - S::kScaleWarp) >> 2;
+    const int block = BLOCKS == 2 ? upper : 0, token0 = BLOCKS == 2 ? 0 : upper * S::kAcc;
     const int col = n0 + (gated ? 0 : 128 * block) + 32 * quad;  // the quadrant's first
     const uint16_t* scales = static_cast<const uint16_t*>(p.g.w[gated ? block : 0].scales);
     constexpr int kGroups = 8 / STEPS;  // of a stage
@@ -288,8 +311,8 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
     };
 #pragma unroll
     for (int u = 0; u < 3; ++u) fetch(u);
-    float acc[BT] = {};
-    const uint32_t d_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(S::kD + block * BT);
+    float acc[S::kAcc] = {};
+    const uint32_t d_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(S::kD + block * BT + token0);
     bool ok = true;
     for (int st = 0; ok && st < st1 - st0; ++st) {
       cp_async_wait<2>();
@@ -307,9 +330,9 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
         tc_fence_after_sync();
         const float s = __uint_as_float(static_cast<uint32_t>(ss[h * 32]) << 16);
 #pragma unroll
-        for (int c = 0; c < BT / 16; ++c) {
+        for (int c = 0; c < S::kAcc / 16; ++c) {
           uint32_t r[16];
-          tmem_load_16cols_async(d_lane + (part & 1) * 2 * BT + c * 16, r);
+          tmem_load_16cols_async(d_lane + (part & 1) * BLOCKS * BT + c * 16, r);
           tmem_wait_ld(r);
 #pragma unroll
           for (int j = 0; j < 16; ++j) acc[c * 16 + j] = fmaf(__uint_as_float(r[j]), s, acc[c * 16 + j]);
@@ -320,17 +343,18 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
       }
     }
     __syncthreads();
-    float* at = red + block * (BT * 128) + quad * 32 + lane;
+    float* at = red + (block * BT + token0) * 128 + quad * 32 + lane;
 #pragma unroll
-    for (int j = 0; j < BT; ++j) at[j * 128] = acc[j];
+    for (int j = 0; j < S::kAcc; ++j) at[j * 128] = acc[j];
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kUnpackRegs));
   }
   cluster_sync_all();  // every CTA's sums are written (a cluster of one: a block barrier)
   const int rows = min(BT, p.g.M - m0);
   const uint32_t red_addr = smem_u32(red);
   // a token of a block of columns a warp; the gated form takes both blocks together
-  for (int i = rank + ranks * (warp - 4); i < (gated ? rows : 2 * rows); i += ranks * (S::kWarps - 4)) {
-    const int j = gated ? i : i >> 1, first = gated ? 0 : i & 1;
+  const bool once = gated || BLOCKS == 1;
+  for (int i = rank + ranks * (warp - 4); i < (once ? rows : 2 * rows); i += ranks * (S::kWarps - 4)) {
+    const int j = once ? i : i >> 1, first = once ? 0 : i & 1;
     const int col = n0 + 128 * first + static_cast<int>(lane) * 4;
     float v[2][4];
 #pragma unroll
