@@ -225,7 +225,9 @@ static cudaError_t launch_gemm_fp8(const GemmLaunch& g, const DeviceCtx& ctx, cu
 }
 
 // Sum of `splits` fp32 parts [rows x cols], in their order, as bf16: eight columns a thread.
-static __global__ void __launch_bounds__(256) k_join_parts(const float* __restrict__ parts, int splits, long long n, __nv_bfloat16* out) {
+static __global__ void __launch_bounds__(256) k_join_parts(const float* parts, int splits, long long n, __nv_bfloat16* out) {
+  griddep_wait();
+  griddep_launch_dependents();
   const long long at = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) * 8;
   if (at >= n) return;
   float v[8] = {};
@@ -295,8 +297,8 @@ static cudaError_t launch_gemm_gated(const GemmLaunch& g, const DeviceCtx& ctx, 
     const cudaError_t e = g.dual ? run_pair<kBN, false, false, kEpiPartial, false, kBalWarps, true>(p, s)
                                  : run_pair<kBN, false, true, kEpiPartial, false, kBalWarps>(p, s);
     if (e != cudaSuccess) return e;
-    k_join_parts<<<static_cast<unsigned>((n / 8 + 255) / 256), 256, 0, s>>>(g.partial, g.splits, n, static_cast<__nv_bfloat16*>(g.out0));
-    return cudaGetLastError();
+    return launch_after(k_join_parts, static_cast<unsigned>((n / 8 + 255) / 256), 256, s, static_cast<const float*>(g.partial), g.splits, n,
+                        static_cast<__nv_bfloat16*>(g.out0));
   }
   constexpr CUtensorMapSwizzle kSw = CU_TENSOR_MAP_SWIZZLE_64B;
   if (make_map(&p.tmC0, g.out0, g.N, g.M, g.ld0, 32, 32, false, kSw)) p.tma_out |= 1;

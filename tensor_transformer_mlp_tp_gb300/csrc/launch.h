@@ -105,6 +105,22 @@ cudaError_t raise_smem_once(K kern, int bytes, const DeviceCtx& ctx, std::atomic
   return e;
 }
 
+// Launch `kern` so that its start overlaps the end of the kernel before it, for which it waits (griddep_wait) before it touches
+// global memory.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), unsigned grid, unsigned block, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // Bounds-check violations counted by the row kernels' / the GEMMs' / the block-scaled / the 4-bit units since the
 // last call (zero in release builds, which check nothing), and the first site; both cleared.
 cudaError_t rowwise_bounds_status(unsigned int* count, unsigned int* site);

@@ -1087,12 +1087,14 @@ __global__ void __launch_bounds__(256) k_gather_rows(const RowParams p) {
 // out[c] = sum over r < rows of partial[r * stride + c], for c < cols; columns c < split go to
 // out0[c], the rest to out1[c - split].  32 columns per block, rows split over the 8 warps and
 // combined in warp order: a fixed summation order, so the result is deterministic.
-__global__ void __launch_bounds__(256) k_column_sum(const float* __restrict__ partial, int rows, int cols,
+__global__ void __launch_bounds__(256) k_column_sum(const float* partial, int rows, int cols,
                                                      long long stride, void* out0, void* out1, int split,
                                                      int out_bf16) {
   __shared__ float red[8][33];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  griddep_wait();
+  griddep_launch_dependents();
   float s = 0.f;
   if (c < cols) {
     // four independent chains (rows slice + 8 (4 k + u)), combined in a fixed order: loads stay in flight
@@ -1693,8 +1695,7 @@ cudaError_t launch_column_sum(const float* partial, int rows, int cols, void* ou
 }
 
 cudaError_t launch_column_sum_pair(const float* partial, int rows, int cols, void* out0, void* out1, cudaStream_t s) {
-  k_column_sum<<<(2 * cols + 31) / 32, 256, 0, s>>>(partial, rows, 2 * cols, 2LL * cols, out0, out1, cols, 1);
-  return cudaGetLastError();
+  return launch_after(k_column_sum, (2 * cols + 31) / 32, 256, s, partial, rows, 2 * cols, 2LL * cols, out0, out1, cols, 1);
 }
 
 cudaError_t launch_cast_fp8(const void* src, int rows, int cols, bool transpose, int fmt, const float* scale,
