@@ -41,32 +41,23 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 // both matrices of the gated form 15.7 (4.4 TB/s; 11.8 without).  Bound by the unpacking: 97 warp instructions for 64 rows of
 // 16 columns, issue 64% of the cycles, the ALU 46%, shared memory 51%.  Not kept: pairs of column tiles that read X once and
 // share a group's scales (10.0 us for one token, 15.6 for 8: fewer warps wait for each copy).
-constexpr int kWarps = 8;        // of a team
-// Two tiles of tokens took 17.3 us for 9 tokens and 21.8 for 16 (K = 4096, N = 16384, groups of 128), the UMMA 15.1 and 15.3.
-constexpr int kW4FewTokens = 8;
-constexpr int kW4Ranks = 4;
-constexpr int kW4Stages = 4;      // copies in flight a team at most
+constexpr int kWarps = kW4FewWarps;
 
-struct W4FewParams {
+struct W4FewParams : W4FewPlan {
   W4Launch g;
-  int ranks, clusters;         // blocks of a cluster; clusters
-  int chunk, stages, round;    // row tiles a copy; a team's copies in flight; column tiles (of either matrix) between joins
   int shift;                   // log2 of the group
-  int x_pitch;                 // bytes of a token's staged row
   unsigned int* err;
   unsigned long long timeout_ns;
 };
 
 template <bool G32, bool ZEROS>
 struct W4FewShape {
-  static constexpr int kTeams = 2;
+  static constexpr int kTeams = kW4FewTeams;
   static constexpr int kConsumers = 32 * kTeams * kWarps, kThreads = kConsumers + 32;
-  static constexpr int kSums = kW4FewTokens * 16;  // of a tile
-  // Scales and zero points of a warp's part of a chunk: 16 columns of each, for every row tile or half of one.
-  static constexpr int kParts = G32 ? 16 : 8, kPartBytes = ZEROS ? 48 : 32, kSlot = kParts * kPartBytes;
-  // rows of zeros, scales in flight, the tokens' powers of two, barriers
-  static constexpr int kFixed = 512 + kTeams * kWarps * 4 * kSlot + kWarps * kW4FewTokens * 4 + 256;
-  static constexpr int kSmem = 232448;
+  static constexpr int kSums = kW4FewSums;
+  static constexpr int kParts = G32 ? 16 : 8, kPartBytes = w4_few_part_bytes(ZEROS), kSlot = w4_few_slot(G32, ZEROS);
+  static constexpr int kFixed = w4_few_fixed(G32, ZEROS);
+  static constexpr int kSmem = kW4FewSmem;
 };
 
 // Row m, column col of the output from the sums (equal for a plain product).
@@ -378,37 +369,14 @@ cudaError_t run_w4_few(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t s) 
   const cudaError_t e = raise_smem_once(kern, S::kSmem, ctx, set);
   if (e != cudaSuccess) return e;
   W4FewParams p{};
+  static std::atomic<int> cache[3][64] = {};
+  static_cast<W4FewPlan&>(p) = w4_few_plan(g.M, g.N, g.K, MATS, S::kFixed, [&](int r) {
+    return r == 1 ? ctx.sm_count : max_clusters(kern, r, S::kSmem, S::kThreads, cache[r / 2]);
+  });
   p.g = g;
   p.shift = g.group == 32 ? 5 : g.group == 64 ? 6 : 7;
   p.err = ctx.err;
   p.timeout_ns = ctx.timeout_ns;
-  const int col_tiles = (g.N + kW4Cols - 1) / kW4Cols, k_tiles = (g.K + kW4Rows - 1) / kW4Rows;
-  // Blocks of a cluster: the number that leaves the busiest SM the least to read, with room for X, for 64 KB of codes in
-  // flight (or half of that, if none has room for it), and for two column tiles' sums.
-  double least = 0;
-  for (int ring_least = 65536; ring_least >= 32768 && p.clusters == 0; ring_least /= 2)
-    for (int r = 1; r <= kW4Ranks && k_tiles >= r; r *= 2) {
-      static std::atomic<int> cache[3][64] = {};
-      const int fit = r == 1 ? ctx.sm_count : max_clusters(kern, r, S::kSmem, S::kThreads, cache[r / 2]);
-      const double load = static_cast<double>((col_tiles + fit - 1) / fit) / r;
-      const int mine = (k_tiles + r - 1) / r, x_pitch = mine * 128 + 16;
-      constexpr int tile_bytes = kWarps * S::kSums * 4;
-      const long long left = S::kSmem - S::kFixed - static_cast<long long>(g.M) * x_pitch;
-      if (left < ring_least + 2 * tile_bytes || (p.clusters != 0 && load > 0.93 * least)) continue;
-      least = load;
-      p.ranks = r;
-      p.clusters = fit < col_tiles ? fit : col_tiles;
-      p.x_pitch = x_pitch;
-      // a round is all of the cluster's tiles, or as many as leave the ring its part
-      const int most = static_cast<int>((left - ring_least) / tile_bytes) / 2 * 2;
-      const int all = (col_tiles + p.clusters - 1) / p.clusters * MATS;
-      p.round = all < most ? all : most;
-      const int ring = static_cast<int>(left) - p.round * tile_bytes;
-      p.chunk = mine < 64 ? mine : 64;
-      while (p.chunk > 16 && ring / (S::kTeams * (p.chunk * 512 + 16)) < 2) p.chunk /= 2;
-      p.stages = ring / (S::kTeams * (p.chunk * 512 + 16));
-      if (p.stages > kW4Stages) p.stages = kW4Stages;
-    }
   if (p.clusters == 0) return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.ranks * p.clusters);

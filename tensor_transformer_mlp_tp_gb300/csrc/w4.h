@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include "launch.h"
+#include "w4_few.h"
 
 namespace tpmlp {
 
@@ -38,8 +39,6 @@ struct W4Pack {
   uint8_t* zeros;
   int K, N, group;
 };
-
-constexpr int kW4Cols = 16, kW4Rows = 64;  // of a tile
 
 cudaError_t launch_gemm_w4(const W4Launch& g, const DeviceCtx& ctx, cudaStream_t s);
 cudaError_t launch_quantize_w4(const W4Pack& p, cudaStream_t s);
