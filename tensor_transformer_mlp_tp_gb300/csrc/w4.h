@@ -11,7 +11,7 @@
 #include <stdint.h>
 
 #include "launch.h"
-#include "w4_few.h"
+#include "few_plan_w4.h"
 
 namespace tpmlp {
 

@@ -10,7 +10,7 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 
 PROGRAM = r"""
 #include <stdio.h>
-#include "w4_few.h"
+#include "few_plan_w4.h"
 
 int main() {
   int M, N, K, mats, g32, zeros, fit1, fit2, fit4;
