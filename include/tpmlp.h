@@ -561,7 +561,8 @@ TPMLP_API tpmlp_status tpmlp_dequantize_w4(const void* Q, const void* scales, co
 /* Y [M x N] bf16 = X [M x K] W + bias (bias [N] bf16 or NULL): per group the sum
  * of x (q - z), exact products in fp32, is scaled as a whole and added to an
  * fp32 sum, so the weights are never rounded.  For M <= 8 a token's values are
- * taken to 2^-39 of its largest (exact within 2^-32 of it).  Any M; made for up
+ * taken to 2^-39 of its largest (exact within 2^-32 of it).  Scaled sums are
+ * at Y's own scale, whatever the sizes of X and the scales.  Any M; made for up
  * to a few hundred tokens: a long prompt's product is faster in bf16 on the
  * weights of tpmlp_dequantize_w4.  zeros hold 0..15.  Reads of X, Q, scales and
  * zeros only; Y must not overlap them.  M or N == 0 is an empty call; K == 0 is
