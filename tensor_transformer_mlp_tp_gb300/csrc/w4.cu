@@ -575,12 +575,12 @@ __global__ void __launch_bounds__(256) k_dequantize_w4(const __grid_constant__ W
         const long long at = static_cast<long long>(grp) * p.N + min(col, p.N - 1);
         const __nv_bfloat16 v = static_cast<const __nv_bfloat16*>(p.scales)[at];
         s[h][c] = __nv_bfloat162(v, v);
-        base[h][c] = ZEROS ? w4_base(p.zeros[at] & 15u) : kW4Base8;
+        base[h][c] = w4_base<kW4One>(ZEROS ? p.zeros[at] & 15u : 8u);
       }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t a[4];
-      w4_unpack_bf16(q[j], base[j >> 1][0], base[j >> 1][1], a);
+      w4_unpack_bf16<kW4One>(q[j], base[j >> 1][0], base[j >> 1][1], a);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(a + i), s[j >> 1][i & 1]);

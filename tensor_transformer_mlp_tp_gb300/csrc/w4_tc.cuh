@@ -5,9 +5,11 @@
 // UMMA's rows and up to BT tokens as its columns (128 tokens: one block, plain products only); a cluster of CTAs shares K.
 // Warp 0 copies codes and X (TMA boxes), warp 1 issues, sixteen warps unpack: a lane's 16 bytes of a 16 x 64 tile are
 // registers in the order of the m16n8k16 product's A operand, which is that of tcgen05.st's 16x128b shape, so tiles go to
-// tensor memory by one instruction as the UMMA's A operand.  Codes become bf16 q - z, exact.  Eight warps scale: the UMMAs
-// of a group make a partial sum in TMEM, a thread has those of one column of W, one scale for all of them.  The cluster's
-// sums are joined through distributed shared memory in rank order.
+// tensor memory by one instruction as the UMMA's A operand.  Codes become bf16 (q - z) 2^-11, exact: a group's
+// products with X's largest numbers then sum up below fp32's largest, and 2^11 comes back behind all sums (measured to 2^-130:
+// subnormal products and sums are not flushed).  Eight warps scale: the UMMAs of a group make a partial sum in TMEM, a
+// thread has those of one column of W, one scale for all of them.  The cluster's sums are joined through distributed
+// shared memory in rank order.
 //
 // Measured, K = 4096, N = 16384, groups of 128: 14.2 us for 17 tokens, 17.3 for 64, 25.6 for 128, 49.7 for 256 (groups of 32
 // with zero points: 29.7 for 64).  A stage (128 rows of 256 columns) takes about 1100 cycles, of which its 16 UMMAs are 540:
@@ -23,6 +25,7 @@ namespace tpmlp {
 
 constexpr int kW4TcRanks = 8;  // CTAs of a cluster at most
 constexpr int kW4TcRows = 128;  // of W a stage: two row tiles
+constexpr float kW4TcBack = 0x1p11f;  // what the unpacked weights are too small by (kW4OneLow)
 
 struct W4TcParams {
   CUtensorMap tmX;      // boxes of 64 x box_rows
@@ -273,14 +276,14 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + stage);
       uint32_t a[4 * kWords];
-      uint32_t b0 = kW4Base8, b1 = kW4Base8;
+      uint32_t b0 = w4_base<kW4OneLow>(8u), b1 = b0;
 #pragma unroll
       for (int j = 0; j < kWords; ++j) {
         if (ZEROS && j % STEPS == 0) {
-          b0 = w4_base(zs[j / STEPS * 16] & 15u);
-          b1 = w4_base(zs[j / STEPS * 16 + 8] & 15u);
+          b0 = w4_base<kW4OneLow>(zs[j / STEPS * 16] & 15u);
+          b1 = w4_base<kW4OneLow>(zs[j / STEPS * 16 + 8] & 15u);
         }
-        w4_unpack_bf16(q[j], b0, b1, a + 4 * j);
+        w4_unpack_bf16<kW4OneLow>(q[j], b0, b1, a + 4 * j);
       }
       if (!warp_wait_spin(a_empty + abuf, (static_cast<uint32_t>(st / ABUFS) & 1u) ^ 1u, wc, kSiteW4TcUnpackA)) break;
       tc_fence_after_sync();
@@ -370,6 +373,8 @@ __global__ void __launch_bounds__(W4TcShape<BT>::kThreads, 1) k_gemm_w4_tc(const
       for (int r = 0; r < kW4TcRanks; ++r) {  // in rank order
         v[b][0] += q[r].x; v[b][1] += q[r].y; v[b][2] += q[r].z; v[b][3] += q[r].w;
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[b][i] *= kW4TcBack;
       const void* bias = p.g.w[b].bias;
       if (bias != nullptr && col < N) {
         const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(bias) + col));

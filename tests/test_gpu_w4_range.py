@@ -93,3 +93,40 @@ def test_gated_small_tokens_on_the_largest_scales(M, group, zeros):
     X[:, :8] = 0.75 * 2.0 ** -20
     mats = [pack(W.to(BF16), group, zeros) for W in (Wg, Wu)]
     check_gated(X.to(BF16), mats, K, N, group, binding.ACT_GELU)
+
+
+@pytest.mark.parametrize("M", [1, 8, 9, 24, 40, 100, 150])
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, False), (128, True)])
+def test_large_tokens_on_small_scales(M, group, zeros):
+    """Tokens near the largest number on weights far below one: a group's sum before its scale is past the largest number."""
+    K, N = 392, 136
+    g = torch.Generator(device="cuda").manual_seed(M + group + 1)
+    m = pack((normal(g, K, N) * 2.0 ** -90).to(BF16), group, zeros)
+    check_product((normal(g, M, K) * 2.0 ** 124).to(BF16), m, K, N, group)
+
+
+@pytest.mark.parametrize("M", [2, 12, 70])
+@pytest.mark.parametrize("group,zeros", [(32, False), (128, True)])
+@pytest.mark.parametrize("act", [binding.ACT_SILU, binding.ACT_GELU])
+def test_gated_large_tokens_on_small_scales(M, group, zeros, act):
+    K, N = 392, 136
+    g = torch.Generator(device="cuda").manual_seed(M + group + 2)
+    mats = [pack((normal(g, K, N) * 2.0 ** -95).to(BF16), group, zeros) for _ in range(2)]
+    check_gated((normal(g, M, K) * 2.0 ** 124).to(BF16), mats, K, N, group, act)
+
+
+@pytest.mark.parametrize("M", [1, 8, 16, 64, 128])
+@pytest.mark.parametrize("power", [-116, -124, -128])
+def test_tokens_near_the_smallest_numbers(M, power):
+    """Beside the usual errors, an addition in fp32 is off by up to its smallest step, 2^-149, of sums that are kept 2^-11 times
+    their size."""
+    K, N, group = 1024, 256, 128
+    g = torch.Generator(device="cuda").manual_seed(M)
+    m = pack(normal(g, K, N).to(BF16), group, False)
+    X = (normal(g, M, K).to(F64) * 2.0 ** power).to(BF16)
+    Y = Guarded((M, N))
+    binding.tpmlp_gemm_w4(X, m[0], m[1], group, Y.t)
+    w, x = values(m, K, N, group), X.to(F64)
+    y, e = x @ w, error(x, w, group) + (K + 32) * 2.0 ** -138 * m[1].to(F64).abs().amax(0).clamp(min=1)
+    gated.check("Y", Y.t, (y, e + gated.HALF * (y.abs() + e) + gated.TINY))
+    assert bool((Y.t != 0).any()) and Y.intact()
