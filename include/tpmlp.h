@@ -537,6 +537,7 @@ TPMLP_API tpmlp_status tpmlp_gemm_dx_gated(const void* dG, const void* dU, const
  * for each element and a bf16 scale s and a zero point z for each group of 32,
  * 64 or 128 consecutive rows of a column (the last group may be shorter):
  *   scales [G x N] bf16, zeros [G x N] bytes or NULL (z = 8), G = ceil(K / group).
+ * A zero point is the low four bits of its byte, in every call.
  * Codes Q: tiles of 16 columns x 64 rows, 512 bytes each, tile (nt, kt) at
  * nt ceil(K / 64) + kt; in a tile, with column 8 c + g (g < 8) and row
  * 16 j + 8 r + 2 t + h (t < 4, h < 2), the code is in 32-bit word
@@ -564,9 +565,8 @@ TPMLP_API tpmlp_status tpmlp_dequantize_w4(const void* Q, const void* scales, co
  * taken to 2^-39 of its largest (exact within 2^-32 of it).  Scaled sums are
  * at Y's own scale, whatever the sizes of X and the scales.  Any M; made for up
  * to a few hundred tokens: a long prompt's product is faster in bf16 on the
- * weights of tpmlp_dequantize_w4.  zeros hold 0..15.  Reads of X, Q, scales and
- * zeros only; Y must not overlap them.  M or N == 0 is an empty call; K == 0 is
- * an error. */
+ * weights of tpmlp_dequantize_w4.  Reads of X, Q, scales and zeros only; Y must
+ * not overlap them.  M or N == 0 is an empty call; K == 0 is an error. */
 TPMLP_API tpmlp_status tpmlp_gemm_w4(const void* X, const void* Q, const void* scales, const uint8_t* zeros,
                                      const void* bias, int64_t M, int64_t N, int64_t K, int group, void* Y,
                                      tpmlp_stream_t stream);

@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(W4FewShape<G32, ZEROS>::kThreads, 1) k_gemm_w4
           for (int j0 = 0; j0 < 4; j0 += kSteps, sl += S::kPartBytes) {
             const float s0 = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sl)[g]);
             const float s1 = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(sl)[g + 8]);
-            const uint32_t z0 = w4_base0(ZEROS ? sl[32 + g] : 8u), z1 = w4_base1(ZEROS ? sl[40 + g] : 8u);
+            const uint32_t z0 = w4_base0(ZEROS ? sl[32 + g] & 15u : 8u), z1 = w4_base1(ZEROS ? sl[40 + g] & 15u : 8u);
             float c4[4] = {};
 #pragma unroll
             for (int j = j0; j < j0 + kSteps; ++j) {
