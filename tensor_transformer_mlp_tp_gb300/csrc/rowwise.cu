@@ -1695,7 +1695,7 @@ cudaError_t launch_column_sum(const float* partial, int rows, int cols, void* ou
 }
 
 cudaError_t launch_column_sum_pair(const float* partial, int rows, int cols, void* out0, void* out1, cudaStream_t s) {
-  return launch_after(k_column_sum, (2 * cols + 31) / 32, 256, s, partial, rows, 2 * cols, 2LL * cols, out0, out1, cols, 1);
+  return launch_after(k_column_sum, (2u * static_cast<unsigned>(cols) + 31) / 32, 256, s, partial, rows, 2 * cols, 2LL * cols, out0, out1, cols, 1);
 }
 
 cudaError_t launch_cast_fp8(const void* src, int rows, int cols, bool transpose, int fmt, const float* scale,
