@@ -527,7 +527,9 @@ TPMLP_API tpmlp_status tpmlp_gemm_dh_gated(const void* dY, const void* B, const 
                                            void* workspace, size_t workspace_bytes, tpmlp_stream_t stream);
 
 /* dX = sum_i dG_i Ag_i^T + dU_i Au_i^T.  The other gradients are tpmlp_gemm_wgrad_b (dB from H) and tpmlp_gemm_wgrad_a
- * (dAg from dG, dAu from dU). */
+ * (dAg from dG, dAu from dU).  Without a workspace this step cannot split K: on
+ * few tokens tpmlp_gated_backward, which does, is the faster way (320 tokens of
+ * 1024 x 4096: this step 39 us, the whole backward 42). */
 TPMLP_API tpmlp_status tpmlp_gemm_dx_gated(const void* dG, const void* dU, const void* Ag, const void* Au,
                                            const tpmlp_shape* shape, void* dX, tpmlp_stream_t stream);
 
@@ -543,7 +545,8 @@ TPMLP_API tpmlp_status tpmlp_gemm_dx_gated(const void* dG, const void* dU, const
  * 16 j + 8 r + 2 t + h (t < 4, h < 2), the code is in 32-bit word
  * 4 (4 g + t) + j, bits 4 (c + 2 r) + 16 h and up.  512 ceil(N / 16) ceil(K / 64)
  * bytes; places past K or N hold 8.  (The pages have no counterpart.)
- *   N % 8 == 0, K % 8 == 0, pointers 16-byte aligned. */
+ *   N % 8 == 0, K % 8 == 0, pointers 16-byte aligned.  Larger sizes than those
+ * stated at a call are TPMLP_ERR_UNSUPPORTED. */
 
 /* Q, scales and (when not NULL) zeros of W [K x N] bf16, per group:
  *   zeros == NULL:  s = bf16(a / 7), a the largest magnitude, z = 8;
@@ -551,28 +554,32 @@ TPMLP_API tpmlp_status tpmlp_gemm_dx_gated(const void* dG, const void* dU, const
  *                   hi = max(0, largest), z = rint(-lo / s) within 0..15;
  *   q = rint(w / s) + z within 0..15, halves to even.
  * Range and quotients in fp32; a and hi - lo are kept within 2^-100 and bf16's
- * largest number.  A NaN counts as 0; an infinity takes an end of the codes. */
+ * largest number.  A NaN counts as 0; an infinity takes an end of the codes.
+ * K up to 8388480, N up to 2^30 - 8. */
 TPMLP_API tpmlp_status tpmlp_quantize_w4(const void* W, int64_t K, int64_t N, int group, void* Q, void* scales,
                                          uint8_t* zeros, tpmlp_stream_t stream);
 
-/* The inverse: W = bf16((q - z) s), for the bf16 products of a long prompt. */
+/* The inverse: W = bf16((q - z) s), for the bf16 products of a long prompt.  K and
+ * N as for the quantiser. */
 TPMLP_API tpmlp_status tpmlp_dequantize_w4(const void* Q, const void* scales, const uint8_t* zeros, int64_t K, int64_t N,
                                            int group, void* W, tpmlp_stream_t stream);
 
-/* Y [M x N] bf16 = X [M x K] W + bias (bias [N] bf16 or NULL): per group the sum
- * of x (q - z), exact products in fp32, is scaled as a whole and added to an
- * fp32 sum, so the weights are never rounded.  For M <= 8 a token's values are
- * taken to 2^-39 of its largest (exact within 2^-32 of it).  Scaled sums are
- * at Y's own scale, whatever the sizes of X and the scales.  Any M; made for up
- * to a few hundred tokens: a long prompt's product is faster in bf16 on the
- * weights of tpmlp_dequantize_w4.  Reads of X, Q, scales and zeros only; Y must
- * not overlap them.  M or N == 0 is an empty call; K == 0 is an error. */
+/* Y [M x N] bf16 = X [M x K] W + bias (bias [N] bf16 or NULL): per group (for
+ * M <= 8 per 64 rows of it at most) the sum of x (q - z), exact products in fp32,
+ * is scaled as a whole and added to an fp32 sum, so the weights are never
+ * rounded.  For M <= 8 a token's values are taken to 2^-39 of its largest (exact
+ * within 2^-32 of it).  Scaled sums are at Y's own scale, whatever the sizes of
+ * X and the scales.  M up to 8388480, N and K up to 2^30 - 8; made for up to a
+ * few hundred tokens: a long prompt's product is faster in bf16 on the weights
+ * of tpmlp_dequantize_w4.  Reads of X, Q, scales and zeros only; Y must not
+ * overlap them.  M or N == 0 is an empty call; K == 0 is an error. */
 TPMLP_API tpmlp_status tpmlp_gemm_w4(const void* X, const void* Q, const void* scales, const uint8_t* zeros,
                                      const void* bias, int64_t M, int64_t N, int64_t K, int group, void* Y,
                                      tpmlp_stream_t stream);
 
 /* tpmlp_gemm1_gated on 4-bit weights: H = act(X Wg + bg) * (X Wu + bu), Wg and Wu
- * [d x F] with the same group and both with zero points or both without. */
+ * [d x F] with the same group and both with zero points or both without.  Up to
+ * 4194240 tokens. */
 TPMLP_API tpmlp_status tpmlp_gemm1_gated_w4(const void* X, const void* Qg, const void* g_scales, const uint8_t* g_zeros,
                                             const void* bg, const void* Qu, const void* u_scales,
                                             const uint8_t* u_zeros, const void* bu, int act, int group,

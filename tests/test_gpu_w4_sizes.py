@@ -76,3 +76,34 @@ def test_gated_product_in_several_rounds(M, K, N, group, zeros):
     h, err = a * v[1], ea * v[1].abs() + a.abs() * e[1] + ea * e[1]
     gated.check("H", H.t, (h, err + gated.HALF * (h.abs() + err) + gated.TINY))
     assert H.intact()
+
+
+def test_the_most_tokens_of_a_call():
+    """Up to as many as the header states, and an error past them."""
+    K, N, group = 8, 8, 32
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for most, gated_form in ((8388480, False), (4194240, True)):
+        Q = ref.pack(torch.randint(0, 16, (K, N), generator=g, device="cuda").to(U8))
+        s = torch.ones(1, N, dtype=BF16, device="cuda")
+        w = ref.values(ref.unpack(Q, K, N)[:K, :N], s, None, group)
+        X = torch.zeros(most + 1, K, dtype=BF16, device="cuda")
+        X[torch.arange(most + 1, device="cuda"), torch.arange(most + 1, device="cuda") % K] = 1
+
+        def call(M, Y):
+            if gated_form:
+                binding.tpmlp_gemm1_gated_w4(X[:M], Q, s, Q, s, group, Y, act=binding.ACT_GELU)
+            else:
+                binding.tpmlp_gemm_w4(X[:M], Q, s, group, Y)
+
+        Y = Guarded((most, N))
+        call(most, Y.t)
+        rows = torch.tensor([0, 1, 127, 128, most // 2, most - 129, most - 1], device="cuda")
+        y = w[rows % K]
+        if gated_form:
+            y = gated.act64(y, binding.ACT_GELU)[0] * y
+            gated.check("H", Y.t[rows], (y, 1e-6 * (1 + y.abs() ** 2) + gated.HALF * y.abs() + gated.TINY))
+        else:
+            assert torch.equal(Y.t[rows].to(F64), y)
+        assert Y.intact()
+        with pytest.raises(binding.TpMlpError, match="unsupported"):
+            call(most + 1, torch.empty(most + 1, N, dtype=BF16, device="cuda"))
