@@ -183,9 +183,9 @@ cudaError_t launch_gather_rows(const RowParams& r, const DeviceCtx& ctx, cudaStr
 cudaError_t launch_dropout_bwd(const RowParams& r, float* partial, void* dbias2, cudaStream_t s);
 size_t dropout_bwd_scratch_floats(int rows, int d);
 // out[c] = sum_r partial[r * cols + c] over r < rows, fixed order; bf16 or fp32 output.
-// The same for two outputs side by side: columns 0 .. cols - 1 of a partial row (2 cols floats) to out0, the rest to out1.
-cudaError_t launch_column_sum_pair(const float* partial, int rows, int cols, void* out0, void* out1, cudaStream_t s);
 cudaError_t launch_column_sum(const float* partial, int rows, int cols, void* out, bool out_bf16, cudaStream_t s);
+// The same for two bf16 outputs side by side: columns 0 .. cols - 1 of a partial row (2 cols floats) to out0, the rest to out1.
+cudaError_t launch_column_sum_pair(const float* partial, int rows, int cols, void* out0, void* out1, cudaStream_t s);
 // out[c] (bf16) = sum_r src[r ld + c] for a bf16 matrix [rows x cols] (cols and ld multiples of 8), through
 // `partial` (column_sum_bf16_scratch_floats(rows, cols) floats) in a fixed order.
 cudaError_t launch_column_sum_bf16(const void* src, int rows, int cols, long long ld, float* partial, void* out,

@@ -40,10 +40,12 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 // bytes and 16 apart (conflict-free); lanes past the last token read a row of zeros.  The sums of a round of tiles are joined
 // in a fixed order, the warps' and then the blocks'.
 //
-// Measured (groups of 128): one token of 4096 x 16384 9.7 us (3.6 TB/s; 7.0 without the products), 4 tokens 10.8, 8 14.4;
-// both matrices of the gated form 15.7 (4.4 TB/s; 11.8 without).  Bound by the unpacking: 97 warp instructions for 64 rows of
-// 16 columns, issue 64% of the cycles, the ALU 46%, shared memory 51%.  Not kept: pairs of column tiles that read X once and
-// share a group's scales (10.0 us for one token, 15.6 for 8: fewer warps wait for each copy).
+// Measured (groups of 128): one token of 4096 x 16384 9.8 us (3.5 TB/s; 7.0 without the products), 8 tokens 14.4; both
+// matrices of the gated form 15.9 (4.4 TB/s; 11.8 without).  Bound by a tile's instructions and the start: 90 warp instructions
+// for 64 rows of 16 columns, 36 of which unpack (the others scale, load X, multiply, wait and fetch), issue 53% of the cycles
+// in which an SM has the block, 36% of all under ncu; with more columns, where the start counts less, 64% (N = 65536).  Not kept:
+// pairs of column tiles that read X once and share a group's scales (10.0 us for one token, 15.6 for 8: fewer warps wait for each
+// copy).
 constexpr int kWarps = kW4FewWarps;
 
 struct W4FewParams : W4FewPlan {

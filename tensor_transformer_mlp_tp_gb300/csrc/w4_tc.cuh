@@ -11,11 +11,12 @@
 // thread has those of one column of W, one scale for all of them.  The cluster's sums are joined through distributed
 // shared memory in rank order.
 //
-// Measured, K = 4096, N = 16384, groups of 128: 14.2 us for 17 tokens, 17.3 for 64, 25.6 for 128, 49.7 for 256 (groups of 32
-// with zero points: 29.7 for 64).  A stage (128 rows of 256 columns) takes about 1100 cycles, of which its 16 UMMAs are 540:
-// the chain of copy, unpacking, UMMAs and scaling binds, no part of it alone (each left out by itself: 1 to 2 us less).
-// Eight unpacking warps: 15.2 and 18.6; scaling and unpacking by the same warps 22.7; a third buffer of unpacked stages, at
-// 32 tokens: no change.
+// Measured, K = 4096, N = 16384, groups of 128: 14.4 us for 17 tokens, 17.5 for 64, 25.4 for 128, 49.7 for 256 (groups of 32
+// with zero points: 30.1 for 64); the gated form 22.7 for 16, 29.4 for 64, 114.7 for 256.  A stage (128 rows of 256
+// columns) takes about 1100 cycles, of which its 16 UMMAs are 540: in a stage the chain of copy, unpacking, UMMAs and scaling
+// binds, no part of it alone (each left out by itself: 1 to 2 us less).  At 64 tokens the 16 stages of a CTA are then 17600
+// cycles, half of the time; the other half is start, first copies and the cluster's join.  Eight unpacking warps: 15.2 and
+// 18.6; scaling and unpacking by the same warps 22.7; a third buffer of unpacked stages, at 32 tokens: no change.
 #pragma once
 
 #include "gated.cuh"
