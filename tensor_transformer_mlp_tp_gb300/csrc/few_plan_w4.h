@@ -6,7 +6,8 @@ namespace tpmlp {
 
 constexpr int kW4Cols = 16, kW4Rows = 64;  // of a tile of codes: 512 bytes
 
-// Two tiles of tokens took 17.3 us for 9 tokens and 21.8 for 16 (K = 4096, N = 16384, groups of 128), the UMMA 15.1 and 15.3.
+// Two tiles of tokens took 17.3 us for 9 tokens and 21.8 for 16 (K = 4096, N = 16384, groups of 128), the UMMA 15.1 and 15.3
+// (14.3 since).
 constexpr int kW4FewTokens = 8;
 constexpr int kW4FewWarps = 8;    // of a team
 constexpr int kW4FewTeams = 2;

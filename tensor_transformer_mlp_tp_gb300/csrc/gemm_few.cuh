@@ -5,8 +5,8 @@
 // k-blocks are split over a cluster of CTAs, whose fp32 sums are joined through distributed shared memory in rank order: no
 // workspace, no atomics, the same bits every time.
 //
-// Measured, d = 4096, F = 16384, both products of the gated block (403 MB of weights): 60.9 us for one token (6.6 TB/s, 0.99 of
-// the measured copy rate), 61.9 for 8, 65.8 for 32, 69.5 for 64, 78.5 for 128.  Two CTAs an SM up to 32 rows: while one joins
+// Measured, d = 4096, F = 16384, both products of the gated block (403 MB of weights): 60.3 us for one token (6.6 TB/s, 0.99 of
+// the measured copy rate), 61.1 for 8, 65.3 for 32, 68.6 for 64, 77.5 for 128.  Two CTAs an SM up to 32 rows: while one joins
 // or starts, the other keeps copies in flight.
 //
 // Warp 0 copies (TMA ring), warp 1 issues, warps 2..5 bring the sums from TMEM to shared memory; then every warp finishes
