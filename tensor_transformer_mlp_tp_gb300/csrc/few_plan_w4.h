@@ -33,8 +33,8 @@ struct W4FewPlan {
 // Blocks of a cluster: the number that leaves the busiest SM the least to read, with room for X, for 64 KB of codes in
 // flight (or half of that, if none has room for it), and for two column tiles' sums.  A larger cluster has to save 7% of that
 // for its joins (K = 4096, groups of 128, one token; clusters of two that save nothing: 20480 columns 11.7 -> 14.1 us, 24576
-// 13.2 -> 15.7).  The rest of what it should save is open: clusters of two that read 8% less lose as well (12288 columns 10.9 us,
-// single blocks 8.9).  fit(r): clusters of r blocks that the device holds at once.
+// 13.2 -> 15.7).  Clusters of two that read 8% less still lose (12288 columns 10.9 us, single blocks 8.9), so the right share is
+// larger; which, was not measured.  fit(r): clusters of r blocks that the device holds at once.
 template <typename Fit>
 inline W4FewPlan w4_few_plan(int M, int N, int K, int mats, int fixed, Fit fit) {
   W4FewPlan p{};
